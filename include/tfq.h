@@ -68,6 +68,7 @@ extern "C" {
 #define TF_E_TIMEOUT 6            /* a bounded device-side wait gave up */
 #define TF_E_INTERNAL 7           /* a launch-plan invariant failed on the device (a library bug;
                                      recorded in the status word like TF_E_TIMEOUT) */
+#define TF_E_CACHE_FULL 8         /* not enough free pages in a K/V cache (recorded in the status word) */
 
 #define TF_DTYPE_BF16 0
 #define TF_DTYPE_F32 1
@@ -426,6 +427,194 @@ size_t tf_generate_workspace_bytes(const tf_decoder_desc* d);
 int tf_generate_greedy(const tf_decoder_desc* d, const int32_t* prompt, int64_t prompt_len, int64_t max_new,
                        int max_draft, int max_ngram, int32_t* out, int64_t* n_out, int64_t* n_steps,
                        int64_t* n_accepted, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- K/V cache */
+
+/*
+ * A paged cache of keys and values, shared by the layers of one decoder. Everything
+ * is device memory owned by the caller:
+ *   data  bf16 [n_layers][2][n_pages][n_kv][page_size][head_dim]; [.][0] K, [.][1] V.
+ *         One head's rows of a page are contiguous, so a page of a head is one copy.
+ *   book  int32, three tables in this order (tf_kvcache_book_elems of them in all):
+ *           len   [n_seqs]             tokens held by each sequence slot
+ *           refs  [n_pages]            how many table entries name a page (0: free)
+ *           table [n_seqs][max_pages]  pages of each slot; -1 past ceil(len / page_size)
+ * The calls below keep two rules, which a caller who writes the book keeps too: entries
+ * past a slot's pages are -1, and a slot's last page, when not full, is named by no
+ * other slot (so that appending to it changes nobody else's tokens).
+ * tf_kvcache describes it on the host and is read during a call only.
+ *
+ * Free pages are taken lowest index first, in slot order of the call's list, so the
+ * book after a call depends on nothing but the book before it and the arguments.
+ */
+typedef struct tf_kvcache {
+    uint32_t magic;     /* TF_KVCACHE_MAGIC once filled by tf_kvcache_init */
+    int32_t n_layers;
+    int32_t n_kv;       /* key/value heads, 1..256 */
+    int32_t head_dim;   /* 64, 128 or 256 */
+    int32_t page_size;  /* token rows of a page: 16, 32, 64 or 128 */
+    int32_t n_seqs;     /* sequence slots, 1..1024 */
+    int32_t n_pages;
+    int32_t max_pages;  /* page-table columns of a slot */
+    void* data;         /* 16-byte aligned */
+    int32_t* book;      /* 4-byte aligned */
+} tf_kvcache;
+#define TF_KVCACHE_MAGIC 0x314B5654u /* "TVK1" */
+#define TF_MAX_DRAFT_ROWS 64 /* rows of a sequence that one attention or keep call takes */
+
+/* Bytes of `data` and int32 elements of `book`; 0 for an unsupported shape. */
+size_t tf_kvcache_data_bytes(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages);
+size_t tf_kvcache_book_elems(int64_t n_pages, int n_seqs, int64_t max_pages);
+
+/*
+ * Fill a descriptor (host only). The data is left as it is; the book too: empty it with
+ * tf_kvcache_reset before first use, or hand one over that holds to the rules above.
+ * Requirements: the ranges stated at the fields, n_pages * page_size < 2^31,
+ * max_pages * page_size < 2^31, and fewer than 2^31 rows (head_dim elements each) in all.
+ */
+int tf_kvcache_init(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages, int n_seqs,
+                    int64_t max_pages, void* data, size_t data_bytes, int32_t* book, size_t book_elems,
+                    tf_kvcache* desc);
+
+/* Empty every slot and free every page (the data stays as it is). */
+int tf_kvcache_reset(const tf_kvcache* c, void* stream);
+
+/* Workspace of the three calls below (256-aligned, zeroed once; its status word is read
+ * with tf_workspace_status). They and tf_tree_attn_run leave more than zeros behind in
+ * theirs: give each kind of call a workspace of its own, apart from the projections'. */
+size_t tf_kvcache_workspace_bytes(const tf_kvcache* c);
+
+/*
+ * Make room for new rows: slot seqs[b] grows by q_start[b + 1] - q_start[b] tokens, b < B.
+ *   seqs      device int32 [B], distinct slots; 1 <= B <= n_seqs
+ *   q_start   device int32 [B + 1], nondecreasing, within [0, M]: sequence b's rows among
+ *             the M rows of the caller's activations (a step's drafts, or a prompt's chunk)
+ *   masks     device uint64 [M] or NULL: the rows' tree masks (see tf_tree_attn_run)
+ *   slots     device int32 [M], output: page * page_size + row in the page for each row
+ *             (what tf_qk_norm_rope_run stores to); -1 for rows of no sequence
+ *   positions device int32 [M], output (may be NULL): the row's position in its sequence,
+ *             length before the call + depth in the tree (popcount(mask) - 1; without
+ *             masks, the row's index in its block); 0 for rows of no sequence
+ * All or nothing: with too few free pages (TF_E_CACHE_FULL in the status word), a slot out
+ * of range or named twice, a length beyond max_pages, a q_start out of order, or a shared
+ * unfilled last page (TF_E_INVALID_ARG), the book stays as it was and every slot is -1.
+ */
+int tf_kvcache_extend(const tf_kvcache* c, const int32_t* seqs, const int32_t* q_start, int64_t B, int64_t M,
+                      const uint64_t* masks, int32_t* slots, int32_t* positions, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/*
+ * Fork, reorder and free slots in one step. parent: device int32 [n_seqs]; afterwards slot
+ * s holds what slot parent[s] held before the call (parent[s] = s: unchanged; -1: empty).
+ * Full pages are shared; of an unfilled last page one slot keeps the original (the parent
+ * itself when it stays, else the lowest slot that takes it) and every other gets a fresh
+ * page with the filled rows copied, in all layers. Pages that no slot names any more are
+ * free after the call; they are not used by the same call. Errors are all or nothing as above
+ * (TF_E_CACHE_FULL, or TF_E_INVALID_ARG for a parent or a table entry out of range).
+ */
+int tf_kvcache_fork(const tf_kvcache* c, const int32_t* parent, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Compact after a verify step: of the last T_b = q_start[b + 1] - q_start[b] tokens of slot
+ * seqs[b] keep n_keep[b], the rows keep[q_start[b] + j], j < n_keep[b] (strictly increasing
+ * indices among the T_b), moved up to follow the tokens before them in all layers; the slot's
+ * length becomes its length before the block + n_keep[b] and pages past it are freed.
+ *   keep device int32 [M], n_keep device int32 [B]; the rest as for tf_kvcache_extend
+ * A sequence whose arguments do not hold (T_b > TF_MAX_DRAFT_ROWS or beyond its length, keep
+ * not increasing or out of range, a slot out of range, a page of the block that is shared)
+ * is left as it was and TF_E_INVALID_ARG recorded; the others are done. A slot named twice
+ * leaves every sequence as it was.
+ */
+int tf_kvcache_keep(const tf_kvcache* c, const int32_t* seqs, const int32_t* q_start, const int32_t* keep,
+                    const int32_t* n_keep, int64_t B, int64_t M, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- norm + rotation */
+
+/*
+ * Rotation frequencies in the form the kernels take: turns[i] = inv_freq[i] / (2 pi) in
+ * 64-bit fixed point (units of 2^-64 turn), so that position * turns[i] modulo 2^64 is the
+ * angle exactly reduced, however far the position. Host only; inv_freq in radians a token,
+ * finite, |inv_freq| < 2 pi. A scaled schedule is a matter of the inv_freq handed over.
+ */
+int tf_rope_turns(const double* inv_freq, int64_t n, uint64_t* turns);
+
+/*
+ * One pass over the rows of a qkv projection, row m = [q heads | k heads | v heads]:
+ *   q, k heads: x * rsqrt(mean(x^2) + eps) * gamma over the head (skipped when its gamma is
+ *   NULL), then the rotation of the head's first rot_dim elements by positions[m] * inv_freq:
+ *     (a, b) -> (a cos - b sin, b cos + a sin), pairs (i, i + rot_dim / 2), or (2i, 2i + 1)
+ *     with `interleaved` non-zero;
+ *   q heads go to q [M][n_q * head_dim]; k and v heads (v as they are) to the cache's layer
+ *   at slots[m]. fp32 inside, one rounding to bf16 at the end.
+ *   qkv       bf16 [M], leading dimension ld >= (n_q + 2 n_kv) * head_dim, 16-byte aligned rows
+ *   positions device int32 [M], any sign
+ *   slots     device int32 [M] (tf_kvcache_extend); negative: nothing is stored for the row;
+ *             outside the cache: the same, and TF_E_INVALID_ARG in the status word. Two rows
+ *             of one call must not name the same slot.
+ *   turns     device uint64 [rot_dim / 2] (tf_rope_turns), may be NULL when rot_dim is 0
+ *   rot_dim   0..head_dim, a multiple of 16
+ *   q         bf16 [M][n_q * head_dim], 16-byte aligned; may not overlap qkv
+ *   ws        256 zeroed, 256-aligned bytes (status word)
+ * 1 <= n_q <= 1024, 1 <= M < 2^31 / 64. TF_RUN_PDL: gammas and turns may be read before the
+ * previous kernel on the stream has finished.
+ */
+int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, const uint16_t* q_gamma,
+                        const uint16_t* k_gamma, float eps, const int32_t* positions, const uint64_t* turns,
+                        int rot_dim, int interleaved, uint16_t* q, const tf_kvcache* c, int layer,
+                        const int32_t* slots, void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------- attention */
+
+/*
+ * Attention of drafted rows over the cache. Sequence b's rows are q_start[b] .. q_start[b + 1)
+ * of q (T_b of them, at most max_rows) and the last T_b tokens of slot seqs[b]: the rows'
+ * own keys and values are in the cache already (tf_kvcache_extend, tf_qk_norm_rope_run).
+ * With base = len[seqs[b]] - T_b, row i sees every token before base, and token base + j
+ * where bit j of masks[row] is set (normally its ancestors in the tree of drafts, and itself);
+ * masks NULL: j <= i, a chain. One token is T_b = 1.
+ *   o[row][h] = sum_j softmax_j(scale * q[row][h] . k_j[h / (n_q / n_kv)]) v_j[...]
+ * over the tokens the row sees; a row that sees none gives zeros. Tokens it does not see take
+ * no part, whatever is stored there (NaN and infinities included).
+ *   q       bf16 [M], leading dimension ldq >= n_q * head_dim (a multiple of 8), 16-byte aligned
+ *   o       bf16 [M][n_q * head_dim], 16-byte aligned; rows of no sequence are left as they were
+ *   n_q     a multiple of n_kv, at most 64 query heads to a key/value head
+ *   B       1..1024; a slot may appear twice
+ *   max_rows  1..TF_MAX_DRAFT_ROWS, no T_b above it
+ *   scale   finite
+ *   ws      tf_tree_attn_workspace_bytes(c, n_q, B, max_rows) bytes
+ * A sequence whose arguments do not hold (slot out of range, more rows than max_rows or than
+ * tokens, q_start out of order) gives zero rows (none where the rows themselves are out of
+ * range), a page out of range counts as zero keys and values; both record TF_E_INVALID_ARG.
+ * fp32 scores, sums and accumulators; the softmax weights are rounded to bf16 for the product
+ * with V (relative error 2^-9 each, under the output's own rounding). A row's last bits may
+ * depend on the other sequences of the call, since the context is split over the GPU by the
+ * whole call's length; the same call gives the same bits every time.
+ */
+size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int max_rows);
+int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
+                     const int32_t* seqs, const int32_t* q_start, int64_t B, int max_rows, const uint64_t* masks,
+                     float scale, uint16_t* o, void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------- log probabilities */
+
+/*
+ * For each row of logits v [M][N] (bf16 or fp32 by dtype, leading dimension ld >= N):
+ *   logp[m][i]     = v[m][targets[m][i]] - lse_m, lse_m = log sum_n exp(v[m][n]), i < n_targets
+ *   entropy[m]     = -sum_n p_n log p_n, p_n = exp(v[m][n] - lse_m)  (may be NULL)
+ *   top_idx[m][j]  = index of the j-th largest logit (ties: lower index first), j < top_k
+ *   top_logp[m][j] = its log probability
+ * in one pass over the logits. A target outside [0, N) gives NaN and TF_E_INVALID_ARG in the
+ * status word, except -1, which asks for nothing and gives 0. -inf logits have probability
+ * 0; a row of nothing else has logp -inf and entropy 0. A NaN or +inf in a row makes its
+ * logp, entropy and top_logp NaN; NaN ranks below every number, as in tf_argmax_rows.
+ *   M 1..2^31 / 64, N 1..2^31 - 1; 0 <= top_k <= min(32, N); 0 <= n_targets <= 1024
+ *   (targets, logp may be NULL when n_targets is 0, top_idx and top_logp when top_k is 0)
+ *   ws  tf_logprobs_workspace_bytes(M, N, top_k) bytes
+ */
+size_t tf_logprobs_workspace_bytes(int64_t M, int64_t N, int top_k);
+int tf_logprobs_rows(const void* v, int dtype, int64_t ld, int64_t M, int64_t N, const int32_t* targets,
+                     int n_targets, int top_k, float* logp, float* entropy, int32_t* top_idx, float* top_logp,
+                     void* ws, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------- diagnostics */
 

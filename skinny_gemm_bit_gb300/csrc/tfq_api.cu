@@ -528,6 +528,7 @@ const char* tf_status_str(int status)
     case TF_E_CUDA: return "TF_E_CUDA";
     case TF_E_TIMEOUT: return "TF_E_TIMEOUT";
     case TF_E_INTERNAL: return "TF_E_INTERNAL";
+    case TF_E_CACHE_FULL: return "TF_E_CACHE_FULL";
     default: return "TF_E_UNKNOWN";
     }
 }
@@ -1271,7 +1272,8 @@ int tf_workspace_status(void* ws, void* stream)
     if (e != cudaSuccess)
         return cuda_fail(e, "tf_workspace_status");
     if (st != 0)
-        fail(st, "a device-side wait gave up (status recorded in the workspace)");
+        fail(st, st == TF_E_TIMEOUT ? "a device-side wait gave up (status recorded in the workspace)"
+                                    : "recorded in the workspace by a kernel that used it");
     return st;
 }
 

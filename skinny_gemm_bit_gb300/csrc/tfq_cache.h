@@ -1,0 +1,52 @@
+// The K/V cache as its kernels see it, and the checks its entry points share.
+#pragma once
+
+#include "tfq_internal.h"
+
+namespace tfq {
+
+constexpr int kMaxSeqs = 1024;
+constexpr int kMaxDraftRows = TF_MAX_DRAFT_ROWS;
+
+// Passed by value. Row r of page p of head h (K: kv = 0, V: 1) of a layer starts at element
+//   ((((layer * 2 + kv) * n_pages + p) * n_kv + h) * page_size + r) * head_dim   (64 bits)
+struct CacheView {
+    uint16_t* data;
+    int32_t *len, *refs, *table;
+    int n_layers, n_kv, head_dim, page_size, page_shift;
+    int n_seqs, n_pages, max_pages;
+
+    __host__ __device__ int64_t row_of(int layer, int kv, int page, int head) const
+    {
+        return (((int64_t)(layer * 2 + kv) * n_pages + page) * n_kv + head) * page_size;
+    }
+};
+
+// Validate a descriptor filled by tf_kvcache_init; fills `v` (tfq_kvcache.cu).
+int check_cache(const tf_kvcache* c, const char* name, CacheView* v);
+// ws at least `need` bytes, 256-byte aligned
+int check_ws(const void* ws, size_t ws_bytes, size_t need, const char* name);
+
+inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Launch with (or without) programmatic dependent launch on the previous kernel.
+template <class... KArgs, class... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,
+                       Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+__device__ __forceinline__ void record_status(int* status, int code) { atomicCAS(status, 0, code); }
+
+}  // namespace tfq

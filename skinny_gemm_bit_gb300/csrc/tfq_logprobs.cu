@@ -1,0 +1,467 @@
+// Log probabilities of given tokens, entropy and top alternatives of rows of logits, in one
+// pass over them.
+//
+// A row's softmax statistics are kept as (m, n, r, w): the largest value m, how many elements
+// equal it, and over the others r = sum e^(x - m) and w = sum e^(x - m) (x - m). Then
+//   lse = m + log(n + r),  logp = (x - m) - log(n + r),  entropy = log(n + r) - w / (n + r)
+// and for n = 1 log(n + r) is log1p(r): the largest element's own 1 never meets the sum of
+// the rest, so a sure row's entropy keeps its digits.
+//
+// Bound by memory for many rows (two or four bytes a logit against about six instructions) and
+// by latency for few. A row is cut into 16-byte units; few rows are spread over a thread-block
+// cluster each, whose first block joins the parts through distributed shared memory. A warp
+// shares one m, so the sums need no test per element: a batch of kBatch units a lane whose
+// largest value lies below m (all but a few of them) takes the straight path.
+//
+// The top k: each thread notes its largest value. The k-th largest of those is a bound that at
+// least k elements reach, and only threads whose largest reaches it can hold one of the k; their
+// units are read again (from L2) by whole warps, which keep sorted lists of 32 (value, index)
+// keys, one a lane. About k threads pass, so this costs the row's latency, not its bandwidth.
+#include <cmath>
+#include <cooperative_groups.h>
+
+#include "tfq_cache.h"
+#include "tfq_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace tfq {
+namespace {
+
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kBatch = 4;        // 16-byte units a lane takes at once
+constexpr int kMaxCluster = 8;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct LpParams {
+    const void* v;
+    int64_t ld, M, N;
+    const int32_t* targets;
+    int n_targets, top_k;
+    float *logp, *entropy;
+    int32_t* top_idx;
+    float* top_logp;
+    int* status;
+};
+
+struct Stats {
+    float m, n, r, w;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Takes the sums of (m, n, r, w) over to a larger reference.
+__device__ __forceinline__ void rebase(Stats& s, float m)
+{
+    if (s.m == m)
+        return;
+    if (s.m == -INFINITY) {  // nothing yet
+        s = Stats{m, 0.f, s.r, s.w};  // r, w are 0, or NaN
+        return;
+    }
+    const float d = s.m - m, all = s.n + s.r, f = expf(d);
+    s.w = f == 0.f ? 0.f * s.w : (s.w + d * all) * f;
+    s.r = all * f;
+    s.n = 0.f;
+    s.m = m;
+}
+
+__device__ __forceinline__ Stats join(Stats a, Stats b)
+{
+    const float m = fmaxf(a.m, b.m);
+    rebase(a, m);
+    rebase(b, m);
+    return Stats{m, a.n + b.n, a.r + b.r, a.w + b.w};
+}
+
+// A value as an unsigned integer of the same order; -0 as +0, NaN as 0, below every number.
+__device__ __forceinline__ uint32_t order_of(float x)
+{
+    if (x != x)
+        return 0u;
+    const uint32_t u = __float_as_uint(x + 0.f);  // -0 + 0 = +0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float of_order(uint32_t u)
+{
+    return u == 0u ? NAN : __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
+}
+
+// (order, lower index first); 0 is no element
+__device__ __forceinline__ uint64_t key_of(float x, int64_t n) { return (uint64_t)order_of(x) << 32 | (0xFFFFFFFFu - (uint32_t)n); }
+
+template <class K>
+__device__ __forceinline__ K shfl_xor(K v, int o)
+{
+    return __shfl_xor_sync(0xffffffffu, v, o);
+}
+
+// The lanes' keys, largest first (bitonic sort of 32).
+template <class K>
+__device__ __forceinline__ K sort32(K v, int lane)
+{
+#pragma unroll
+    for (int size = 2; size <= 32; size *= 2)
+#pragma unroll
+        for (int o = size / 2; o > 0; o /= 2) {
+            const K u = shfl_xor(v, o);
+            const bool up = ((lane & size) != 0) == ((lane & o) == 0);  // keep the smaller
+            v = (u < v) == up ? u : v;
+        }
+    return v;
+}
+
+// The 32 largest of two sorted lists, sorted.
+template <class K>
+__device__ __forceinline__ K merge32(K a, K b, int lane)
+{
+    const K br = __shfl_sync(0xffffffffu, b, 31 - lane);
+    K v = a > br ? a : br;
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) {
+        const K u = shfl_xor(v, o);
+        const bool up = (lane & o) != 0;
+        v = (u < v) == up ? u : v;
+    }
+    return v;
+}
+
+// Joins the warps' sorted lists in shared memory; the result is in lists[0]. All threads.
+template <class K>
+__device__ void join_lists(K (*lists)[32], int warp, int lane)
+{
+    for (int half = kLpWarps / 2; half > 0; half /= 2) {
+        __syncthreads();
+        if (warp < half)
+            lists[warp][lane] = merge32(lists[warp][lane], lists[warp + half][lane], lane);
+    }
+    __syncthreads();
+}
+
+template <class T>
+struct Unit;  // 16 bytes of logits
+
+template <>
+struct Unit<uint16_t> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void widen(const uint4& u, float (&f)[8])
+    {
+        f[0] = bf16lo_f32(u.x), f[1] = bf16hi_f32(u.x), f[2] = bf16lo_f32(u.y), f[3] = bf16hi_f32(u.y);
+        f[4] = bf16lo_f32(u.z), f[5] = bf16hi_f32(u.z), f[6] = bf16lo_f32(u.w), f[7] = bf16hi_f32(u.w);
+    }
+    static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
+};
+
+template <>
+struct Unit<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void widen(const uint4& u, float (&f)[4])
+    {
+        f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
+    }
+    static __device__ __forceinline__ float one(const float* p) { return *p; }
+};
+
+// The row's units: unit u covers elements u * N - lead .. + N; the first and the last may reach
+// beyond the row and are read element by element, with -inf in the place of what is not there.
+template <class T>
+struct RowUnits {
+    static constexpr int N = Unit<T>::N;
+    const T* row;
+    int64_t n, units;
+    int lead;
+
+    __device__ RowUnits(const T* r, int64_t count) : row(r), n(count)
+    {
+        lead = (int)(reinterpret_cast<uintptr_t>(r) % 16 / sizeof(T));
+        units = (lead + n + N - 1) / N;
+    }
+    __device__ __forceinline__ int64_t first(int64_t u) const { return u * N - lead; }
+    __device__ __forceinline__ void load(int64_t u, float (&f)[N]) const
+    {
+        const int64_t at = first(u);
+        if (at >= 0 && at + N <= n) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + at);
+            Unit<T>::widen(v, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                f[i] = at + i >= 0 && at + i < n ? Unit<T>::one(row + at + i) : -INFINITY;
+        }
+    }
+};
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2)
+        v = fmaxf(v, shfl_xor(v, o));
+    return v;
+}
+
+struct Shared {
+    uint64_t lists[kLpWarps][32];
+    uint32_t maxima[kLpWarps][32];
+    Stats stats[kLpWarps];
+    // what the cluster's first block reads of the others
+    Stats part;
+    uint64_t top[32];
+    int flagged, flags[kLpThreads];
+};
+
+template <class T>
+__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_constant__ LpParams p)
+{
+    constexpr int N = Unit<T>::N;
+    __shared__ Shared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int parts = cluster.num_blocks(), part = cluster.block_rank();
+    const int64_t m = blockIdx.x / parts;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const T* row = static_cast<const T*>(p.v) + m * p.ld;
+    const RowUnits<T> ru(row, p.N);
+    // this block's units, whole batches of the block's
+    const int64_t u0 = ru.units * part / parts, u1 = ru.units * (part + 1) / parts;
+
+    Stats s{-INFINITY, 0.f, 0.f, 0.f};
+    float big = -INFINITY;  // this thread's largest
+    for (int64_t u = u0 + threadIdx.x; u - lane < u1; u += kBatch * kLpThreads) {
+        float f[kBatch][N];
+        float top = -INFINITY, low = INFINITY;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (u + b * kLpThreads >= u1)
+                continue;
+            ru.load(u + b * kLpThreads, f[b]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                top = fmaxf(top, f[b][i]);
+                low = fminf(low, f[b][i]);
+            }
+        }
+        big = fmaxf(big, top);
+        // straight: nothing here reaches m, no product below overflows (-inf and the type's
+        // lowest value, as masks write them, go the other way), and m is not so far from 0 that
+        // the rounding of m log2 e (2^-11 at 1e4) is more than a first-order matter
+        const bool plain = __all_sync(0xffffffffu, top < s.m && low > -1e38f && fabsf(s.m) < 1e4f);
+        if (plain) {
+            // z = x log2 e - ref is rounded once; what rounding m log2 e to ref left over is
+            // the same for every element and put right on the batch's sums
+            const float ref = s.m * kLog2e, left = fmaf(s.m, kLog2e, -ref);
+            float r[4] = {}, w[4] = {};
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (u + b * kLpThreads >= u1)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float z = fmaf(f[b][i], kLog2e, -ref), e = ex2(z);
+                    r[i & 3] += e;
+                    w[i & 3] = fmaf(e, z, w[i & 3]);
+                }
+            }
+            const float rs = (r[0] + r[1]) + (r[2] + r[3]), ws = (w[0] + w[1]) + (w[2] + w[3]);
+            const float fix = 1.f - left * kLn2;
+            s.r = fmaf(rs, fix, s.r);
+            s.w = fmaf(fmaf(-left, rs, ws) * fix, kLn2, s.w);
+        } else {
+            const float wm = warp_max(top);
+            if (wm > s.m)
+                rebase(s, wm);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (u + b * kLpThreads >= u1)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float x = f[b][i];
+                    if (x == s.m && x != -INFINITY) {
+                        s.n += 1.f;
+                    } else if (x != -INFINITY) {  // NaN takes this way
+                        const float z = x - s.m, e = expf(z);
+                        s.r += e;
+                        s.w = fmaf(e, fmaxf(z, -200.f), s.w);
+                    }
+                }
+            }
+        }
+    }
+    const bool nan = s.r != s.r;
+    // +inf: no finite statistics
+    if (s.m == INFINITY)
+        s.r = NAN;
+    for (int o = 16; o > 0; o /= 2) {
+        const Stats t{shfl_xor(s.m, o), shfl_xor(s.n, o), shfl_xor(s.r, o), shfl_xor(s.w, o)};
+        s = join(s, t);
+    }
+    if (lane == 0)
+        sh.stats[warp] = s;
+    if (threadIdx.x == 0)
+        sh.flagged = 0;
+
+    if (p.top_k > 0) {
+        // a value that at least top_k elements of this block's part reach: 0, which everything
+        // reaches, where fewer threads than that have a unit, or where a NaN hides an element
+        const bool has = (int64_t)threadIdx.x < u1 - u0;
+        const uint32_t mine = has ? order_of(big) : 0u;
+        sh.maxima[warp][lane] = sort32(mine, lane);
+        const bool any_nan = __syncthreads_or(nan);
+        join_lists(sh.maxima, warp, lane);
+        const uint32_t bound = any_nan ? 0u : sh.maxima[0][p.top_k - 1];
+        if (has && mine >= bound)
+            sh.flags[atomicAdd(&sh.flagged, 1)] = threadIdx.x;
+        __syncthreads();
+        uint64_t list = 0;          // lane i: the warp's i-th largest key
+        uint64_t last = 0;          // its top_k-th
+        for (int f = warp; f < sh.flagged; f += kLpWarps) {
+            const int64_t own = u0 + sh.flags[f];
+            for (int64_t v0 = own; v0 < u1; v0 += 32 * kLpThreads) {
+                const int64_t v = v0 + (int64_t)lane * kLpThreads;
+                float x[N];
+                if (v < u1)
+                    ru.load(v, x);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const int64_t at = ru.first(v) + i;
+                    uint64_t key = 0;
+                    if (v < u1 && at >= 0 && at < p.N && order_of(x[i]) >= bound)
+                        key = key_of(x[i], at);
+                    unsigned come = __ballot_sync(0xffffffffu, key > last);
+                    while (come) {
+                        const uint64_t k = __shfl_sync(0xffffffffu, key, __ffs(come) - 1);
+                        come &= come - 1;
+                        if (k <= last)
+                            continue;
+                        const int before = __popc(__ballot_sync(0xffffffffu, list > k));
+                        const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+                        list = lane < before ? list : lane == before ? k : up;
+                        last = __shfl_sync(0xffffffffu, list, p.top_k - 1);
+                    }
+                }
+            }
+        }
+        sh.lists[warp][lane] = list;
+        join_lists(sh.lists, warp, lane);
+    } else {
+        __syncthreads();
+    }
+    if (warp == 0) {
+        s = lane < kLpWarps ? sh.stats[lane] : Stats{-INFINITY, 0.f, 0.f, 0.f};
+        for (int o = 16; o > 0; o /= 2) {
+            const Stats t{shfl_xor(s.m, o), shfl_xor(s.n, o), shfl_xor(s.r, o), shfl_xor(s.w, o)};
+            s = join(s, t);
+        }
+        if (lane == 0)
+            sh.part = s;
+        if (p.top_k > 0)
+            sh.top[lane] = sh.lists[0][lane];
+    }
+    if (parts > 1)
+        cluster.sync();
+    if (part == 0 && warp == 0) {
+        uint64_t list = p.top_k > 0 ? sh.top[lane] : 0;
+        for (int o = 1; o < parts; ++o) {
+            const Shared* other = cluster.map_shared_rank(&sh, o);
+            s = join(s, other->part);
+            if (p.top_k > 0)
+                list = merge32(list, other->top[lane], lane);
+        }
+        // n is 0 only for a row without numbers above -inf
+        const bool none = s.m == -INFINITY && s.r == 0.f;
+        const float log_total = s.n == 1.f ? log1pf(s.r) : logf(s.n) + log1pf(s.r / s.n);
+        const bool odd = !(s.r == s.r) || (s.n == 0.f && !none);  // NaN or +inf in the row
+        if (p.entropy != nullptr && lane == 0)
+            p.entropy[m] = odd ? NAN : none ? 0.f : log_total - s.w / (s.n + s.r);
+        for (int i = lane; i < p.n_targets; i += 32) {
+            const int64_t t = p.targets[m * p.n_targets + i];
+            float y;
+            if (t >= 0 && t < p.N) {
+                y = odd ? NAN : none ? -INFINITY : Unit<T>::one(row + t) - s.m - log_total;
+            } else {
+                y = t == -1 ? 0.f : NAN;
+                if (t != -1)
+                    record_status(p.status, TF_E_INVALID_ARG);
+            }
+            p.logp[m * p.n_targets + i] = y;
+        }
+        if (lane < p.top_k) {
+            p.top_idx[m * p.top_k + lane] = (int32_t)(0xFFFFFFFFu - (uint32_t)list);
+            p.top_logp[m * p.top_k + lane] = odd ? NAN : none ? -INFINITY : of_order((uint32_t)(list >> 32)) - s.m - log_total;
+        }
+    }
+    if (parts > 1)
+        cluster.sync();  // the others' shared memory stays until it has been read
+}
+
+bool logprobs_shape_ok(int64_t M, int64_t N, int top_k)
+{
+    return M >= 1 && M < ((int64_t)1 << 31) / 64 && N >= 1 && N <= INT32_MAX && top_k >= 0 && top_k <= 32 && top_k <= N;
+}
+
+}  // namespace
+}  // namespace tfq
+
+using namespace tfq;
+
+extern "C" {
+
+size_t tf_logprobs_workspace_bytes(int64_t M, int64_t N, int top_k)
+{
+    if (!logprobs_shape_ok(M, N, top_k)) {
+        report_error(TF_E_UNSUPPORTED_SHAPE, "tf_logprobs_workspace_bytes: M, N or top_k out of range");
+        return 0;
+    }
+    return 256;
+}
+
+int tf_logprobs_rows(const void* v, int dtype, int64_t ld, int64_t M, int64_t N, const int32_t* targets,
+                     int n_targets, int top_k, float* logp, float* entropy, int32_t* top_idx, float* top_logp,
+                     void* ws, size_t ws_bytes, void* stream)
+{
+    const char* name = "tf_logprobs_rows";
+    if (v == nullptr)
+        return report_error(TF_E_INVALID_ARG, "%s: v is NULL", name);
+    if (dtype != TF_DTYPE_BF16 && dtype != TF_DTYPE_F32)
+        return report_error(TF_E_INVALID_ARG, "%s: dtype must be TF_DTYPE_BF16 or TF_DTYPE_F32", name);
+    if (!logprobs_shape_ok(M, N, top_k) || n_targets < 0 || n_targets > 1024 || ld < N)
+        return report_error(TF_E_UNSUPPORTED_SHAPE,
+                            "%s: need 1 <= M < 2^25, 1 <= N < 2^31, ld >= N, 0 <= top_k <= min(32, N), 0 <= n_targets <= 1024",
+                            name);
+    if (!is_aligned(v, dtype == TF_DTYPE_F32 ? 4 : 2))
+        return report_error(TF_E_INVALID_ARG, "%s: v misaligned", name);
+    if ((n_targets > 0 && (targets == nullptr || logp == nullptr)) ||
+        (top_k > 0 && (top_idx == nullptr || top_logp == nullptr)))
+        return report_error(TF_E_INVALID_ARG, "%s: NULL output or targets", name);
+    int rc = check_ws(ws, ws_bytes, 256, name);
+    if (rc)
+        return rc;
+    const LpParams p{v, ld, M, N, targets, n_targets, top_k, logp, entropy, top_idx, top_logp, static_cast<int*>(ws)};
+    // few rows: as many blocks a row (a power of two up to 8) as the SMs hold, if each still
+    // has a batch of units a thread
+    int parts = 1;
+    const int64_t batch = (int64_t)kLpThreads * kBatch * (dtype == TF_DTYPE_F32 ? 4 : 8);
+    while (parts < kMaxCluster && M * parts * 2 <= device_sms() && N >= batch * parts)
+        parts *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(M * parts));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = dtype == TF_DTYPE_F32 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<float>, p)
+                                                : cudaLaunchKernelEx(&cfg, logprobs_kernel<uint16_t>, p);
+    return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
+}
+
+}  // extern "C"

@@ -8,6 +8,7 @@ raises, there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -24,6 +25,7 @@ TF_E_BAD_PACK = 4
 TF_E_CUDA = 5
 TF_E_TIMEOUT = 6
 TF_E_INTERNAL = 7
+TF_E_CACHE_FULL = 8
 TF_DTYPE_BF16 = 0
 TF_DTYPE_F32 = 1
 TF_RUN_PDL = 1
@@ -38,6 +40,8 @@ TF_TUNE_STAGES = 3
 TF_TUNE_WARPS = 4
 TF_TUNE_MODE = 5
 TF_TUNE_CHAIN = 6
+TF_KVCACHE_MAGIC = 0x314B5654
+TF_MAX_DRAFT_ROWS = 64
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
@@ -60,6 +64,11 @@ class tf_decoder_desc(ctypes.Structure):
     _fields_ = [("n_layers", I32), ("d_model", I64), ("d_ff", I64), ("q_dim", I64), ("kv_dim", I64),
                 ("vocab", I64), ("eps", ctypes.c_float), ("layers", ctypes.POINTER(tf_decoder_layer)),
                 ("final_norm", P), ("readout", tf_qweight)]
+
+
+class tf_kvcache(ctypes.Structure):
+    _fields_ = [("magic", ctypes.c_uint32), ("n_layers", I32), ("n_kv", I32), ("head_dim", I32), ("page_size", I32),
+                ("n_seqs", I32), ("n_pages", I32), ("max_pages", I32), ("data", P), ("book", P)]
 
 
 class TfqError(RuntimeError):
@@ -106,6 +115,25 @@ _SIGS = {
     "tf_generate_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(tf_decoder_desc)]),
     "tf_generate_greedy": (ctypes.c_int, [ctypes.POINTER(tf_decoder_desc), P, I64, I64, ctypes.c_int, ctypes.c_int, P,
                                           P, P, P, P, ctypes.c_size_t, P]),
+    "tf_kvcache_data_bytes": (SZ, [ctypes.c_int] * 4 + [I64]),
+    "tf_kvcache_book_elems": (SZ, [I64, ctypes.c_int, I64]),
+    "tf_kvcache_init": (ctypes.c_int, [ctypes.c_int] * 4 + [I64, ctypes.c_int, I64, P, SZ, P, SZ,
+                                                           ctypes.POINTER(tf_kvcache)]),
+    "tf_kvcache_reset": (ctypes.c_int, [ctypes.POINTER(tf_kvcache), P]),
+    "tf_kvcache_workspace_bytes": (SZ, [ctypes.POINTER(tf_kvcache)]),
+    "tf_kvcache_extend": (ctypes.c_int, [ctypes.POINTER(tf_kvcache), P, P, I64, I64, P, P, P, P, SZ, P]),
+    "tf_kvcache_fork": (ctypes.c_int, [ctypes.POINTER(tf_kvcache), P, P, SZ, P]),
+    "tf_kvcache_keep": (ctypes.c_int, [ctypes.POINTER(tf_kvcache), P, P, P, P, I64, I64, P, SZ, P]),
+    "tf_rope_turns": (ctypes.c_int, [P, I64, P]),
+    "tf_qk_norm_rope_run": (ctypes.c_int, [P, I64, I64, ctypes.c_int, P, P, ctypes.c_float, P, P, ctypes.c_int,
+                                           ctypes.c_int, P, ctypes.POINTER(tf_kvcache), ctypes.c_int, P, P, SZ,
+                                           ctypes.c_uint, P]),
+    "tf_tree_attn_workspace_bytes": (SZ, [ctypes.POINTER(tf_kvcache), ctypes.c_int, I64, ctypes.c_int]),
+    "tf_tree_attn_run": (ctypes.c_int, [P, I64, I64, ctypes.c_int, ctypes.POINTER(tf_kvcache), ctypes.c_int, P, P, I64,
+                                        ctypes.c_int, P, ctypes.c_float, P, P, SZ, ctypes.c_uint, P]),
+    "tf_logprobs_workspace_bytes": (SZ, [I64, I64, ctypes.c_int]),
+    "tf_logprobs_rows": (ctypes.c_int, [P, ctypes.c_int, I64, I64, I64, P, ctypes.c_int, ctypes.c_int, P, P, P, P, P,
+                                        SZ, P]),
     "tf_workspace_status": (ctypes.c_int, [P, P]),
     "tf_selftest_wait_timeout": (ctypes.c_int, [P, ctypes.c_uint64, P]),
     "tf_tune_set": (ctypes.c_int, [ctypes.c_int, ctypes.c_int]),
@@ -502,3 +530,244 @@ def tf_generate_greedy(dec: Decoder, prompt, max_new: int, max_draft: int = 7, m
                                     out.ctypes.data, ctypes.byref(n_out), ctypes.byref(n_steps), ctypes.byref(n_acc),
                                     _ptr(ws), ws.numel(), _stream(stream)))
     return out[:n_out.value].tolist(), n_steps.value, n_acc.value
+
+
+# ---------------------------------------------------------------- K/V cache
+
+def _raw_stream(stream, device) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(stream):
+    """What a call allocates for itself (outputs, a workspace) is allocated on its own stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _want(t: torch.Tensor, dtype, device, least: int, name: str) -> int:
+    """The address of a contiguous tensor of `least` or more elements on the call's device."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {least} elements on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _want_ws(ws: torch.Tensor, device) -> int:
+    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device} (tfq.workspace)")
+    return ws.data_ptr()
+
+
+def _current(device):
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current CUDA device "
+                         f"(torch.cuda.set_device, or a torch.cuda.device block)")
+
+
+class KVCache:
+    """A paged K/V cache: bf16 data [layers, 2, pages, kv heads, page rows, head dim] and an int32
+    book [n_seqs lengths | pages' reference counts | n_seqs x max_pages page table]."""
+
+    def __init__(self, data: torch.Tensor, book: torch.Tensor, n_seqs: int, max_pages: int):
+        if data.dim() != 6 or data.shape[1] != 2 or data.dtype != torch.bfloat16 or not data.is_contiguous():
+            raise ValueError("data must be a contiguous bfloat16 tensor [layers, 2, pages, kv heads, page rows, head dim]")
+        if book.dim() != 1 or book.dtype != torch.int32 or not book.is_contiguous() or book.device != data.device:
+            raise ValueError("book must be a contiguous 1-D int32 tensor on the data's device")
+        L, _, n_pages, n_kv, page, hd = data.shape
+        self.data, self.book, self.device = data, book, data.device
+        self.n_seqs, self.max_pages, self.n_pages = n_seqs, max_pages, n_pages
+        self.n_layers, self.n_kv, self.page_size, self.head_dim = L, n_kv, page, hd
+        self.desc = tf_kvcache()
+        _check(lib().tf_kvcache_init(L, n_kv, hd, page, n_pages, n_seqs, max_pages, data.data_ptr(),
+                                     data.numel() * 2, book.data_ptr(), book.numel(), ctypes.byref(self.desc)))
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def create(cls, n_layers: int, n_kv: int, head_dim: int, page_size: int, n_pages: int, n_seqs: int, max_pages: int,
+               device="cuda") -> "KVCache":
+        """An empty cache in tensors of its own."""
+        data = torch.zeros((n_layers, 2, n_pages, n_kv, page_size, head_dim), dtype=torch.bfloat16, device=device)
+        book = torch.zeros(n_seqs + n_pages + n_seqs * max_pages, dtype=torch.int32, device=device)
+        book[n_seqs + n_pages:] = -1
+        return cls(data, book, n_seqs, max_pages)
+
+    @property
+    def len(self) -> torch.Tensor:
+        return self.book[:self.n_seqs]
+
+    @property
+    def refs(self) -> torch.Tensor:
+        return self.book[self.n_seqs:self.n_seqs + self.n_pages]
+
+    @property
+    def table(self) -> torch.Tensor:
+        at = self.n_seqs + self.n_pages
+        return self.book[at:at + self.n_seqs * self.max_pages].view(self.n_seqs, self.max_pages)
+
+
+def tf_kvcache_workspace_bytes(cache: KVCache) -> int:
+    return lib().tf_kvcache_workspace_bytes(cache.ref)
+
+
+def _cache_ws(cache, ws, stream):
+    if ws is not None:
+        return ws
+    with _on(stream):
+        return workspace(tf_kvcache_workspace_bytes(cache), cache.device)
+
+
+def tf_kvcache_reset(cache: KVCache, stream=None):
+    _current(cache.device)
+    _check(lib().tf_kvcache_reset(cache.ref, _raw_stream(stream, cache.device)))
+
+
+def tf_kvcache_extend(cache: KVCache, seqs, q_start, rows: int, masks=None, slots=None, positions=None, ws=None,
+                      stream=None):
+    """(slots, positions), int32 [rows] each: room for the new rows of the slots `seqs`."""
+    dev = cache.device
+    _current(dev)
+    B = seqs.numel()
+    with _on(stream):
+        if slots is None:
+            slots = torch.empty(rows, dtype=torch.int32, device=dev)
+        if positions is None:
+            positions = torch.empty(rows, dtype=torch.int32, device=dev)
+    ws = _cache_ws(cache, ws, stream)
+    _check(lib().tf_kvcache_extend(
+        cache.ref, _want(seqs, torch.int32, dev, 1, "seqs"), _want(q_start, torch.int32, dev, B + 1, "q_start"), B, rows,
+        None if masks is None else _want(masks, torch.int64, dev, rows, "masks"),
+        _want(slots, torch.int32, dev, rows, "slots"), _want(positions, torch.int32, dev, rows, "positions"),
+        _want_ws(ws, dev), ws.numel(), _raw_stream(stream, dev)))
+    return slots, positions
+
+
+def tf_kvcache_fork(cache: KVCache, parent, ws=None, stream=None):
+    """Slot s takes what slot parent[s] holds (-1: nothing), int32 [n_seqs]."""
+    dev = cache.device
+    _current(dev)
+    ws = _cache_ws(cache, ws, stream)
+    _check(lib().tf_kvcache_fork(cache.ref, _want(parent, torch.int32, dev, cache.n_seqs, "parent"), _want_ws(ws, dev),
+                                 ws.numel(), _raw_stream(stream, dev)))
+
+
+def tf_kvcache_keep(cache: KVCache, seqs, q_start, keep, n_keep, ws=None, stream=None):
+    """Of each slot's last q_start[b + 1] - q_start[b] tokens keep the n_keep[b] that `keep` lists."""
+    dev = cache.device
+    _current(dev)
+    B, M = seqs.numel(), keep.numel()
+    ws = _cache_ws(cache, ws, stream)
+    _check(lib().tf_kvcache_keep(
+        cache.ref, _want(seqs, torch.int32, dev, 1, "seqs"), _want(q_start, torch.int32, dev, B + 1, "q_start"),
+        _want(keep, torch.int32, dev, 1, "keep"), _want(n_keep, torch.int32, dev, B, "n_keep"), B, M,
+        _want_ws(ws, dev), ws.numel(), _raw_stream(stream, dev)))
+
+
+# ---------------------------------------------------------------- norm + rotation, attention
+
+class RopeTable:
+    """Rotation frequencies on the device: inv_freq (radians a token, fp64) of rot_dim / 2 pairs,
+    the pairs (i, i + rot_dim / 2) of a head, or (2 i, 2 i + 1) with pairs=True."""
+
+    def __init__(self, inv_freq, pairs: bool = False, device="cuda"):
+        f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        turns = np.zeros(f.size, dtype=np.uint64)
+        _check(lib().tf_rope_turns(f.ctypes.data, f.size, turns.ctypes.data))
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.rot_dim = 2 * f.size
+        self.pairs = bool(pairs)
+
+
+def tf_qk_norm_rope_run(qkv: torch.Tensor, cache: KVCache, layer: int, positions, slots, rope: RopeTable, q_gamma=None,
+                        k_gamma=None, eps: float = 1e-6, n_q=None, out=None, ws=None, flags: int = 0,
+                        stream=None) -> torch.Tensor:
+    """q [M, n_q * head_dim], normalised and rotated; k and v go to the cache's layer at `slots`."""
+    dev, hd = cache.device, cache.head_dim
+    _current(dev)
+    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.dtype is not torch.bfloat16 or qkv.device != dev:
+        raise ValueError(f"qkv must be bfloat16 [M, (n_q + 2 n_kv) * head_dim] on {dev} with unit column stride")
+    M = qkv.shape[0]
+    if n_q is None:
+        n_q = qkv.shape[1] // hd - 2 * cache.n_kv
+    if n_q < 1 or (n_q + 2 * cache.n_kv) * hd > qkv.shape[1]:
+        raise ValueError(f"qkv has {qkv.shape[1]} columns, too few for {n_q} + 2 * {cache.n_kv} heads of {hd}")
+    with _on(stream):
+        if out is None:
+            out = torch.empty((M, n_q * hd), dtype=torch.bfloat16, device=dev)
+        if ws is None:
+            ws = workspace(256, dev)
+    _check(lib().tf_qk_norm_rope_run(
+        qkv.data_ptr(), qkv.stride(0) if M > 1 else qkv.shape[1] // 8 * 8, M, n_q,
+        None if q_gamma is None else _want(q_gamma, torch.bfloat16, dev, hd, "q_gamma"),
+        None if k_gamma is None else _want(k_gamma, torch.bfloat16, dev, hd, "k_gamma"), eps,
+        _want(positions, torch.int32, dev, M, "positions"), _want(rope.turns, torch.int64, dev, 0, "rope.turns"),
+        rope.rot_dim, rope.pairs, _want(out, torch.bfloat16, dev, M * n_q * hd, "out"), cache.ref, layer,
+        _want(slots, torch.int32, dev, M, "slots"), _want_ws(ws, dev), ws.numel(), flags, _raw_stream(stream, dev)))
+    return out
+
+
+def tf_tree_attn_workspace_bytes(cache: KVCache, n_q: int, B: int, max_rows: int) -> int:
+    return lib().tf_tree_attn_workspace_bytes(cache.ref, n_q, B, max_rows)
+
+
+def tf_tree_attn_run(q: torch.Tensor, cache: KVCache, layer: int, seqs, q_start, masks=None, max_rows: int = TF_MAX_DRAFT_ROWS,
+                     scale=None, out=None, ws=None, flags: int = 0, stream=None) -> torch.Tensor:
+    """o [M, n_q * head_dim]: attention of the drafted rows q over the cache (scale: head_dim ** -0.5)."""
+    dev, hd = cache.device, cache.head_dim
+    _current(dev)
+    if q.dim() != 2 or q.stride(1) != 1 or q.dtype is not torch.bfloat16 or q.device != dev or q.shape[1] % hd != 0:
+        raise ValueError(f"q must be bfloat16 [M, n_q * {hd}] on {dev} with unit column stride")
+    M, n_q, B = q.shape[0], q.shape[1] // hd, seqs.numel()
+    with _on(stream):
+        if out is None:
+            out = torch.empty((M, n_q * hd), dtype=torch.bfloat16, device=dev)
+        if ws is None:
+            ws = workspace(tf_tree_attn_workspace_bytes(cache, n_q, B, max_rows), dev)
+    _check(lib().tf_tree_attn_run(
+        q.data_ptr(), q.stride(0) if M > 1 else q.shape[1], M, n_q, cache.ref, layer,
+        _want(seqs, torch.int32, dev, 1, "seqs"), _want(q_start, torch.int32, dev, B + 1, "q_start"), B, max_rows,
+        None if masks is None else _want(masks, torch.int64, dev, M, "masks"), hd ** -0.5 if scale is None else scale,
+        _want(out, torch.bfloat16, dev, M * n_q * hd, "out"), _want_ws(ws, dev), ws.numel(), flags,
+        _raw_stream(stream, dev)))
+    return out
+
+
+# ---------------------------------------------------------------- log probabilities
+
+def tf_logprobs_workspace_bytes(M: int, N: int, top_k: int) -> int:
+    return lib().tf_logprobs_workspace_bytes(M, N, top_k)
+
+
+def tf_logprobs_rows(v: torch.Tensor, targets=None, top_k: int = 0, logp=None, entropy=None, top_idx=None, top_logp=None,
+                     ws=None, stream=None):
+    """(logp [M, targets], entropy [M], top_idx [M, top_k], top_logp [M, top_k]) of logits [M, N]."""
+    dev = v.device
+    _current(dev)
+    if v.dim() != 2 or v.stride(1) != 1 or (v.dtype is not torch.bfloat16 and v.dtype is not torch.float32):
+        raise ValueError("v must be bfloat16 or float32 [M, N] with unit column stride")
+    M, N = v.shape
+    nt = 0
+    if targets is not None:
+        if targets.shape[0] != M or targets.dim() > 2:
+            raise ValueError("targets must be int32 [M] or [M, n]")
+        nt = 1 if targets.dim() == 1 else targets.shape[1]
+    with _on(stream):
+        if logp is None and targets is not None:
+            logp = torch.empty(targets.shape, dtype=torch.float32, device=dev)
+        if entropy is None:
+            entropy = torch.empty(M, dtype=torch.float32, device=dev)
+        if top_k > 0 and top_idx is None:
+            top_idx = torch.empty((M, top_k), dtype=torch.int32, device=dev)
+        if top_k > 0 and top_logp is None:
+            top_logp = torch.empty((M, top_k), dtype=torch.float32, device=dev)
+        if ws is None:
+            ws = workspace(tf_logprobs_workspace_bytes(M, N, top_k), dev)
+    _check(lib().tf_logprobs_rows(
+        v.data_ptr(), TF_DTYPE_F32 if v.dtype is torch.float32 else TF_DTYPE_BF16, v.stride(0) if M > 1 else N, M, N,
+        None if nt == 0 else _want(targets, torch.int32, dev, M * nt, "targets"), nt, top_k,
+        None if nt == 0 else _want(logp, torch.float32, dev, M * nt, "logp"),
+        _want(entropy, torch.float32, dev, M, "entropy"),
+        None if top_k < 1 else _want(top_idx, torch.int32, dev, M * top_k, "top_idx"),
+        None if top_k < 1 else _want(top_logp, torch.float32, dev, M * top_k, "top_logp"), _want_ws(ws, dev), ws.numel(),
+        _raw_stream(stream, dev)))
+    return logp, entropy, top_idx, top_logp
