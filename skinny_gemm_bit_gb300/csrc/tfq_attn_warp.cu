@@ -420,8 +420,8 @@ template <int HD, int RW>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream, bool pdl)
 {
     const size_t smem = Cfg<HD>::smem(p.B);
-    const cudaError_t e = cudaFuncSetAttribute(tree_attn_warp_kernel<HD, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)Cfg<HD>::smem(kMaxAttnSeqs));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(tree_attn_warp_kernel<HD, RW>, (int)Cfg<HD>::smem(kMaxAttnSeqs), done);
     if (e != cudaSuccess)
         return e;
     return launch_pdl(tree_attn_warp_kernel<HD, RW>, dim3(device_sms()), dim3(kCtaThreads), smem, stream, pdl, p, map);

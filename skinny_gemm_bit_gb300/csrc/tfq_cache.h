@@ -1,6 +1,8 @@
 // The K/V cache as its kernels see it, and the checks its entry points share.
 #pragma once
 
+#include <atomic>
+
 #include "tfq_internal.h"
 
 namespace tfq {
@@ -45,6 +47,23 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+// Raise a kernel's dynamic shared-memory limit, once for each device. `done` is the kernel's own.
+template <class Kernel>
+cudaError_t allow_smem(Kernel* kernel, int bytes, std::atomic<uint64_t>& done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit != 0 && (done.load(std::memory_order_relaxed) & bit))
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 __device__ __forceinline__ void record_status(int* status, int code) { atomicCAS(status, 0, code); }

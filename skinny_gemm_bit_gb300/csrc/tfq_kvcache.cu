@@ -636,8 +636,8 @@ int tf_kvcache_fork(const tf_kvcache* c, const int32_t* parent, void* ws, size_t
         return rc;
     const size_t smem = (size_t)v.n_seqs * kForkCols * sizeof(int32_t);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fork_apply_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kMaxSeqs * kForkCols * (int)sizeof(int32_t));
+        static std::atomic<uint64_t> done{0};
+        const cudaError_t e = allow_smem(fork_apply_kernel, kMaxSeqs * kForkCols * (int)sizeof(int32_t), done);
         if (e != cudaSuccess)
             return launched(e, name);
     }

@@ -535,9 +535,7 @@ def tf_generate_greedy(dec: Decoder, prompt, max_new: int, max_draft: int = 7, m
 # ---------------------------------------------------------------- K/V cache
 
 def _raw_stream(stream, device) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _on(stream):
@@ -545,24 +543,20 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _want(t: torch.Tensor, dtype, device, least: int, name: str) -> int:
+def _want(t: torch.Tensor, dtype, index: int, least: int, name: str) -> int:
     """The address of a contiguous tensor of `least` or more elements on the call's device."""
-    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or t.numel() < least:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {least} elements on {device}, "
+    if t.dtype is not dtype or t.get_device() != index or t.numel() < least or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {least} elements on cuda:{index}, "
                          f"got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _want_ws(ws: torch.Tensor, device) -> int:
-    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device} (tfq.workspace)")
-    return ws.data_ptr()
-
-
-def _current(device):
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+def _current(device) -> int:
+    """The call's device index, which must be the current device's."""
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {device}, which is not the current CUDA device "
                          f"(torch.cuda.set_device, or a torch.cuda.device block)")
+    return device.index
 
 
 class KVCache:
@@ -626,41 +620,40 @@ def tf_kvcache_extend(cache: KVCache, seqs, q_start, rows: int, masks=None, slot
                       stream=None):
     """(slots, positions), int32 [rows] each: room for the new rows of the slots `seqs`."""
     dev = cache.device
-    _current(dev)
+    at = _current(dev)
     B = seqs.numel()
-    with _on(stream):
-        if slots is None:
-            slots = torch.empty(rows, dtype=torch.int32, device=dev)
-        if positions is None:
-            positions = torch.empty(rows, dtype=torch.int32, device=dev)
+    if slots is None or positions is None:
+        with _on(stream):
+            slots = torch.empty(rows, dtype=torch.int32, device=dev) if slots is None else slots
+            positions = torch.empty(rows, dtype=torch.int32, device=dev) if positions is None else positions
     ws = _cache_ws(cache, ws, stream)
     _check(lib().tf_kvcache_extend(
-        cache.ref, _want(seqs, torch.int32, dev, 1, "seqs"), _want(q_start, torch.int32, dev, B + 1, "q_start"), B, rows,
-        None if masks is None else _want(masks, torch.int64, dev, rows, "masks"),
-        _want(slots, torch.int32, dev, rows, "slots"), _want(positions, torch.int32, dev, rows, "positions"),
-        _want_ws(ws, dev), ws.numel(), _raw_stream(stream, dev)))
+        cache.ref, _want(seqs, torch.int32, at, 1, "seqs"), _want(q_start, torch.int32, at, B + 1, "q_start"), B, rows,
+        None if masks is None else _want(masks, torch.int64, at, rows, "masks"),
+        _want(slots, torch.int32, at, rows, "slots"), _want(positions, torch.int32, at, rows, "positions"),
+        _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), _raw_stream(stream, dev)))
     return slots, positions
 
 
 def tf_kvcache_fork(cache: KVCache, parent, ws=None, stream=None):
     """Slot s takes what slot parent[s] holds (-1: nothing), int32 [n_seqs]."""
     dev = cache.device
-    _current(dev)
+    at = _current(dev)
     ws = _cache_ws(cache, ws, stream)
-    _check(lib().tf_kvcache_fork(cache.ref, _want(parent, torch.int32, dev, cache.n_seqs, "parent"), _want_ws(ws, dev),
+    _check(lib().tf_kvcache_fork(cache.ref, _want(parent, torch.int32, at, cache.n_seqs, "parent"), _want(ws, torch.uint8, at, 1, "ws"),
                                  ws.numel(), _raw_stream(stream, dev)))
 
 
 def tf_kvcache_keep(cache: KVCache, seqs, q_start, keep, n_keep, ws=None, stream=None):
     """Of each slot's last q_start[b + 1] - q_start[b] tokens keep the n_keep[b] that `keep` lists."""
     dev = cache.device
-    _current(dev)
+    at = _current(dev)
     B, M = seqs.numel(), keep.numel()
     ws = _cache_ws(cache, ws, stream)
     _check(lib().tf_kvcache_keep(
-        cache.ref, _want(seqs, torch.int32, dev, 1, "seqs"), _want(q_start, torch.int32, dev, B + 1, "q_start"),
-        _want(keep, torch.int32, dev, 1, "keep"), _want(n_keep, torch.int32, dev, B, "n_keep"), B, M,
-        _want_ws(ws, dev), ws.numel(), _raw_stream(stream, dev)))
+        cache.ref, _want(seqs, torch.int32, at, 1, "seqs"), _want(q_start, torch.int32, at, B + 1, "q_start"),
+        _want(keep, torch.int32, at, 1, "keep"), _want(n_keep, torch.int32, at, B, "n_keep"), B, M,
+        _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), _raw_stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- norm + rotation, attention
@@ -683,26 +676,25 @@ def tf_qk_norm_rope_run(qkv: torch.Tensor, cache: KVCache, layer: int, positions
                         stream=None) -> torch.Tensor:
     """q [M, n_q * head_dim], normalised and rotated; k and v go to the cache's layer at `slots`."""
     dev, hd = cache.device, cache.head_dim
-    _current(dev)
-    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.dtype is not torch.bfloat16 or qkv.device != dev:
+    at = _current(dev)
+    if qkv.dim() != 2 or qkv.stride(1) != 1 or qkv.dtype is not torch.bfloat16 or qkv.get_device() != at:
         raise ValueError(f"qkv must be bfloat16 [M, (n_q + 2 n_kv) * head_dim] on {dev} with unit column stride")
     M = qkv.shape[0]
     if n_q is None:
         n_q = qkv.shape[1] // hd - 2 * cache.n_kv
     if n_q < 1 or (n_q + 2 * cache.n_kv) * hd > qkv.shape[1]:
         raise ValueError(f"qkv has {qkv.shape[1]} columns, too few for {n_q} + 2 * {cache.n_kv} heads of {hd}")
-    with _on(stream):
-        if out is None:
-            out = torch.empty((M, n_q * hd), dtype=torch.bfloat16, device=dev)
-        if ws is None:
-            ws = workspace(256, dev)
+    if out is None or ws is None:
+        with _on(stream):
+            out = torch.empty((M, n_q * hd), dtype=torch.bfloat16, device=dev) if out is None else out
+            ws = workspace(256, dev) if ws is None else ws
     _check(lib().tf_qk_norm_rope_run(
         qkv.data_ptr(), qkv.stride(0) if M > 1 else qkv.shape[1] // 8 * 8, M, n_q,
-        None if q_gamma is None else _want(q_gamma, torch.bfloat16, dev, hd, "q_gamma"),
-        None if k_gamma is None else _want(k_gamma, torch.bfloat16, dev, hd, "k_gamma"), eps,
-        _want(positions, torch.int32, dev, M, "positions"), _want(rope.turns, torch.int64, dev, 0, "rope.turns"),
-        rope.rot_dim, rope.pairs, _want(out, torch.bfloat16, dev, M * n_q * hd, "out"), cache.ref, layer,
-        _want(slots, torch.int32, dev, M, "slots"), _want_ws(ws, dev), ws.numel(), flags, _raw_stream(stream, dev)))
+        None if q_gamma is None else _want(q_gamma, torch.bfloat16, at, hd, "q_gamma"),
+        None if k_gamma is None else _want(k_gamma, torch.bfloat16, at, hd, "k_gamma"), eps,
+        _want(positions, torch.int32, at, M, "positions"), _want(rope.turns, torch.int64, at, 0, "rope.turns"),
+        rope.rot_dim, rope.pairs, _want(out, torch.bfloat16, at, M * n_q * hd, "out"), cache.ref, layer,
+        _want(slots, torch.int32, at, M, "slots"), _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), flags, _raw_stream(stream, dev)))
     return out
 
 
@@ -714,20 +706,19 @@ def tf_tree_attn_run(q: torch.Tensor, cache: KVCache, layer: int, seqs, q_start,
                      scale=None, out=None, ws=None, flags: int = 0, stream=None) -> torch.Tensor:
     """o [M, n_q * head_dim]: attention of the drafted rows q over the cache (scale: head_dim ** -0.5)."""
     dev, hd = cache.device, cache.head_dim
-    _current(dev)
-    if q.dim() != 2 or q.stride(1) != 1 or q.dtype is not torch.bfloat16 or q.device != dev or q.shape[1] % hd != 0:
+    at = _current(dev)
+    if q.dim() != 2 or q.stride(1) != 1 or q.dtype is not torch.bfloat16 or q.get_device() != at or q.shape[1] % hd != 0:
         raise ValueError(f"q must be bfloat16 [M, n_q * {hd}] on {dev} with unit column stride")
     M, n_q, B = q.shape[0], q.shape[1] // hd, seqs.numel()
-    with _on(stream):
-        if out is None:
-            out = torch.empty((M, n_q * hd), dtype=torch.bfloat16, device=dev)
-        if ws is None:
-            ws = workspace(tf_tree_attn_workspace_bytes(cache, n_q, B, max_rows), dev)
+    if out is None or ws is None:
+        with _on(stream):
+            out = torch.empty((M, n_q * hd), dtype=torch.bfloat16, device=dev) if out is None else out
+            ws = workspace(tf_tree_attn_workspace_bytes(cache, n_q, B, max_rows), dev) if ws is None else ws
     _check(lib().tf_tree_attn_run(
         q.data_ptr(), q.stride(0) if M > 1 else q.shape[1], M, n_q, cache.ref, layer,
-        _want(seqs, torch.int32, dev, 1, "seqs"), _want(q_start, torch.int32, dev, B + 1, "q_start"), B, max_rows,
-        None if masks is None else _want(masks, torch.int64, dev, M, "masks"), hd ** -0.5 if scale is None else scale,
-        _want(out, torch.bfloat16, dev, M * n_q * hd, "out"), _want_ws(ws, dev), ws.numel(), flags,
+        _want(seqs, torch.int32, at, 1, "seqs"), _want(q_start, torch.int32, at, B + 1, "q_start"), B, max_rows,
+        None if masks is None else _want(masks, torch.int64, at, M, "masks"), hd ** -0.5 if scale is None else scale,
+        _want(out, torch.bfloat16, at, M * n_q * hd, "out"), _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), flags,
         _raw_stream(stream, dev)))
     return out
 
@@ -742,7 +733,7 @@ def tf_logprobs_rows(v: torch.Tensor, targets=None, top_k: int = 0, logp=None, e
                      ws=None, stream=None):
     """(logp [M, targets], entropy [M], top_idx [M, top_k], top_logp [M, top_k]) of logits [M, N]."""
     dev = v.device
-    _current(dev)
+    at = _current(dev)
     if v.dim() != 2 or v.stride(1) != 1 or (v.dtype is not torch.bfloat16 and v.dtype is not torch.float32):
         raise ValueError("v must be bfloat16 or float32 [M, N] with unit column stride")
     M, N = v.shape
@@ -751,23 +742,19 @@ def tf_logprobs_rows(v: torch.Tensor, targets=None, top_k: int = 0, logp=None, e
         if targets.shape[0] != M or targets.dim() > 2:
             raise ValueError("targets must be int32 [M] or [M, n]")
         nt = 1 if targets.dim() == 1 else targets.shape[1]
-    with _on(stream):
-        if logp is None and targets is not None:
-            logp = torch.empty(targets.shape, dtype=torch.float32, device=dev)
-        if entropy is None:
-            entropy = torch.empty(M, dtype=torch.float32, device=dev)
-        if top_k > 0 and top_idx is None:
-            top_idx = torch.empty((M, top_k), dtype=torch.int32, device=dev)
-        if top_k > 0 and top_logp is None:
-            top_logp = torch.empty((M, top_k), dtype=torch.float32, device=dev)
-        if ws is None:
-            ws = workspace(tf_logprobs_workspace_bytes(M, N, top_k), dev)
+    if (logp is None and nt > 0) or entropy is None or (top_k > 0 and (top_idx is None or top_logp is None)) or ws is None:
+        with _on(stream):
+            logp = torch.empty(targets.shape, dtype=torch.float32, device=dev) if logp is None and nt > 0 else logp
+            entropy = torch.empty(M, dtype=torch.float32, device=dev) if entropy is None else entropy
+            top_idx = torch.empty((M, top_k), dtype=torch.int32, device=dev) if top_k > 0 and top_idx is None else top_idx
+            top_logp = torch.empty((M, top_k), dtype=torch.float32, device=dev) if top_k > 0 and top_logp is None else top_logp
+            ws = workspace(tf_logprobs_workspace_bytes(M, N, top_k), dev) if ws is None else ws
     _check(lib().tf_logprobs_rows(
         v.data_ptr(), TF_DTYPE_F32 if v.dtype is torch.float32 else TF_DTYPE_BF16, v.stride(0) if M > 1 else N, M, N,
-        None if nt == 0 else _want(targets, torch.int32, dev, M * nt, "targets"), nt, top_k,
-        None if nt == 0 else _want(logp, torch.float32, dev, M * nt, "logp"),
-        _want(entropy, torch.float32, dev, M, "entropy"),
-        None if top_k < 1 else _want(top_idx, torch.int32, dev, M * top_k, "top_idx"),
-        None if top_k < 1 else _want(top_logp, torch.float32, dev, M * top_k, "top_logp"), _want_ws(ws, dev), ws.numel(),
+        None if nt == 0 else _want(targets, torch.int32, at, M * nt, "targets"), nt, top_k,
+        None if nt == 0 else _want(logp, torch.float32, at, M * nt, "logp"),
+        _want(entropy, torch.float32, at, M, "entropy"),
+        None if top_k < 1 else _want(top_idx, torch.int32, at, M * top_k, "top_idx"),
+        None if top_k < 1 else _want(top_logp, torch.float32, at, M * top_k, "top_logp"), _want(ws, torch.uint8, at, 1, "ws"), ws.numel(),
         _raw_stream(stream, dev)))
     return logp, entropy, top_idx, top_logp
