@@ -11,7 +11,8 @@
 // by latency for few. A row is cut into 16-byte units; few rows are spread over a thread-block
 // cluster each, whose first block joins the parts through distributed shared memory. A warp
 // shares one m, so the sums need no test per element: a batch of kBatch units a lane whose
-// largest value lies below m (all but a few of them) takes the straight path.
+// largest value lies below m (all but a few of them) takes the straight path. The next batch's
+// loads are under way while one is summed.
 //
 // The top k: each thread notes its largest value. The k-th largest of those is a bound that at
 // least k elements reach, and only threads whose largest reaches it can hold one of the k; their
@@ -28,10 +29,10 @@ namespace cg = cooperative_groups;
 namespace tfq {
 namespace {
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kBatch = 4;        // 16-byte units a lane takes at once
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8;  // at most kLpWarps: a warp reads a part's list
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct LpParams {
@@ -156,6 +157,19 @@ struct Unit<uint16_t> {
         f[0] = bf16lo_f32(u.x), f[1] = bf16hi_f32(u.x), f[2] = bf16lo_f32(u.y), f[3] = bf16hi_f32(u.y);
         f[4] = bf16lo_f32(u.z), f[5] = bf16hi_f32(u.z), f[6] = bf16lo_f32(u.w), f[7] = bf16hi_f32(u.w);
     }
+    // largest and smallest of the units a, b (pairs at once; NaN is passed over)
+    struct Range {
+        __nv_bfloat162 hi, lo;
+    };
+    static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
+    static __device__ __forceinline__ Range range(const uint4& u)
+    {
+        const __nv_bfloat162 a = pair(u.x), b = pair(u.y), c = pair(u.z), d = pair(u.w);
+        return {__hmax2(__hmax2(a, b), __hmax2(c, d)), __hmin2(__hmin2(a, b), __hmin2(c, d))};
+    }
+    static __device__ __forceinline__ Range both(const Range& a, const Range& b) { return {__hmax2(a.hi, b.hi), __hmin2(a.lo, b.lo)}; }
+    static __device__ __forceinline__ float top(const Range& r) { return fmaxf(__low2float(r.hi), __high2float(r.hi)); }
+    static __device__ __forceinline__ float low(const Range& r) { return fminf(__low2float(r.lo), __high2float(r.lo)); }
     static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 };
 
@@ -166,36 +180,19 @@ struct Unit<float> {
     {
         f[0] = __uint_as_float(u.x), f[1] = __uint_as_float(u.y), f[2] = __uint_as_float(u.z), f[3] = __uint_as_float(u.w);
     }
+    struct Range {
+        float hi, lo;
+    };
+    static __device__ __forceinline__ Range range(const uint4& u)
+    {
+        float f[4];
+        widen(u, f);
+        return {fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3])), fminf(fminf(f[0], f[1]), fminf(f[2], f[3]))};
+    }
+    static __device__ __forceinline__ Range both(const Range& a, const Range& b) { return {fmaxf(a.hi, b.hi), fminf(a.lo, b.lo)}; }
+    static __device__ __forceinline__ float top(const Range& r) { return r.hi; }
+    static __device__ __forceinline__ float low(const Range& r) { return r.lo; }
     static __device__ __forceinline__ float one(const float* p) { return *p; }
-};
-
-// The row's units: unit u covers elements u * N - lead .. + N; the first and the last may reach
-// beyond the row and are read element by element, with -inf in the place of what is not there.
-template <class T>
-struct RowUnits {
-    static constexpr int N = Unit<T>::N;
-    const T* row;
-    int64_t n, units;
-    int lead;
-
-    __device__ RowUnits(const T* r, int64_t count) : row(r), n(count)
-    {
-        lead = (int)(reinterpret_cast<uintptr_t>(r) % 16 / sizeof(T));
-        units = (lead + n + N - 1) / N;
-    }
-    __device__ __forceinline__ int64_t first(int64_t u) const { return u * N - lead; }
-    __device__ __forceinline__ void load(int64_t u, float (&f)[N]) const
-    {
-        const int64_t at = first(u);
-        if (at >= 0 && at + N <= n) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + at);
-            Unit<T>::widen(v, f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                f[i] = at + i >= 0 && at + i < n ? Unit<T>::one(row + at + i) : -INFINITY;
-        }
-    }
 };
 
 __device__ __forceinline__ float warp_max(float v)
@@ -204,6 +201,15 @@ __device__ __forceinline__ float warp_max(float v)
     for (int o = 16; o > 0; o /= 2)
         v = fmaxf(v, shfl_xor(v, o));
     return v;
+}
+
+__device__ __forceinline__ Stats warp_join(Stats s)
+{
+    for (int o = 16; o > 0; o /= 2) {
+        const Stats t{shfl_xor(s.m, o), shfl_xor(s.n, o), shfl_xor(s.r, o), shfl_xor(s.w, o)};
+        s = join(s, t);
+    }
+    return s;
 }
 
 struct Shared {
@@ -216,91 +222,140 @@ struct Shared {
     int flagged, flags[kLpThreads];
 };
 
-template <class T>
-__global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_constant__ LpParams p)
+// The sums of a batch against the warp's m. COUNT: an element may equal m.
+template <class T, bool COUNT>
+__device__ __forceinline__ void add_batch(Stats& s, const uint4 (&raw)[kBatch], int units)
 {
     constexpr int N = Unit<T>::N;
+    // z = x log2 e - ref is rounded once; what rounding m log2 e to ref left over is the same for
+    // every element and put right on the batch's sums
+    const float ref = s.m * kLog2e, left = fmaf(s.m, kLog2e, -ref);
+    float r[4] = {}, w[4] = {};
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+        if (b >= units)
+            continue;
+        float f[N];
+        Unit<T>::widen(raw[b], f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float z = fmaf(f[i], kLog2e, -ref);
+            float e = ex2(z);
+            if (COUNT && f[i] == s.m) {
+                e = 0.f;
+                s.n += 1.f;
+            }
+            r[i & 3] += e;
+            w[i & 3] = fmaf(e, z, w[i & 3]);
+        }
+    }
+    const float rs = (r[0] + r[1]) + (r[2] + r[3]), ws = (w[0] + w[1]) + (w[2] + w[3]);
+    const float fix = 1.f - left * kLn2;
+    s.r = fmaf(rs, fix, s.r);
+    s.w = fmaf(fmaf(-left, rs, ws) * fix, kLn2, s.w);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_constant__ LpParams p)
+{
+    using U = Unit<T>;
+    constexpr int N = U::N;
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int parts = cluster.num_blocks(), part = cluster.block_rank();
     const int64_t m = blockIdx.x / parts;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T* row = static_cast<const T*>(p.v) + m * p.ld;
-    const RowUnits<T> ru(row, p.N);
-    // this block's units, whole batches of the block's
-    const int64_t u0 = ru.units * part / parts, u1 = ru.units * (part + 1) / parts;
+    // elements before the first and behind the last whole unit go one by one (block 0)
+    const int head = (int)min((int64_t)((16 - reinterpret_cast<uintptr_t>(row) % 16) % 16 / sizeof(T)), p.N);
+    const int64_t units = (p.N - head) / N;
+    const int tail = (int)(p.N - head - units * N);
+    const uint4* body = reinterpret_cast<const uint4*>(row + head);
+    const int64_t u0 = units * part / parts, u1 = units * (part + 1) / parts;
 
     Stats s{-INFINITY, 0.f, 0.f, 0.f};
     float big = -INFINITY;  // this thread's largest
+    uint4 raw[kBatch], next[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+        if (u0 + threadIdx.x + b * kLpThreads < u1)
+            next[b] = __ldg(body + u0 + threadIdx.x + b * kLpThreads);
     for (int64_t u = u0 + threadIdx.x; u - lane < u1; u += kBatch * kLpThreads) {
-        float f[kBatch][N];
+        const int have = u < u1 ? (int)min((int64_t)kBatch, (u1 - u + kLpThreads - 1) / kLpThreads) : 0;
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            raw[b] = next[b];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            if (u + (kBatch + b) * kLpThreads < u1)
+                next[b] = __ldg(body + u + (kBatch + b) * kLpThreads);
         float top = -INFINITY, low = INFINITY;
+        if (have == kBatch) {
+            const typename U::Range x = U::both(U::both(U::range(raw[0]), U::range(raw[1])), U::both(U::range(raw[2]), U::range(raw[3])));
+            top = fmaxf(top, U::top(x));
+            low = fminf(low, U::low(x));
+        } else {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if (u + b * kLpThreads >= u1)
-                continue;
-            ru.load(u + b * kLpThreads, f[b]);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                top = fmaxf(top, f[b][i]);
-                low = fminf(low, f[b][i]);
-            }
+            for (int b = 0; b < kBatch - 1; ++b)
+                if (b < have) {
+                    const typename U::Range x = U::range(raw[b]);
+                    top = fmaxf(top, U::top(x));
+                    low = fminf(low, U::low(x));
+                }
         }
         big = fmaxf(big, top);
-        // straight: nothing here reaches m, no product below overflows (-inf and the type's
-        // lowest value, as masks write them, go the other way), and m is not so far from 0 that
-        // the rounding of m log2 e (2^-11 at 1e4) is more than a first-order matter
-        const bool plain = __all_sync(0xffffffffu, top < s.m && low > -1e38f && fabsf(s.m) < 1e4f);
-        if (plain) {
-            // z = x log2 e - ref is rounded once; what rounding m log2 e to ref left over is
-            // the same for every element and put right on the batch's sums
-            const float ref = s.m * kLog2e, left = fmaf(s.m, kLog2e, -ref);
-            float r[4] = {}, w[4] = {};
+        // nothing overflows below (-inf and the type's lowest value, as masks write them, go the
+        // last way), and m is not so far from 0 that the rounding of m log2 e (2^-11 at 1e4) is
+        // more than a first-order matter
+        if (__all_sync(0xffffffffu, top < s.m && low > -1e38f && fabsf(s.m) < 1e4f)) {
+            if (have == kBatch)
+                add_batch<T, false>(s, raw, kBatch);
+            else
+                add_batch<T, false>(s, raw, have);
+            continue;
+        }
+        const float wm = warp_max(top);
+        if (wm > s.m)
+            rebase(s, wm);
+        if (__all_sync(0xffffffffu, low > -1e38f && fabsf(s.m) < 1e4f)) {
+            add_batch<T, true>(s, raw, have);
+            continue;
+        }
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                if (u + b * kLpThreads >= u1)
-                    continue;
+        for (int b = 0; b < kBatch; ++b) {
+            if (b >= have)
+                continue;
+            float f[N];
+            U::widen(raw[b], f);
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+                float x = f[0];  // a rotation of the array keeps this loop small
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float z = fmaf(f[b][i], kLog2e, -ref), e = ex2(z);
-                    r[i & 3] += e;
-                    w[i & 3] = fmaf(e, z, w[i & 3]);
-                }
-            }
-            const float rs = (r[0] + r[1]) + (r[2] + r[3]), ws = (w[0] + w[1]) + (w[2] + w[3]);
-            const float fix = 1.f - left * kLn2;
-            s.r = fmaf(rs, fix, s.r);
-            s.w = fmaf(fmaf(-left, rs, ws) * fix, kLn2, s.w);
-        } else {
-            const float wm = warp_max(top);
-            if (wm > s.m)
-                rebase(s, wm);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                if (u + b * kLpThreads >= u1)
-                    continue;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float x = f[b][i];
-                    if (x == s.m && x != -INFINITY) {
-                        s.n += 1.f;
-                    } else if (x != -INFINITY) {  // NaN takes this way
-                        const float z = x - s.m, e = expf(z);
-                        s.r += e;
-                        s.w = fmaf(e, fmaxf(z, -200.f), s.w);
-                    }
+                for (int j = 0; j + 1 < N; ++j)
+                    f[j] = f[j + 1];
+                if (x == s.m && x != -INFINITY) {
+                    s.n += 1.f;
+                } else if (x != -INFINITY) {  // NaN takes this way
+                    const float z = x - s.m, e = expf(z);
+                    s.r += e;
+                    s.w = fmaf(e, fmaxf(z, -200.f), s.w);
                 }
             }
         }
     }
     const bool nan = s.r != s.r;
+    // the single elements: one a lane of warp 0
+    uint64_t single = 0;
+    if (part == 0 && warp == 0 && lane < head + tail) {
+        const int64_t at = lane < head ? lane : p.N - tail + (lane - head);
+        const float x = U::one(row + at);
+        single = key_of(x, at);
+        s = join(s, x == x ? Stats{x, x == -INFINITY ? 0.f : 1.f, 0.f, 0.f} : Stats{-INFINITY, 0.f, x, x});
+    }
     // +inf: no finite statistics
     if (s.m == INFINITY)
         s.r = NAN;
-    for (int o = 16; o > 0; o /= 2) {
-        const Stats t{shfl_xor(s.m, o), shfl_xor(s.n, o), shfl_xor(s.r, o), shfl_xor(s.w, o)};
-        s = join(s, t);
-    }
+    s = warp_join(s);
     if (lane == 0)
         sh.stats[warp] = s;
     if (threadIdx.x == 0)
@@ -318,21 +373,20 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
         if (has && mine >= bound)
             sh.flags[atomicAdd(&sh.flagged, 1)] = threadIdx.x;
         __syncthreads();
-        uint64_t list = 0;          // lane i: the warp's i-th largest key
-        uint64_t last = 0;          // its top_k-th
+        uint64_t list = sort32(single, lane);  // lane i: the warp's i-th largest key
+        uint64_t last = __shfl_sync(0xffffffffu, list, p.top_k - 1);
         for (int f = warp; f < sh.flagged; f += kLpWarps) {
             const int64_t own = u0 + sh.flags[f];
             for (int64_t v0 = own; v0 < u1; v0 += 32 * kLpThreads) {
                 const int64_t v = v0 + (int64_t)lane * kLpThreads;
                 float x[N];
                 if (v < u1)
-                    ru.load(v, x);
+                    U::widen(__ldg(body + v), x);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int64_t at = ru.first(v) + i;
                     uint64_t key = 0;
-                    if (v < u1 && at >= 0 && at < p.N && order_of(x[i]) >= bound)
-                        key = key_of(x[i], at);
+                    if (v < u1 && order_of(x[i]) >= bound)
+                        key = key_of(x[i], head + v * N + i);
                     unsigned come = __ballot_sync(0xffffffffu, key > last);
                     while (come) {
                         const uint64_t k = __shfl_sync(0xffffffffu, key, __ffs(come) - 1);
@@ -349,30 +403,29 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
         }
         sh.lists[warp][lane] = list;
         join_lists(sh.lists, warp, lane);
+        if (warp == 0)
+            sh.top[lane] = sh.lists[0][lane];
     } else {
         __syncthreads();
     }
     if (warp == 0) {
-        s = lane < kLpWarps ? sh.stats[lane] : Stats{-INFINITY, 0.f, 0.f, 0.f};
-        for (int o = 16; o > 0; o /= 2) {
-            const Stats t{shfl_xor(s.m, o), shfl_xor(s.n, o), shfl_xor(s.r, o), shfl_xor(s.w, o)};
-            s = join(s, t);
-        }
+        s = warp_join(lane < kLpWarps ? sh.stats[lane] : Stats{-INFINITY, 0.f, 0.f, 0.f});
         if (lane == 0)
             sh.part = s;
-        if (p.top_k > 0)
-            sh.top[lane] = sh.lists[0][lane];
     }
-    if (parts > 1)
+    if (parts > 1) {
         cluster.sync();
-    if (part == 0 && warp == 0) {
-        uint64_t list = p.top_k > 0 ? sh.top[lane] : 0;
-        for (int o = 1; o < parts; ++o) {
-            const Shared* other = cluster.map_shared_rank(&sh, o);
-            s = join(s, other->part);
-            if (p.top_k > 0)
-                list = merge32(list, other->top[lane], lane);
+        if (part == 0) {  // the parts' lists and statistics, a warp or a lane each
+            if (p.top_k > 0) {
+                sh.lists[warp][lane] = warp < parts ? cluster.map_shared_rank(&sh, warp)->top[lane] : 0;
+                join_lists(sh.lists, warp, lane);
+            }
+            if (warp == 0)
+                s = warp_join(lane < parts ? cluster.map_shared_rank(&sh, lane)->part : Stats{-INFINITY, 0.f, 0.f, 0.f});
         }
+    }
+    if (part == 0 && warp == 0) {
+        const uint64_t list = p.top_k > 0 ? sh.lists[0][lane] : 0;
         // n is 0 only for a row without numbers above -inf
         const bool none = s.m == -INFINITY && s.r == 0.f;
         const float log_total = s.n == 1.f ? log1pf(s.r) : logf(s.n) + log1pf(s.r / s.n);
@@ -383,7 +436,7 @@ __global__ void __launch_bounds__(kLpThreads) logprobs_kernel(const __grid_const
             const int64_t t = p.targets[m * p.n_targets + i];
             float y;
             if (t >= 0 && t < p.N) {
-                y = odd ? NAN : none ? -INFINITY : Unit<T>::one(row + t) - s.m - log_total;
+                y = odd ? NAN : none ? -INFINITY : U::one(row + t) - s.m - log_total;
             } else {
                 y = t == -1 ? 0.f : NAN;
                 if (t != -1)

@@ -51,7 +51,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 
 // LANES lanes take a head (head_dim / 16); a warp takes HEADS = 32 / LANES heads at once.
 template <int LANES>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int HD = LANES * 16, HEADS = 32 / LANES;
     const int lane = threadIdx.x & 31, j = lane % LANES, sub = lane / LANES;
@@ -71,15 +71,6 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
             const int idx = p.interleaved ? (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4) : j * 8 + i;
             f[i] = __ldg(reinterpret_cast<const uint2*>(p.turns + idx));
         }
-    }
-    uint4 gq0 = {}, gq1 = {}, gk0 = {}, gk1 = {};
-    if (p.q_gamma != nullptr) {
-        gq0 = __ldg(reinterpret_cast<const uint4*>(p.q_gamma) + c0);
-        gq1 = __ldg(reinterpret_cast<const uint4*>(p.q_gamma) + c1);
-    }
-    if (p.k_gamma != nullptr) {
-        gk0 = __ldg(reinterpret_cast<const uint4*>(p.k_gamma) + c0);
-        gk1 = __ldg(reinterpret_cast<const uint4*>(p.k_gamma) + c1);
     }
     pdl_wait();
     pdl_launch_dependents();
@@ -118,7 +109,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
             b = __ldcg(row + h * (HD / 8) + c1);
         }
         const bool is_q = h < p.n_q, is_k = !is_q && h < p.n_q + n_kv;
-        const bool norm = is_q ? p.q_gamma != nullptr : is_k && p.k_gamma != nullptr;
+        const uint4* gamma = reinterpret_cast<const uint4*>(is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr);
+        const bool norm = gamma != nullptr;
         float x[8], y[8];
         unpack8(a, x);
         unpack8(b, y);
@@ -132,8 +124,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const __grid
         if (norm) {
             const float r = rsqrtf(ss * (1.f / HD) + p.eps);
             float g0[8], g1[8];
-            unpack8(is_q ? gq0 : gk0, g0);
-            unpack8(is_q ? gq1 : gk1, g1);
+            unpack8(__ldg(gamma + c0), g0);
+            unpack8(__ldg(gamma + c1), g1);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 x[i] = x[i] * r * g0[i];
