@@ -9,11 +9,14 @@
 namespace tfq {
 namespace {
 
-// Query rows of an item: the least tile that holds a sequence's rows of a key/value head.
-int attn_rows(int max_rows, int group)
+// Query rows of an item, and with them the kernel: up to 64 the warp MMAs, above the tensor-memory
+// MMAs (which need the head's output of two row groups in tensor memory: head_dim up to 128).
+int attn_rows(int max_rows, int group, int head_dim)
 {
     const int r = max_rows * group;
-    return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+    if (r <= 32 || head_dim > 128)
+        return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+    return r <= 128 ? 128 : 256;
 }
 
 struct AttnLayout {
@@ -25,7 +28,7 @@ AttnLayout attn_layout(int head_dim, int rows)
     AttnLayout L{};
     L.counters = 256;
     L.parts = L.counters + ((size_t)device_sms() * sizeof(unsigned) + 255) / 256 * 256;
-    L.total = L.parts + attn_warp_ws(head_dim, rows, device_sms());
+    L.total = L.parts + (size_t)2 * device_sms() * rows * (head_dim + 2) * sizeof(float);  // two parts a CTA
     return L;
 }
 
@@ -49,16 +52,16 @@ EncodeTiled encode_tiled()
     return fn;
 }
 
-// The pool as {64 columns, rows, head_dim / 64}: a box is `rows` rows with all their columns,
-// 64 columns (128 bytes, swizzled) after the other.
-bool encode_rows(const CacheView& c, int total_rows, int rows, CUtensorMap* map)
+// The pool as {64 columns, rows, head_dim / 64}: a box is `rows` rows of `halves` times 64 columns
+// (128 bytes a row, swizzled), one 64 after the other.
+bool encode_rows(const CacheView& c, int total_rows, int rows, int halves, CUtensorMap* map)
 {
     const EncodeTiled fn = encode_tiled();
     if (fn == nullptr)
         return false;
     const cuuint64_t dims[3] = {64, (cuuint64_t)total_rows, (cuuint64_t)c.head_dim / 64};
     const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * 2, 128};
-    const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)c.head_dim / 64}, one[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)halves}, one[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -80,7 +83,7 @@ size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int
         report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q, B or max_rows out of range", name);
         return 0;
     }
-    return attn_layout(v.head_dim, attn_rows(max_rows, n_q / v.n_kv)).total;
+    return attn_layout(v.head_dim, attn_rows(max_rows, n_q / v.n_kv, v.head_dim)).total;
 }
 
 int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
@@ -124,14 +127,17 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     p.status = static_cast<int*>(ws);
     p.total_rows = (int)p.c.row_of(p.c.n_layers, 0, 0, 0);
     p.limit_ns = kDefaultWaitLimitNs;
-    const int rows = attn_rows(max_rows, p.group);
+    const int rows = attn_rows(max_rows, p.group, p.c.head_dim);
     const AttnLayout L = attn_layout(p.c.head_dim, rows);
     p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + L.counters);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
     CUtensorMap map;
-    if (!encode_rows(p.c, p.total_rows, p.c.page_size < 64 ? p.c.page_size : 64, &map))
+    const bool tc = rows > 64;
+    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(rows, p.c.page_size) : p.c.page_size < 64 ? p.c.page_size : 64,
+                     tc ? 1 : p.c.head_dim / 64, &map))
         return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
-    const cudaError_t e = launch_attn_warp(p, rows, map, static_cast<cudaStream_t>(stream), (flags & TF_RUN_PDL) != 0);
+    const cudaError_t e = (tc ? launch_attn_tc : launch_attn_warp)(p, rows, map, static_cast<cudaStream_t>(stream),
+                                                                   (flags & TF_RUN_PDL) != 0);
     return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }
 

@@ -218,8 +218,10 @@ __device__ __forceinline__ float4 join_parts(const float* parts, int c0, int c1,
 
 __device__ __forceinline__ uint2 bf16x4(float4 a) { return make_uint2(f32x2_to_bf16x2(a.x, a.y), f32x2_to_bf16x2(a.z, a.w)); }
 
-// launchers (tfq_attn_warp.cu)
-size_t attn_warp_ws(int head_dim, int rows, int ctas);
+// rows: query rows of an item. tfq_attn_warp.cu: 16, 32 or 64; tfq_attn_tc.cu: 128 or 256,
+// head_dim 64 or 128.
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl);
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl);
+int attn_tc_box(int rows, int page_size);  // rows of a box
 
 }  // namespace tfq

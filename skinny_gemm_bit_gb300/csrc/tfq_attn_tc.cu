@@ -1,0 +1,621 @@
+// Attention of many query rows: tcgen05 MMAs with scores, weights and output in tensor memory.
+//
+// More than some 32 query rows to a key/value head (a tree of drafts times the heads that share
+// the keys) make enough arithmetic that the warp MMAs fall behind the cache's bytes. Here a CTA
+// (one an SM) has a producer warp (TMA, a ring of K and V tiles), an MMA thread, and two groups
+// of four softmax warps, a thread a query row, so that a row's maximum and sum need no shuffle:
+//
+//   S[w] = Q K^T          128 rows x KT keys, both operands in shared memory
+//   p = 2^(S - m)         the row's thread, S and P in tensor memory (P over S, as bf16)
+//   O[w] += P V           A from tensor memory, V as it lies in the cache (N-major)
+//
+// The groups take turns: while one forms its weights the tensor cores work for the other. Up to
+// 128 query rows (PAIR false) both groups have the same rows and every other tile of 64 keys, and
+// their outputs are joined at the end; that is bound by the cache's bytes, and small tiles keep
+// more of the ring in flight. Above (PAIR true) each group has 128 rows of its own and both read
+// every tile of 128 keys, so a tile is fetched once for 256 rows.
+//
+// The reference m of a row moves only when its maximum has grown by more than 2^8: until then
+// the weights stay below 256 and the sums are exact enough, and the output in tensor memory
+// needs no rescaling. MMAs of one thread complete in order: when a tile's scores are there, the
+// group's last product with V is done too, and its output may be rescaled.
+#include "tfq_attn.cuh"
+
+namespace tfq {
+namespace {
+
+constexpr int kTcThreads = 320;  // eight softmax warps, the producer, the MMA warp
+constexpr int kSoftThreads = 256;
+constexpr int kMaxSlots_ = 12;
+constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w] at 128 w, O[w] at 256 + 128 w
+constexpr float kGrow = 8.f;
+
+// offsets in shared memory
+constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 272, kTcQReady = 288, kTcOFull = 296, kTcFin = 304;
+constexpr int kTcTmem = 320, kTcFlags = 336 /* [0] abort [1] last [2] abort as of a segment's end */, kTcOdd = 352;
+constexpr int kTcMl = 1024;  // [2][128] (m, l)
+constexpr int kTcSched = 3072;
+static_assert(kMaxSlots_ * 8 <= 128, "slots");
+
+template <int HD, bool PAIR>
+struct TcCfg {
+    static constexpr int KT = PAIR ? 128 : 64;
+    static constexpr int ROWS = PAIR ? 256 : 128;
+    static constexpr int kSlotBytes = KT * HD * 2;
+    static constexpr int kQBytes = ROWS * HD * 2 < 32768 ? 32768 : ROWS * HD * 2;  // also the groups' exchange, 2 x 16 KB
+    static size_t q_off(int B) { return (kTcSched + Schedule::bytes(B) + 1023) / 1024 * 1024; }
+    static int slots(int B)
+    {
+        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes) / kSlotBytes;
+        return n < kMaxSlots_ ? (int)n : kMaxSlots_;
+    }
+    static size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes; }
+};
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// Waits for the thread's loads; the operands keep the uses of r behind it.
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of the thread's tensor-memory lane; the values are there after tc_wait_ld
+__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* a)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 :: "r"(addr), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7]),
+                    "r"(a[8]), "r"(a[9]), "r"(a[10]), "r"(a[11]), "r"(a[12]), "r"(a[13]), "r"(a[14]), "r"(a[15]),
+                    "r"(a[16]), "r"(a[17]), "r"(a[18]), "r"(a[19]), "r"(a[20]), "r"(a[21]), "r"(a[22]), "r"(a[23]),
+                    "r"(a[24]), "r"(a[25]), "r"(a[26]), "r"(a[27]), "r"(a[28]), "r"(a[29]), "r"(a[30]), "r"(a[31])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// D (tensor memory) (+)= A B, A and B in shared memory / A in tensor memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)add) : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)add) : "memory");
+}
+
+// Shared-memory matrix descriptor, 128-byte swizzle: start, the step between blocks of 64
+// elements along a contiguous N (lbo; unused for K-major), the step between groups of 8 rows (sbo)
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: fp32 accumulator, bf16 A (K-major) and B, M = 128
+__host__ __device__ constexpr uint32_t instr_desc(int n, bool b_n_major)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int y, int z, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(0), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
+
+// Infinities and NaN among the block's values were taken out of the product with V: what they add
+// to columns c0 .. c0 + 31 of a row that sees their tokens. Rare, so the scores are formed anew.
+template <int HD>
+__device__ __forceinline__ void add_odd(const AttnParams& p, const SeqRows& q, int head, int row, uint64_t odd, uint64_t mask,
+                                        float sc, float sign, float ref, int c0, float (&acc)[32])
+{
+    const uint16_t* qr = p.q + (q.r0 + row / p.group) * p.ldq + (int64_t)(head * p.group + row % p.group) * HD;
+    for (odd &= mask; odd != 0; odd &= odd - 1) {
+        const int tok = q.base + __ffsll((long long)odd) - 1;
+        const int page = p.c.table[(int64_t)q.slot * p.c.max_pages + (tok >> p.c.page_shift)];
+        if (page < 0 || page >= p.c.n_pages)
+            continue;
+        const int off = tok & (p.c.page_size - 1);
+        const uint16_t* k = p.c.data + (p.c.row_of(p.layer, 0, page, head) + off) * HD;
+        const uint16_t* v = p.c.data + (p.c.row_of(p.layer, 1, page, head) + off) * HD;
+        float s = 0.f;
+        for (int d = 0; d < HD; ++d)
+            s = fmaf(__uint_as_float((uint32_t)qr[d] << 16), __uint_as_float((uint32_t)k[d] << 16), s);
+        const float w = attn_ex2(fmaf(s * sign, sc, -ref));
+#pragma unroll
+        for (int d = 0; d < 32; ++d)
+            if (nonfinite16(v[c0 + d]))
+                acc[d] += w * __uint_as_float((uint32_t)v[c0 + d] << 16);
+    }
+}
+
+template <int HD, bool PAIR>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map, uint32_t slots, int q_off)
+{
+    using C = TcCfg<HD, PAIR>;
+    constexpr int KT = C::KT, ROWS = C::ROWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTcFull);
+    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + kTcEmpty);
+    uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + kTcSFull);
+    uint64_t* p_ready = reinterpret_cast<uint64_t*>(smem + kTcPReady);
+    uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + kTcQReady);
+    uint64_t* o_full = reinterpret_cast<uint64_t*>(smem + kTcOFull);
+    uint64_t* fin = reinterpret_cast<uint64_t*>(smem + kTcFin);
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + kTcFlags);
+    unsigned* odd = reinterpret_cast<unsigned*>(smem + kTcOdd);
+    float* ml = reinterpret_cast<float*>(smem + kTcMl);
+    uint8_t* qbuf = smem + q_off;
+    uint8_t* ring = qbuf + C::kQBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < slots; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&s_full[w], 1);
+            mbar_init(&p_ready[w], 4);
+        }
+        mbar_init(q_ready, 8);
+        mbar_init(o_full, 1);
+        mbar_init(fin, 1);
+        flags[0] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem + kTcTmem)), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    Shares<ROWS, KT> shares(p, smem + kTcSched);
+    tc_fence_before();
+    shares.build();  // its barriers publish the tensor-memory address as well
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTcTmem);
+    const int64_t u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
+
+    if (warp == 8) {
+        // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
+        const int box = min(p.c.page_size, KT), pieces = KT / box;
+        const int z = lane / pieces, piece = lane % pieces;
+        const bool active = lane < pieces * (HD / 64);
+        uint32_t slot = 0, pass = 0;
+        int64_t issued = 0;
+        bool gone = false;
+        for (int64_t u = u0; u < u1 && !gone;) {
+            const Segment g = shares.segment(u, u1);
+            const SeqRows q = shares.s.seq[g.b];
+            const int32_t* table = p.c.table + (int64_t)q.slot * p.c.max_pages;
+            const int len = q.len();
+            auto page_at = [&](int t) {
+                const int row = t * KT + piece * box;
+                return active && t < g.t1 && row < len ? __ldcg(table + (row >> p.c.page_shift)) : -1;
+            };
+            int page = page_at(g.t0);
+            for (int t = g.t0; t < g.t1 && !gone; ++t) {
+                const int next = page_at(t + 1);
+                const int row = t * KT + piece * box;
+                const bool in = active && row < len, good = page >= 0 && page < p.c.n_pages;
+                if (in && !good)
+                    record_status(p.status, TF_E_INVALID_ARG);
+                for (int kv = 0; kv < 2; ++kv) {
+                    const bool ok = pass == 0 || attn_wait(&empty[slot], (pass - 1) & 1, flags, p.status, p.limit_ns);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        gone = true;
+                        break;
+                    }
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
+                    __syncwarp();
+                    if (active) {
+                        const int y = in && good ? (int)p.c.row_of(p.layer, kv, page, g.h) + (row & (p.c.page_size - 1)) : p.total_rows;
+                        tma_box(smem_u32(ring + (size_t)slot * C::kSlotBytes + z * KT * 128 + piece * box * 128), &map, y, z, &full[slot]);
+                    }
+                    ++issued;
+                    if (++slot == slots) {
+                        slot = 0;
+                        ++pass;
+                    }
+                }
+                page = next;
+            }
+            u += g.t1 - g.t0;
+        }
+        if (gone)  // no copy may be in flight when the CTA leaves
+            for (int64_t i = issued > slots ? issued - slots : 0; i < issued; ++i)
+                mbar_wait_bounded(&full[i % slots], (uint32_t)(i / slots) & 1, p.limit_ns);
+    } else if (warp == 9) {
+        // ---- MMA thread
+        if (lane == 0) {
+            constexpr uint32_t kIdS = instr_desc(KT, false), kIdO = instr_desc(HD, true);
+            const uint32_t qa = smem_u32(qbuf), ra = smem_u32(ring);
+            uint32_t p_phase[2] = {0, 0};
+            uint32_t tiles = 0;  // before this segment
+            uint32_t seg = 0;
+            bool ok = true;
+            auto wait_slot = [&](uint32_t pos) { return attn_wait(&full[pos % slots], (pos / slots) & 1, flags, p.status, p.limit_ns); };
+            for (int64_t u = u0; u < u1 && ok; ++seg) {
+                const Segment g = shares.segment(u, u1);
+                const int n = g.t1 - g.t0, ns = PAIR ? 2 * n : n;
+                ok = attn_wait(q_ready, seg & 1, flags, p.status, p.limit_ns);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                auto scores = [&](int i) {
+                    const int w = i & 1;
+                    const uint32_t pos = 2 * (tiles + (PAIR ? i >> 1 : i));
+                    if (!wait_slot(pos))
+                        return false;
+                    const uint32_t kb = ra + (uint32_t)(pos % slots) * C::kSlotBytes;
+#pragma unroll
+                    for (int ks = 0; ks < HD / 16; ++ks)
+                        tc_mma_ss(tmem + 128 * w,
+                                  smem_desc(qa + (PAIR ? w * (128 * HD * 2) : 0) + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 16, 1024),
+                                  smem_desc(kb + (ks >> 2) * (KT * 128) + (ks & 3) * 32, 16, 1024), kIdS, ks > 0);
+                    tc_commit(&s_full[w]);
+                    if (!PAIR || w == 1)
+                        tc_commit(&empty[pos % slots]);
+                    return true;
+                };
+                for (int i = 0; i < 2 && i < ns && ok; ++i)
+                    ok = scores(i);
+                for (int i = 0; i < ns && ok; ++i) {
+                    const int w = i & 1;
+                    const uint32_t pos = 2 * (tiles + (PAIR ? i >> 1 : i)) + 1;
+                    ok = attn_wait(&p_ready[w], p_phase[w], flags, p.status, p.limit_ns) && wait_slot(pos);
+                    if (!ok)
+                        break;
+                    p_phase[w] ^= 1;
+                    tc_fence_after();
+                    const uint32_t vb = ra + (uint32_t)(pos % slots) * C::kSlotBytes;
+#pragma unroll
+                    for (int ks = 0; ks < KT / 16; ++ks)
+                        tc_mma_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 8 * ks, smem_desc(vb + ks * 2048, KT * 128, 1024), kIdO,
+                                  i > 1 || ks > 0);
+                    if (!PAIR || w == 1)
+                        tc_commit(&empty[pos % slots]);
+                    if (i + 2 < ns)
+                        ok = scores(i + 2);
+                }
+                if (ok)
+                    tc_commit(o_full);
+                tiles += n;
+                u += n;
+            }
+            // no MMA may be under way when the tensor memory is given back
+            tc_commit(fin);
+            mbar_wait_bounded(fin, 0, p.limit_ns);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax: group w, a thread a row
+        const int w = warp >> 2, wt = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_at = tmem + lanes + 128 * w, o_at = tmem + lanes + kOCol + 128 * w;
+        const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale goes into Q
+        const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
+        uint32_t s_phase = 0, seg = 0;
+        uint32_t tiles = 0;
+        for (int64_t u = u0; u < u1; ++seg) {
+            const Segment g = shares.segment(u, u1);
+            const SeqRows q = shares.s.seq[g.b];
+            const int n = g.t1 - g.t0, len = q.len(), n_rows = q.rows * p.group;
+            for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kSoftThreads) {
+                const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row < n_rows) {
+                    v = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + row / p.group) * p.ldq +
+                                                              (int64_t)(g.h * p.group + row % p.group) * HD + c * 8));
+                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+                }
+                *reinterpret_cast<uint4*>(qbuf + (r >> 7) * (128 * HD * 2) + (c >> 3) * (128 * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+            }
+            if (threadIdx.x == 0)
+                odd[0] = odd[1] = 0;
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_ready);
+            const int row = g.rt * ROWS + (PAIR ? w * 128 : 0) + wt;
+            const bool valid = row < n_rows, busy = __any_sync(0xffffffffu, valid);
+            uint64_t mask = 0;
+            if (valid) {
+                const int t = row / p.group;
+                mask = p.masks == nullptr ? ~0ull >> (63 - t) : p.masks[q.r0 + t];
+            }
+            float m = -INFINITY, l = 0.f;  // the reference, in score units, and the sum against it
+            bool had = false, ok = true;
+            for (int t = g.t0 + (PAIR ? 0 : w); t < g.t1; t += PAIR ? 1 : 2) {
+                ok = __all_sync(0xffffffffu, attn_wait(&s_full[w], s_phase, flags, p.status, p.limit_ns));
+                if (!ok)
+                    break;
+                s_phase ^= 1;
+                tc_fence_after();
+                const int k0 = t * KT;
+                const bool edge = k0 + KT > q.base;
+                if (edge && (!PAIR || w == 0)) {
+                    // values behind the sequence's end become zeros, and infinities and NaN among the
+                    // block's own are noted and taken out: a row that does not see them may not meet
+                    // them, not even as 0 times NaN
+                    const uint32_t pos = 2 * (tiles + t - g.t0) + 1;
+                    ok = __all_sync(0xffffffffu, attn_wait(&full[pos % slots], (pos / slots) & 1, flags, p.status, p.limit_ns));
+                    if (!ok)
+                        break;
+                    const int tok = k0 + wt;
+                    if (wt < KT && tok >= q.base) {
+                        uint8_t* v = ring + (size_t)(pos % slots) * C::kSlotBytes + wt * 128;
+                        bool bad = false;
+                        for (int c = 0; c < HD / 8; ++c) {
+                            uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + (c & 7) * 16);
+                            uint32_t x[4];
+                            *reinterpret_cast<uint4*>(x) = *at;
+                            for (int j = 0; j < 4; ++j) {
+                                if (tok >= len) {
+                                    x[j] = 0;
+                                    continue;
+                                }
+                                const bool lo = nonfinite16(x[j]), hi = nonfinite16(x[j] >> 16);
+                                bad |= lo | hi;
+                                x[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                            }
+                            *at = *reinterpret_cast<uint4*>(x);
+                        }
+                        if (bad)
+                            atomicOr(&odd[(tok - q.base) >> 5], 1u << ((tok - q.base) & 31));
+                    }
+                    fence_async_smem();
+                }
+                if (busy) {
+                    // 64 columns at a time; of 128 the last 64 are read twice, so that the rest of the
+                    // thread's state stays in registers. P's columns reach only scores already read.
+                    uint32_t s[64];
+                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto read = [&](int c0) {
+                        tc_ld32(s_at + c0, s);
+                        tc_ld32(s_at + c0 + 32, s + 32);
+                        tc_wait_ld(s);
+                        tc_wait_ld(s + 32);
+                        if (edge) {
+#pragma unroll
+                            for (int c = 0; c < 64; ++c) {
+                                const int tok = k0 + c0 + c, j = tok - q.base;
+                                const bool see = j < 0 || (tok < len && (mask >> (j & 63) & 1));
+                                s[c] = see ? s[c] : 0xFF800000u;  // -inf
+                            }
+                        }
+                    };
+#pragma unroll
+                    for (int c0 = KT - 64; c0 >= 0; c0 -= 64) {
+                        read(c0);
+#pragma unroll
+                        for (int c = 0; c < 64; ++c)
+                            x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
+                    }
+                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    if (!had) {
+                        m = top;
+                    } else {
+                        const bool grown = (top - m) * sc > kGrow;
+                        if (__any_sync(0xffffffffu, grown)) {
+                            const float f = grown ? attn_ex2((m - top) * sc) : 1.f;
+                            if (grown)
+                                m = top;
+                            l *= f;
+#pragma unroll 1
+                            for (int c = 0; c < HD; c += 32) {
+                                uint32_t o[32];
+                                tc_ld32(o_at + c, o);
+                                tc_wait_ld(o);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                tc_st32(o_at + c, o);
+                            }
+                        }
+                    }
+                    const float ref = m == -INFINITY ? 0.f : m * sc;
+                    float sum[4] = {};
+#pragma unroll
+                    for (int c0 = 0; c0 < KT; c0 += 64) {
+                        if (c0 > 0)
+                            read(c0);
+#pragma unroll
+                        for (int c = 0; c < 64; c += 2) {
+                            const float a = attn_ex2(fmaf(__uint_as_float(s[c]), sc, -ref));
+                            const float b = attn_ex2(fmaf(__uint_as_float(s[c + 1]), sc, -ref));
+                            sum[c & 2] += a;
+                            sum[(c & 2) + 1] += b;
+                            s[c / 2] = f32x2_to_bf16x2(a, b);  // weights in V's type: 2^-8 each, under the output's own rounding
+                        }
+                        tc_st32(s_at + c0 / 2, s);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc_wait_st();
+                }
+                had = true;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_ready[w]);
+            }
+            ok = ok && __all_sync(0xffffffffu, attn_wait(o_full, seg & 1, flags, p.status, p.limit_ns));
+            tc_fence_after();
+
+            // ---- the segment's end
+            const bool whole = g.t0 == 0 && g.t1 == g.nt;
+            float* part = p.parts + (int64_t)(g.t0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * (ROWS * (HD + 2));
+            const int prow = (PAIR ? w * 128 : 0) + wt;  // the row within the tile
+            float mine = m == -INFINITY ? -INFINITY : m * sc, top = mine, all = l;
+            if (!PAIR) {
+                ml[(w * 128 + wt) * 2] = mine;
+                ml[(w * 128 + wt) * 2 + 1] = l;
+            }
+            named_bar_sync(1, kSoftThreads);  // also: nobody reads Q or marks odd values any more
+            if (!PAIR) {
+                const float other = ml[((w ^ 1) * 128 + wt) * 2];
+                top = fmaxf(mine, other);
+                const float r = top == -INFINITY ? 0.f : top;
+                all = l * attn_ex2(mine - r) + ml[((w ^ 1) * 128 + wt) * 2 + 1] * attn_ex2(other - r);
+            }
+            const float ref = top == -INFINITY ? 0.f : top, scale = PAIR ? 1.f : attn_ex2(mine - ref);
+            const float inv = all == 0.f ? 0.f : 1.f / all;
+            const uint64_t odd_bits = (uint64_t)odd[1] << 32 | odd[0];
+            auto put = [&](float (&a)[32], int c0) {  // columns c0 .. c0 + 31 of the row, unscaled
+                if (!valid)
+                    return;
+                if (odd_bits != 0)
+                    add_odd<HD>(p, q, g.h, row, odd_bits, mask, sc, sign, ref, c0, a);
+                if (whole) {
+                    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)(q.r0 + row / p.group) * p.n_q + g.h * p.group + row % p.group) * HD + c0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[i] = make_uint4(f32x2_to_bf16x2(a[8 * i] * inv, a[8 * i + 1] * inv), f32x2_to_bf16x2(a[8 * i + 2] * inv, a[8 * i + 3] * inv),
+                                          f32x2_to_bf16x2(a[8 * i + 4] * inv, a[8 * i + 5] * inv), f32x2_to_bf16x2(a[8 * i + 6] * inv, a[8 * i + 7] * inv));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        __stcg(reinterpret_cast<float4*>(part + prow * HD + c0 + 4 * i), make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+                    if (c0 == 0)
+                        __stcg(reinterpret_cast<float2*>(part + ROWS * HD + 2 * prow), make_float2(top, all));
+                }
+            };
+            auto load = [&](int c0, float (&a)[32]) {
+                uint32_t o[32];
+                if (had) {  // the output was never written otherwise
+                    tc_ld32(o_at + c0, o);
+                    tc_wait_ld(o);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    a[i] = had ? __uint_as_float(o[i]) * scale : 0.f;
+            };
+            if (PAIR) {
+                if (busy)
+#pragma unroll 1
+                    for (int c0 = 0; c0 < HD; c0 += 32) {
+                        float a[32];
+                        load(c0, a);
+                        put(a, c0);
+                    }
+            } else {
+                // group 0 finishes the first half of the columns, group 1 the second; the other half
+                // goes over in the Q buffer, 32 columns at a time
+                float* give = reinterpret_cast<float*>(qbuf) + (w ^ 1) * (32 * 128);
+                const float* take = reinterpret_cast<const float*>(qbuf) + w * (32 * 128);
+#pragma unroll 1
+                for (int c = 0; c < HD / 2; c += 32) {
+                    float a[32];
+                    load((w ^ 1) * (HD / 2) + c, a);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        give[i * 128 + wt] = a[i];
+                    named_bar_sync(1, kSoftThreads);
+                    load(w * (HD / 2) + c, a);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        a[i] += take[i * 128 + wt];
+                    put(a, w * (HD / 2) + c);
+                    named_bar_sync(1, kSoftThreads);
+                }
+            }
+            if (!whole) {
+                const int64_t first = g.u - g.t0;  // the item's first unit
+                const int ca = shares.cta_of(first), cz = shares.cta_of(first + g.nt - 1);
+                __threadfence();
+                named_bar_sync(1, kSoftThreads);
+                if (threadIdx.x == 0) {
+                    const int last = !flags[0] && atom_add_acq_rel_gpu(&p.counters[ca], 1u) == (unsigned)(cz - ca);
+                    if (last)
+                        p.counters[ca] = 0;
+                    flags[1] = last;
+                }
+                named_bar_sync(1, kSoftThreads);
+                if (flags[1]) {
+                    __threadfence();
+                    for (int i = threadIdx.x; i < ROWS * (HD / 4); i += kSoftThreads) {
+                        const int r = i / (HD / 4), c = i % (HD / 4) * 4, at = g.rt * ROWS + r;
+                        if (at < n_rows)
+                            *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + at / p.group) * p.n_q + g.h * p.group + at % p.group) * HD + c) =
+                                bf16x4(join_parts<ROWS, HD>(p.parts, ca, cz, r, c));
+                    }
+                }
+            }
+            if (threadIdx.x == 0)
+                flags[2] = flags[0];
+            tc_fence_before();                // the output has been read
+            named_bar_sync(1, kSoftThreads);  // the Q buffer may be written again
+            if (flags[2])                     // one answer for all warps
+                break;
+            tiles += n;
+            u += n;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+template <int HD, bool PAIR>
+cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream, bool pdl)
+{
+    using C = TcCfg<HD, PAIR>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(tree_attn_tc_kernel<HD, PAIR>, 227 * 1024, done);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(tree_attn_tc_kernel<HD, PAIR>, dim3(device_sms()), dim3(kTcThreads), C::smem(p.B), stream, pdl, p, map,
+                      (uint32_t)C::slots(p.B), (int)C::q_off(p.B));
+}
+
+}  // namespace
+
+int attn_tc_box(int rows, int page_size) { return rows == 256 ? page_size : page_size < 64 ? page_size : 64; }
+
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl)
+{
+    if (p.c.head_dim == 64)
+        return rows == 128 ? launch<64, false>(p, map, stream, pdl) : launch<64, true>(p, map, stream, pdl);
+    return rows == 128 ? launch<128, false>(p, map, stream, pdl) : launch<128, true>(p, map, stream, pdl);
+}
+
+}  // namespace tfq

@@ -429,8 +429,6 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t str
 
 }  // namespace
 
-size_t attn_warp_ws(int head_dim, int rows, int ctas) { return (size_t)2 * ctas * rows * (head_dim + 2) * sizeof(float); }
-
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl)
 {
     if (p.c.head_dim == 64)
