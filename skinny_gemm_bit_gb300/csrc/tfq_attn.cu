@@ -9,13 +9,15 @@
 namespace tfq {
 namespace {
 
-// Query rows of an item, and with them the kernel: up to 64 the warp MMAs, above the tensor-memory
-// MMAs (which need the head's output of two row groups in tensor memory: head_dim up to 128).
+// Query rows of an item, and with them the kernel: up to 32 the warp MMAs, above the tensor-memory
+// MMAs (which need the output of two row groups in tensor memory: head_dim up to 128).
 int attn_rows(int max_rows, int group, int head_dim)
 {
     const int r = max_rows * group;
-    if (r <= 32 || head_dim > 128)
-        return r <= 16 ? 16 : r <= 32 ? 32 : 64;
+    if (head_dim > 128 || r <= 16)
+        return 16;
+    if (r <= 32)
+        return 32;
     return r <= 128 ? 128 : 256;
 }
 
@@ -133,7 +135,7 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
     CUtensorMap map;
     const bool tc = rows > 64;
-    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(rows, p.c.page_size) : p.c.page_size < 64 ? p.c.page_size : 64,
+    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(rows, p.c.page_size) : attn_warp_box(p.c.head_dim, p.c.page_size),
                      tc ? 1 : p.c.head_dim / 64, &map))
         return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
     const cudaError_t e = (tc ? launch_attn_tc : launch_attn_warp)(p, rows, map, static_cast<cudaStream_t>(stream),

@@ -61,14 +61,8 @@ __device__ __forceinline__ SeqRows seq_rows(const AttnParams& p, int b)
     return s;
 }
 
-// The call's units in shared memory: first[b] units before sequence b, and the sequences.
-struct Schedule {
-    int64_t* first;
-    SeqRows* seq;
-
-    static __host__ __device__ size_t bytes(int B) { return (size_t)(B + 1) * 8 + (size_t)B * sizeof(SeqRows) + 8; }
-    __device__ Schedule(void* at, int B) : first(static_cast<int64_t*>(at)), seq(reinterpret_cast<SeqRows*>(first + B + 1 + ((B + 1) & 1))) {}
-};
+// Shared memory of a call's schedule: the units before each sequence.
+constexpr size_t schedule_bytes(int B) { return (size_t)(B + 1) * 8; }
 
 struct Segment {
     int b, h, rt;    // item: sequence, key/value head, row tile
@@ -78,11 +72,14 @@ struct Segment {
 
 template <int ROWS, int KEYS>
 struct Shares {
-    Schedule s;
+    int64_t* first;  // [B + 1], shared memory: units before each sequence
     const AttnParams& p;
     int64_t total, ctas;  // units; CTAs that have some: every one of them has at least one
 
-    __device__ Shares(const AttnParams& params, void* smem) : s(smem, params.B), p(params), total(0), ctas(0) {}
+    __device__ Shares(const AttnParams& params, void* smem) : first(static_cast<int64_t*>(smem)), p(params), total(0), ctas(0) {}
+
+    // Read anew from the cache that build() has filled: shared memory is the ring's.
+    __device__ __forceinline__ SeqRows seq(int b) const { return seq_rows(p, b); }
 
     __device__ __forceinline__ int row_tiles(const SeqRows& q) const { return (q.rows * p.group + ROWS - 1) / ROWS; }
     __device__ __forceinline__ int key_tiles(const SeqRows& q) const { return (q.len() + KEYS - 1) / KEYS; }
@@ -91,34 +88,33 @@ struct Shares {
     __device__ void build()
     {
         for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-            const SeqRows q = seq_rows(p, b);
-            s.seq[b] = q;
-            s.first[b + 1] = q.base < 0 ? 0 : (int64_t)p.c.n_kv * row_tiles(q) * key_tiles(q);
+            const SeqRows q = seq(b);
+            first[b + 1] = q.base < 0 ? 0 : (int64_t)p.c.n_kv * row_tiles(q) * key_tiles(q);
         }
         __syncthreads();
         if (threadIdx.x < 32) {
             int64_t sum = 0;
             for (int b0 = 0; b0 < p.B; b0 += 32) {
                 const int b = b0 + threadIdx.x;
-                int64_t x = b < p.B ? s.first[b + 1] : 0;
+                int64_t x = b < p.B ? first[b + 1] : 0;
                 for (int o = 1; o < 32; o <<= 1) {
                     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
                     if ((int)threadIdx.x >= o)
                         x += y;
                 }
                 if (b < p.B)
-                    s.first[b + 1] = sum + x;
+                    first[b + 1] = sum + x;
                 sum += __shfl_sync(0xffffffffu, x, 31);
             }
             if (threadIdx.x == 0)
-                s.first[0] = 0;
+                first[0] = 0;
         }
         __syncthreads();
-        total = s.first[p.B];
+        total = first[p.B];
         ctas = total < gridDim.x ? total : gridDim.x;
         // sequences whose arguments do not hold: zero rows
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            const SeqRows q = s.seq[b];
+            const SeqRows q = seq(b);
             if (q.base >= 0)
                 continue;
             if (threadIdx.x == 0)
@@ -139,7 +135,7 @@ struct Shares {
         int lo = 0, hi = p.B - 1;  // the last sequence whose first unit is not behind u
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (s.first[mid] <= u)
+            if (first[mid] <= u)
                 lo = mid;
             else
                 hi = mid - 1;
@@ -147,10 +143,10 @@ struct Shares {
         Segment g;
         g.b = lo;
         g.u = u;
-        const SeqRows& q = s.seq[lo];
+        const SeqRows q = seq(lo);
         g.nt = key_tiles(q);
         const int rt = row_tiles(q);
-        const int64_t local = u - s.first[lo];
+        const int64_t local = u - first[lo];
         const int64_t item = local / g.nt;
         g.t0 = (int)(local - item * g.nt);
         g.h = (int)(item / rt);
@@ -196,21 +192,34 @@ __device__ __forceinline__ float4 join_parts(const float* parts, int c0, int c1,
 {
     constexpr int kFloats = ROWS * (HD + 2);
     auto at = [&](int c) { return parts + (int64_t)(c == c0 ? 2 * c0 + 1 : 2 * c) * kFloats; };
-    float m = -INFINITY;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c)
-        m = fmaxf(m, __ldcg(at(c) + ROWS * HD + 2 * row));
-    const float ref = m == -INFINITY ? 0.f : m;
+    // eight parts at a time, in order: their loads together, then the running softmax over them
+    float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c) {
-        const float* s = at(c);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(s + ROWS * HD + 2 * row));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + row * HD + col));
-        const float w = attn_ex2(ml.x - ref);
-        l = fmaf(w, ml.y, l);
-        a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
+    for (int c = c0; c <= c1; c += 8) {
+        float2 ml[8];
+        float4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i <= c1) {
+                ml[i] = __ldcg(reinterpret_cast<const float2*>(at(c + i) + ROWS * HD + 2 * row));
+                v[i] = __ldcg(reinterpret_cast<const float4*>(at(c + i) + row * HD + col));
+            }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i <= c1)
+                top = fmaxf(top, ml[i].x);
+        const float ref = top == -INFINITY ? 0.f : top, f = attn_ex2(m - ref);
+        m = top;
+        l *= f;
+        a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i <= c1) {
+                const float w = attn_ex2(ml[i].x - ref);
+                l = fmaf(w, ml[i].y, l);
+                a.x = fmaf(w, v[i].x, a.x), a.y = fmaf(w, v[i].y, a.y), a.z = fmaf(w, v[i].z, a.z), a.w = fmaf(w, v[i].w, a.w);
+            }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     return make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
@@ -218,10 +227,11 @@ __device__ __forceinline__ float4 join_parts(const float* parts, int c0, int c1,
 
 __device__ __forceinline__ uint2 bf16x4(float4 a) { return make_uint2(f32x2_to_bf16x2(a.x, a.y), f32x2_to_bf16x2(a.z, a.w)); }
 
-// rows: query rows of an item. tfq_attn_warp.cu: 16, 32 or 64; tfq_attn_tc.cu: 128 or 256,
-// head_dim 64 or 128.
+// rows: query rows of an item. tfq_attn_warp.cu: 16, and up to head_dim 128 also 32;
+// tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128. *_box: cache rows of a tensor-map box.
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl);
 cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl);
-int attn_tc_box(int rows, int page_size);  // rows of a box
+int attn_warp_box(int head_dim, int page_size);
+int attn_tc_box(int rows, int page_size);
 
 }  // namespace tfq

@@ -43,7 +43,7 @@ struct TcCfg {
     static constexpr int ROWS = PAIR ? 256 : 128;
     static constexpr int kSlotBytes = KT * HD * 2;
     static constexpr int kQBytes = ROWS * HD * 2 < 32768 ? 32768 : ROWS * HD * 2;  // also the groups' exchange, 2 x 16 KB
-    static size_t q_off(int B) { return (kTcSched + Schedule::bytes(B) + 1023) / 1024 * 1024; }
+    static size_t q_off(int B) { return (kTcSched + schedule_bytes(B) + 1023) / 1024 * 1024; }
     static int slots(int B)
     {
         const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes) / kSlotBytes;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool gone = false;
         for (int64_t u = u0; u < u1 && !gone;) {
             const Segment g = shares.segment(u, u1);
-            const SeqRows q = shares.s.seq[g.b];
+            const SeqRows q = shares.seq(g.b);
             const int32_t* table = p.c.table + (int64_t)q.slot * p.c.max_pages;
             const int len = q.len();
             auto page_at = [&](int t) {
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t tiles = 0;
         for (int64_t u = u0; u < u1; ++seg) {
             const Segment g = shares.segment(u, u1);
-            const SeqRows q = shares.s.seq[g.b];
+            const SeqRows q = shares.seq(g.b);
             const int n = g.t1 - g.t0, len = q.len(), n_rows = q.rows * p.group;
             for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kSoftThreads) {
                 const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;

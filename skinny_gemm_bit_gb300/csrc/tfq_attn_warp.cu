@@ -1,12 +1,16 @@
-// Attention of few query rows: warp MMAs (m16n8k16), a ring of key tiles filled by TMA.
+// Attention of few query rows: warp MMAs (m16n8k16), every warp with a ring of its own.
 //
 // What bounds it is the cache's bytes: a key/value head of 128 is 512 bytes a token for 4 * 128
-// operations a query row, so up to some 64 rows the arithmetic has room. A CTA an SM: one
-// producer warp keeps a ring of 64-key tiles (K and V, 32 KB at head_dim 128) full, eight warps
-// take the tiles apart: a warp holds 16 query rows (fragments in registers) and takes 16 keys
-// at a time, with its own running maximum, sum and output, so that nothing is exchanged until
-// the segment ends and the warps' parts are joined through shared memory. More than 16 query
-// rows: 2 or 4 warps share a piece of keys, each with 16 rows of its own.
+// operations a query row, so up to some 32 rows the arithmetic has room. One CTA of eight warps an
+// SM; of a segment's key tiles (32 keys; 16 at head_dim 256) warp w takes every eighth. A
+// warp fetches its own tiles: as soon as it has read a K or V tile it asks the TMA for the
+// next one into the same slot (three slots of 8 KB a warp, 192 KB an SM), so there is no
+// producer to wait for and the ring is full while a segment ends or the next begins. Each
+// warp keeps its own running maximum, sum and output; they meet in shared memory once a
+// segment.
+//
+// A shared ring with a producer warp and 16 keys a warp and step kept a tile 1700 cycles from
+// its release and measured 242 us on 64 ragged sequences of 8190 (this: see DESIGN's table).
 //
 // Tiles land with the 128-byte swizzle (16-byte piece c of row r at c ^ (r % 8)), so the eight
 // rows of an ldmatrix fall in different banks. A box is one page's rows of a tile.
@@ -15,27 +19,27 @@
 namespace tfq {
 namespace {
 
-constexpr int kKeys = 64;         // keys of a tile
-constexpr int kWarps = 8;         // consumer warps
-constexpr int kCtaThreads = (kWarps + 1) * 32;
-constexpr int kRingBytes = 128 * 1024;
-constexpr int kOutCols = 128;     // columns joined at once
-constexpr int kOutStride = 136;   // floats; 8 banks on a row, so that a fragment's rows do not collide
-constexpr int kOutBytes = kWarps * 16 * kOutStride * 4;
+constexpr int kWarps = 8;
+constexpr int kCtaThreads = kWarps * 32;
+constexpr float kGrow = 8.f;  // the reference of a row moves when its maximum has grown by 2^8
 
-template <int HD>
+template <int HD, int RW>
 struct Cfg {
-    static constexpr int kTileBytes = 2 * kKeys * HD * 2;
-    static constexpr int kStages = kRingBytes / kTileBytes;
-    static constexpr int kMlOff = 0;                                  // [kWarps][16][2] floats
-    static constexpr int kBarOff = kMlOff + kWarps * 16 * 2 * 4;      // full[kStages], empty[kStages]
-    static constexpr int kFlagOff = kBarOff + 2 * 16 * 8;             // [0] abort [1] last [2] abort, as of a segment's end
-    static constexpr int kOutOff = 2048;
-    static constexpr int kSchedOff = kOutOff + kOutBytes;
-    static size_t smem(int B)
-    {
-        return 1024 + ((kSchedOff + Schedule::bytes(B) + 1023) / 1024 * 1024) + (size_t)kStages * kTileBytes;
-    }
+    static constexpr int CH = HD == 256 ? 1 : 2;          // 16-key pieces of a tile
+    static constexpr int KT = 16 * CH;
+    static constexpr int ROWS = 16 * RW;
+    static constexpr int kSlotBytes = KT * HD * 2;        // K or V of a tile
+    static constexpr int kSlots = 24576 / kSlotBytes;     // of a warp: 3, or 6 at head_dim 64
+    static constexpr int kCols = HD == 256 ? 16 : RW == 2 ? 8 : 32;  // output columns joined at once, as shared memory allows
+    static constexpr int kStride = kCols + 4;             // floats
+    static constexpr int kMlOff = 0;                      // [kWarps][ROWS][2] floats
+    static constexpr int kBarOff = kMlOff + kWarps * ROWS * 2 * 4;
+    static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;  // [0] abort [1] last [2] abort, as of a segment's end
+    static constexpr int kOutOff = (kFlagOff + 16 + 127) / 128 * 128;
+    static constexpr int kQOff = (kOutOff + kWarps * ROWS * kStride * 4 + 1023) / 1024 * 1024;
+    static constexpr int kSchedOff = kQOff + ROWS * HD * 2;
+    static constexpr __host__ __device__ size_t ring(int B) { return (kSchedOff + schedule_bytes(B) + 1023) / 1024 * 1024; }
+    static constexpr __host__ __device__ size_t smem(int B) { return 1024 + ring(B) + (size_t)kWarps * kSlots * kSlotBytes; }
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
@@ -70,372 +74,460 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x)
     return ((x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// RW row tiles of 16 (16 RW query rows an item); 8 / RW groups of warps share out the keys.
+// RW row tiles of 16 (16 RW query rows an item).
 template <int HD, int RW>
 __global__ void __launch_bounds__(kCtaThreads, 1)
     tree_attn_warp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map)
 {
-    using C = Cfg<HD>;
-    constexpr int ROWS = 16 * RW, KG = kWarps / RW, NC = HD / 8, KS = HD / 16;
-    constexpr int CH = RW == 4 ? 2 : 1;       // 16-key pieces a warp takes of a tile
-    constexpr int TEAMS = RW == 1 ? 2 : 1;    // warps that take turns on the tiles
-    constexpr int kUsers = kWarps / TEAMS;    // warps that read a tile
+    using C = Cfg<HD, RW>;
+    constexpr int ROWS = C::ROWS, KT = C::KT, CH = C::CH, NC = HD / 8, KS = HD / 16, NS = C::kSlots;
+    constexpr bool kQRegs = RW == 1 && HD <= 128;  // the rows' A fragments in registers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);
-    uint64_t* empty = full + C::kStages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * NS;  // the warp's own
     volatile int* flags = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
     float* outbuf = reinterpret_cast<float*>(smem + C::kOutOff);
-    uint8_t* ring = smem + (C::kSchedOff + Schedule::bytes(p.B) + 1023) / 1024 * 1024;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* qbuf = smem + C::kQOff;
+    uint8_t* ring = smem + C::ring(p.B) + (size_t)warp * NS * C::kSlotBytes;
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i)
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], kUsers);
-        }
-        flags[0] = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x == 0) {
+        flags[0] = 0;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
+    }
     pdl_wait();
-    Shares<ROWS, kKeys> shares(p, smem + C::kSchedOff);
+    Shares<ROWS, KT> shares(p, smem + C::kSchedOff);
     shares.build();
     pdl_launch_dependents();
     const int64_t u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
-    const int box = min(p.c.page_size, kKeys);
 
-    if (warp == kWarps) {
-        // ---- producer: lanes 0 .. boxes - 1 take the tile's K boxes, the next as many its V boxes
-        const int boxes = kKeys / box, kv = lane / boxes, mine = lane % boxes;
-        const bool active = lane < 2 * boxes;
-        int n = 0;
-        bool gone = false;
-        for (int64_t u = u0; u < u1 && !gone;) {
-            const Segment g = shares.segment(u, u1);
-            const SeqRows q = shares.s.seq[g.b];
-            const int32_t* table = p.c.table + (int64_t)q.slot * p.c.max_pages;
-            const int len = q.len();
-            // the table entry of the lane's box of the next tile is read a tile ahead
-            auto page_at = [&](int t) {
-                const int row = t * kKeys + mine * box;
-                return active && t < g.t1 && row < len ? __ldcg(table + (row >> p.c.page_shift)) : -1;
-            };
-            int page = page_at(g.t0);
-            for (int t = g.t0; t < g.t1; ++t, ++n) {
-                const int next = page_at(t + 1);
-                const int st = n % C::kStages;
-                const bool ok = n < C::kStages || attn_wait(&empty[st], (n / C::kStages - 1) & 1, flags, p.status, p.limit_ns);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    gone = true;
-                    break;
-                }
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&full[st], C::kTileBytes);
-                __syncwarp();
-                if (active) {
-                    const int row = t * kKeys + mine * box;
-                    int y = p.total_rows;  // zeros
-                    if (row < len) {
-                        if (page >= 0 && page < p.c.n_pages)
-                            y = (int)p.c.row_of(p.layer, kv, page, g.h) + (row & (p.c.page_size - 1));
-                        else
-                            record_status(p.status, TF_E_INVALID_ARG);
-                    }
-                    tma_rows(smem_u32(ring + (size_t)st * C::kTileBytes + kv * (C::kTileBytes / 2) + mine * box * HD * 2), &map,
-                             y, &full[st]);
-                }
-                page = next;
-            }
-            u += g.t1 - g.t0;
+    // ---- the warp's loads, in the order it will read them: K, V of its first tile, of its next ...
+    const int box = min(p.c.page_size, KT), boxes = KT / box;
+    int64_t lu = u0;             // first unit of the segment that the next load belongs to
+    Segment lg{};                // that segment
+    int64_t ltable = 0;          // its sequence's row of the page table
+    int lt = 0, lkv = 0;         // the next load: tile, K or V
+    int lpage = -1, llen = 0;    // the lane's page of that tile; the sequence's tokens
+    uint32_t issued = 0, taken = 0;
+    auto look = [&]() {  // the page of the lane's box, read well before the load that needs it
+        const int row = lt * KT + lane * box;
+        lpage = lane < boxes && row < llen ? p.c.table[ltable + (row >> p.c.page_shift)] : -1;
+    };
+    auto enter = [&]() {
+        lg = shares.segment(lu, u1);
+        lt = lg.t0 + warp;
+        const SeqRows q = shares.seq(lg.b);
+        llen = q.len();
+        ltable = (int64_t)q.slot * p.c.max_pages;
+    };
+    auto settle = [&]() {  // from a tile behind its segment's end to the next segment that has one
+        while (lt >= lg.t1) {
+            lu += lg.t1 - lg.t0;
+            if (lu >= u1)
+                return;
+            enter();
         }
-        if (gone)  // no copy may be in flight when the CTA leaves
-            for (int i = max(0, n - C::kStages); i < n; ++i)
-                mbar_wait_bounded(&full[i % C::kStages], (i / C::kStages) & 1, p.limit_ns);
-        return;
+        look();
+    };
+    auto load = [&]() {
+        if (lu >= u1)
+            return;
+        const uint32_t slot = issued % NS;
+        if (lane == 0)
+            mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
+        __syncwarp();
+        if (lane < boxes) {
+            const int row = lt * KT + lane * box;
+            int y = p.total_rows;  // zeros
+            if (row < llen) {
+                if (lpage >= 0 && lpage < p.c.n_pages)
+                    y = (int)p.c.row_of(p.layer, lkv, lpage, lg.h) + (row & (p.c.page_size - 1));
+                else
+                    record_status(p.status, TF_E_INVALID_ARG);
+            }
+            tma_rows(smem_u32(ring + slot * C::kSlotBytes + lane * box * HD * 2), &map, y, &full[slot]);
+        }
+        ++issued;
+        if (lkv == 0) {
+            lkv = 1;
+        } else {
+            lkv = 0;
+            lt += kWarps;
+            settle();
+        }
+    };
+    if (u0 < u1) {
+        enter();
+        settle();
+        for (int i = 0; i < NS; ++i)
+            load();
     }
 
-    // ---- consumers
-    const int rw = warp % RW, kg = warp / RW;
     const int gi = lane >> 2, ti = lane & 3;
-    const int team = TEAMS == 2 ? kg / 4 : 0, piece = TEAMS == 2 ? kg % 4 : kg * CH;
     const int k_row = (lane >> 4) * 8 + (lane & 7), k_bit = (lane >> 3) & 1;  // ldmatrix rows: K
-    const int v_row = ((lane >> 3) & 1) * 8 + (lane & 7), v_bit = lane >> 4;  // V (transposed)
+    const int v_row = ((lane >> 3) & 1) * 8 + (lane & 7), v_bit = lane >> 4;  // V (transposed), and Q
     const int half = box * 128;                                              // bytes of a box's 64 columns
-    int n = 0;
+    bool alive = true;
     for (int64_t u = u0; u < u1;) {
         const Segment g = shares.segment(u, u1);
-        const SeqRows q = shares.s.seq[g.b];
+        const SeqRows q = shares.seq(g.b);
         const int len = q.len(), n_rows = q.rows * p.group;
-        // the lane's two query rows, their masks and the A fragments
-        const int row0 = g.rt * ROWS + rw * 16 + gi, row1 = row0 + 8;
-        uint64_t mask0 = 0, mask1 = 0;
-        uint32_t qa[KS][4];
-        {
-            const bool in0 = row0 < n_rows, in1 = row1 < n_rows;
-            const int t0 = in0 ? row0 / p.group : 0, t1 = in1 ? row1 / p.group : 0;
-            const uint16_t* q0 = p.q + (q.r0 + t0) * p.ldq + (int64_t)(g.h * p.group + (in0 ? row0 % p.group : 0)) * HD;
-            const uint16_t* q1 = p.q + (q.r0 + t1) * p.ldq + (int64_t)(g.h * p.group + (in1 ? row1 % p.group : 0)) * HD;
-            if (in0)
-                mask0 = p.masks == nullptr ? ~0ull >> (63 - t0) : p.masks[q.r0 + t0];
-            if (in1)
-                mask1 = p.masks == nullptr ? ~0ull >> (63 - t1) : p.masks[q.r0 + t1];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int col = ks * 16 + ti * 2;
-                qa[ks][0] = in0 ? __ldcg(reinterpret_cast<const uint32_t*>(q0 + col)) : 0u;
-                qa[ks][1] = in1 ? __ldcg(reinterpret_cast<const uint32_t*>(q1 + col)) : 0u;
-                qa[ks][2] = in0 ? __ldcg(reinterpret_cast<const uint32_t*>(q0 + col + 8)) : 0u;
-                qa[ks][3] = in1 ? __ldcg(reinterpret_cast<const uint32_t*>(q1 + col + 8)) : 0u;
-            }
+        // the item's rows of q, swizzled as the tiles are
+        for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kCtaThreads) {
+            const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < n_rows)
+                v = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + row / p.group) * p.ldq +
+                                                          (int64_t)(g.h * p.group + row % p.group) * HD + c * 8));
+            *reinterpret_cast<uint4*>(qbuf + (c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
         }
-        float o[NC][4];
+        // the masks of the lane's rows
+        uint64_t mask[RW][2];
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-            o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int i = 0; i < 2 * RW; ++i) {
+            const int row = g.rt * ROWS + (i >> 1) * 16 + (i & 1) * 8 + gi, t = row / p.group;
+            mask[i >> 1][i & 1] = row >= n_rows ? 0 : p.masks == nullptr ? ~0ull >> (63 - t) : p.masks[q.r0 + t];
+        }
+        named_bar_sync(1, kCtaThreads);
+        const uint32_t q_at = smem_u32(qbuf);
+        auto q_frag = [&](uint32_t (&a)[4], int rw, int ks) {
+            ldsm4(a, q_at + (ks >> 2) * (ROWS * 128) + (rw * 16 + v_row) * 128 + ((((ks & 3) * 2 + v_bit) ^ (v_row & 7)) << 4));
+        };
+        uint32_t qa[kQRegs ? KS : 1][4];
+        if (kQRegs) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+                q_frag(qa[kQRegs ? ks : 0], 0, ks);
+        }
+        float o[RW][NC][4];
+        float m[RW][2], l[RW][2];  // the rows' references and sums
+#pragma unroll
+        for (int r = 0; r < RW; ++r) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                o[r][i][0] = o[r][i][1] = o[r][i][2] = o[r][i][3] = 0.f;
+            m[r][0] = m[r][1] = -INFINITY;
+            l[r][0] = l[r][1] = 0.f;
+        }
 
-        for (int t = g.t0; t < g.t1; ++t, ++n) {
-            if (TEAMS == 2 && (n & 1) != team)
-                continue;
-            const int st = n % C::kStages;
-            const bool ok = attn_wait(&full[st], (n / C::kStages) & 1, flags, p.status, p.limit_ns);
-            if (!__all_sync(0xffffffffu, ok))
+        for (int t = g.t0 + warp; t < g.t1 && alive; t += kWarps) {
+            const int k0 = t * KT;
+            const uint32_t ks_slot = taken % NS;
+            alive = __all_sync(0xffffffffu, attn_wait(&full[ks_slot], (taken / NS) & 1, flags, p.status, p.limit_ns));
+            if (!alive)
                 break;
-            const uint32_t tile = smem_u32(ring + (size_t)st * C::kTileBytes);
+            // S = Q K^T
+            const uint32_t k_at = smem_u32(ring + ks_slot * C::kSlotBytes);
+            float s[RW][2 * CH][4] = {};
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
-                const int r0 = (piece + ch) * 16, k0 = t * kKeys + r0;
-                if (k0 >= len)
-                    break;
-                const uint32_t at = tile + (r0 / box) * (box * HD * 2) + (r0 % box) * 128;
-                // S = Q K^T
-                float s[2][4] = {};
+                const uint32_t at = k_at + (ch * 16 / box) * (box * HD * 2) + (ch * 16 % box) * 128 + k_row * 128;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t b[4];
-                    ldsm4(b, at + (ks >> 2) * half + k_row * 128 + ((((ks & 3) * 2 + k_bit) ^ (k_row & 7)) << 4));
-                    mma_bf16_16816(s[0], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b[0], b[1]);
-                    mma_bf16_16816(s[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b[2], b[3]);
-                }
-                const bool edge = k0 + 16 > q.base;  // the block's own tokens, or what lies behind them
-                unsigned see0 = 0xFu, see1 = 0xFu;   // bits: keys 2 ti, 2 ti + 1, 2 ti + 8, 2 ti + 9
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int kq = 0; kq < KS; kq += 4) {  // four fragments ahead of the MMAs that take them
+                    uint32_t b[4][4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        s[i][j] *= p.scale_log2;
+                        ldsm4(b[j], at + (kq >> 2) * half + (((j * 2 + k_bit) ^ (k_row & 7)) << 4));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) {
+                            uint32_t a[4];
+                            if (kQRegs)
+                                a[0] = qa[kQRegs ? kq + j : 0][0], a[1] = qa[kQRegs ? kq + j : 0][1], a[2] = qa[kQRegs ? kq + j : 0][2], a[3] = qa[kQRegs ? kq + j : 0][3];
+                            else
+                                q_frag(a, r, kq + j);
+                            mma_bf16_16816(s[r][2 * ch], a[0], a[1], a[2], a[3], b[j][0], b[j][1]);
+                            mma_bf16_16816(s[r][2 * ch + 1], a[0], a[1], a[2], a[3], b[j][2], b[j][3]);
+                        }
+                }
+            }
+            ++taken;
+            __syncwarp();
+            load();  // into the slot just read
+
+            const bool edge = k0 + KT > q.base;  // the block's own tokens, or what lies behind them
+            unsigned see[RW][2];                 // bit 2 i + j: key 8 i + 2 ti + j
+#pragma unroll
+            for (int r = 0; r < RW; ++r) {
+#pragma unroll
+                for (int i = 0; i < 2 * CH; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[r][i][j] *= p.scale_log2;
                 if (edge) {
-                    see0 = see1 = 0u;
+                    see[r][0] = see[r][1] = 0u;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int k = k0 + (i >> 1) * 8 + ti * 2 + (i & 1), j = k - q.base;
-                        const bool ctx = j < 0, in = k < len;
-                        if (ctx || (in && (mask0 >> (j & 63) & 1)))
-                            see0 |= 1u << i;
-                        else
-                            s[i >> 1][i & 1] = -INFINITY;
-                        if (ctx || (in && (mask1 >> (j & 63) & 1)))
-                            see1 |= 1u << i;
-                        else
-                            s[i >> 1][2 + (i & 1)] = -INFINITY;
+                    for (int i = 0; i < 4 * CH; ++i) {
+                        const int tok = k0 + (i >> 1) * 8 + ti * 2 + (i & 1), j = tok - q.base;
+                        const bool ctx = j < 0, in = tok < len;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (ctx || (in && (mask[r][h] >> (j & 63) & 1)))
+                                see[r][h] |= 1u << i;
+                            else
+                                s[r][i >> 1][2 * h + (i & 1)] = -INFINITY;
+                        }
                     }
                 }
-                // running maximum of each row, over its four lanes
-                float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-                float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
-                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-                if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
-                    const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-                    const float f0 = n0 == -INFINITY ? 1.f : attn_ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : attn_ex2(m1 - n1);
-                    m0 = n0, m1 = n1;
-                    l0 *= f0, l1 *= f1;
+                // each row's largest, over its four lanes
+                float x[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        o[i][0] *= f0, o[i][1] *= f0;
-                        o[i][2] *= f1, o[i][3] *= f1;
+                for (int i = 0; i < 2 * CH; ++i) {
+                    x[0] = fmaxf(x[0], fmaxf(s[r][i][0], s[r][i][1]));
+                    x[1] = fmaxf(x[1], fmaxf(s[r][i][2], s[r][i][3]));
+                }
+#pragma unroll
+                for (int f = 1; f < 4; f *= 2) {
+                    x[0] = fmaxf(x[0], __shfl_xor_sync(0xffffffffu, x[0], f));
+                    x[1] = fmaxf(x[1], __shfl_xor_sync(0xffffffffu, x[1], f));
+                }
+                if (__any_sync(0xffffffffu, x[0] > m[r][0] + kGrow || x[1] > m[r][1] + kGrow)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float now = fmaxf(m[r][h], x[h]), f = now == -INFINITY ? 1.f : attn_ex2(m[r][h] - now);
+                        m[r][h] = now;
+                        l[r][h] *= f;
+#pragma unroll
+                        for (int i = 0; i < NC; ++i)
+                            o[r][i][2 * h] *= f, o[r][i][2 * h + 1] *= f;
                     }
                 }
-                const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
+                const float ref0 = m[r][0] == -INFINITY ? 0.f : m[r][0], ref1 = m[r][1] == -INFINITY ? 0.f : m[r][1];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    s[i][0] = attn_ex2(s[i][0] - ref0), s[i][1] = attn_ex2(s[i][1] - ref0);
-                    s[i][2] = attn_ex2(s[i][2] - ref1), s[i][3] = attn_ex2(s[i][3] - ref1);
-                    l0 += s[i][0] + s[i][1];
-                    l1 += s[i][2] + s[i][3];
+                for (int i = 0; i < 2 * CH; ++i) {
+                    s[r][i][0] = attn_ex2(s[r][i][0] - ref0), s[r][i][1] = attn_ex2(s[r][i][1] - ref0);
+                    s[r][i][2] = attn_ex2(s[r][i][2] - ref1), s[r][i][3] = attn_ex2(s[r][i][3] - ref1);
+                    l[r][0] += s[r][i][0] + s[r][i][1];
+                    l[r][1] += s[r][i][2] + s[r][i][3];
                 }
-                // weights rounded to bf16, the type of V: 2^-8 each, under the output's own rounding
-                const uint32_t a0 = f32x2_to_bf16x2(s[0][0], s[0][1]), a1 = f32x2_to_bf16x2(s[0][2], s[0][3]);
-                const uint32_t a2 = f32x2_to_bf16x2(s[1][0], s[1][1]), a3 = f32x2_to_bf16x2(s[1][2], s[1][3]);
-                const uint32_t vat = at + C::kTileBytes / 2;
-                uint32_t odd = 0;
-                const int left = len - k0;  // keys of the piece that exist
+            }
+            // weights rounded to bf16, the type of V: 2^-8 each, under the output's own rounding
+            uint32_t w[RW][CH][4];
+#pragma unroll
+            for (int r = 0; r < RW; ++r)
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) {
+                    w[r][ch][0] = f32x2_to_bf16x2(s[r][2 * ch][0], s[r][2 * ch][1]);
+                    w[r][ch][1] = f32x2_to_bf16x2(s[r][2 * ch][2], s[r][2 * ch][3]);
+                    w[r][ch][2] = f32x2_to_bf16x2(s[r][2 * ch + 1][0], s[r][2 * ch + 1][1]);
+                    w[r][ch][3] = f32x2_to_bf16x2(s[r][2 * ch + 1][2], s[r][2 * ch + 1][3]);
+                }
+
+            // O += P V
+            const uint32_t vs = taken % NS;
+            alive = __all_sync(0xffffffffu, attn_wait(&full[vs], (taken / NS) & 1, flags, p.status, p.limit_ns));
+            if (!alive)
+                break;
+            const uint32_t v_at = smem_u32(ring + vs * C::kSlotBytes);
+#pragma unroll
+            for (int ch = 0; ch < CH; ++ch) {
+                const uint32_t at = v_at + (ch * 16 / box) * (box * HD * 2) + (ch * 16 % box) * 128;
+                if (!edge) {
+#pragma unroll
+                    for (int i = 0; i < NC / 2; i += 4) {
+                        uint32_t b[4][4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            ldsm4_trans(b[j], at + (i >> 2) * half + v_row * 128 + (((j * 2 + v_bit) ^ (v_row & 7)) << 4));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int r = 0; r < RW; ++r) {
+                                mma_bf16_16816(o[r][2 * (i + j)], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], b[j][0], b[j][1]);
+                                mma_bf16_16816(o[r][2 * (i + j) + 1], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], b[j][2], b[j][3]);
+                            }
+                    }
+                    continue;
+                }
+                const int left = len - (k0 + ch * 16);  // keys of the piece that exist
+                if (left <= 0)
+                    continue;
                 // nothing behind the sequence's end takes part: not even as 0 times NaN
                 const uint32_t in_lo = (2 * ti < left ? 0xFFFFu : 0u) | (2 * ti + 1 < left ? 0xFFFF0000u : 0u);
                 const uint32_t in_hi = (2 * ti + 8 < left ? 0xFFFFu : 0u) | (2 * ti + 9 < left ? 0xFFFF0000u : 0u);
+                uint32_t odd = 0;
 #pragma unroll
                 for (int i = 0; i < NC / 2; ++i) {
                     uint32_t b[4];
-                    ldsm4_trans(b, vat + (i >> 2) * half + v_row * 128 + ((((i & 3) * 2 + v_bit) ^ (v_row & 7)) << 4));
-                    if (edge) {
-                        b[0] &= in_lo, b[1] &= in_hi, b[2] &= in_lo, b[3] &= in_hi;
+                    ldsm4_trans(b, at + (i >> 2) * half + v_row * 128 + ((((i & 3) * 2 + v_bit) ^ (v_row & 7)) << 4));
+                    b[0] &= in_lo, b[1] &= in_hi, b[2] &= in_lo, b[3] &= in_hi;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t x = nonfinite2(b[j]);
-                            odd |= x;
-                            b[j] &= ~x;
-                        }
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t x = nonfinite2(b[j]);
+                        odd |= x;
+                        b[j] &= ~x;
                     }
-                    mma_bf16_16816(o[2 * i], a0, a1, a2, a3, b[0], b[1]);
-                    mma_bf16_16816(o[2 * i + 1], a0, a1, a2, a3, b[2], b[3]);
-                }
-                if (edge && __any_sync(0xffffffffu, odd != 0)) {
-                    // infinities and NaN among the values: they reach the rows that see their key alone
-                    for (int k = 0; k < 16 && k < left; ++k) {
-                        const int src = (lane & ~3) | ((k & 7) >> 1), bit = (k >> 3) * 2 + (k & 1);
-                        const uint32_t w01 = k < 8 ? a0 : a2, w23 = k < 8 ? a1 : a3;
-                        const uint32_t p0 = __shfl_sync(0xffffffffu, w01, src), p1 = __shfl_sync(0xffffffffu, w23, src);
-                        const bool r0s = __shfl_sync(0xffffffffu, see0, src) >> bit & 1, r1s = __shfl_sync(0xffffffffu, see1, src) >> bit & 1;
-                        const float w0 = k & 1 ? bf16hi_f32(p0) : bf16lo_f32(p0), w1 = k & 1 ? bf16hi_f32(p1) : bf16lo_f32(p1);
 #pragma unroll
-                        for (int i = 0; i < NC; ++i) {
-                            uint32_t v;
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(vat + (i >> 3) * half + k * 128 + (((i & 7) ^ (k & 7)) << 4) + ti * 4) : "memory");
-                            const uint32_t x = nonfinite2(v);
-                            if (x & 0xFFFFu) {
-                                if (r0s) o[i][0] += w0 * bf16lo_f32(v);
-                                if (r1s) o[i][2] += w1 * bf16lo_f32(v);
-                            }
-                            if (x >> 16) {
-                                if (r0s) o[i][1] += w0 * bf16hi_f32(v);
-                                if (r1s) o[i][3] += w1 * bf16hi_f32(v);
+                    for (int r = 0; r < RW; ++r) {
+                        mma_bf16_16816(o[r][2 * i], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], b[0], b[1]);
+                        mma_bf16_16816(o[r][2 * i + 1], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], b[2], b[3]);
+                    }
+                }
+                if (__any_sync(0xffffffffu, odd != 0)) {
+                    // infinities and NaN among the values: they reach the rows that see their key alone
+#pragma unroll 1
+                    for (int k = 0; k < 16 && k < left; ++k) {
+                        const int src = (lane & ~3) | ((k & 7) >> 1), bit = ch * 4 + (k >> 3) * 2 + (k & 1);
+#pragma unroll
+                        for (int r = 0; r < RW; ++r) {
+                            const uint32_t p0 = __shfl_sync(0xffffffffu, k < 8 ? w[r][ch][0] : w[r][ch][2], src);
+                            const uint32_t p1 = __shfl_sync(0xffffffffu, k < 8 ? w[r][ch][1] : w[r][ch][3], src);
+                            const bool s0 = __shfl_sync(0xffffffffu, see[r][0], src) >> bit & 1, s1 = __shfl_sync(0xffffffffu, see[r][1], src) >> bit & 1;
+                            const float w0 = k & 1 ? bf16hi_f32(p0) : bf16lo_f32(p0), w1 = k & 1 ? bf16hi_f32(p1) : bf16lo_f32(p1);
+#pragma unroll
+                            for (int i = 0; i < NC; ++i) {
+                                uint32_t v;
+                                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + (i >> 3) * half + k * 128 + (((i & 7) ^ (k & 7)) << 4) + ti * 4) : "memory");
+                                const uint32_t x = nonfinite2(v);
+                                if (x & 0xFFFFu) {
+                                    if (s0) o[r][i][0] += w0 * bf16lo_f32(v);
+                                    if (s1) o[r][i][2] += w1 * bf16lo_f32(v);
+                                }
+                                if (x >> 16) {
+                                    if (s0) o[r][i][1] += w0 * bf16hi_f32(v);
+                                    if (s1) o[r][i][3] += w1 * bf16hi_f32(v);
+                                }
                             }
                         }
                     }
                 }
             }
+            ++taken;
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&empty[st]);
+            load();
         }
 
-        // ---- the segment's end: the key groups' parts of each row joined
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        if (ti == 0) {
-            ml[(warp * 16 + gi) * 2] = m0;
-            ml[(warp * 16 + gi) * 2 + 1] = l0;
-            ml[(warp * 16 + gi + 8) * 2] = m1;
-            ml[(warp * 16 + gi + 8) * 2 + 1] = l1;
-        }
-        named_bar_sync(1, kWarps * 32);
-        float top0 = -INFINITY, top1 = -INFINITY;
+        // ---- the segment's end: the warps' parts of each row joined, some columns at a time
 #pragma unroll
-        for (int k = 0; k < KG; ++k) {
-            top0 = fmaxf(top0, ml[((k * RW + rw) * 16 + gi) * 2]);
-            top1 = fmaxf(top1, ml[((k * RW + rw) * 16 + gi + 8) * 2]);
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                l[r][h] += __shfl_xor_sync(0xffffffffu, l[r][h], 1);
+                l[r][h] += __shfl_xor_sync(0xffffffffu, l[r][h], 2);
+                if (ti == 0)
+                    *reinterpret_cast<float2*>(ml + (warp * ROWS + r * 16 + h * 8 + gi) * 2) = make_float2(m[r][h], l[r][h]);
+            }
+        named_bar_sync(1, kCtaThreads);
+        float f[RW][2];
+#pragma unroll
+        for (int r = 0; r < RW; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k)
+                    top = fmaxf(top, ml[(k * ROWS + r * 16 + h * 8 + gi) * 2]);
+                f[r][h] = top == -INFINITY ? 1.f : attn_ex2(m[r][h] - top);
+            }
+        // a thread sums four columns of a row over the warps
+        constexpr int kQuads = C::kCols / 4;
+        const bool sums = threadIdx.x < ROWS * kQuads;
+        const int sr = threadIdx.x / kQuads, sc = threadIdx.x % kQuads * 4;
+        float top = -INFINITY, all = 0.f;
+        if (sums) {
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k)
+                top = fmaxf(top, ml[(k * ROWS + sr) * 2]);
+            const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k)
+                all = fmaf(attn_ex2(ml[(k * ROWS + sr) * 2] - ref), ml[(k * ROWS + sr) * 2 + 1], all);
         }
-        const float f0 = top0 == -INFINITY ? 1.f : attn_ex2(m0 - top0), f1 = top1 == -INFINITY ? 1.f : attn_ex2(m1 - top1);
+        const float inv = all == 0.f ? 0.f : 1.f / all;
         const bool whole = g.t0 == 0 && g.t1 == g.nt;
-        const int slot = g.t0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1;
-        float* part = p.parts + (int64_t)slot * (ROWS * (HD + 2));
-        for (int c0 = 0; c0 < HD; c0 += kOutCols) {
+        float* part = p.parts + (int64_t)(g.t0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * (ROWS * (HD + 2));
+        const int row = g.rt * ROWS + sr;
+        uint16_t* out = p.o + ((int64_t)(q.r0 + row / p.group) * p.n_q + g.h * p.group + row % p.group) * HD;
+        if (sums && !whole && sc == 0 && row < n_rows)
+            __stcg(reinterpret_cast<float2*>(part + ROWS * HD + 2 * sr), make_float2(top, all));
+#pragma unroll
+        for (int c0 = 0; c0 < HD; c0 += C::kCols) {
             if (c0 > 0)
-                named_bar_sync(1, kWarps * 32);  // the last columns have been read
-            float* mine = outbuf + (warp * 16 + gi) * kOutStride + ti * 2;
+                named_bar_sync(1, kCtaThreads);  // the last columns have been read
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (i * 8 >= c0 && i * 8 < c0 + kOutCols) {
-                    *reinterpret_cast<float2*>(mine + i * 8 - c0) = make_float2(o[i][0] * f0, o[i][1] * f0);
-                    *reinterpret_cast<float2*>(mine + 8 * kOutStride + i * 8 - c0) = make_float2(o[i][2] * f1, o[i][3] * f1);
-                }
-            named_bar_sync(1, kWarps * 32);
-            constexpr int kQuads = (HD < kOutCols ? HD : kOutCols) / 4;
-            for (int i = threadIdx.x; i < ROWS * kQuads; i += kWarps * 32) {
-                const int r = i / kQuads, c = i % kQuads * 4, w = r / 16, rr = r % 16;
-                float top = -INFINITY, l = 0.f;
+            for (int r = 0; r < RW; ++r) {
+                float* mine = outbuf + (warp * ROWS + r * 16 + gi) * C::kStride + ti * 2;
 #pragma unroll
-                for (int k = 0; k < KG; ++k)
-                    top = fmaxf(top, ml[((k * RW + w) * 16 + rr) * 2]);
-                const float ref = top == -INFINITY ? 0.f : top;
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < KG; ++k) {
-                    const int wk = k * RW + w;
-                    l = fmaf(attn_ex2(ml[(wk * 16 + rr) * 2] - ref), ml[(wk * 16 + rr) * 2 + 1], l);
-                    const float4 v = *reinterpret_cast<const float4*>(outbuf + (wk * 16 + rr) * kOutStride + c);
-                    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-                }
-                const int row = g.rt * ROWS + r;
-                if (row >= n_rows)
-                    continue;
-                if (whole) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + row / p.group) * p.n_q + g.h * p.group + row % p.group) * HD + c0 + c) =
-                        bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
-                } else {
-                    __stcg(reinterpret_cast<float4*>(part + r * HD + c0 + c), a);
-                    if (c0 + c == 0)
-                        __stcg(reinterpret_cast<float2*>(part + ROWS * HD + 2 * r), make_float2(top, l));
+                for (int i = 0; i < C::kCols / 8; ++i) {
+                    const float* v = o[r][c0 / 8 + i];
+                    *reinterpret_cast<float2*>(mine + i * 8) = make_float2(v[0] * f[r][0], v[1] * f[r][0]);
+                    *reinterpret_cast<float2*>(mine + 8 * C::kStride + i * 8) = make_float2(v[2] * f[r][1], v[3] * f[r][1]);
                 }
             }
+            named_bar_sync(1, kCtaThreads);
+            if (sums && row < n_rows) {
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kWarps; ++k) {
+                    const float4 v = *reinterpret_cast<const float4*>(outbuf + (k * ROWS + sr) * C::kStride + sc);
+                    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                }
+                if (whole)
+                    *reinterpret_cast<uint2*>(out + c0 + sc) = bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+                else
+                    __stcg(reinterpret_cast<float4*>(part + sr * HD + c0 + sc), a);
+            }
         }
+        if (threadIdx.x == 0)
+            flags[2] = flags[0];
         if (!whole) {
             const int64_t first = g.u - g.t0;  // the item's first unit
             const int ca = shares.cta_of(first), cz = shares.cta_of(first + g.nt - 1);
-            __threadfence();
-            named_bar_sync(1, kWarps * 32);
-            if (threadIdx.x == 0) {
+            named_bar_sync(1, kCtaThreads);
+            if (threadIdx.x == 0) {  // the barrier above and this release cover every thread's part
                 const int last = !flags[0] && atom_add_acq_rel_gpu(&p.counters[ca], 1u) == (unsigned)(cz - ca);
                 if (last)
                     p.counters[ca] = 0;
                 flags[1] = last;
             }
-            named_bar_sync(1, kWarps * 32);
-            if (flags[1]) {
-                __threadfence();
-                for (int i = threadIdx.x; i < ROWS * (HD / 4); i += kWarps * 32) {
-                    const int r = i / (HD / 4), c = i % (HD / 4) * 4, row = g.rt * ROWS + r;
-                    if (row < n_rows)
-                        *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + row / p.group) * p.n_q + g.h * p.group + row % p.group) * HD + c) =
+            named_bar_sync(1, kCtaThreads);
+            if (flags[1])
+                for (int i = threadIdx.x; i < ROWS * (HD / 4); i += kCtaThreads) {
+                    const int r = i / (HD / 4), c = i % (HD / 4) * 4, at = g.rt * ROWS + r;
+                    if (at < n_rows)
+                        *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + at / p.group) * p.n_q + g.h * p.group + at % p.group) * HD + c) =
                             bf16x4(join_parts<ROWS, HD>(p.parts, ca, cz, r, c));
                 }
-            }
         }
-        if (threadIdx.x == 0)
-            flags[2] = flags[0];
-        named_bar_sync(1, kWarps * 32);  // the buffers may be written again
+        named_bar_sync(1, kCtaThreads);  // the buffers may be written again
         if (flags[2])                    // one answer for all warps
             break;
         u += g.t1 - g.t0;
     }
+    // no copy may be in flight when the CTA leaves (after a wait that gave up)
+    for (; taken < issued; ++taken)
+        mbar_wait_bounded(&full[taken % NS], (taken / NS) & 1, p.limit_ns);
 }
 
 template <int HD, int RW>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream, bool pdl)
 {
-    const size_t smem = Cfg<HD>::smem(p.B);
+    static_assert(Cfg<HD, RW>::smem(kMaxAttnSeqs) <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(tree_attn_warp_kernel<HD, RW>, (int)Cfg<HD>::smem(kMaxAttnSeqs), done);
+    const cudaError_t e = allow_smem(tree_attn_warp_kernel<HD, RW>, (int)Cfg<HD, RW>::smem(kMaxAttnSeqs), done);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(tree_attn_warp_kernel<HD, RW>, dim3(device_sms()), dim3(kCtaThreads), smem, stream, pdl, p, map);
+    return launch_pdl(tree_attn_warp_kernel<HD, RW>, dim3(device_sms()), dim3(kCtaThreads), Cfg<HD, RW>::smem(p.B), stream, pdl, p, map);
 }
 
 }  // namespace
 
+int attn_warp_box(int head_dim, int page_size) { return head_dim == 256 ? 16 : page_size < 32 ? page_size : 32; }
+
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl)
 {
     if (p.c.head_dim == 64)
-        return rows == 16 ? launch<64, 1>(p, map, stream, pdl) : rows == 32 ? launch<64, 2>(p, map, stream, pdl) : launch<64, 4>(p, map, stream, pdl);
+        return rows == 16 ? launch<64, 1>(p, map, stream, pdl) : launch<64, 2>(p, map, stream, pdl);
     if (p.c.head_dim == 128)
-        return rows == 16 ? launch<128, 1>(p, map, stream, pdl) : rows == 32 ? launch<128, 2>(p, map, stream, pdl) : launch<128, 4>(p, map, stream, pdl);
-    return rows == 16 ? launch<256, 1>(p, map, stream, pdl) : rows == 32 ? launch<256, 2>(p, map, stream, pdl) : launch<256, 4>(p, map, stream, pdl);
+        return rows == 16 ? launch<128, 1>(p, map, stream, pdl) : launch<128, 2>(p, map, stream, pdl);
+    return launch<256, 1>(p, map, stream, pdl);
 }
 
 }  // namespace tfq
