@@ -61,98 +61,111 @@ __device__ __forceinline__ SeqRows seq_rows(const AttnParams& p, int b)
     return s;
 }
 
-// Shared memory of a call's schedule: the units before each sequence.
-constexpr size_t schedule_bytes(int B) { return (size_t)(B + 1) * 8; }
+// A sequence of the call's schedule, in shared memory.
+struct SeqEntry {
+    int first;      // units before it
+    int r0, base;   // as in SeqRows
+    int slot_rows;  // slot | rows << 16
+};
+constexpr size_t schedule_bytes(int B) { return (size_t)(B + 1) * sizeof(SeqEntry); }
 
 struct Segment {
-    int b, h, rt;    // item: sequence, key/value head, row tile
-    int t0, t1, nt;  // key tiles t0 .. t1 of nt
-    int64_t u;       // the first unit
+    SeqRows q;       // item: sequence, key/value head, row tile
+    int h, rt;
+    int t0, t1, nt;  // key tiles t0 .. t1 of nt; none of them: t0 == t1
+    int units;       // units it takes
+    int first;       // the item's first key tile, in units
 };
 
-template <int ROWS, int KEYS>
+// An item counts kOver units before its key tiles: what a segment costs apart from them (its
+// queries, joining the warps' parts, the hand-over), so that CTAs with many short items get no more
+// than their share. A CTA has kLeast units or more, so that a short item is not torn apart.
+template <int ROWS, int KEYS, int kOver, int kLeast>
 struct Shares {
-    int64_t* first;  // [B + 1], shared memory: units before each sequence
+    SeqEntry* seq;  // [B + 1]
     const AttnParams& p;
     int64_t total, ctas;  // units; CTAs that have some: every one of them has at least one
 
-    __device__ Shares(const AttnParams& params, void* smem) : first(static_cast<int64_t*>(smem)), p(params), total(0), ctas(0) {}
+    __device__ Shares(const AttnParams& params, void* smem) : seq(static_cast<SeqEntry*>(smem)), p(params), total(0), ctas(0) {}
 
-    // Read anew from the cache that build() has filled: shared memory is the ring's.
-    __device__ __forceinline__ SeqRows seq(int b) const { return seq_rows(p, b); }
+    __device__ __forceinline__ int row_tiles(int rows) const { return (rows * p.group + ROWS - 1) / ROWS; }
+    __device__ __forceinline__ int key_tiles(int len) const { return (int)(((int64_t)len + KEYS - 1) / KEYS); }
 
-    __device__ __forceinline__ int row_tiles(const SeqRows& q) const { return (q.rows * p.group + ROWS - 1) / ROWS; }
-    __device__ __forceinline__ int key_tiles(const SeqRows& q) const { return (q.len() + KEYS - 1) / KEYS; }
-
-    // All threads of the CTA (a multiple of 32); ends with a barrier.
+    // All threads of the CTA (a multiple of 32); has barriers.
     __device__ void build()
     {
         for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-            const SeqRows q = seq(b);
-            first[b + 1] = q.base < 0 ? 0 : (int64_t)p.c.n_kv * row_tiles(q) * key_tiles(q);
+            const SeqRows q = seq_rows(p, b);
+            SeqEntry e{0, q.r0, q.base, 0};
+            if (q.base >= 0) {
+                e.slot_rows = q.slot | q.rows << 16;
+                const int64_t n = (int64_t)p.c.n_kv * row_tiles(q.rows) * (key_tiles(q.len()) + kOver);
+                e.first = n < INT32_MAX ? (int)n : INT32_MAX;
+            } else if (blockIdx.x == b % gridDim.x) {
+                // arguments that do not hold: zero rows, here and there among the CTAs
+                record_status(p.status, TF_E_INVALID_ARG);
+                const int64_t n = (int64_t)q.rows * p.n_q * p.c.head_dim / 8;
+                uint4* o = reinterpret_cast<uint4*>(p.o + (int64_t)q.r0 * p.n_q * p.c.head_dim);
+                for (int64_t i = 0; i < n; ++i)
+                    o[i] = make_uint4(0, 0, 0, 0);
+            }
+            seq[b] = e;
         }
         __syncthreads();
         if (threadIdx.x < 32) {
             int64_t sum = 0;
             for (int b0 = 0; b0 < p.B; b0 += 32) {
                 const int b = b0 + threadIdx.x;
-                int64_t x = b < p.B ? first[b + 1] : 0;
+                const int64_t n = b < p.B ? seq[b].first : 0;
+                int64_t x = n;
                 for (int o = 1; o < 32; o <<= 1) {
                     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
                     if ((int)threadIdx.x >= o)
                         x += y;
                 }
                 if (b < p.B)
-                    first[b + 1] = sum + x;
+                    seq[b].first = (int)min(sum + x - n, (int64_t)INT32_MAX);
                 sum += __shfl_sync(0xffffffffu, x, 31);
             }
             if (threadIdx.x == 0)
-                first[0] = 0;
+                seq[p.B].first = (int)min(sum, (int64_t)INT32_MAX);
         }
         __syncthreads();
-        total = first[p.B];
-        ctas = total < gridDim.x ? total : gridDim.x;
-        // sequences whose arguments do not hold: zero rows
-        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            const SeqRows q = seq(b);
-            if (q.base >= 0)
-                continue;
-            if (threadIdx.x == 0)
-                record_status(p.status, TF_E_INVALID_ARG);
-            const int64_t n = (int64_t)q.rows * p.n_q * p.c.head_dim / 8;
-            uint4* o = reinterpret_cast<uint4*>(p.o + (int64_t)q.r0 * p.n_q * p.c.head_dim);
-            for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
-                o[i] = make_uint4(0, 0, 0, 0);
+        total = seq[p.B].first;
+        if (total == INT32_MAX) {  // more than the units' 31 bits: nothing is done
+            if (blockIdx.x == 0 && threadIdx.x == 0)
+                record_status(p.status, TF_E_UNSUPPORTED_SHAPE);
+            total = 0;
         }
+        ctas = min((total + kLeast - 1) / kLeast, (int64_t)gridDim.x);
     }
 
-    __device__ __forceinline__ int64_t start_of(int64_t cta) const { return cta >= ctas ? total : total * cta / ctas; }
+    __device__ __forceinline__ int start_of(int cta) const { return cta >= ctas ? (int)total : (int)(total * cta / ctas); }
     // the CTA that takes unit u
-    __device__ __forceinline__ int cta_of(int64_t u) const { return (int)(((u + 1) * ctas - 1) / total); }
+    __device__ __forceinline__ int cta_of(int u) const { return (int)(((u + 1) * ctas - 1) / total); }
 
-    __device__ __forceinline__ Segment segment(int64_t u, int64_t end) const
+    __device__ __forceinline__ Segment segment(int u, int end) const
     {
         int lo = 0, hi = p.B - 1;  // the last sequence whose first unit is not behind u
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (first[mid] <= u)
+            if (seq[mid].first <= u)
                 lo = mid;
             else
                 hi = mid - 1;
         }
+        const SeqEntry e = seq[lo];
         Segment g;
-        g.b = lo;
-        g.u = u;
-        const SeqRows q = seq(lo);
-        g.nt = key_tiles(q);
-        const int rt = row_tiles(q);
-        const int64_t local = u - first[lo];
-        const int64_t item = local / g.nt;
-        g.t0 = (int)(local - item * g.nt);
-        g.h = (int)(item / rt);
-        g.rt = (int)(item - (int64_t)g.h * rt);
-        const int64_t left = end - u;
-        g.t1 = left < g.nt - g.t0 ? g.t0 + (int)left : g.nt;
+        g.q = SeqRows{e.slot_rows & 0xFFFF, e.r0, e.slot_rows >> 16, e.base};
+        g.nt = key_tiles(g.q.len());
+        const int rt = row_tiles(g.q.rows), per = g.nt + kOver;
+        const int local = u - e.first, item = local / per, off = local - item * per;
+        g.h = item / rt;
+        g.rt = item - g.h * rt;
+        g.units = min(end - u, per - off);
+        g.t0 = max(off - kOver, 0);
+        g.t1 = max(off + g.units - kOver, 0);
+        g.first = u - off + kOver;
         return g;
     }
 };
@@ -185,47 +198,74 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
-// The joined output of one row's four columns over parts c0 .. c1 of an item (part c0 is the
-// slot 2 c0 + 1, which starts the item; the others continue it in slot 2 c).
-template <int ROWS, int HD>
-__device__ __forceinline__ float4 join_parts(const float* parts, int c0, int c1, int row, int col)
-{
-    constexpr int kFloats = ROWS * (HD + 2);
-    auto at = [&](int c) { return parts + (int64_t)(c == c0 ? 2 * c0 + 1 : 2 * c) * kFloats; };
-    // eight parts at a time, in order: their loads together, then the running softmax over them
-    float m = -INFINITY, l = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0; c <= c1; c += 8) {
-        float2 ml[8];
-        float4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i <= c1) {
-                ml[i] = __ldcg(reinterpret_cast<const float2*>(at(c + i) + ROWS * HD + 2 * row));
-                v[i] = __ldcg(reinterpret_cast<const float4*>(at(c + i) + row * HD + col));
-            }
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i <= c1)
-                top = fmaxf(top, ml[i].x);
-        const float ref = top == -INFINITY ? 0.f : top, f = attn_ex2(m - ref);
-        m = top;
-        l *= f;
-        a.x *= f, a.y *= f, a.z *= f, a.w *= f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i <= c1) {
-                const float w = attn_ex2(ml[i].x - ref);
-                l = fmaf(w, ml[i].y, l);
-                a.x = fmaf(w, v[i].x, a.x), a.y = fmaf(w, v[i].y, a.y), a.z = fmaf(w, v[i].z, a.z), a.w = fmaf(w, v[i].w, a.w);
-            }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    return make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-}
-
 __device__ __forceinline__ uint2 bf16x4(float4 a) { return make_uint2(f32x2_to_bf16x2(a.x, a.y), f32x2_to_bf16x2(a.z, a.w)); }
+
+// Joins parts c0 .. c1 of an item (part c0 is the slot 2 c0 + 1, which starts the item; the others
+// continue it in slot 2 c) and writes the output rows row0 .. row0 + rows. All THREADS threads; few
+// rows: several lanes share four columns of a row and take every lp-th part, so that all parts
+// are asked for at once (their latency, across two dies, is what this costs). The order in which
+// parts are added depends on the call alone.
+template <int ROWS, int HD, int THREADS>
+__device__ __forceinline__ void join_item(const AttnParams& p, const SeqRows& q, int head, int row0, int rows, int c0, int c1)
+{
+    constexpr int kFloats = ROWS * (HD + 2), kQuads = HD / 4;
+    const int items = rows * kQuads;
+    int lp = 1;
+    while (lp < 8 && items * lp * 2 <= THREADS && lp < c1 - c0 + 1)
+        lp *= 2;
+    const int sub = threadIdx.x % lp;
+    for (int i0 = 0; i0 < items; i0 += THREADS / lp) {
+        const int item = i0 + threadIdx.x / lp;
+        const bool in = item < items;
+        const int row = in ? item / kQuads : 0, col = in ? item % kQuads * 4 : 0;
+        float m = -INFINITY, l = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0 + sub; c <= c1; c += 10 * lp) {
+            float2 ml[10];
+            float4 v[10];
+#pragma unroll
+            for (int i = 0; i < 10; ++i)
+                if (c + i * lp <= c1) {
+                    const int cc = c + i * lp;
+                    const float* s = p.parts + (int64_t)(cc == c0 ? 2 * c0 + 1 : 2 * cc) * kFloats;
+                    ml[i] = __ldcg(reinterpret_cast<const float2*>(s + ROWS * HD + 2 * row));
+                    v[i] = __ldcg(reinterpret_cast<const float4*>(s + row * HD + col));
+                }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < 10; ++i)
+                if (c + i * lp <= c1)
+                    top = fmaxf(top, ml[i].x);
+            const float ref = top == -INFINITY ? 0.f : top, f = attn_ex2(m - ref);
+            m = top;
+            l *= f;
+            a.x *= f, a.y *= f, a.z *= f, a.w *= f;
+#pragma unroll
+            for (int i = 0; i < 10; ++i)
+                if (c + i * lp <= c1) {
+                    const float w = attn_ex2(ml[i].x - ref);
+                    l = fmaf(w, ml[i].y, l);
+                    a.x = fmaf(w, v[i].x, a.x), a.y = fmaf(w, v[i].y, a.y), a.z = fmaf(w, v[i].z, a.z), a.w = fmaf(w, v[i].w, a.w);
+                }
+        }
+        for (int o = 1; o < lp; o *= 2) {
+            const float om = __shfl_xor_sync(0xffffffffu, m, o), top = fmaxf(m, om), ref = top == -INFINITY ? 0.f : top;
+            const float f = attn_ex2(m - ref), g = attn_ex2(om - ref);
+            l = l * f + __shfl_xor_sync(0xffffffffu, l, o) * g;
+            a.x = a.x * f + __shfl_xor_sync(0xffffffffu, a.x, o) * g;
+            a.y = a.y * f + __shfl_xor_sync(0xffffffffu, a.y, o) * g;
+            a.z = a.z * f + __shfl_xor_sync(0xffffffffu, a.z, o) * g;
+            a.w = a.w * f + __shfl_xor_sync(0xffffffffu, a.w, o) * g;
+            m = top;
+        }
+        if (in && sub == 0) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int at = row0 + row;
+            *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + at / p.group) * p.n_q + head * p.group + at % p.group) * HD + col) =
+                bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+        }
+    }
+}
 
 // rows: query rows of an item. tfq_attn_warp.cu: 16, and up to head_dim 128 also 32;
 // tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128. *_box: cache rows of a tensor-map box.

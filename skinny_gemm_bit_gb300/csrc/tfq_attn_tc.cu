@@ -28,6 +28,7 @@ constexpr int kTcThreads = 320;  // eight softmax warps, the producer, the MMA w
 constexpr int kSoftThreads = 256;
 constexpr int kMaxSlots_ = 12;
 constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w] at 128 w, O[w] at 256 + 128 w
+constexpr int kTcOver = 6;  // a segment's own cost, in key tiles
 constexpr float kGrow = 8.f;
 
 // offsets in shared memory
@@ -201,14 +202,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    Shares<ROWS, KT> shares(p, smem + kTcSched);
+    Shares<ROWS, KT, kTcOver, 1> shares(p, smem + kTcSched);
     tc_fence_before();
     shares.build();  // its barriers publish the tensor-memory address as well
     __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTcTmem);
-    const int64_t u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
+    const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
 
     if (warp == 8) {
         // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
@@ -218,9 +219,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         uint32_t slot = 0, pass = 0;
         int64_t issued = 0;
         bool gone = false;
-        for (int64_t u = u0; u < u1 && !gone;) {
+        for (int u = u0; u < u1 && !gone;) {
             const Segment g = shares.segment(u, u1);
-            const SeqRows q = shares.seq(g.b);
+            u += g.units;
+            const SeqRows& q = g.q;
             const int32_t* table = p.c.table + (int64_t)q.slot * p.c.max_pages;
             const int len = q.len();
             auto page_at = [&](int t) {
@@ -255,7 +257,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 page = next;
             }
-            u += g.t1 - g.t0;
         }
         if (gone)  // no copy may be in flight when the CTA leaves
             for (int64_t i = issued > slots ? issued - slots : 0; i < issued; ++i)
@@ -270,9 +271,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t seg = 0;
             bool ok = true;
             auto wait_slot = [&](uint32_t pos) { return attn_wait(&full[pos % slots], (pos / slots) & 1, flags, p.status, p.limit_ns); };
-            for (int64_t u = u0; u < u1 && ok; ++seg) {
+            for (int u = u0; u < u1 && ok;) {
                 const Segment g = shares.segment(u, u1);
+                u += g.units;
                 const int n = g.t1 - g.t0, ns = PAIR ? 2 * n : n;
+                if (n == 0)
+                    continue;
                 ok = attn_wait(q_ready, seg & 1, flags, p.status, p.limit_ns);
                 if (!ok)
                     break;
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (ok)
                     tc_commit(o_full);
                 tiles += n;
-                u += n;
+                ++seg;
             }
             // no MMA may be under way when the tensor memory is given back
             tc_commit(fin);
@@ -333,9 +337,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         uint32_t s_phase = 0, seg = 0;
         uint32_t tiles = 0;
-        for (int64_t u = u0; u < u1; ++seg) {
+        for (int u = u0; u < u1;) {
             const Segment g = shares.segment(u, u1);
-            const SeqRows q = shares.seq(g.b);
+            u += g.units;
+            if (g.t0 == g.t1)
+                continue;
+            const SeqRows& q = g.q;
             const int n = g.t1 - g.t0, len = q.len(), n_rows = q.rows * p.group;
             for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kSoftThreads) {
                 const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;
@@ -556,26 +563,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (!whole) {
-                const int64_t first = g.u - g.t0;  // the item's first unit
-                const int ca = shares.cta_of(first), cz = shares.cta_of(first + g.nt - 1);
-                __threadfence();
+                const int ca = shares.cta_of(g.first), cz = shares.cta_of(g.first + g.nt - 1);
                 named_bar_sync(1, kSoftThreads);
-                if (threadIdx.x == 0) {
+                if (threadIdx.x == 0) {  // the barrier above and this release cover every thread's part
                     const int last = !flags[0] && atom_add_acq_rel_gpu(&p.counters[ca], 1u) == (unsigned)(cz - ca);
                     if (last)
                         p.counters[ca] = 0;
                     flags[1] = last;
                 }
                 named_bar_sync(1, kSoftThreads);
-                if (flags[1]) {
-                    __threadfence();
-                    for (int i = threadIdx.x; i < ROWS * (HD / 4); i += kSoftThreads) {
-                        const int r = i / (HD / 4), c = i % (HD / 4) * 4, at = g.rt * ROWS + r;
-                        if (at < n_rows)
-                            *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + at / p.group) * p.n_q + g.h * p.group + at % p.group) * HD + c) =
-                                bf16x4(join_parts<ROWS, HD>(p.parts, ca, cz, r, c));
-                    }
-                }
+                if (flags[1])
+                    join_item<ROWS, HD, kSoftThreads>(p, q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), ca, cz);
             }
             if (threadIdx.x == 0)
                 flags[2] = flags[0];
@@ -584,7 +582,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (flags[2])                     // one answer for all warps
                 break;
             tiles += n;
-            u += n;
+            ++seg;
         }
     }
     tc_fence_before();

@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kCtaThreads = kWarps * 32;
+constexpr int kOver = 16;     // a segment's own cost, in key tiles
 constexpr float kGrow = 8.f;  // the reference of a row moves when its maximum has grown by 2^8
 
 template <int HD, int RW>
@@ -30,14 +31,15 @@ struct Cfg {
     static constexpr int ROWS = 16 * RW;
     static constexpr int kSlotBytes = KT * HD * 2;        // K or V of a tile
     static constexpr int kSlots = 24576 / kSlotBytes;     // of a warp: 3, or 6 at head_dim 64
-    static constexpr int kCols = HD == 256 ? 16 : RW == 2 ? 8 : 32;  // output columns joined at once, as shared memory allows
+    static constexpr int kCols = RW == 2 ? 8 : 16;         // output columns joined at once, as shared memory allows
     static constexpr int kStride = kCols + 4;             // floats
     static constexpr int kMlOff = 0;                      // [kWarps][ROWS][2] floats
     static constexpr int kBarOff = kMlOff + kWarps * ROWS * 2 * 4;
     static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;  // [0] abort [1] last [2] abort, as of a segment's end
-    static constexpr int kOutOff = (kFlagOff + 16 + 127) / 128 * 128;
-    static constexpr int kQOff = (kOutOff + kWarps * ROWS * kStride * 4 + 1023) / 1024 * 1024;
-    static constexpr int kSchedOff = kQOff + ROWS * HD * 2;
+    // the item's queries, and after its last tile what the warps hand over
+    static constexpr int kQOff = (kFlagOff + 16 + 1023) / 1024 * 1024;
+    static constexpr int kOutBytes = kWarps * ROWS * kStride * 4;
+    static constexpr int kSchedOff = kQOff + (ROWS * HD * 2 > kOutBytes ? ROWS * HD * 2 : kOutBytes);
     static constexpr __host__ __device__ size_t ring(int B) { return (kSchedOff + schedule_bytes(B) + 1023) / 1024 * 1024; }
     static constexpr __host__ __device__ size_t smem(int B) { return 1024 + ring(B) + (size_t)kWarps * kSlots * kSlotBytes; }
 };
@@ -88,8 +90,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     float* ml = reinterpret_cast<float*>(smem + C::kMlOff);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff) + warp * NS;  // the warp's own
     volatile int* flags = reinterpret_cast<volatile int*>(smem + C::kFlagOff);
-    float* outbuf = reinterpret_cast<float*>(smem + C::kOutOff);
     uint8_t* qbuf = smem + C::kQOff;
+    float* outbuf = reinterpret_cast<float*>(qbuf);
     uint8_t* ring = smem + C::ring(p.B) + (size_t)warp * NS * C::kSlotBytes;
 
     if (lane == 0) {
@@ -102,52 +104,50 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     }
     pdl_wait();
-    Shares<ROWS, KT> shares(p, smem + C::kSchedOff);
+    Shares<ROWS, KT, kOver, kWarps> shares(p, smem + C::kSchedOff);
     shares.build();
     pdl_launch_dependents();
-    const int64_t u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
+    const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
 
     // ---- the warp's loads, in the order it will read them: K, V of its first tile, of its next ...
     const int box = min(p.c.page_size, KT), boxes = KT / box;
-    int64_t lu = u0;             // first unit of the segment that the next load belongs to
-    Segment lg{};                // that segment
-    int64_t ltable = 0;          // its sequence's row of the page table
-    int lt = 0, lkv = 0;         // the next load: tile, K or V
-    int lpage = -1, llen = 0;    // the lane's page of that tile; the sequence's tokens
+    const int ahead = 32 / boxes;  // tiles whose pages the lanes hold at once
+    int lu = u0;                   // first unit of the segment that the next load belongs to
+    Segment lg{};                  // that segment
+    int lt = 0, lkv = 0;           // the next load: tile, K or V
+    int lpages = -1, lj = 0;       // the lane's page (tile lane / boxes of those, box lane % boxes); which of them is next
     uint32_t issued = 0, taken = 0;
-    auto look = [&]() {  // the page of the lane's box, read well before the load that needs it
-        const int row = lt * KT + lane * box;
-        lpage = lane < boxes && row < llen ? p.c.table[ltable + (row >> p.c.page_shift)] : -1;
-    };
-    auto enter = [&]() {
-        lg = shares.segment(lu, u1);
-        lt = lg.t0 + warp;
-        const SeqRows q = shares.seq(lg.b);
-        llen = q.len();
-        ltable = (int64_t)q.slot * p.c.max_pages;
+    auto look = [&]() {
+        const int t = lt + kWarps * (lane / boxes), row = t * KT + lane % boxes * box;
+        lpages = t < lg.t1 && row < lg.q.len() ? p.c.table[(int64_t)lg.q.slot * p.c.max_pages + (row >> p.c.page_shift)] : -1;
+        lj = 0;
     };
     auto settle = [&]() {  // from a tile behind its segment's end to the next segment that has one
         while (lt >= lg.t1) {
-            lu += lg.t1 - lg.t0;
+            lu += lg.units;
             if (lu >= u1)
                 return;
-            enter();
+            lg = shares.segment(lu, u1);
+            lt = lg.t0 + warp;
+            lj = ahead;
         }
-        look();
+        if (lj == ahead)
+            look();
     };
     auto load = [&]() {
         if (lu >= u1)
             return;
         const uint32_t slot = issued % NS;
+        const int page = __shfl_sync(0xffffffffu, lpages, (lj * boxes + lane) & 31);
         if (lane == 0)
             mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
         __syncwarp();
         if (lane < boxes) {
             const int row = lt * KT + lane * box;
             int y = p.total_rows;  // zeros
-            if (row < llen) {
-                if (lpage >= 0 && lpage < p.c.n_pages)
-                    y = (int)p.c.row_of(p.layer, lkv, lpage, lg.h) + (row & (p.c.page_size - 1));
+            if (row < lg.q.len()) {
+                if (page >= 0 && page < p.c.n_pages)
+                    y = (int)p.c.row_of(p.layer, lkv, page, lg.h) + (row & (p.c.page_size - 1));
                 else
                     record_status(p.status, TF_E_INVALID_ARG);
             }
@@ -159,12 +159,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         } else {
             lkv = 0;
             lt += kWarps;
+            ++lj;
             settle();
         }
     };
     if (u0 < u1) {
-        enter();
-        settle();
+        settle();  // from the empty segment
         for (int i = 0; i < NS; ++i)
             load();
     }
@@ -174,9 +174,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     const int v_row = ((lane >> 3) & 1) * 8 + (lane & 7), v_bit = lane >> 4;  // V (transposed), and Q
     const int half = box * 128;                                              // bytes of a box's 64 columns
     bool alive = true;
-    for (int64_t u = u0; u < u1;) {
+    for (int u = u0; u < u1;) {
         const Segment g = shares.segment(u, u1);
-        const SeqRows q = shares.seq(g.b);
+        u += g.units;
+        if (g.t0 == g.t1)
+            continue;
+        const SeqRows& q = g.q;
         const int len = q.len(), n_rows = q.rows * p.group;
         // the item's rows of q, swizzled as the tiles are
         for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kCtaThreads) {
@@ -478,8 +481,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         if (threadIdx.x == 0)
             flags[2] = flags[0];
         if (!whole) {
-            const int64_t first = g.u - g.t0;  // the item's first unit
-            const int ca = shares.cta_of(first), cz = shares.cta_of(first + g.nt - 1);
+            const int ca = shares.cta_of(g.first), cz = shares.cta_of(g.first + g.nt - 1);
             named_bar_sync(1, kCtaThreads);
             if (threadIdx.x == 0) {  // the barrier above and this release cover every thread's part
                 const int last = !flags[0] && atom_add_acq_rel_gpu(&p.counters[ca], 1u) == (unsigned)(cz - ca);
@@ -489,17 +491,11 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             }
             named_bar_sync(1, kCtaThreads);
             if (flags[1])
-                for (int i = threadIdx.x; i < ROWS * (HD / 4); i += kCtaThreads) {
-                    const int r = i / (HD / 4), c = i % (HD / 4) * 4, at = g.rt * ROWS + r;
-                    if (at < n_rows)
-                        *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + at / p.group) * p.n_q + g.h * p.group + at % p.group) * HD + c) =
-                            bf16x4(join_parts<ROWS, HD>(p.parts, ca, cz, r, c));
-                }
+                join_item<ROWS, HD, kCtaThreads>(p, q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), ca, cz);
         }
         named_bar_sync(1, kCtaThreads);  // the buffers may be written again
         if (flags[2])                    // one answer for all warps
             break;
-        u += g.t1 - g.t0;
     }
     // no copy may be in flight when the CTA leaves (after a wait that gave up)
     for (; taken < issued; ++taken)
