@@ -29,7 +29,7 @@ AttnLayout attn_layout(int head_dim, int rows)
 {
     AttnLayout L{};
     L.counters = 256;
-    L.parts = L.counters + ((size_t)device_sms() * sizeof(unsigned) + 255) / 256 * 256;
+    L.parts = L.counters + ((size_t)device_sms() * 2 * sizeof(unsigned) + 255) / 256 * 256;
     L.total = L.parts + (size_t)2 * device_sms() * rows * (head_dim + 2) * sizeof(float);  // two parts a CTA
     return L;
 }
@@ -127,6 +127,7 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     p.scale_log2 = scale * 1.4426950408889634f;
     p.o = o;
     p.status = static_cast<int*>(ws);
+    (void)flags;  // the launch is cooperative, which excludes a programmatic dependent one
     p.total_rows = (int)p.c.row_of(p.c.n_layers, 0, 0, 0);
     p.limit_ns = kDefaultWaitLimitNs;
     const int rows = attn_rows(max_rows, p.group, p.c.head_dim);
@@ -138,8 +139,7 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(rows, p.c.page_size) : attn_warp_box(p.c.head_dim, p.c.page_size),
                      tc ? 1 : p.c.head_dim / 64, &map))
         return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
-    const cudaError_t e = (tc ? launch_attn_tc : launch_attn_warp)(p, rows, map, static_cast<cudaStream_t>(stream),
-                                                                   (flags & TF_RUN_PDL) != 0);
+    const cudaError_t e = (tc ? launch_attn_tc : launch_attn_warp)(p, rows, map, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }
 

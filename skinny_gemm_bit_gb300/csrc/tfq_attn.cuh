@@ -5,9 +5,12 @@
 // an item's keys come in tiles of kKeyTile. The CTAs of a persistent grid take equal shares of
 // all (item, key tile) units in that order, so the load is even whatever the lengths are, and
 // few rows over a long context still use the whole GPU. A CTA that holds all of an item writes
-// its output; otherwise each writes its part (running maximum, sum and unscaled output) to
-// the workspace and the last to arrive joins them in key order, so the result does not depend
-// on who that is. The lengths are read on the device: a captured call follows them.
+// its output; otherwise each writes its part (running maximum, sum and unscaled output) to the
+// workspace, and once all of an item's parts are there each of its CTAs joins a slice of the
+// output, parts in key order. (Joined by the last to arrive, 19 parts of 16 rows by 128 took one CTA
+// 8 us of a 36 us call.) CTAs wait for one another at their very end only, when all their parts are
+// written; the launch is cooperative, so all of them run. The lengths are read on the device: a
+// captured call follows them.
 #pragma once
 
 #include <cuda.h>
@@ -32,7 +35,7 @@ struct AttnParams {
     float scale_log2;  // scale * log2(e)
     uint16_t* o;
     int* status;
-    unsigned* counters;  // [CTAs], zero between calls
+    unsigned* counters;  // [CTAs][2], zero between calls: parts written, CTAs done with them
     float* parts;        // [2 * CTAs][part_floats]
     uint64_t limit_ns;
 };
@@ -178,6 +181,23 @@ __device__ __forceinline__ float attn_ex2(float x)
     return y;
 }
 
+// Launch with all CTAs running at once (they wait for one another).
+template <class... KArgs, class... Args>
+cudaError_t launch_coop(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 // Bounded wait that also ends when another thread of the CTA has given up.
 __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
                                           uint64_t limit_ns)
@@ -200,49 +220,77 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volati
 
 __device__ __forceinline__ uint2 bf16x4(float4 a) { return make_uint2(f32x2_to_bf16x2(a.x, a.y), f32x2_to_bf16x2(a.z, a.w)); }
 
-// Joins parts c0 .. c1 of an item (part c0 is the slot 2 c0 + 1, which starts the item; the others
-// continue it in slot 2 c) and writes the output rows row0 .. row0 + rows. All THREADS threads; few
-// rows: several lanes share four columns of a row and take every lp-th part, so that all parts
-// are asked for at once (their latency, across two dies, is what this costs). The order in which
-// parts are added depends on the call alone.
+// An item that several CTAs have parts of: c0 .. c1 (part c0 is the slot 2 c0 + 1, which starts the
+// item; the others continue it in slot 2 c).
+struct SplitItem {
+    SeqRows q;
+    int h, row0, rows;  // head; first row and rows of the item
+    int c0, c1;         // c0 > c1: none
+};
+
+// All the CTA's output threads have written its part; one thread of them says so.
+__device__ __forceinline__ void part_written(const AttnParams& p, const SplitItem& s)
+{
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p.counters + 2 * s.c0), "r"(1u) : "memory");
+}
+
+// Waits for the item's parts and writes this CTA's slice of its output. THREADS threads, which
+// share named barrier 1; several lanes share four columns of a row and take every lp-th part, so
+// that all parts are asked for at once. The order in which they are added depends on the call alone.
 template <int ROWS, int HD, int THREADS>
-__device__ __forceinline__ void join_item(const AttnParams& p, const SeqRows& q, int head, int row0, int rows, int c0, int c1)
+__device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem& s, volatile int* abort_flag)
 {
     constexpr int kFloats = ROWS * (HD + 2), kQuads = HD / 4;
-    const int items = rows * kQuads;
+    const int n = s.c1 - s.c0 + 1, me = blockIdx.x - s.c0;
+    if (threadIdx.x == 0) {
+        const long long start = clock64(), limit = (long long)(p.limit_ns * 2);
+        unsigned there = 0;
+        while (true) {
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(there) : "l"(p.counters + 2 * s.c0) : "memory");
+            if (there >= (unsigned)n || *abort_flag)
+                break;
+            if (clock64() - start > limit) {
+                *abort_flag = 1;
+                record_status(p.status, TF_E_TIMEOUT);
+                break;
+            }
+        }
+    }
+    named_bar_sync(1, THREADS);
+    const int items = s.rows * kQuads, i0 = (int)((int64_t)items * me / n), i1 = (int)((int64_t)items * (me + 1) / n);
     int lp = 1;
-    while (lp < 8 && items * lp * 2 <= THREADS && lp < c1 - c0 + 1)
+    while (lp < 8 && (i1 - i0) * lp * 2 <= THREADS && lp < n)
         lp *= 2;
     const int sub = threadIdx.x % lp;
-    for (int i0 = 0; i0 < items; i0 += THREADS / lp) {
-        const int item = i0 + threadIdx.x / lp;
-        const bool in = item < items;
+    for (int at = i0; at < i1; at += THREADS / lp) {
+        const int item = at + threadIdx.x / lp;
+        const bool in = item < i1;
         const int row = in ? item / kQuads : 0, col = in ? item % kQuads * 4 : 0;
         float m = -INFINITY, l = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0 + sub; c <= c1; c += 10 * lp) {
-            float2 ml[10];
-            float4 v[10];
+        for (int c = s.c0 + sub; c <= s.c1; c += 4 * lp) {
+            float2 ml[4];
+            float4 v[4];
 #pragma unroll
-            for (int i = 0; i < 10; ++i)
-                if (c + i * lp <= c1) {
+            for (int i = 0; i < 4; ++i)
+                if (c + i * lp <= s.c1) {
                     const int cc = c + i * lp;
-                    const float* s = p.parts + (int64_t)(cc == c0 ? 2 * c0 + 1 : 2 * cc) * kFloats;
-                    ml[i] = __ldcg(reinterpret_cast<const float2*>(s + ROWS * HD + 2 * row));
-                    v[i] = __ldcg(reinterpret_cast<const float4*>(s + row * HD + col));
+                    const float* part = p.parts + (int64_t)(cc == s.c0 ? 2 * cc + 1 : 2 * cc) * kFloats;
+                    ml[i] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * HD + 2 * row));
+                    v[i] = __ldcg(reinterpret_cast<const float4*>(part + row * HD + col));
                 }
             float top = m;
 #pragma unroll
-            for (int i = 0; i < 10; ++i)
-                if (c + i * lp <= c1)
+            for (int i = 0; i < 4; ++i)
+                if (c + i * lp <= s.c1)
                     top = fmaxf(top, ml[i].x);
             const float ref = top == -INFINITY ? 0.f : top, f = attn_ex2(m - ref);
             m = top;
             l *= f;
             a.x *= f, a.y *= f, a.z *= f, a.w *= f;
 #pragma unroll
-            for (int i = 0; i < 10; ++i)
-                if (c + i * lp <= c1) {
+            for (int i = 0; i < 4; ++i)
+                if (c + i * lp <= s.c1) {
                     const float w = attn_ex2(ml[i].x - ref);
                     l = fmaf(w, ml[i].y, l);
                     a.x = fmaf(w, v[i].x, a.x), a.y = fmaf(w, v[i].y, a.y), a.z = fmaf(w, v[i].z, a.z), a.w = fmaf(w, v[i].w, a.w);
@@ -260,17 +308,23 @@ __device__ __forceinline__ void join_item(const AttnParams& p, const SeqRows& q,
         }
         if (in && sub == 0) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int at = row0 + row;
-            *reinterpret_cast<uint2*>(p.o + ((int64_t)(q.r0 + at / p.group) * p.n_q + head * p.group + at % p.group) * HD + col) =
+            const int r = s.row0 + row;
+            *reinterpret_cast<uint2*>(p.o + ((int64_t)(s.q.r0 + r / p.group) * p.n_q + s.h * p.group + r % p.group) * HD + col) =
                 bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
         }
+    }
+    // the last CTA to have read the parts leaves the counters as the next call wants them
+    named_bar_sync(1, THREADS);
+    if (threadIdx.x == 0 && !*abort_flag && atom_add_acq_rel_gpu(p.counters + 2 * s.c0 + 1, 1u) == (unsigned)(n - 1)) {
+        p.counters[2 * s.c0] = 0;
+        p.counters[2 * s.c0 + 1] = 0;
     }
 }
 
 // rows: query rows of an item. tfq_attn_warp.cu: 16, and up to head_dim 128 also 32;
 // tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128. *_box: cache rows of a tensor-map box.
-cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl);
-cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl);
+cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
 int attn_warp_box(int head_dim, int page_size);
 int attn_tc_box(int rows, int page_size);
 

@@ -33,7 +33,7 @@ constexpr float kGrow = 8.f;
 
 // offsets in shared memory
 constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 272, kTcQReady = 288, kTcOFull = 296, kTcFin = 304;
-constexpr int kTcTmem = 320, kTcFlags = 336 /* [0] abort [1] last [2] abort as of a segment's end */, kTcOdd = 352;
+constexpr int kTcTmem = 320, kTcFlags = 336 /* [0] abort [2] abort as of a segment's end */, kTcOdd = 352;
 constexpr int kTcMl = 1024;  // [2][128] (m, l)
 constexpr int kTcSched = 3072;
 static_assert(kMaxSlots_ * 8 <= 128, "slots");
@@ -336,6 +336,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
         uint32_t s_phase = 0, seg = 0;
+        SplitItem split[2];  // the item that the CTA continues, the one that it starts
+        split[0].c0 = split[1].c0 = 1;
+        split[0].c1 = split[1].c1 = 0;
         uint32_t tiles = 0;
         for (int u = u0; u < u1;) {
             const Segment g = shares.segment(u, u1);
@@ -562,28 +565,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     named_bar_sync(1, kSoftThreads);
                 }
             }
-            if (!whole) {
-                const int ca = shares.cta_of(g.first), cz = shares.cta_of(g.first + g.nt - 1);
-                named_bar_sync(1, kSoftThreads);
-                if (threadIdx.x == 0) {  // the barrier above and this release cover every thread's part
-                    const int last = !flags[0] && atom_add_acq_rel_gpu(&p.counters[ca], 1u) == (unsigned)(cz - ca);
-                    if (last)
-                        p.counters[ca] = 0;
-                    flags[1] = last;
-                }
-                named_bar_sync(1, kSoftThreads);
-                if (flags[1])
-                    join_item<ROWS, HD, kSoftThreads>(p, q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), ca, cz);
-            }
             if (threadIdx.x == 0)
                 flags[2] = flags[0];
             tc_fence_before();                // the output has been read
-            named_bar_sync(1, kSoftThreads);  // the Q buffer may be written again
+            named_bar_sync(1, kSoftThreads);  // the Q buffer may be written again; the part is written
             if (flags[2])                     // one answer for all warps
                 break;
+            if (!whole) {
+                SplitItem& s = split[g.t0 > 0 ? 0 : 1];
+                s = SplitItem{q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), shares.cta_of(g.first), shares.cta_of(g.first + g.nt - 1)};
+                if (threadIdx.x == 0)  // the barrier above and this release cover every thread's part
+                    part_written(p, s);
+            }
             tiles += n;
             ++seg;
         }
+        for (int i = 0; i < 2; ++i)
+            if (split[i].c0 <= split[i].c1)
+                join_slice<ROWS, HD, kSoftThreads>(p, split[i], flags);
     }
     tc_fence_before();
     __syncthreads();
@@ -594,26 +593,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 template <int HD, bool PAIR>
-cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream, bool pdl)
+cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
 {
     using C = TcCfg<HD, PAIR>;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(tree_attn_tc_kernel<HD, PAIR>, 227 * 1024, done);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(tree_attn_tc_kernel<HD, PAIR>, dim3(device_sms()), dim3(kTcThreads), C::smem(p.B), stream, pdl, p, map,
-                      (uint32_t)C::slots(p.B), (int)C::q_off(p.B));
+    return launch_coop(tree_attn_tc_kernel<HD, PAIR>, dim3(device_sms()), dim3(kTcThreads), C::smem(p.B), stream, p, map,
+                       (uint32_t)C::slots(p.B), (int)C::q_off(p.B));
 }
 
 }  // namespace
 
 int attn_tc_box(int rows, int page_size) { return rows == 256 ? page_size : page_size < 64 ? page_size : 64; }
 
-cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl)
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream)
 {
     if (p.c.head_dim == 64)
-        return rows == 128 ? launch<64, false>(p, map, stream, pdl) : launch<64, true>(p, map, stream, pdl);
-    return rows == 128 ? launch<128, false>(p, map, stream, pdl) : launch<128, true>(p, map, stream, pdl);
+        return rows == 128 ? launch<64, false>(p, map, stream) : launch<64, true>(p, map, stream);
+    return rows == 128 ? launch<128, false>(p, map, stream) : launch<128, true>(p, map, stream);
 }
 
 }  // namespace tfq

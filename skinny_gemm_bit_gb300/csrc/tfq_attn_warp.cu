@@ -35,7 +35,7 @@ struct Cfg {
     static constexpr int kStride = kCols + 4;             // floats
     static constexpr int kMlOff = 0;                      // [kWarps][ROWS][2] floats
     static constexpr int kBarOff = kMlOff + kWarps * ROWS * 2 * 4;
-    static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;  // [0] abort [1] last [2] abort, as of a segment's end
+    static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;  // [0] abort [2] abort, as of a segment's end
     // the item's queries, and after its last tile what the warps hand over
     static constexpr int kQOff = (kFlagOff + 16 + 1023) / 1024 * 1024;
     static constexpr int kOutBytes = kWarps * ROWS * kStride * 4;
@@ -173,6 +173,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     const int k_row = (lane >> 4) * 8 + (lane & 7), k_bit = (lane >> 3) & 1;  // ldmatrix rows: K
     const int v_row = ((lane >> 3) & 1) * 8 + (lane & 7), v_bit = lane >> 4;  // V (transposed), and Q
     const int half = box * 128;                                              // bytes of a box's 64 columns
+    SplitItem split[2];  // the item that the CTA continues, the one that it starts
+    split[0].c0 = split[1].c0 = 1;
+    split[0].c1 = split[1].c1 = 0;
     bool alive = true;
     for (int u = u0; u < u1;) {
         const Segment g = shares.segment(u, u1);
@@ -480,50 +483,46 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         }
         if (threadIdx.x == 0)
             flags[2] = flags[0];
-        if (!whole) {
-            const int ca = shares.cta_of(g.first), cz = shares.cta_of(g.first + g.nt - 1);
-            named_bar_sync(1, kCtaThreads);
-            if (threadIdx.x == 0) {  // the barrier above and this release cover every thread's part
-                const int last = !flags[0] && atom_add_acq_rel_gpu(&p.counters[ca], 1u) == (unsigned)(cz - ca);
-                if (last)
-                    p.counters[ca] = 0;
-                flags[1] = last;
-            }
-            named_bar_sync(1, kCtaThreads);
-            if (flags[1])
-                join_item<ROWS, HD, kCtaThreads>(p, q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), ca, cz);
-        }
-        named_bar_sync(1, kCtaThreads);  // the buffers may be written again
+        named_bar_sync(1, kCtaThreads);  // the buffers may be written again; the part is written
         if (flags[2])                    // one answer for all warps
             break;
+        if (!whole) {
+            SplitItem& s = split[g.t0 > 0 ? 0 : 1];
+            s = SplitItem{q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), shares.cta_of(g.first), shares.cta_of(g.first + g.nt - 1)};
+            if (threadIdx.x == 0)  // the barrier above and this release cover every thread's part
+                part_written(p, s);
+        }
     }
+    for (int i = 0; i < 2; ++i)
+        if (split[i].c0 <= split[i].c1)
+            join_slice<ROWS, HD, kCtaThreads>(p, split[i], flags);
     // no copy may be in flight when the CTA leaves (after a wait that gave up)
     for (; taken < issued; ++taken)
         mbar_wait_bounded(&full[taken % NS], (taken / NS) & 1, p.limit_ns);
 }
 
 template <int HD, int RW>
-cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream, bool pdl)
+cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
 {
     static_assert(Cfg<HD, RW>::smem(kMaxAttnSeqs) <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(tree_attn_warp_kernel<HD, RW>, (int)Cfg<HD, RW>::smem(kMaxAttnSeqs), done);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(tree_attn_warp_kernel<HD, RW>, dim3(device_sms()), dim3(kCtaThreads), Cfg<HD, RW>::smem(p.B), stream, pdl, p, map);
+    return launch_coop(tree_attn_warp_kernel<HD, RW>, dim3(device_sms()), dim3(kCtaThreads), Cfg<HD, RW>::smem(p.B), stream, p, map);
 }
 
 }  // namespace
 
 int attn_warp_box(int head_dim, int page_size) { return head_dim == 256 ? 16 : page_size < 32 ? page_size : 32; }
 
-cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream, bool pdl)
+cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream)
 {
     if (p.c.head_dim == 64)
-        return rows == 16 ? launch<64, 1>(p, map, stream, pdl) : launch<64, 2>(p, map, stream, pdl);
+        return rows == 16 ? launch<64, 1>(p, map, stream) : launch<64, 2>(p, map, stream);
     if (p.c.head_dim == 128)
-        return rows == 16 ? launch<128, 1>(p, map, stream, pdl) : launch<128, 2>(p, map, stream, pdl);
-    return launch<256, 1>(p, map, stream, pdl);
+        return rows == 16 ? launch<128, 1>(p, map, stream) : launch<128, 2>(p, map, stream);
+    return launch<256, 1>(p, map, stream);
 }
 
 }  // namespace tfq
