@@ -136,7 +136,7 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
     CUtensorMap map;
     const bool tc = rows > 64;
-    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(rows, p.c.page_size) : attn_warp_box(p.c.head_dim, p.c.page_size),
+    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(p.c.page_size) : attn_warp_box(p.c.head_dim, p.c.page_size),
                      tc ? 1 : p.c.head_dim / 64, &map))
         return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
     const cudaError_t e = (tc ? launch_attn_tc : launch_attn_warp)(p, rows, map, static_cast<cudaStream_t>(stream));

@@ -326,6 +326,6 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
 cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
 int attn_warp_box(int head_dim, int page_size);
-int attn_tc_box(int rows, int page_size);
+int attn_tc_box(int page_size);
 
 }  // namespace tfq

@@ -9,16 +9,18 @@
 //   p = 2^(S - m)         the row's thread, S and P in tensor memory (P over S, as bf16)
 //   O[w] += P V           A from tensor memory, V as it lies in the cache (N-major)
 //
-// The groups take turns: while one forms its weights the tensor cores work for the other. Up to
-// 128 query rows (PAIR false) both groups have the same rows and every other tile of 64 keys, and
-// their outputs are joined at the end; that is bound by the cache's bytes, and small tiles keep
-// more of the ring in flight. Above (PAIR true) each group has 128 rows of its own and both read
-// every tile of 128 keys, so a tile is fetched once for 256 rows.
+// Each group has two score buffers: the scores of its next tile are formed while it works on this
+// one's weights, so neither it nor the tensor cores wait for the other's latency (with one buffer
+// and 128-key tiles a group spent 2600 of 6600 cycles a tile waiting: 206 us against 2 x fewer on
+// trees of 64 rows and 8 heads over 8 x 16001 tokens). Up to 128 query rows (PAIR false) both
+// groups have the same rows and every other tile, and their outputs are joined at the end; that is
+// bound by the cache's bytes. Above (PAIR true) each group has 128 rows of its own and both read
+// every tile, so a tile is fetched once for 256 rows. Tiles are 64 keys: two buffers of them a group
+// and the output fill the tensor memory (4 * 64 + 2 * 128 columns).
 //
 // The reference m of a row moves only when its maximum has grown by more than 2^8: until then
 // the weights stay below 256 and the sums are exact enough, and the output in tensor memory
-// needs no rescaling. MMAs of one thread complete in order: when a tile's scores are there, the
-// group's last product with V is done too, and its output may be rescaled.
+// needs no rescaling; when it does, the group first waits for its last product with V.
 #include "tfq_attn.cuh"
 
 namespace tfq {
@@ -26,21 +28,21 @@ namespace {
 
 constexpr int kTcThreads = 320;  // eight softmax warps, the producer, the MMA warp
 constexpr int kSoftThreads = 256;
-constexpr int kMaxSlots_ = 12;
-constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w] at 128 w, O[w] at 256 + 128 w
-constexpr int kTcOver = 6;  // a segment's own cost, in key tiles
+constexpr int kMaxSlots = 12;
+constexpr int KT = 64;                            // keys of a tile
+constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w][buffer] at 128 w + 64 buffer, O[w] at 256 + 128 w
+constexpr int kTcOver = 12;  // a segment's own cost, in key tiles
 constexpr float kGrow = 8.f;
 
 // offsets in shared memory
-constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 272, kTcQReady = 288, kTcOFull = 296, kTcFin = 304;
-constexpr int kTcTmem = 320, kTcFlags = 336 /* [0] abort [2] abort as of a segment's end */, kTcOdd = 352;
+constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 288, kTcODone = 320, kTcQReady = 352, kTcOFull = 360, kTcFin = 368;
+constexpr int kTcTmem = 384, kTcFlags = 400 /* [0] abort [2] abort as of a segment's end */, kTcOdd = 416;
 constexpr int kTcMl = 1024;  // [2][128] (m, l)
 constexpr int kTcSched = 3072;
-static_assert(kMaxSlots_ * 8 <= 128, "slots");
+static_assert(kMaxSlots * 8 <= 128, "slots");
 
 template <int HD, bool PAIR>
 struct TcCfg {
-    static constexpr int KT = PAIR ? 128 : 64;
     static constexpr int ROWS = PAIR ? 256 : 128;
     static constexpr int kSlotBytes = KT * HD * 2;
     static constexpr int kQBytes = ROWS * HD * 2 < 32768 ? 32768 : ROWS * HD * 2;  // also the groups' exchange, 2 x 16 KB
@@ -48,7 +50,7 @@ struct TcCfg {
     static int slots(int B)
     {
         const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes) / kSlotBytes;
-        return n < kMaxSlots_ ? (int)n : kMaxSlots_;
+        return n < kMaxSlots ? (int)n : kMaxSlots;
     }
     static size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes; }
 };
@@ -93,21 +95,33 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* a)
                  : "memory");
 }
 
-__device__ __forceinline__ void tc_commit(uint64_t* bar)
+// The MMA warp runs as a whole, so that descriptors stay in uniform registers (issued from a
+// one-lane branch, an MMA took 80 cycles to hand over); `one` is true in the lane that issues.
+__device__ __forceinline__ bool elect_one()
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar, bool one)
+{
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+                 " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar)), "r"((int)one) : "memory");
 }
 
 // D (tensor memory) (+)= A B, A and B in shared memory / A in tensor memory
-__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add, bool one)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
-                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)add) : "memory");
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((int)add), "r"((int)one) : "memory");
 }
-__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, bool one)
 {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)add) : "memory");
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+                 " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+                 ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((int)add), "r"((int)one) : "memory");
 }
 
 // Shared-memory matrix descriptor, 128-byte swizzle: start, the step between blocks of 64
@@ -165,13 +179,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tree_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map, uint32_t slots, int q_off)
 {
     using C = TcCfg<HD, PAIR>;
-    constexpr int KT = C::KT, ROWS = C::ROWS;
+    constexpr int ROWS = C::ROWS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTcFull);
     uint64_t* empty = reinterpret_cast<uint64_t*>(smem + kTcEmpty);
+    // [2 w + buffer]: scores there; weights there; the product with V done
     uint64_t* s_full = reinterpret_cast<uint64_t*>(smem + kTcSFull);
     uint64_t* p_ready = reinterpret_cast<uint64_t*>(smem + kTcPReady);
+    uint64_t* o_done = reinterpret_cast<uint64_t*>(smem + kTcODone);
     uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + kTcQReady);
     uint64_t* o_full = reinterpret_cast<uint64_t*>(smem + kTcOFull);
     uint64_t* fin = reinterpret_cast<uint64_t*>(smem + kTcFin);
@@ -187,9 +203,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(&s_full[w], 1);
-            mbar_init(&p_ready[w], 4);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], 4);
+            mbar_init(&o_done[i], 1);
         }
         mbar_init(q_ready, 8);
         mbar_init(o_full, 1);
@@ -262,68 +279,79 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int64_t i = issued > slots ? issued - slots : 0; i < issued; ++i)
                 mbar_wait_bounded(&full[i % slots], (uint32_t)(i / slots) & 1, p.limit_ns);
     } else if (warp == 9) {
-        // ---- MMA thread
-        if (lane == 0) {
+        // ---- MMA warp
+        {
+            const bool one = elect_one();
             constexpr uint32_t kIdS = instr_desc(KT, false), kIdO = instr_desc(HD, true);
             const uint32_t qa = smem_u32(qbuf), ra = smem_u32(ring);
-            uint32_t p_phase[2] = {0, 0};
-            uint32_t tiles = 0;  // before this segment
-            uint32_t seg = 0;
+            // the ring's slots of the next K and the next V tile: every second one
+            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, p_phase = 0 /* a bit a buffer */, seg = 0;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
+            };
+            auto forward = [&](uint32_t& slot, uint32_t& phase) {
+                slot += 2;
+                if (slot >= slots) {
+                    slot -= slots;
+                    phase ^= 1;
+                }
+            };
             bool ok = true;
-            auto wait_slot = [&](uint32_t pos) { return attn_wait(&full[pos % slots], (pos / slots) & 1, flags, p.status, p.limit_ns); };
             for (int u = u0; u < u1 && ok;) {
                 const Segment g = shares.segment(u, u1);
                 u += g.units;
                 const int n = g.t1 - g.t0, ns = PAIR ? 2 * n : n;
                 if (n == 0)
                     continue;
-                ok = attn_wait(q_ready, seg & 1, flags, p.status, p.limit_ns);
+                ok = wait(q_ready, seg & 1);
                 if (!ok)
                     break;
                 tc_fence_after();
+                // step i: group i % 2, its tile i / 2, buffer (i / 2) % 2
                 auto scores = [&](int i) {
-                    const int w = i & 1;
-                    const uint32_t pos = 2 * (tiles + (PAIR ? i >> 1 : i));
-                    if (!wait_slot(pos))
+                    const int w = i & 1, buf = 2 * w + (i >> 1 & 1);
+                    if (!wait(&full[k_slot], k_phase))
                         return false;
-                    const uint32_t kb = ra + (uint32_t)(pos % slots) * C::kSlotBytes;
+                    const uint64_t ad = smem_desc(qa + (PAIR ? w * (128 * HD * 2) : 0), 16, 1024);
+                    const uint64_t bd = smem_desc(ra + k_slot * C::kSlotBytes, 16, 1024);
 #pragma unroll
-                    for (int ks = 0; ks < HD / 16; ++ks)
-                        tc_mma_ss(tmem + 128 * w,
-                                  smem_desc(qa + (PAIR ? w * (128 * HD * 2) : 0) + (ks >> 2) * (128 * 128) + (ks & 3) * 32, 16, 1024),
-                                  smem_desc(kb + (ks >> 2) * (KT * 128) + (ks & 3) * 32, 16, 1024), kIdS, ks > 0);
-                    tc_commit(&s_full[w]);
-                    if (!PAIR || w == 1)
-                        tc_commit(&empty[pos % slots]);
+                    for (int ks = 0; ks < HD / 16; ++ks)  // 32 bytes on within 64 columns, then the next 64
+                        tc_mma_ss(tmem + 64 * buf, ad + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                                  bd + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), kIdS, ks > 0, one);
+                    tc_commit(&s_full[buf], one);
+                    if (!PAIR || w == 1) {
+                        tc_commit(&empty[k_slot], one);
+                        forward(k_slot, k_phase);
+                    }
                     return true;
                 };
-                for (int i = 0; i < 2 && i < ns && ok; ++i)
+                for (int i = 0; i < 4 && i < ns && ok; ++i)
                     ok = scores(i);
                 for (int i = 0; i < ns && ok; ++i) {
-                    const int w = i & 1;
-                    const uint32_t pos = 2 * (tiles + (PAIR ? i >> 1 : i)) + 1;
-                    ok = attn_wait(&p_ready[w], p_phase[w], flags, p.status, p.limit_ns) && wait_slot(pos);
+                    const int w = i & 1, buf = 2 * w + (i >> 1 & 1);
+                    ok = wait(&p_ready[buf], p_phase >> buf & 1) && wait(&full[v_slot], v_phase);
                     if (!ok)
                         break;
-                    p_phase[w] ^= 1;
+                    p_phase ^= 1u << buf;
                     tc_fence_after();
-                    const uint32_t vb = ra + (uint32_t)(pos % slots) * C::kSlotBytes;
+                    const uint64_t bd = smem_desc(ra + v_slot * C::kSlotBytes, KT * 128, 1024);
 #pragma unroll
                     for (int ks = 0; ks < KT / 16; ++ks)
-                        tc_mma_ts(tmem + kOCol + 128 * w, tmem + 128 * w + 8 * ks, smem_desc(vb + ks * 2048, KT * 128, 1024), kIdO,
-                                  i > 1 || ks > 0);
-                    if (!PAIR || w == 1)
-                        tc_commit(&empty[pos % slots]);
-                    if (i + 2 < ns)
-                        ok = scores(i + 2);
+                        tc_mma_ts(tmem + kOCol + 128 * w, tmem + 64 * buf + 8 * ks, bd + (ks * 2048 >> 4), kIdO, i > 1 || ks > 0, one);
+                    tc_commit(&o_done[buf], one);
+                    if (!PAIR || w == 1) {
+                        tc_commit(&empty[v_slot], one);
+                        forward(v_slot, v_phase);
+                    }
+                    if (i + 4 < ns)
+                        ok = scores(i + 4);
                 }
                 if (ok)
-                    tc_commit(o_full);
-                tiles += n;
+                    tc_commit(o_full, one);
                 ++seg;
             }
             // no MMA may be under way when the tensor memory is given back
-            tc_commit(fin);
+            tc_commit(fin, one);
             mbar_wait_bounded(fin, 0, p.limit_ns);
         }
         __syncwarp();
@@ -331,11 +359,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- softmax: group w, a thread a row
         const int w = warp >> 2, wt = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t s_at = tmem + lanes + 128 * w, o_at = tmem + lanes + kOCol + 128 * w;
+        const uint32_t o_at = tmem + lanes + kOCol + 128 * w;
         const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale goes into Q
         const float sc = fmaxf(fabsf(p.scale_log2), 1e-37f);
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u;
-        uint32_t s_phase = 0, seg = 0;
+        uint32_t phase = 0 /* a bit a buffer */, seg = 0;
         SplitItem split[2];  // the item that the CTA continues, the one that it starts
         split[0].c0 = split[1].c0 = 1;
         split[0].c1 = split[1].c1 = 0;
@@ -372,11 +400,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             float m = -INFINITY, l = 0.f;  // the reference, in score units, and the sum against it
             bool had = false, ok = true;
-            for (int t = g.t0 + (PAIR ? 0 : w); t < g.t1; t += PAIR ? 1 : 2) {
-                ok = __all_sync(0xffffffffu, attn_wait(&s_full[w], s_phase, flags, p.status, p.limit_ns));
+            int buf = 0;
+            for (int t = g.t0 + (PAIR ? 0 : w); t < g.t1; t += PAIR ? 1 : 2, buf ^= 1) {
+                ok = __all_sync(0xffffffffu, attn_wait(&s_full[2 * w + buf], phase >> buf & 1, flags, p.status, p.limit_ns));
                 if (!ok)
                     break;
-                s_phase ^= 1;
+                const uint32_t s_at = tmem + lanes + 128 * w + 64 * buf;
                 tc_fence_after();
                 const int k0 = t * KT;
                 const bool edge = k0 + KT > q.base;
@@ -413,37 +442,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     fence_async_smem();
                 }
                 if (busy) {
-                    // 64 columns at a time; of 128 the last 64 are read twice, so that the rest of the
-                    // thread's state stays in registers. P's columns reach only scores already read.
-                    uint32_t s[64];
-                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto read = [&](int c0) {
-                        tc_ld32(s_at + c0, s);
-                        tc_ld32(s_at + c0 + 32, s + 32);
-                        tc_wait_ld(s);
-                        tc_wait_ld(s + 32);
-                        if (edge) {
+                    uint32_t s[KT];
+                    tc_ld32(s_at, s);
+                    tc_ld32(s_at + 32, s + 32);
+                    tc_wait_ld(s);
+                    tc_wait_ld(s + 32);
+                    if (edge) {
 #pragma unroll
-                            for (int c = 0; c < 64; ++c) {
-                                const int tok = k0 + c0 + c, j = tok - q.base;
-                                const bool see = j < 0 || (tok < len && (mask >> (j & 63) & 1));
-                                s[c] = see ? s[c] : 0xFF800000u;  // -inf
-                            }
+                        for (int c = 0; c < KT; ++c) {
+                            const int tok = k0 + c, j = tok - q.base;
+                            const bool see = j < 0 || (tok < len && (mask >> (j & 63) & 1));
+                            s[c] = see ? s[c] : 0xFF800000u;  // -inf
                         }
-                    };
-#pragma unroll
-                    for (int c0 = KT - 64; c0 >= 0; c0 -= 64) {
-                        read(c0);
-#pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
                     }
+                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < KT; ++c)
+                        x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
                     const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                     if (!had) {
                         m = top;
                     } else {
                         const bool grown = (top - m) * sc > kGrow;
                         if (__any_sync(0xffffffffu, grown)) {
+                            // the other buffer's phase has moved on since its scores were read: its
+                            // product with V is the one that counted as `phase` then
+                            ok = __all_sync(0xffffffffu, attn_wait(&o_done[2 * w + (buf ^ 1)], (phase >> (buf ^ 1) & 1) ^ 1, flags, p.status, p.limit_ns));
+                            tc_fence_after();
                             const float f = grown ? attn_ex2((m - top) * sc) : 1.f;
                             if (grown)
                                 m = top;
@@ -463,27 +488,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const float ref = m == -INFINITY ? 0.f : m * sc;
                     float sum[4] = {};
 #pragma unroll
-                    for (int c0 = 0; c0 < KT; c0 += 64) {
-                        if (c0 > 0)
-                            read(c0);
-#pragma unroll
-                        for (int c = 0; c < 64; c += 2) {
-                            const float a = attn_ex2(fmaf(__uint_as_float(s[c]), sc, -ref));
-                            const float b = attn_ex2(fmaf(__uint_as_float(s[c + 1]), sc, -ref));
-                            sum[c & 2] += a;
-                            sum[(c & 2) + 1] += b;
-                            s[c / 2] = f32x2_to_bf16x2(a, b);  // weights in V's type: 2^-8 each, under the output's own rounding
-                        }
-                        tc_st32(s_at + c0 / 2, s);
+                    for (int c = 0; c < KT; c += 2) {
+                        const float a = attn_ex2(fmaf(__uint_as_float(s[c]), sc, -ref));
+                        const float b = attn_ex2(fmaf(__uint_as_float(s[c + 1]), sc, -ref));
+                        sum[c & 2] += a;
+                        sum[(c & 2) + 1] += b;
+                        s[c / 2] = f32x2_to_bf16x2(a, b);  // weights in V's type: 2^-8 each, under the output's own rounding
                     }
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc_st32(s_at, s);
                     tc_wait_st();
                 }
                 had = true;
+                phase ^= 1u << buf;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&p_ready[w]);
+                    mbar_arrive(&p_ready[2 * w + buf]);
             }
             ok = ok && __all_sync(0xffffffffu, attn_wait(o_full, seg & 1, flags, p.status, p.limit_ns));
             tc_fence_after();
@@ -606,7 +627,7 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t str
 
 }  // namespace
 
-int attn_tc_box(int rows, int page_size) { return rows == 256 ? page_size : page_size < 64 ? page_size : 64; }
+int attn_tc_box(int page_size) { return page_size < KT ? page_size : KT; }
 
 cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream)
 {
