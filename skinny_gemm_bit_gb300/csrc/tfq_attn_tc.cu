@@ -26,7 +26,7 @@
 namespace tfq {
 namespace {
 
-constexpr int kTcThreads = 320;  // eight softmax warps, the producer, the MMA warp
+constexpr int kTcThreads = 352;  // eight softmax warps, the producer, an MMA warp for each group
 constexpr int kSoftThreads = 256;
 constexpr int kMaxSlots = 12;
 constexpr int KT = 64;                            // keys of a tile
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < slots; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], PAIR ? 2 : 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
@@ -209,8 +209,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_init(&o_done[i], 1);
         }
         mbar_init(q_ready, 8);
-        mbar_init(o_full, 1);
-        mbar_init(fin, 1);
+        mbar_init(o_full, 2);
+        mbar_init(fin, 2);
         flags[0] = 0;
         fence_mbar_init();
     }
@@ -227,14 +227,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pdl_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTcTmem);
     const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
+    // Slots: one ring for both groups, or half of them for each. Every use of a slot is waited for, in
+    // order, by each MMA warp that its ring serves: a wait can then not take the phase before last
+    // for the one it is after.
+    const uint32_t ring_slots = PAIR ? slots : slots / 2;
 
     if (warp == 8) {
         // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
         const int box = min(p.c.page_size, KT), pieces = KT / box;
         const int z = lane / pieces, piece = lane % pieces;
         const bool active = lane < pieces * (HD / 64);
-        uint32_t slot = 0, pass = 0;
-        int64_t issued = 0;
+        uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0};
         bool gone = false;
         for (int u = u0; u < u1 && !gone;) {
             const Segment g = shares.segment(u, u1);
@@ -253,8 +256,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool in = active && row < len, good = page >= 0 && page < p.c.n_pages;
                 if (in && !good)
                     record_status(p.status, TF_E_INVALID_ARG);
+                const int r = PAIR ? 0 : (t - g.t0) & 1;
                 for (int kv = 0; kv < 2; ++kv) {
-                    const bool ok = pass == 0 || attn_wait(&empty[slot], (pass - 1) & 1, flags, p.status, p.limit_ns);
+                    const uint32_t slot = r * ring_slots + next_slot[r];
+                    const bool ok = pass[r] == 0 || attn_wait(&empty[slot], (pass[r] - 1) & 1, flags, p.status, p.limit_ns);
                     if (!__all_sync(0xffffffffu, ok)) {
                         gone = true;
                         break;
@@ -266,94 +271,94 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const int y = in && good ? (int)p.c.row_of(p.layer, kv, page, g.h) + (row & (p.c.page_size - 1)) : p.total_rows;
                         tma_box(smem_u32(ring + (size_t)slot * C::kSlotBytes + z * KT * 128 + piece * box * 128), &map, y, z, &full[slot]);
                     }
-                    ++issued;
-                    if (++slot == slots) {
-                        slot = 0;
-                        ++pass;
+                    if (++next_slot[r] == ring_slots) {
+                        next_slot[r] = 0;
+                        ++pass[r];
                     }
                 }
                 page = next;
             }
         }
-        if (gone)  // no copy may be in flight when the CTA leaves
-            for (int64_t i = issued > slots ? issued - slots : 0; i < issued; ++i)
-                mbar_wait_bounded(&full[i % slots], (uint32_t)(i / slots) & 1, p.limit_ns);
-    } else if (warp == 9) {
-        // ---- MMA warp
-        {
-            const bool one = elect_one();
-            constexpr uint32_t kIdS = instr_desc(KT, false), kIdO = instr_desc(HD, true);
-            const uint32_t qa = smem_u32(qbuf), ra = smem_u32(ring);
-            // the ring's slots of the next K and the next V tile: every second one
-            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, p_phase = 0 /* a bit a buffer */, seg = 0;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
-            };
-            auto forward = [&](uint32_t& slot, uint32_t& phase) {
-                slot += 2;
-                if (slot >= slots) {
-                    slot -= slots;
-                    phase ^= 1;
+        if (gone)  // no copy may be in flight when the CTA leaves: each slot's last one
+            for (int r = 0; r < (PAIR ? 1 : 2); ++r)
+                for (uint32_t s = 0; s < ring_slots; ++s) {
+                    const uint32_t uses = pass[r] + (s < next_slot[r] ? 1 : 0);
+                    if (uses > 0)
+                        mbar_wait_bounded(&full[r * ring_slots + s], (uses - 1) & 1, p.limit_ns);
                 }
-            };
-            bool ok = true;
-            for (int u = u0; u < u1 && ok;) {
-                const Segment g = shares.segment(u, u1);
-                u += g.units;
-                const int n = g.t1 - g.t0, ns = PAIR ? 2 * n : n;
-                if (n == 0)
-                    continue;
-                ok = wait(q_ready, seg & 1);
+    } else if (warp >= 9) {
+        // ---- an MMA warp: group w's scores and its products with V (one warp for both groups spent
+        // 1340 cycles a step on its waits, one after the other, for 640 of MMAs)
+        const int w = warp - 9;
+        const bool one = elect_one();
+        constexpr uint32_t kIdS = instr_desc(KT, false), kIdO = instr_desc(HD, true);
+        const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
+        const uint32_t ra = smem_u32(ring) + first_slot * C::kSlotBytes;
+        const uint64_t ad = smem_desc(smem_u32(qbuf) + (PAIR ? w * (128 * HD * 2) : 0), 16, 1024);
+        full += first_slot;
+        empty += first_slot;
+        // the ring's slots of the next K and the next V tile: every second one
+        uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, p_phase = 0 /* a bit a buffer */, seg = 0;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
+        };
+        auto forward = [&](uint32_t& slot, uint32_t& phase) {
+            slot += 2;
+            if (slot >= ring_slots) {
+                slot -= ring_slots;
+                phase ^= 1;
+            }
+        };
+        auto scores = [&](int buf) {
+            if (!wait(&full[k_slot], k_phase))
+                return false;
+            const uint64_t bd = smem_desc(ra + k_slot * C::kSlotBytes, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < HD / 16; ++ks)  // 32 bytes on within 64 columns, then the next 64
+                tc_mma_ss(tmem + 64 * (2 * w + buf), ad + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                          bd + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), kIdS, ks > 0, one);
+            tc_commit(&s_full[2 * w + buf], one);
+            tc_commit(&empty[k_slot], one);
+            forward(k_slot, k_phase);
+            return true;
+        };
+        bool ok = true;
+        for (int u = u0; u < u1 && ok;) {
+            const Segment g = shares.segment(u, u1);
+            u += g.units;
+            if (g.t0 == g.t1)
+                continue;
+            const int n = PAIR ? g.t1 - g.t0 : (g.t1 - g.t0 + 1 - w) / 2;  // the group's tiles
+            ok = wait(q_ready, seg & 1);
+            if (!ok)
+                break;
+            tc_fence_after();
+            for (int k = 0; k < 2 && k < n && ok; ++k)
+                ok = scores(k);
+            for (int k = 0; k < n && ok; ++k) {
+                const int buf = k & 1;
+                ok = wait(&p_ready[2 * w + buf], p_phase >> buf & 1) && wait(&full[v_slot], v_phase);
                 if (!ok)
                     break;
+                p_phase ^= 1u << buf;
                 tc_fence_after();
-                // step i: group i % 2, its tile i / 2, buffer (i / 2) % 2
-                auto scores = [&](int i) {
-                    const int w = i & 1, buf = 2 * w + (i >> 1 & 1);
-                    if (!wait(&full[k_slot], k_phase))
-                        return false;
-                    const uint64_t ad = smem_desc(qa + (PAIR ? w * (128 * HD * 2) : 0), 16, 1024);
-                    const uint64_t bd = smem_desc(ra + k_slot * C::kSlotBytes, 16, 1024);
+                const uint64_t bd = smem_desc(ra + v_slot * C::kSlotBytes, KT * 128, 1024);
 #pragma unroll
-                    for (int ks = 0; ks < HD / 16; ++ks)  // 32 bytes on within 64 columns, then the next 64
-                        tc_mma_ss(tmem + 64 * buf, ad + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                                  bd + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), kIdS, ks > 0, one);
-                    tc_commit(&s_full[buf], one);
-                    if (!PAIR || w == 1) {
-                        tc_commit(&empty[k_slot], one);
-                        forward(k_slot, k_phase);
-                    }
-                    return true;
-                };
-                for (int i = 0; i < 4 && i < ns && ok; ++i)
-                    ok = scores(i);
-                for (int i = 0; i < ns && ok; ++i) {
-                    const int w = i & 1, buf = 2 * w + (i >> 1 & 1);
-                    ok = wait(&p_ready[buf], p_phase >> buf & 1) && wait(&full[v_slot], v_phase);
-                    if (!ok)
-                        break;
-                    p_phase ^= 1u << buf;
-                    tc_fence_after();
-                    const uint64_t bd = smem_desc(ra + v_slot * C::kSlotBytes, KT * 128, 1024);
-#pragma unroll
-                    for (int ks = 0; ks < KT / 16; ++ks)
-                        tc_mma_ts(tmem + kOCol + 128 * w, tmem + 64 * buf + 8 * ks, bd + (ks * 2048 >> 4), kIdO, i > 1 || ks > 0, one);
-                    tc_commit(&o_done[buf], one);
-                    if (!PAIR || w == 1) {
-                        tc_commit(&empty[v_slot], one);
-                        forward(v_slot, v_phase);
-                    }
-                    if (i + 4 < ns)
-                        ok = scores(i + 4);
-                }
-                if (ok)
-                    tc_commit(o_full, one);
-                ++seg;
+                for (int ks = 0; ks < KT / 16; ++ks)
+                    tc_mma_ts(tmem + kOCol + 128 * w, tmem + 64 * (2 * w + buf) + 8 * ks, bd + (ks * 2048 >> 4), kIdO, k > 0 || ks > 0, one);
+                tc_commit(&o_done[2 * w + buf], one);
+                tc_commit(&empty[v_slot], one);
+                forward(v_slot, v_phase);
+                if (k + 2 < n)
+                    ok = scores(buf);
             }
-            // no MMA may be under way when the tensor memory is given back
-            tc_commit(fin, one);
-            mbar_wait_bounded(fin, 0, p.limit_ns);
+            if (ok)
+                tc_commit(o_full, one);
+            ++seg;
         }
+        // no MMA may be under way when the tensor memory is given back
+        tc_commit(fin, one);
+        mbar_wait_bounded(fin, 0, p.limit_ns);
         __syncwarp();
     } else {
         // ---- softmax: group w, a thread a row
@@ -367,14 +372,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         SplitItem split[2];  // the item that the CTA continues, the one that it starts
         split[0].c0 = split[1].c0 = 1;
         split[0].c1 = split[1].c1 = 0;
-        uint32_t tiles = 0;
+        const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
+        uint32_t tiles = 0;  // the group's tiles so far
         for (int u = u0; u < u1;) {
             const Segment g = shares.segment(u, u1);
             u += g.units;
             if (g.t0 == g.t1)
                 continue;
             const SeqRows& q = g.q;
-            const int n = g.t1 - g.t0, len = q.len(), n_rows = q.rows * p.group;
+            const int len = q.len(), n_rows = q.rows * p.group;
             for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kSoftThreads) {
                 const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;
                 uint4 v = make_uint4(0, 0, 0, 0);
@@ -409,17 +415,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_fence_after();
                 const int k0 = t * KT;
                 const bool edge = k0 + KT > q.base;
-                if (edge && (!PAIR || w == 0)) {
+                if (edge) {
                     // values behind the sequence's end become zeros, and infinities and NaN among the
                     // block's own are noted and taken out: a row that does not see them may not meet
-                    // them, not even as 0 times NaN
-                    const uint32_t pos = 2 * (tiles + t - g.t0) + 1;
-                    ok = __all_sync(0xffffffffu, attn_wait(&full[pos % slots], (pos / slots) & 1, flags, p.status, p.limit_ns));
+                    // them, not even as 0 times NaN. (Of a pair each group does it: what the other has
+                    // done it finds done, and its own product follows its own pass.)
+                    const uint32_t pos = 2 * tiles + 1;
+                    ok = __all_sync(0xffffffffu, attn_wait(&full[first_slot + pos % ring_slots], (pos / ring_slots) & 1, flags, p.status, p.limit_ns));
                     if (!ok)
                         break;
                     const int tok = k0 + wt;
                     if (wt < KT && tok >= q.base) {
-                        uint8_t* v = ring + (size_t)(pos % slots) * C::kSlotBytes + wt * 128;
+                        uint8_t* v = ring + (size_t)(first_slot + pos % ring_slots) * C::kSlotBytes + wt * 128;
                         bool bad = false;
                         for (int c = 0; c < HD / 8; ++c) {
                             uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + (c & 7) * 16);
@@ -500,6 +507,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_wait_st();
                 }
                 had = true;
+                ++tiles;
                 phase ^= 1u << buf;
                 tc_fence_before();
                 __syncwarp();
@@ -598,7 +606,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (threadIdx.x == 0)  // the barrier above and this release cover every thread's part
                     part_written(p, s);
             }
-            tiles += n;
             ++seg;
         }
         for (int i = 0; i < 2; ++i)
