@@ -36,7 +36,7 @@ struct AttnParams {
     uint16_t* o;
     int* status;
     unsigned* counters;  // [CTAs][2], zero between calls: parts written, CTAs done with them
-    float* parts;        // [2 * CTAs][part_floats]
+    float* parts;        // [2 * CTAs] of a part: [head_dim / 4][ROWS] float4, then [ROWS] (m, l)
     uint64_t limit_ns;
 };
 
@@ -265,7 +265,7 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
     for (int at = i0; at < i1; at += THREADS / lp) {
         const int item = at + threadIdx.x / lp;
         const bool in = item < i1;
-        const int row = in ? item / kQuads : 0, col = in ? item % kQuads * 4 : 0;
+        const int quad = in ? item / s.rows : 0, row = in ? item - quad * s.rows : 0, col = quad * 4;
         float m = -INFINITY, l = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c = s.c0 + sub; c <= s.c1; c += 4 * lp) {
@@ -277,7 +277,7 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
                     const int cc = c + i * lp;
                     const float* part = p.parts + (int64_t)(cc == s.c0 ? 2 * cc + 1 : 2 * cc) * kFloats;
                     ml[i] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * HD + 2 * row));
-                    v[i] = __ldcg(reinterpret_cast<const float4*>(part + row * HD + col));
+                    v[i] = __ldcg(reinterpret_cast<const float4*>(part + (quad * ROWS + row) * 4));
                 }
             float top = m;
 #pragma unroll

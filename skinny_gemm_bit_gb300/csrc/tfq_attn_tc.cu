@@ -381,15 +381,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 continue;
             const SeqRows& q = g.q;
             const int len = q.len(), n_rows = q.rows * p.group;
-            for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kSoftThreads) {
-                const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row < n_rows) {
-                    v = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + row / p.group) * p.ldq +
-                                                              (int64_t)(g.h * p.group + row % p.group) * HD + c * 8));
-                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+            // the item's queries, swizzled as the tiles are; a thread loads eight pieces before it stores one
+            constexpr int kRowsAtOnce = kSoftThreads / (HD / 8);  // rows that the threads hold a piece each of
+            const int qc = threadIdx.x % (HD / 8);
+#pragma unroll 1
+            for (int r0 = threadIdx.x / (HD / 8); r0 < ROWS; r0 += 8 * kRowsAtOnce) {
+                uint4 v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = g.rt * ROWS + r0 + i * kRowsAtOnce;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (row < n_rows)
+                        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + row / p.group) * p.ldq +
+                                                                     (int64_t)(g.h * p.group + row % p.group) * HD + qc * 8));
                 }
-                *reinterpret_cast<uint4*>(qbuf + (r >> 7) * (128 * HD * 2) + (c >> 3) * (128 * 128) + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = r0 + i * kRowsAtOnce;
+                    *reinterpret_cast<uint4*>(qbuf + (r >> 7) * (128 * HD * 2) + (qc >> 3) * (128 * 128) + (r & 127) * 128 + (((qc & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+                }
             }
             if (threadIdx.x == 0)
                 odd[0] = odd[1] = 0;
@@ -493,16 +504,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                     }
                     const float ref = m == -INFINITY ? 0.f : m * sc;
-                    float sum[4] = {};
+                    // pairs in the packed fp32 instructions
+                    const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                     for (int c = 0; c < KT; c += 2) {
-                        const float a = attn_ex2(fmaf(__uint_as_float(s[c]), sc, -ref));
-                        const float b = attn_ex2(fmaf(__uint_as_float(s[c + 1]), sc, -ref));
-                        sum[c & 2] += a;
-                        sum[(c & 2) + 1] += b;
-                        s[c / 2] = f32x2_to_bf16x2(a, b);  // weights in V's type: 2^-8 each, under the output's own rounding
+                        float2 e = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ref2);
+                        e.x = attn_ex2(e.x);
+                        e.y = attn_ex2(e.y);
+                        sum[c >> 1 & 1] = __fadd2_rn(sum[c >> 1 & 1], e);
+                        s[c / 2] = f32x2_to_bf16x2(e.x, e.y);  // weights in V's type: 2^-8 each, under the output's own rounding
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    const float2 both = __fadd2_rn(sum[0], sum[1]);
+                    l += both.x + both.y;
                     tc_st32(s_at, s);
                     tc_wait_st();
                 }
@@ -550,7 +564,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        __stcg(reinterpret_cast<float4*>(part + prow * HD + c0 + 4 * i), make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
+                        __stcg(reinterpret_cast<float4*>(part + ((c0 / 4 + i) * ROWS + prow) * 4), make_float4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]));
                     if (c0 == 0)
                         __stcg(reinterpret_cast<float2*>(part + ROWS * HD + 2 * prow), make_float2(top, all));
                 }

@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                 if (whole)
                     *reinterpret_cast<uint2*>(out + c0 + sc) = bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
                 else
-                    __stcg(reinterpret_cast<float4*>(part + sr * HD + c0 + sc), a);
+                    __stcg(reinterpret_cast<float4*>(part + ((c0 + sc) / 4 * ROWS + sr) * 4), a);
             }
         }
         if (threadIdx.x == 0)
