@@ -118,6 +118,7 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     p.M = M;
     p.n_q = n_q;
     p.group = n_q / p.c.n_kv;
+    p.group_inv = ((1u << 20) + p.group - 1) / p.group;
     p.layer = layer;
     p.seqs = seqs;
     p.q_start = q_start;

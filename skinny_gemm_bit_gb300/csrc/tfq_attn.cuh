@@ -26,6 +26,7 @@ struct AttnParams {
     const uint16_t* q;
     int64_t ldq, M;
     int n_q, group;  // query heads; query heads of a key/value head
+    unsigned group_inv;  // 2^20 / group, rounded up
     CacheView c;
     int layer;
     int total_rows;  // rows of the pool: a row coordinate that the tensor map fills with zeros
@@ -38,6 +39,11 @@ struct AttnParams {
     unsigned* counters;  // [CTAs][2], zero between calls: parts written, CTAs done with them
     float* parts;        // [2 * CTAs] of a part: [head_dim / 4][ROWS] float4, then [ROWS] (m, l)
     uint64_t limit_ns;
+
+    // Query row r of a key/value head is head r % group of its sequence's row r / group. The product
+    // is exact for r < 64 * 64 and group <= 64: it is over by less than r / 2^20 < 1 / group.
+    __device__ __forceinline__ int token_of(int r) const { return (int)((unsigned)r * group_inv >> 20); }
+    __device__ __forceinline__ int head_of(int r) const { return r - token_of(r) * group; }
 };
 
 // Sequence b of the call: its rows and tokens, or why it has none.
@@ -309,7 +315,7 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
         if (in && sub == 0) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int r = s.row0 + row;
-            *reinterpret_cast<uint2*>(p.o + ((int64_t)(s.q.r0 + r / p.group) * p.n_q + s.h * p.group + r % p.group) * HD + col) =
+            *reinterpret_cast<uint2*>(p.o + ((int64_t)(s.q.r0 + p.token_of(r)) * p.n_q + s.h * p.group + p.head_of(r)) * HD + col) =
                 bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
         }
     }

@@ -154,7 +154,7 @@ template <int HD>
 __device__ __forceinline__ void add_odd(const AttnParams& p, const SeqRows& q, int head, int row, uint64_t odd, uint64_t mask,
                                         float sc, float sign, float ref, int c0, float (&acc)[32])
 {
-    const uint16_t* qr = p.q + (q.r0 + row / p.group) * p.ldq + (int64_t)(head * p.group + row % p.group) * HD;
+    const uint16_t* qr = p.q + (q.r0 + p.token_of(row)) * p.ldq + (int64_t)(head * p.group + row % p.group) * HD;
     for (odd &= mask; odd != 0; odd &= odd - 1) {
         const int tok = q.base + __ffsll((long long)odd) - 1;
         const int page = p.c.table[(int64_t)q.slot * p.c.max_pages + (tok >> p.c.page_shift)];
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int row = g.rt * ROWS + r0 + i * kRowsAtOnce;
                     v[i] = make_uint4(0, 0, 0, 0);
                     if (row < n_rows)
-                        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + row / p.group) * p.ldq +
-                                                                     (int64_t)(g.h * p.group + row % p.group) * HD + qc * 8));
+                        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + p.token_of(row)) * p.ldq +
+                                                                     (int64_t)(g.h * p.group + p.head_of(row)) * HD + qc * 8));
                 }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool valid = row < n_rows, busy = __any_sync(0xffffffffu, valid);
             uint64_t mask = 0;
             if (valid) {
-                const int t = row / p.group;
+                const int t = p.token_of(row);
                 mask = p.masks == nullptr ? ~0ull >> (63 - t) : p.masks[q.r0 + t];
             }
             float m = -INFINITY, l = 0.f;  // the reference, in score units, and the sum against it
@@ -461,62 +461,73 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
                 if (busy) {
                     uint32_t s[KT];
-                    tc_ld32(s_at, s);
-                    tc_ld32(s_at + 32, s + 32);
-                    tc_wait_ld(s);
-                    tc_wait_ld(s + 32);
-                    if (edge) {
+                    auto read = [&]() {
+                        tc_ld32(s_at, s);
+                        tc_ld32(s_at + 32, s + 32);
+                        tc_wait_ld(s);
+                        tc_wait_ld(s + 32);
+                        if (edge) {
 #pragma unroll
-                        for (int c = 0; c < KT; ++c) {
-                            const int tok = k0 + c, j = tok - q.base;
-                            const bool see = j < 0 || (tok < len && (mask >> (j & 63) & 1));
-                            s[c] = see ? s[c] : 0xFF800000u;  // -inf
-                        }
-                    }
-                    float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < KT; ++c)
-                        x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
-                    const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-                    if (!had) {
-                        m = top;
-                    } else {
-                        const bool grown = (top - m) * sc > kGrow;
-                        if (__any_sync(0xffffffffu, grown)) {
-                            // the other buffer's phase has moved on since its scores were read: its
-                            // product with V is the one that counted as `phase` then
-                            ok = __all_sync(0xffffffffu, attn_wait(&o_done[2 * w + (buf ^ 1)], (phase >> (buf ^ 1) & 1) ^ 1, flags, p.status, p.limit_ns));
-                            tc_fence_after();
-                            const float f = grown ? attn_ex2((m - top) * sc) : 1.f;
-                            if (grown)
-                                m = top;
-                            l *= f;
-#pragma unroll 1
-                            for (int c = 0; c < HD; c += 32) {
-                                uint32_t o[32];
-                                tc_ld32(o_at + c, o);
-                                tc_wait_ld(o);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tc_st32(o_at + c, o);
+                            for (int c = 0; c < KT; ++c) {
+                                const int tok = k0 + c, j = tok - q.base;
+                                const bool see = j < 0 || (tok < len && (mask >> (j & 63) & 1));
+                                s[c] = see ? s[c] : 0xFF800000u;  // -inf
                             }
                         }
-                    }
-                    const float ref = m == -INFINITY ? 0.f : m * sc;
-                    // pairs in the packed fp32 instructions
-                    const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    };
+                    auto largest = [&]() {
+                        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int c = 0; c < KT; c += 2) {
-                        float2 e = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ref2);
-                        e.x = attn_ex2(e.x);
-                        e.y = attn_ex2(e.y);
-                        sum[c >> 1 & 1] = __fadd2_rn(sum[c >> 1 & 1], e);
-                        s[c / 2] = f32x2_to_bf16x2(e.x, e.y);  // weights in V's type: 2^-8 each, under the output's own rounding
+                        for (int c = 0; c < KT; ++c)
+                            x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
+                        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                    };
+                    // the weights of the tile against m, in place of the scores, and their sum
+                    auto weigh = [&]() {
+                        const float ref = m == -INFINITY ? 0.f : m * sc;
+                        const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
+                        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                        for (int c = 0; c < KT; c += 2) {
+                            float2 e = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc2, ref2);
+                            e.x = attn_ex2(e.x);
+                            e.y = attn_ex2(e.y);
+                            sum[c >> 1 & 1] = __fadd2_rn(sum[c >> 1 & 1], e);
+                            s[c / 2] = f32x2_to_bf16x2(e.x, e.y);  // weights in V's type: 2^-8 each, under the output's own rounding
+                        }
+                        const float2 both = __fadd2_rn(sum[0], sum[1]);
+                        return both.x + both.y;
+                    };
+                    read();
+                    const float top = largest();
+                    if (!had)
+                        m = top;
+                    // the last reference serves nearly always, so the weights do not wait for the
+                    // tile's maximum; when it has grown they are formed again
+                    float added = weigh();
+                    const bool grown = had && (top - m) * sc > kGrow;
+                    if (__any_sync(0xffffffffu, grown)) {
+                        // the last product with V: the other buffer's, whose phase has moved on since
+                        ok = __all_sync(0xffffffffu, attn_wait(&o_done[2 * w + (buf ^ 1)], (phase >> (buf ^ 1) & 1) ^ 1, flags, p.status, p.limit_ns));
+                        tc_fence_after();
+                        const float f = grown ? attn_ex2((m - top) * sc) : 1.f;
+                        if (grown)
+                            m = top;
+                        l *= f;
+#pragma unroll 1
+                        for (int c = 0; c < HD; c += 32) {
+                            uint32_t o[32];
+                            tc_ld32(o_at + c, o);
+                            tc_wait_ld(o);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            tc_st32(o_at + c, o);
+                        }
+                        read();
+                        added = weigh();
                     }
-                    const float2 both = __fadd2_rn(sum[0], sum[1]);
-                    l += both.x + both.y;
+                    l += added;
                     tc_st32(s_at, s);
                     tc_wait_st();
                 }
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (odd_bits != 0)
                     add_odd<HD>(p, q, g.h, row, odd_bits, mask, sc, sign, ref, c0, a);
                 if (whole) {
-                    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)(q.r0 + row / p.group) * p.n_q + g.h * p.group + row % p.group) * HD + c0);
+                    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)(q.r0 + p.token_of(row)) * p.n_q + g.h * p.group + p.head_of(row)) * HD + c0);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         o[i] = make_uint4(f32x2_to_bf16x2(a[8 * i] * inv, a[8 * i + 1] * inv), f32x2_to_bf16x2(a[8 * i + 2] * inv, a[8 * i + 3] * inv),

@@ -189,15 +189,15 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;
             uint4 v = make_uint4(0, 0, 0, 0);
             if (row < n_rows)
-                v = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + row / p.group) * p.ldq +
-                                                          (int64_t)(g.h * p.group + row % p.group) * HD + c * 8));
+                v = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + p.token_of(row)) * p.ldq +
+                                                          (int64_t)(g.h * p.group + p.head_of(row)) * HD + c * 8));
             *reinterpret_cast<uint4*>(qbuf + (c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
         }
         // the masks of the lane's rows
         uint64_t mask[RW][2];
 #pragma unroll
         for (int i = 0; i < 2 * RW; ++i) {
-            const int row = g.rt * ROWS + (i >> 1) * 16 + (i & 1) * 8 + gi, t = row / p.group;
+            const int row = g.rt * ROWS + (i >> 1) * 16 + (i & 1) * 8 + gi, t = p.token_of(row);
             mask[i >> 1][i & 1] = row >= n_rows ? 0 : p.masks == nullptr ? ~0ull >> (63 - t) : p.masks[q.r0 + t];
         }
         named_bar_sync(1, kCtaThreads);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         const bool whole = g.t0 == 0 && g.t1 == g.nt;
         float* part = p.parts + (int64_t)(g.t0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * (ROWS * (HD + 2));
         const int row = g.rt * ROWS + sr;
-        uint16_t* out = p.o + ((int64_t)(q.r0 + row / p.group) * p.n_q + g.h * p.group + row % p.group) * HD;
+        uint16_t* out = p.o + ((int64_t)(q.r0 + p.token_of(row)) * p.n_q + g.h * p.group + p.head_of(row)) * HD;
         if (sums && !whole && sc == 0 && row < n_rows)
             __stcg(reinterpret_cast<float2*>(part + ROWS * HD + 2 * sr), make_float2(top, all));
 #pragma unroll
