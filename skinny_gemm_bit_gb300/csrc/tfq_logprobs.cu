@@ -14,10 +14,13 @@
 // largest value lies below m (all but a few of them) takes the straight path. The next batch's
 // loads are under way while one is summed.
 //
-// The top k: each thread notes its largest value. The k-th largest of those is a bound that at
-// least k elements reach, and only threads whose largest reaches it can hold one of the k; their
-// units are read again (from L2) by whole warps, which keep sorted lists of 32 (value, index)
-// keys, one a lane. About k threads pass, so this costs the row's latency, not its bandwidth.
+// The top k: each thread notes its largest value. The k-th largest of the warps' largest few of
+// those (32 in all) is a bound that k elements of the row (or the block's part of it) reach, and
+// seldom many more do. Only threads whose largest reaches it can hold one: their units are read
+// again (from L2) by whole warps, four loads under way, and what reaches the bound is collected and
+// sorted as (value, lower index first) keys, 32 a warp. That costs a row's latency, not its
+// bandwidth. Rows with more than kMaxCand such elements (ties without end, NaN) take their units
+// through sorted lists instead, one key a lane.
 #include <cmath>
 #include <cooperative_groups.h>
 
@@ -31,6 +34,7 @@ namespace {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kMaxCand = kLpThreads;  // collected keys: 32 a warp
 constexpr int kBatch = 4;        // 16-byte units a lane takes at once
 constexpr int kMaxCluster = 8;  // at most kLpWarps: a warp reads a part's list
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -219,7 +223,7 @@ struct Shared {
     // what the cluster's first block reads of the others
     Stats part;
     uint64_t top[32];
-    int flagged, flags[kLpThreads];
+    int flagged, found, flags[kLpThreads];
 };
 
 // The sums of a batch against the warp's m. COUNT: an element may equal m.
@@ -230,7 +234,8 @@ __device__ __forceinline__ void add_batch(Stats& s, const uint4 (&raw)[kBatch], 
     // z = x log2 e - ref is rounded once; what rounding m log2 e to ref left over is the same for
     // every element and put right on the batch's sums
     const float ref = s.m * kLog2e, left = fmaf(s.m, kLog2e, -ref);
-    float r[4] = {}, w[4] = {};
+    const float2 log2e2 = make_float2(kLog2e, kLog2e), ref2 = make_float2(-ref, -ref);
+    float2 r[2] = {}, w[2] = {};  // pairs in the packed fp32 instructions
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
         if (b >= units)
@@ -238,18 +243,24 @@ __device__ __forceinline__ void add_batch(Stats& s, const uint4 (&raw)[kBatch], 
         float f[N];
         Unit<T>::widen(raw[b], f);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float z = fmaf(f[i], kLog2e, -ref);
-            float e = ex2(z);
-            if (COUNT && f[i] == s.m) {
-                e = 0.f;
-                s.n += 1.f;
+        for (int i = 0; i < N; i += 2) {
+            const float2 z = __ffma2_rn(make_float2(f[i], f[i + 1]), log2e2, ref2);
+            float2 e = make_float2(ex2(z.x), ex2(z.y));
+            if (COUNT) {
+                if (f[i] == s.m) {
+                    e.x = 0.f;
+                    s.n += 1.f;
+                }
+                if (f[i + 1] == s.m) {
+                    e.y = 0.f;
+                    s.n += 1.f;
+                }
             }
-            r[i & 3] += e;
-            w[i & 3] = fmaf(e, z, w[i & 3]);
+            r[i >> 1 & 1] = __fadd2_rn(r[i >> 1 & 1], e);
+            w[i >> 1 & 1] = __ffma2_rn(e, z, w[i >> 1 & 1]);
         }
     }
-    const float rs = (r[0] + r[1]) + (r[2] + r[3]), ws = (w[0] + w[1]) + (w[2] + w[3]);
+    const float rs = (r[0].x + r[0].y) + (r[1].x + r[1].y), ws = (w[0].x + w[0].y) + (w[1].x + w[1].y);
     const float fix = 1.f - left * kLn2;
     s.r = fmaf(rs, fix, s.r);
     s.w = fmaf(fmaf(-left, rs, ws) * fix, kLn2, s.w);
@@ -359,50 +370,114 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
     if (lane == 0)
         sh.stats[warp] = s;
     if (threadIdx.x == 0)
-        sh.flagged = 0;
+        sh.flagged = sh.found = 0;
 
     if (p.top_k > 0) {
-        // a value that at least top_k elements of this block's part reach: 0, which everything
-        // reaches, where fewer threads than that have a unit, or where a NaN hides an element
         const bool has = (int64_t)threadIdx.x < u1 - u0;
         const uint32_t mine = has ? order_of(big) : 0u;
+        // over the warps whose lanes all have a unit; without one, the few elements there are all reach 0
+        const int warps = (int)min((u1 - u0) / 32, (int64_t)kLpWarps);
         sh.maxima[warp][lane] = sort32(mine, lane);
         const bool any_nan = __syncthreads_or(nan);
-        join_lists(sh.maxima, warp, lane);
-        const uint32_t bound = any_nan ? 0u : sh.maxima[0][p.top_k - 1];
+        uint32_t bound = 0u;
+        if (warps > 0)
+            bound = __shfl_sync(0xffffffffu, sort32(sh.maxima[lane % warps][lane / warps], lane), p.top_k - 1);
+        if (any_nan)  // it may hide an element that the bound does not count
+            bound = 0u;
         if (has && mine >= bound)
             sh.flags[atomicAdd(&sh.flagged, 1)] = threadIdx.x;
+        uint64_t* cand = &sh.lists[0][0];
+        auto collect = [&](uint64_t key) {  // keys of the lanes, 0 for none
+            const unsigned come = __ballot_sync(0xffffffffu, key != 0);
+            if (come == 0)
+                return;
+            int at = 0;
+            if (lane == 0)
+                at = atomicAdd(&sh.found, __popc(come));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(come & ((1u << lane) - 1));
+            if (key != 0 && at < kMaxCand)
+                cand[at] = key;
+        };
         __syncthreads();
-        uint64_t list = sort32(single, lane);  // lane i: the warp's i-th largest key
-        uint64_t last = __shfl_sync(0xffffffffu, list, p.top_k - 1);
-        for (int f = warp; f < sh.flagged; f += kLpWarps) {
-            const int64_t own = u0 + sh.flags[f];
-            for (int64_t v0 = own; v0 < u1; v0 += 32 * kLpThreads) {
-                const int64_t v = v0 + (int64_t)lane * kLpThreads;
-                float x[N];
-                if (v < u1)
-                    U::widen(__ldg(body + v), x);
+        if (part == 0 && warp == 0)
+            collect((uint32_t)(single >> 32) >= bound ? single : 0);
+        // item: 32 units of a flagged thread
+        const int flagged = sh.flagged, rounds = (int)((u1 - u0 + 32 * kLpThreads - 1) / (32 * kLpThreads));
+        for (int f = warp; f < flagged * rounds; f += 4 * kLpWarps) {
+            uint4 four[4];
+            int64_t at[4];
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
+            for (int j = 0; j < 4; ++j) {
+                const int item = f + j * kLpWarps;
+                at[j] = item < flagged * rounds ? u0 + sh.flags[item / rounds] + ((int64_t)(item % rounds) * 32 + lane) * kLpThreads : u1;
+                if (at[j] < u1)
+                    four[j] = __ldg(body + at[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool reaches = at[j] < u1 && (bound == 0u || order_of(U::top(U::range(four[j]))) >= bound);
+                for (unsigned come = __ballot_sync(0xffffffffu, reaches); come != 0; come &= come - 1) {
+                    const int src = __ffs(come) - 1;  // a unit at a time, an element a lane
+                    uint4 x;
+                    x.x = __shfl_sync(0xffffffffu, four[j].x, src), x.y = __shfl_sync(0xffffffffu, four[j].y, src);
+                    x.z = __shfl_sync(0xffffffffu, four[j].z, src), x.w = __shfl_sync(0xffffffffu, four[j].w, src);
+                    const int64_t unit = __shfl_sync(0xffffffffu, at[j], src);
                     uint64_t key = 0;
-                    if (v < u1 && order_of(x[i]) >= bound)
-                        key = key_of(x[i], head + v * N + i);
-                    unsigned come = __ballot_sync(0xffffffffu, key > last);
-                    while (come) {
-                        const uint64_t k = __shfl_sync(0xffffffffu, key, __ffs(come) - 1);
-                        come &= come - 1;
-                        if (k <= last)
-                            continue;
-                        const int before = __popc(__ballot_sync(0xffffffffu, list > k));
-                        const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
-                        list = lane < before ? list : lane == before ? k : up;
-                        last = __shfl_sync(0xffffffffu, list, p.top_k - 1);
-                    }
+                    float y[N];
+                    U::widen(x, y);
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        if (lane == i && order_of(y[i]) >= bound)
+                            key = key_of(y[i], head + unit * N + i);
+                    collect(key);
                 }
             }
         }
-        sh.lists[warp][lane] = list;
-        join_lists(sh.lists, warp, lane);
+        __syncthreads();
+        const int found = sh.found;
+        if (found <= kMaxCand) {
+            uint64_t list = 0;
+            if (warp * 32 < found)
+                list = sort32(warp * 32 + lane < found ? cand[warp * 32 + lane] : 0, lane);
+            if (found > 32) {
+                sh.lists[warp][lane] = list;  // each warp its own 32
+                join_lists(sh.lists, warp, lane);
+            } else if (warp == 0) {
+                sh.lists[0][lane] = list;
+            }
+        } else {
+            uint64_t list = part == 0 && warp == 0 ? sort32(single, lane) : 0;  // lane i: the warp's i-th largest key
+            uint64_t last = __shfl_sync(0xffffffffu, list, p.top_k - 1);
+            for (int f = warp; f < sh.flagged; f += kLpWarps) {
+                const int64_t own = u0 + sh.flags[f];
+                for (int64_t v0 = own; v0 < u1; v0 += 32 * kLpThreads) {
+                    const int64_t v = v0 + (int64_t)lane * kLpThreads;
+                    float x[N];
+                    if (v < u1)
+                        U::widen(__ldg(body + v), x);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        uint64_t key = 0;
+                        if (v < u1 && order_of(x[i]) >= bound)
+                            key = key_of(x[i], head + v * N + i);
+                        unsigned come = __ballot_sync(0xffffffffu, key > last);
+                        while (come) {
+                            const uint64_t k = __shfl_sync(0xffffffffu, key, __ffs(come) - 1);
+                            come &= come - 1;
+                            if (k <= last)
+                                continue;
+                            const int before = __popc(__ballot_sync(0xffffffffu, list > k));
+                            const uint64_t up = __shfl_up_sync(0xffffffffu, list, 1);
+                            list = lane < before ? list : lane == before ? k : up;
+                            last = __shfl_sync(0xffffffffu, list, p.top_k - 1);
+                        }
+                    }
+                }
+            }
+            __syncthreads();  // the collected keys have been dropped
+            sh.lists[warp][lane] = list;
+            join_lists(sh.lists, warp, lane);
+        }
         if (warp == 0)
             sh.top[lane] = sh.lists[0][lane];
     } else {
@@ -415,16 +490,21 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
     }
     if (parts > 1) {
         cluster.sync();
-        if (part == 0) {  // the parts' lists and statistics, a warp or a lane each
+        if (part != 0) {
+            cluster.sync();  // this shared memory stays until block 0 has read it
+            return;
+        }
+        {  // the parts' lists and statistics, a warp or a lane each
             if (p.top_k > 0) {
                 sh.lists[warp][lane] = warp < parts ? cluster.map_shared_rank(&sh, warp)->top[lane] : 0;
                 join_lists(sh.lists, warp, lane);
             }
             if (warp == 0)
                 s = warp_join(lane < parts ? cluster.map_shared_rank(&sh, lane)->part : Stats{-INFINITY, 0.f, 0.f, 0.f});
+            cluster.barrier_arrive();  // what it needs of the others it has
         }
     }
-    if (part == 0 && warp == 0) {
+    if (warp == 0) {
         const uint64_t list = p.top_k > 0 ? sh.lists[0][lane] : 0;
         // n is 0 only for a row without numbers above -inf
         const bool none = s.m == -INFINITY && s.r == 0.f;
@@ -449,8 +529,6 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
             p.top_logp[m * p.top_k + lane] = odd ? NAN : none ? -INFINITY : of_order((uint32_t)(list >> 32)) - s.m - log_total;
         }
     }
-    if (parts > 1)
-        cluster.sync();  // the others' shared memory stays until it has been read
 }
 
 bool logprobs_shape_ok(int64_t M, int64_t N, int top_k)
