@@ -22,6 +22,7 @@
 // bandwidth. Rows with more than kMaxCand such elements (ties without end, NaN) take their units
 // through sorted lists instead, one key a lane.
 #include <cmath>
+#include <type_traits>
 #include <cooperative_groups.h>
 
 #include "tfq_cache.h"
@@ -227,7 +228,7 @@ struct Shared {
 };
 
 // The sums of a batch against the warp's m. COUNT: an element may equal m.
-template <class T, bool COUNT>
+template <class T, bool COUNT, bool WHOLE>
 __device__ __forceinline__ void add_batch(Stats& s, const uint4 (&raw)[kBatch], int units)
 {
     constexpr int N = Unit<T>::N;
@@ -238,7 +239,7 @@ __device__ __forceinline__ void add_batch(Stats& s, const uint4 (&raw)[kBatch], 
     float2 r[2] = {}, w[2] = {};  // pairs in the packed fp32 instructions
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-        if (b >= units)
+        if (!WHOLE && b >= units)
             continue;
         float f[N];
         Unit<T>::widen(raw[b], f);
@@ -286,28 +287,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
 
     Stats s{-INFINITY, 0.f, 0.f, 0.f};
     float big = -INFINITY;  // this thread's largest
-    uint4 raw[kBatch], next[kBatch];
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-        if (u0 + threadIdx.x + b * kLpThreads < u1)
-            next[b] = __ldg(body + u0 + threadIdx.x + b * kLpThreads);
-    for (int64_t u = u0 + threadIdx.x; u - lane < u1; u += kBatch * kLpThreads) {
-        const int have = u < u1 ? (int)min((int64_t)kBatch, (u1 - u + kLpThreads - 1) / kLpThreads) : 0;
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            raw[b] = next[b];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-            if (u + (kBatch + b) * kLpThreads < u1)
-                next[b] = __ldg(body + u + (kBatch + b) * kLpThreads);
+    // one batch of the warp: `have` units a lane, fewer than kBatch only in the last
+    auto take = [&](const uint4 (&raw)[kBatch], auto whole, int have) {
+        constexpr bool kWhole = decltype(whole)::value;
         float top = -INFINITY, low = INFINITY;
-        if (have == kBatch) {
+        if (kWhole) {
             const typename U::Range x = U::both(U::both(U::range(raw[0]), U::range(raw[1])), U::both(U::range(raw[2]), U::range(raw[3])));
             top = fmaxf(top, U::top(x));
             low = fminf(low, U::low(x));
         } else {
 #pragma unroll
-            for (int b = 0; b < kBatch - 1; ++b)
+            for (int b = 0; b < kBatch; ++b)
                 if (b < have) {
                     const typename U::Range x = U::range(raw[b]);
                     top = fmaxf(top, U::top(x));
@@ -318,19 +308,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
         // nothing overflows below (-inf and the type's lowest value, as masks write them, go the
         // last way), and m is not so far from 0 that the rounding of m log2 e (2^-11 at 1e4) is
         // more than a first-order matter
-        if (__all_sync(0xffffffffu, top < s.m && low > -1e38f && fabsf(s.m) < 1e4f)) {
-            if (have == kBatch)
-                add_batch<T, false>(s, raw, kBatch);
-            else
-                add_batch<T, false>(s, raw, have);
-            continue;
+        if (kWhole && __all_sync(0xffffffffu, top < s.m && low > -1e38f && fabsf(s.m) < 1e4f)) {
+            add_batch<T, false, true>(s, raw, kBatch);
+            return;
         }
         const float wm = warp_max(top);
         if (wm > s.m)
             rebase(s, wm);
         if (__all_sync(0xffffffffu, low > -1e38f && fabsf(s.m) < 1e4f)) {
-            add_batch<T, true>(s, raw, have);
-            continue;
+            add_batch<T, true, kWhole>(s, raw, have);
+            return;
         }
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -352,6 +339,42 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
                     s.w = fmaf(e, fmaxf(z, -200.f), s.w);
                 }
             }
+        }
+    };
+    const int mine_units = (int)(u1 - u0), batches = mine_units / (kBatch * kLpThreads);
+    const uint4* at = body + u0 + threadIdx.x;
+    if (batches > 0) {
+        uint4 raw[kBatch], next[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+            next[b] = __ldg(at + b * kLpThreads);
+#pragma unroll 1
+        for (int i = 0; i < batches; ++i) {
+            at += kBatch * kLpThreads;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                raw[b] = next[b];
+            if (i + 1 < batches) {
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    next[b] = __ldg(at + b * kLpThreads);
+            }
+            take(raw, std::true_type{}, kBatch);
+        }
+    }
+    {
+        const int rest = mine_units - batches * kBatch * kLpThreads;  // units of the last batch
+        if (rest - ((int)threadIdx.x - lane) > 0) {
+            const int have = rest > (int)threadIdx.x ? (rest - (int)threadIdx.x + kLpThreads - 1) / kLpThreads : 0;
+            uint4 raw[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch - 1; ++b)
+                if (b < have)
+                    raw[b] = __ldg(at + b * kLpThreads);
+            // the first lanes of a short batch can have all of theirs
+            if (have == kBatch)
+                raw[kBatch - 1] = __ldg(at + (kBatch - 1) * kLpThreads);
+            take(raw, std::false_type{}, have);
         }
     }
     const bool nan = s.r != s.r;
