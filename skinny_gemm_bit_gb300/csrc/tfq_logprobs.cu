@@ -16,11 +16,13 @@
 //
 // The top k: each thread notes its largest value. The k-th largest of the warps' largest few of
 // those (32 in all) is a bound that k elements of the row (or the block's part of it) reach, and
-// seldom many more do. Only threads whose largest reaches it can hold one: their units are read
-// again (from L2) by whole warps, four loads under way, and what reaches the bound is collected and
-// sorted as (value, lower index first) keys, 32 a warp. That costs a row's latency, not its
-// bandwidth. Rows with more than kMaxCand such elements (ties without end, NaN) take their units
-// through sorted lists instead, one key a lane.
+// seldom many more do. Only threads whose largest reaches it can hold one, and nearly always in
+// the one batch that their largest came from (they note which, and their second largest batch): those
+// batches are read again (from L2), eight a warp at once, and what reaches the bound is collected
+// and sorted as (value, lower index first) keys, 32 a warp. That costs a row's latency, not its
+// bandwidth: 1000 rows of 151,936 take 54 us without alternatives. A thread whose second batch
+// reaches the bound too has all its units read. Rows with more than kMaxCand such elements (ties
+// without end, NaN) take their units through sorted lists instead, one key a lane.
 #include <cmath>
 #include <type_traits>
 #include <cooperative_groups.h>
@@ -36,6 +38,7 @@ namespace {
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kMaxCand = kLpThreads;  // collected keys: 32 a warp
+static_assert(kLpThreads == 256, "a thread's index in eight bits");
 constexpr int kBatch = 4;        // 16-byte units a lane takes at once
 constexpr int kMaxCluster = 8;  // at most kLpWarps: a warp reads a part's list
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -224,7 +227,9 @@ struct Shared {
     // what the cluster's first block reads of the others
     Stats part;
     uint64_t top[32];
-    int flagged, found, flags[kLpThreads];
+    int once, flagged, found;
+    int batch[kLpThreads];  // thread | batch << 8: read that batch again
+    int flags[kLpThreads];  // thread: read all its units again
 };
 
 // The sums of a batch against the warp's m. COUNT: an element may equal m.
@@ -286,9 +291,10 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
     const int64_t u0 = units * part / parts, u1 = units * (part + 1) / parts;
 
     Stats s{-INFINITY, 0.f, 0.f, 0.f};
-    float big = -INFINITY;  // this thread's largest
+    float big = -INFINITY, second = -INFINITY;  // this thread's largest, and its largest of other batches
+    int where = 0;                              // the largest's batch
     // one batch of the warp: `have` units a lane, fewer than kBatch only in the last
-    auto take = [&](const uint4 (&raw)[kBatch], auto whole, int have) {
+    auto take = [&](const uint4 (&raw)[kBatch], auto whole, int have, int batch) {
         constexpr bool kWhole = decltype(whole)::value;
         float top = -INFINITY, low = INFINITY;
         if (kWhole) {
@@ -304,6 +310,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
                     low = fminf(low, U::low(x));
                 }
         }
+        second = fmaxf(second, fminf(top, big));
+        where = top > big ? batch : where;
         big = fmaxf(big, top);
         // nothing overflows below (-inf and the type's lowest value, as masks write them, go the
         // last way), and m is not so far from 0 that the rounding of m log2 e (2^-11 at 1e4) is
@@ -359,7 +367,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
                 for (int b = 0; b < kBatch; ++b)
                     next[b] = __ldg(at + b * kLpThreads);
             }
-            take(raw, std::true_type{}, kBatch);
+            take(raw, std::true_type{}, kBatch, i);
         }
     }
     {
@@ -374,7 +382,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
             // the first lanes of a short batch can have all of theirs
             if (have == kBatch)
                 raw[kBatch - 1] = __ldg(at + (kBatch - 1) * kLpThreads);
-            take(raw, std::false_type{}, have);
+            take(raw, std::false_type{}, have, batches);
         }
     }
     const bool nan = s.r != s.r;
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
     if (lane == 0)
         sh.stats[warp] = s;
     if (threadIdx.x == 0)
-        sh.flagged = sh.found = 0;
+        sh.once = sh.flagged = sh.found = 0;
 
     if (p.top_k > 0) {
         const bool has = (int64_t)threadIdx.x < u1 - u0;
@@ -407,8 +415,13 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
             bound = __shfl_sync(0xffffffffu, sort32(sh.maxima[lane % warps][lane / warps], lane), p.top_k - 1);
         if (any_nan)  // it may hide an element that the bound does not count
             bound = 0u;
-        if (has && mine >= bound)
-            sh.flags[atomicAdd(&sh.flagged, 1)] = threadIdx.x;
+        // (bound 0 is reached by NaN as well, which the largest do not tell of)
+        if (has && mine >= bound) {
+            if (bound != 0u && order_of(second) < bound)
+                sh.batch[atomicAdd(&sh.once, 1)] = threadIdx.x | where << 8;
+            else
+                sh.flags[atomicAdd(&sh.flagged, 1)] = threadIdx.x;
+        }
         uint64_t* cand = &sh.lists[0][0];
         auto collect = [&](uint64_t key) {  // keys of the lanes, 0 for none
             const unsigned come = __ballot_sync(0xffffffffu, key != 0);
@@ -424,37 +437,38 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
         __syncthreads();
         if (part == 0 && warp == 0)
             collect((uint32_t)(single >> 32) >= bound ? single : 0);
-        // item: 32 units of a flagged thread
+        auto collect_unit = [&](bool there, const uint4& raw4, int64_t unit) {
+            const bool reaches = there && (bound == 0u || order_of(U::top(U::range(raw4))) >= bound);
+            if (!__any_sync(0xffffffffu, reaches))
+                return;
+            float y[N];
+            U::widen(raw4, y);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                collect(reaches && order_of(y[i]) >= bound ? key_of(y[i], head + unit * N + i) : 0);
+        };
+        // one batch of a thread: four lanes, a unit each
+        const int once = sh.once;
+        for (int e0 = 0; e0 < once; e0 += 8 * kLpWarps) {
+            const int e = e0 + warp + (lane >> 2) * kLpWarps;
+            int64_t unit = u1;
+            if (e < once) {
+                const int who = sh.batch[e];
+                unit = u0 + (who & 255) + ((int64_t)(who >> 8) * kBatch + (lane & 3)) * kLpThreads;
+            }
+            uint4 raw4 = {};
+            if (unit < u1)
+                raw4 = __ldg(body + unit);
+            collect_unit(unit < u1, raw4, unit);
+        }
+        // all units of a thread: 32 of them an item
         const int flagged = sh.flagged, rounds = (int)((u1 - u0 + 32 * kLpThreads - 1) / (32 * kLpThreads));
-        for (int f = warp; f < flagged * rounds; f += 4 * kLpWarps) {
-            uint4 four[4];
-            int64_t at[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int item = f + j * kLpWarps;
-                at[j] = item < flagged * rounds ? u0 + sh.flags[item / rounds] + ((int64_t)(item % rounds) * 32 + lane) * kLpThreads : u1;
-                if (at[j] < u1)
-                    four[j] = __ldg(body + at[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool reaches = at[j] < u1 && (bound == 0u || order_of(U::top(U::range(four[j]))) >= bound);
-                for (unsigned come = __ballot_sync(0xffffffffu, reaches); come != 0; come &= come - 1) {
-                    const int src = __ffs(come) - 1;  // a unit at a time, an element a lane
-                    uint4 x;
-                    x.x = __shfl_sync(0xffffffffu, four[j].x, src), x.y = __shfl_sync(0xffffffffu, four[j].y, src);
-                    x.z = __shfl_sync(0xffffffffu, four[j].z, src), x.w = __shfl_sync(0xffffffffu, four[j].w, src);
-                    const int64_t unit = __shfl_sync(0xffffffffu, at[j], src);
-                    uint64_t key = 0;
-                    float y[N];
-                    U::widen(x, y);
-#pragma unroll
-                    for (int i = 0; i < N; ++i)
-                        if (lane == i && order_of(y[i]) >= bound)
-                            key = key_of(y[i], head + unit * N + i);
-                    collect(key);
-                }
-            }
+        for (int f = warp; f < flagged * rounds; f += kLpWarps) {
+            const int64_t unit = u0 + sh.flags[f / rounds] + ((int64_t)(f % rounds) * 32 + lane) * kLpThreads;
+            uint4 raw4 = {};
+            if (unit < u1)
+                raw4 = __ldg(body + unit);
+            collect_unit(unit < u1, raw4, unit);
         }
         __syncthreads();
         const int found = sh.found;
@@ -471,8 +485,8 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprobs_kernel(const __grid_co
         } else {
             uint64_t list = part == 0 && warp == 0 ? sort32(single, lane) : 0;  // lane i: the warp's i-th largest key
             uint64_t last = __shfl_sync(0xffffffffu, list, p.top_k - 1);
-            for (int f = warp; f < sh.flagged; f += kLpWarps) {
-                const int64_t own = u0 + sh.flags[f];
+            for (int f = warp; f < once + flagged; f += kLpWarps) {
+                const int64_t own = u0 + (f < once ? sh.batch[f] & 255 : sh.flags[f - once]);
                 for (int64_t v0 = own; v0 < u1; v0 += 32 * kLpThreads) {
                     const int64_t v = v0 + (int64_t)lane * kLpThreads;
                     float x[N];
