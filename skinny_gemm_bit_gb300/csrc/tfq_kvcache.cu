@@ -221,6 +221,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, const
 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(CacheView c, const int32_t* parent, void* ws)
 {
+    pdl_launch_dependents();  // its blocks wait for this one's plan
     __shared__ int64_t buf[33];
     __shared__ int32_t keeper[kMaxSeqs];  // the slot that keeps each parent's unfilled page (-1: itself)
     __shared__ int32_t list[kMaxSeqs];
@@ -352,6 +353,7 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(CacheView c, co
                                                                  const int32_t* keep, const int32_t* n_keep, int B,
                                                                  int64_t M, void* ws)
 {
+    pdl_launch_dependents();  // its blocks wait for this one's plan
     __shared__ unsigned seen[kMaxSeqs / 32];
     __shared__ int twice, bad;
     const int b = threadIdx.x;
@@ -417,45 +419,51 @@ __global__ void __launch_bounds__(kPlanThreads) keep_plan_kernel(CacheView c, co
     c.len[s] = base + n;
 }
 
-// A thread moves one 16-byte column of a (sequence, layer, kv, head) from its kept rows up to
-// the rows behind the base, eight rows at a time: loads first, then stores. A kept row lies at
-// or behind its place and the kept rows increase, so no store reaches a row that a later
-// batch still reads.
-__global__ void __launch_bounds__(kCopyThreads) keep_move_kernel(CacheView c, const int32_t* __restrict__ keep, void* ws)
+// A thread moves one 16-byte column of a sequence's rows (layer, K or V, head, 16 bytes of a row)
+// from the kept rows up to the rows behind the base, eight rows at a time: loads first, then stores.
+// A kept row lies at or behind its place and the kept rows increase, so no store reaches a row
+// that a later batch still reads. The rows' places are the same for every column but for its start.
+__global__ void __launch_bounds__(kCopyThreads) keep_move_kernel(CacheView c, const int32_t* __restrict__ q_start,
+                                                                 const int32_t* __restrict__ keep, int64_t M, void* ws)
 {
     __shared__ SlotPlan pl;
-    __shared__ int32_t from[kMaxDraftRows];
+    __shared__ int64_t src[kMaxDraftRows], dst[kMaxDraftRows];  // elements; src < 0: stays
+    // the lists are the caller's; the plan is the kernel's before this one
+    const int64_t at = (int64_t)q_start[blockIdx.y] + threadIdx.x;
+    const int from = threadIdx.x < kMaxDraftRows && at >= 0 && at < M ? keep[at] : 0;
+    const int row16 = c.head_dim / 8, cols = c.n_layers * 2 * c.n_kv * row16;
+    const int col = blockIdx.x * kCopyThreads + threadIdx.x;
+    const int lkh = col / row16, head = lkh % c.n_kv, lk = lkh / c.n_kv;
+    uint16_t* base = c.data + c.row_of(lk >> 1, lk & 1, 0, head) * c.head_dim + (col - lkh * row16) * 8;
     pdl_wait();
-    if (threadIdx.x == 0)
-        pl = plan_slots(ws)[blockIdx.y];
+    if (threadIdx.x < sizeof(SlotPlan) / 4)
+        reinterpret_cast<int32_t*>(&pl)[threadIdx.x] = __ldcg(reinterpret_cast<const int32_t*>(plan_slots(ws) + blockIdx.y) + threadIdx.x);
     __syncthreads();
     const int n = pl.new_len;
     if (n <= 0)
         return;
-    if ((int)threadIdx.x < n)
-        from[threadIdx.x] = keep[pl.fresh + threadIdx.x];
+    if ((int)threadIdx.x < n) {
+        const int first = pl.old_len >> c.page_shift, j = threadIdx.x;
+        auto place = [&](int i) {
+            const int row = pl.old_len + i;
+            return ((int64_t)pl.pages[(row >> c.page_shift) - first] * c.n_kv * c.page_size + (row & (c.page_size - 1))) * c.head_dim;
+        };
+        src[j] = from == j ? -1 : place(from);
+        dst[j] = place(j);
+    }
     __syncthreads();
-    const int row16 = c.head_dim / 8;
-    const int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x;
-    if (i >= (int64_t)c.n_layers * 2 * c.n_kv * row16)
+    if (col >= cols)
         return;
-    const int chunk = (int)(i % row16), lkh = (int)(i / row16), head = lkh % c.n_kv, lk = lkh / c.n_kv;
-    const int first = pl.old_len >> c.page_shift;
-    auto at = [&](int j) {
-        const int row = pl.old_len + j;
-        return reinterpret_cast<uint4*>(c.data + (c.row_of(lk >> 1, lk & 1, pl.pages[(row >> c.page_shift) - first], head) +
-                                                  (row & (c.page_size - 1))) * c.head_dim + chunk * 8);
-    };
     for (int j0 = 0; j0 < n; j0 += 8) {
         uint4 v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j0 + j < n && from[j0 + j] != j0 + j)
-                v[j] = *at(from[j0 + j]);
+            if (j0 + j < n && src[j0 + j] >= 0)
+                v[j] = *reinterpret_cast<const uint4*>(base + src[j0 + j]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            if (j0 + j < n && from[j0 + j] != j0 + j)
-                *at(j0 + j) = v[j];
+            if (j0 + j < n && src[j0 + j] >= 0)
+                *reinterpret_cast<uint4*>(base + dst[j0 + j]) = v[j];
     }
 }
 
@@ -662,9 +670,9 @@ int tf_kvcache_keep(const tf_kvcache* c, const int32_t* seqs, const int32_t* q_s
     keep_plan_kernel<<<1, kPlanThreads, 0, s>>>(v, seqs, q_start, keep, n_keep, (int)B, M, ws);
     if ((rc = launched(cudaGetLastError(), name)))
         return rc;
-    const int64_t threads = (int64_t)v.n_layers * 2 * v.n_kv * (v.head_dim / 8);
-    return launched(launch_pdl(keep_move_kernel, dim3((unsigned)((threads + kCopyThreads - 1) / kCopyThreads), (unsigned)B),
-                               dim3(kCopyThreads), 0, s, true, v, keep, ws),
+    const int64_t cols = (int64_t)v.n_layers * 2 * v.n_kv * (v.head_dim / 8), per = kCopyThreads;
+    return launched(launch_pdl(keep_move_kernel, dim3((unsigned)((cols + per - 1) / per), (unsigned)B), dim3(kCopyThreads), 0, s,
+                               true, v, q_start, keep, M, ws),
                     name);
 }
 

@@ -76,6 +76,18 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __g
     pdl_launch_dependents();
     if (m >= p.M)
         return;
+    const int n_kv = p.c.n_kv, heads = p.n_q + 2 * n_kv;
+    const uint4* row = reinterpret_cast<const uint4*>(p.qkv + m * p.ld) + sub * (HD / 8);
+    // the next heads' chunks are under way while one set is worked on, the first while the angles are made
+    uint4 na = {}, nb = {};
+    auto fetch = [&](int h0) {
+        if (h0 + sub < heads) {
+            na = __ldcg(row + h0 * (HD / 8) + c0);
+            nb = __ldcg(row + h0 * (HD / 8) + c1);
+        }
+    };
+    fetch(part * HEADS);
+    const int32_t slot = p.slots[m];
     // angle = position * turns modulo one turn, from the top 32 bits of the 64-bit product:
     // exact but for 2^-32 turn, then sine and cosine of an argument within [-pi, pi] by the
     // fast functions, whose absolute error there (2^-21) is far under a bf16 step of the result
@@ -91,23 +103,17 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __g
             __sincosf(a, &sn[i], &cs[i]);
         }
     }
-    const int32_t slot = p.slots[m];
     const bool bad = slot >= 0 && slot >= (int64_t)p.c.n_pages * p.c.page_size;
     if (bad && part == 0 && lane == 0)
         record_status(p.status, TF_E_INVALID_ARG);
     const bool store = slot >= 0 && !bad;
     const int page = store ? slot >> p.c.page_shift : 0, off = slot & (p.c.page_size - 1);
-    const int n_kv = p.c.n_kv, heads = p.n_q + 2 * n_kv;
-    const uint4* row = reinterpret_cast<const uint4*>(p.qkv + m * p.ld);
-#pragma unroll 2
+#pragma unroll 1
     for (int h0 = part * HEADS; h0 < heads; h0 += p.parts * HEADS) {
         const int h = h0 + sub;
         const bool live = h < heads;
-        uint4 a = {}, b = {};
-        if (live) {
-            a = __ldcg(row + h * (HD / 8) + c0);
-            b = __ldcg(row + h * (HD / 8) + c1);
-        }
+        uint4 a = na, b = nb;
+        fetch(h0 + p.parts * HEADS);
         const bool is_q = h < p.n_q, is_k = !is_q && h < p.n_q + n_kv;
         const uint4* gamma = reinterpret_cast<const uint4*>(is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr);
         const bool norm = gamma != nullptr;
