@@ -343,7 +343,8 @@ typedef struct tf_decoder_desc {
  * kernels; "Experiments with a full-step megakernel": what pays is overlapping
  * the next stage's weight loads with the current stage). Per layer, in order:
  *   qkv = rmsnorm(h, attn_norm) . Wqkv^T            [M][q_dim + 2 kv_dim]
- *   h1  = h + qkv[:, :q_dim] . Wo^T                  (q stands in for the attention output)
+ *   h1  = h + qkv[:, :q_dim] . Wo^T                  (q stands in for the attention output;
+ *                                                    tf_decode_step_attn_run has attention)
  *   a   = silu(rmsnorm(h1, mlp_norm) . Wg^T) * (rmsnorm(h1, mlp_norm) . Wu^T)
  *   h   = h1 + a . Wd^T
  * then logits = rmsnorm(h, final_norm) . Wreadout^T. Each projection is one kernel,
@@ -588,12 +589,52 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
  * fp32 scores, sums and accumulators; the softmax weights are rounded to bf16 for the product
  * with V (relative error 2^-9 each, under the output's own rounding). A row's last bits may
  * depend on the other sequences of the call, since the context is split over the GPU by the
- * whole call's length; the same call gives the same bits every time.
+ * whole call's length; the same call gives the same bits every time. The launch is
+ * cooperative: CTAs that share an item wait for one another's parts (bounded; TF_E_TIMEOUT in the
+ * status word, after which the workspace has to be zeroed again). TF_RUN_PDL has no effect.
+ * A call has fewer than 2^31 key tiles (tokens * n_kv * query-row tiles / 32): beyond that it
+ * records TF_E_UNSUPPORTED_SHAPE and writes nothing.
  */
 size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int max_rows);
 int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
                      const int32_t* seqs, const int32_t* q_start, int64_t B, int max_rows, const uint64_t* masks,
                      float scale, uint16_t* o, void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/* ---------------------------------------------------------------- decoder step over a cache */
+
+/* What a decoder's attention needs beside its projections. */
+typedef struct tf_attn_layer {
+    const uint16_t* q_norm;  /* bf16 [head_dim] device, or NULL: no norm */
+    const uint16_t* k_norm;
+} tf_attn_layer;
+
+typedef struct tf_attn_desc {
+    int32_t n_q;                  /* query heads: d->q_dim = n_q * head_dim */
+    float eps;                    /* of the head norms */
+    float scale;                  /* of the scores */
+    int32_t rot_dim, interleaved; /* as for tf_qk_norm_rope_run */
+    const uint64_t* turns;        /* device uint64 [rot_dim / 2] (tf_rope_turns) */
+    const tf_attn_layer* layers;  /* HOST array [n_layers] */
+} tf_attn_desc;
+
+/*
+ * tf_decode_step_run with attention in the place of its stand-in. Per layer, in order:
+ *   qkv = rmsnorm(h, attn_norm) . Wqkv^T
+ *   q, k normalised and rotated, k and v stored to the cache's layer (tf_qk_norm_rope_run)
+ *   o   = attention of the M rows over the cache (tf_tree_attn_run)
+ *   h1  = h + o . Wo^T, and the MLP and the readout as there
+ * on a cache that tf_kvcache_extend has made room in: seqs, q_start, masks, slots and
+ * positions are that call's (device). The caches's layers are used from 0; it has at least
+ * d->n_layers, n_kv * head_dim = d->kv_dim, and M (1..8) rows belong to B sequences.
+ * After a verify step tf_kvcache_keep keeps what was accepted. The results are those of the
+ * separate calls, bit for bit. ws: tf_decode_step_attn_workspace_bytes(d, c, a) bytes, zeroed
+ * once, for this call alone; device-side errors of all its parts are in its status word.
+ */
+size_t tf_decode_step_attn_workspace_bytes(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a);
+int tf_decode_step_attn_run(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a, const uint16_t* x,
+                            int64_t M, const int32_t* seqs, const int32_t* q_start, int64_t B, const uint64_t* masks,
+                            const int32_t* slots, const int32_t* positions, uint16_t* logits, void* ws,
+                            size_t ws_bytes, unsigned flags, void* stream);
 
 /* ---------------------------------------------------------------- log probabilities */
 

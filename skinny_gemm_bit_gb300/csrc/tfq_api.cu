@@ -7,7 +7,7 @@
 #include <algorithm>
 #include <cstring>
 
-#include "tfq_internal.h"
+#include "tfq_cache.h"
 
 namespace tfq {
 
@@ -1251,6 +1251,113 @@ int tf_decode_step_run(const tf_decoder_desc* d, const uint16_t* x, int64_t M, u
     }
     return qlinear_impl(&d->readout, nullptr, h, D, M, d->final_norm, d->eps, nullptr, logits, d->vocab, TF_DTYPE_BF16,
                         ws, red, red_bytes, pdl, s, "tf_decode_step_run: readout");
+}
+
+// ------------------------------------------------------------------ decoder step over a cache
+
+namespace {
+struct AttnStepLayout {
+    StepLayout step;
+    size_t attn;          // the attention's workspace comes first: its status word is the call's
+    size_t q, o, total;   // normalised queries, attention output: bf16 [8][q_dim]
+    size_t base;          // of the step's own layout
+};
+
+int check_attn_step(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a, int64_t M, const char* name)
+{
+    int rc = check_decoder(d, M, name);
+    if (rc)
+        return rc;
+    CacheView v;
+    if ((rc = check_cache(c, name, &v)))
+        return rc;
+    if (a == nullptr || (d->n_layers > 0 && a->layers == nullptr))
+        return fail(TF_E_INVALID_ARG, "%s: attention descriptor or its layers NULL", name);
+    if (a->n_q < 1 || (int64_t)a->n_q * v.head_dim != d->q_dim || (int64_t)v.n_kv * v.head_dim != d->kv_dim ||
+        v.n_layers < d->n_layers)
+        return fail(TF_E_UNSUPPORTED_SHAPE, "%s: the cache's heads or layers do not match the decoder's dimensions", name);
+    return TF_OK;
+}
+
+AttnStepLayout attn_step_layout(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a)
+{
+    AttnStepLayout L{};
+    L.step = step_layout(d, kMaxM);
+    L.attn = align_up(tf_tree_attn_workspace_bytes(c, a->n_q, kMaxM, kMaxM), 256);
+    L.q = L.attn;
+    L.o = L.q + align_up((size_t)kMaxM * d->q_dim * sizeof(uint16_t), 256);
+    L.base = L.o + align_up((size_t)kMaxM * d->q_dim * sizeof(uint16_t), 256);
+    L.total = L.attn == 0 ? 0 : L.base + L.step.total;
+    return L;
+}
+}  // namespace
+
+size_t tf_decode_step_attn_workspace_bytes(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a)
+{
+    if (check_attn_step(d, c, a, 1, "tf_decode_step_attn_workspace_bytes"))
+        return 0;
+    return attn_step_layout(d, c, a).total;
+}
+
+int tf_decode_step_attn_run(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a, const uint16_t* x,
+                            int64_t M, const int32_t* seqs, const int32_t* q_start, int64_t B, const uint64_t* masks,
+                            const int32_t* slots, const int32_t* positions, uint16_t* logits, void* ws,
+                            size_t ws_bytes, unsigned flags, void* stream)
+{
+    const char* name = "tf_decode_step_attn_run";
+    int rc = check_attn_step(d, c, a, M, name);
+    if (rc)
+        return rc;
+    if ((rc = check_act(x, d->d_model, d->d_model, "tf_decode_step_attn_run: x")))
+        return rc;
+    if (logits == nullptr || seqs == nullptr || q_start == nullptr || slots == nullptr || positions == nullptr)
+        return fail(TF_E_INVALID_ARG, "%s: NULL pointer", name);
+    if (B < 1 || B > M)
+        return fail(TF_E_UNSUPPORTED_SHAPE, "%s: need 1 <= B <= M", name);
+    const AttnStepLayout L = attn_step_layout(d, c, a);
+    if (L.total == 0)
+        return TF_E_UNSUPPORTED_SHAPE;  // the attention's query has set the message
+    if ((rc = check_ws(ws, ws_bytes, L.total, name)))
+        return rc;
+    const int64_t D = d->d_model, F = d->d_ff, Q = d->q_dim, KV = d->kv_dim, QKV = Q + 2 * KV;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* wsb = static_cast<uint8_t*>(ws);
+    uint16_t* qn = reinterpret_cast<uint16_t*>(wsb + L.q);
+    uint16_t* ao = reinterpret_cast<uint16_t*>(wsb + L.o);
+    uint8_t* red = wsb + L.base + L.step.red;
+    const size_t red_bytes = ws_bytes - L.base - L.step.red;
+    uint16_t* qkv = reinterpret_cast<uint16_t*>(wsb + L.base + L.step.act);
+    uint16_t* h1 = reinterpret_cast<uint16_t*>(align_up(reinterpret_cast<uintptr_t>(qkv + L.step.qkv_e), 256));
+    uint16_t* up = reinterpret_cast<uint16_t*>(align_up(reinterpret_cast<uintptr_t>(h1 + L.step.h_e), 256));
+    uint16_t* hp[2];
+    hp[0] = reinterpret_cast<uint16_t*>(align_up(reinterpret_cast<uintptr_t>(up + L.step.a_e), 256));
+    hp[1] = reinterpret_cast<uint16_t*>(align_up(reinterpret_cast<uintptr_t>(hp[0] + L.step.h_e), 256));
+    bool pdl = (flags & TF_RUN_PDL) != 0;
+    const uint16_t* h = x;
+    for (int l = 0; l < d->n_layers; ++l) {
+        const tf_decoder_layer& Ly = d->layers[l];
+        if ((rc = qlinear_impl(&Ly.qkv, nullptr, h, D, M, Ly.attn_norm, d->eps, nullptr, qkv, QKV, TF_DTYPE_BF16, ws, red,
+                               red_bytes, pdl, s, "tf_decode_step_attn_run: qkv")))
+            return rc;
+        pdl = true;
+        if ((rc = tf_qk_norm_rope_run(qkv, QKV, M, a->n_q, a->layers[l].q_norm, a->layers[l].k_norm, a->eps, positions,
+                                      a->turns, a->rot_dim, a->interleaved, qn, c, l, slots, ws, 256, TF_RUN_PDL, stream)))
+            return rc;
+        if ((rc = tf_tree_attn_run(qn, Q, M, a->n_q, c, l, seqs, q_start, B, (int)M, masks, a->scale, ao, ws, L.attn, 0, stream)))
+            return rc;
+        if ((rc = qlinear_impl(&Ly.o, nullptr, ao, Q, M, nullptr, 0.f, h, h1, D, TF_DTYPE_BF16, ws, red, red_bytes, pdl, s,
+                               "tf_decode_step_attn_run: o")))
+            return rc;
+        if ((rc = qlinear_impl(&Ly.gate, &Ly.up, h1, D, M, Ly.mlp_norm, d->eps, nullptr, up, F, TF_DTYPE_BF16, ws, red,
+                               red_bytes, pdl, s, "tf_decode_step_attn_run: gate/up")))
+            return rc;
+        if ((rc = qlinear_impl(&Ly.down, nullptr, up, F, M, nullptr, 0.f, h1, hp[l & 1], D, TF_DTYPE_BF16, ws, red, red_bytes,
+                               pdl, s, "tf_decode_step_attn_run: down")))
+            return rc;
+        h = hp[l & 1];
+    }
+    return qlinear_impl(&d->readout, nullptr, h, D, M, d->final_norm, d->eps, nullptr, logits, d->vocab, TF_DTYPE_BF16, ws,
+                        red, red_bytes, pdl, s, "tf_decode_step_attn_run: readout");
 }
 
 // ------------------------------------------------------------------ diagnostics

@@ -71,6 +71,15 @@ class tf_kvcache(ctypes.Structure):
                 ("n_seqs", I32), ("n_pages", I32), ("max_pages", I32), ("data", P), ("book", P)]
 
 
+class tf_attn_layer(ctypes.Structure):
+    _fields_ = [("q_norm", P), ("k_norm", P)]
+
+
+class tf_attn_desc(ctypes.Structure):
+    _fields_ = [("n_q", I32), ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("rot_dim", I32), ("interleaved", I32),
+                ("turns", P), ("layers", ctypes.POINTER(tf_attn_layer))]
+
+
 class TfqError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{status_str(status)}: {msg}")
@@ -131,6 +140,11 @@ _SIGS = {
     "tf_tree_attn_workspace_bytes": (SZ, [ctypes.POINTER(tf_kvcache), ctypes.c_int, I64, ctypes.c_int]),
     "tf_tree_attn_run": (ctypes.c_int, [P, I64, I64, ctypes.c_int, ctypes.POINTER(tf_kvcache), ctypes.c_int, P, P, I64,
                                         ctypes.c_int, P, ctypes.c_float, P, P, SZ, ctypes.c_uint, P]),
+    "tf_decode_step_attn_workspace_bytes": (SZ, [ctypes.POINTER(tf_decoder_desc), ctypes.POINTER(tf_kvcache),
+                                                 ctypes.POINTER(tf_attn_desc)]),
+    "tf_decode_step_attn_run": (ctypes.c_int, [ctypes.POINTER(tf_decoder_desc), ctypes.POINTER(tf_kvcache),
+                                               ctypes.POINTER(tf_attn_desc), P, I64, P, P, I64, P, P, P, P, P, SZ,
+                                               ctypes.c_uint, P]),
     "tf_logprobs_workspace_bytes": (SZ, [I64, I64, ctypes.c_int]),
     "tf_logprobs_rows": (ctypes.c_int, [P, ctypes.c_int, I64, I64, I64, P, ctypes.c_int, ctypes.c_int, P, P, P, P, P,
                                         SZ, P]),
@@ -720,6 +734,53 @@ def tf_tree_attn_run(q: torch.Tensor, cache: KVCache, layer: int, seqs, q_start,
         None if masks is None else _want(masks, torch.int64, at, M, "masks"), hd ** -0.5 if scale is None else scale,
         _want(out, torch.bfloat16, at, M * n_q * hd, "out"), _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), flags,
         _raw_stream(stream, dev)))
+    return out
+
+
+# ---------------------------------------------------------------- decoder step over a cache
+
+class Attention:
+    """What a decoder's attention needs beside its projections: a list of (q_norm, k_norm) per layer
+    (bf16 [head_dim] device tensors or None), the rotation, and the head norms' epsilon."""
+
+    def __init__(self, norms, n_q: int, head_dim: int, rope: RopeTable, eps: float = 1e-6, scale=None):
+        self.norms, self.rope, self.n_q = norms, rope, n_q
+        arr = (tf_attn_layer * max(1, len(norms)))()
+        for i, (q, k) in enumerate(norms):
+            arr[i].q_norm = None if q is None else q.data_ptr()
+            arr[i].k_norm = None if k is None else k.data_ptr()
+        self._arr = arr
+        d = tf_attn_desc()
+        d.n_q, d.eps, d.scale = n_q, eps, head_dim ** -0.5 if scale is None else scale
+        d.rot_dim, d.interleaved, d.turns = rope.rot_dim, rope.pairs, rope.turns.data_ptr()
+        d.layers = ctypes.cast(arr, ctypes.POINTER(tf_attn_layer))
+        self.desc = d
+
+
+def tf_decode_step_attn_workspace_bytes(dec: Decoder, cache: KVCache, attn: Attention) -> int:
+    return lib().tf_decode_step_attn_workspace_bytes(ctypes.byref(dec.desc), cache.ref, ctypes.byref(attn.desc))
+
+
+def tf_decode_step_attn_run(dec: Decoder, cache: KVCache, attn: Attention, x: torch.Tensor, seqs, q_start, slots,
+                            positions, masks=None, out=None, ws=None, flags: int = 0, stream=None) -> torch.Tensor:
+    """logits [M, vocab] bf16 of one decoder step with attention over the cache; seqs, q_start, masks, slots and
+    positions as tf_kvcache_extend took and gave them for the step's rows x [M, d_model]."""
+    dev = cache.device
+    at = _current(dev)
+    M, B = x.shape[0], seqs.numel()
+    if len(attn.norms) < dec.desc.n_layers:
+        raise ValueError(f"norms of {len(attn.norms)} layers for a decoder of {dec.desc.n_layers}")
+    if out is None or ws is None:
+        with _on(stream):
+            out = torch.empty((M, dec.readout.N), dtype=torch.bfloat16, device=dev) if out is None else out
+            ws = workspace(tf_decode_step_attn_workspace_bytes(dec, cache, attn), dev) if ws is None else ws
+    _check(lib().tf_decode_step_attn_run(
+        ctypes.byref(dec.desc), cache.ref, ctypes.byref(attn.desc),
+        _want(x, torch.bfloat16, at, M * dec.desc.d_model, "x"), M, _want(seqs, torch.int32, at, 1, "seqs"),
+        _want(q_start, torch.int32, at, B + 1, "q_start"), B,
+        None if masks is None else _want(masks, torch.int64, at, M, "masks"), _want(slots, torch.int32, at, M, "slots"),
+        _want(positions, torch.int32, at, M, "positions"), _want(out, torch.bfloat16, at, M * dec.readout.N, "out"),
+        _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), flags, _raw_stream(stream, dev)))
     return out
 
 
