@@ -21,6 +21,17 @@ int attn_rows(int max_rows, int group, int head_dim)
     return r <= 128 ? 128 : 256;
 }
 
+// A segment's own cost in key tiles of its kernel, by which the CTAs' shares are measured. With more
+// items than CTAs it is what evens out those that get several short ones (28 of the warp kernel's 32-key
+// tiles: 64 ragged sequences 176 us, 183 with 16, 199 with 8); with fewer, what a CTA gets should
+// still be a tile a warp (one token over 4097: 12.0 us with 16, 13.4 with 24).
+int attn_over(int rows, int64_t items)
+{
+    if (rows > 32)  // 64-key tiles: 64-row trees 145.5 us, 148.5 with 20 or 40, 151.5 with 12
+        return 32;
+    return items > device_sms() ? 28 : 16;
+}
+
 struct AttnLayout {
     size_t counters, parts, total;
 };
@@ -132,6 +143,7 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     p.total_rows = (int)p.c.row_of(p.c.n_layers, 0, 0, 0);
     p.limit_ns = kDefaultWaitLimitNs;
     const int rows = attn_rows(max_rows, p.group, p.c.head_dim);
+    p.over = attn_over(rows, B * p.c.n_kv * ((max_rows * p.group + rows - 1) / rows));
     const AttnLayout L = attn_layout(p.c.head_dim, rows);
     p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + L.counters);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);

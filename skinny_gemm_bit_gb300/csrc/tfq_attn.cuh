@@ -32,6 +32,7 @@ struct AttnParams {
     int total_rows;  // rows of the pool: a row coordinate that the tensor map fills with zeros
     const int32_t *seqs, *q_start;
     int B, max_rows;
+    int over;  // a segment's own cost, in key tiles
     const uint64_t* masks;
     float scale_log2;  // scale * log2(e)
     uint16_t* o;
@@ -86,10 +87,10 @@ struct Segment {
     int first;       // the item's first key tile, in units
 };
 
-// An item counts kOver units before its key tiles: what a segment costs apart from them (its
+// An item counts p.over units before its key tiles: what a segment costs apart from them (its
 // queries, joining the warps' parts, the hand-over), so that CTAs with many short items get no more
 // than their share. A CTA has kLeast units or more, so that a short item is not torn apart.
-template <int ROWS, int KEYS, int kOver, int kLeast>
+template <int ROWS, int KEYS, int kLeast>
 struct Shares {
     SeqEntry* seq;  // [B + 1]
     const AttnParams& p;
@@ -108,7 +109,7 @@ struct Shares {
             SeqEntry e{0, q.r0, q.base, 0};
             if (q.base >= 0) {
                 e.slot_rows = q.slot | q.rows << 16;
-                const int64_t n = (int64_t)p.c.n_kv * row_tiles(q.rows) * (key_tiles(q.len()) + kOver);
+                const int64_t n = (int64_t)p.c.n_kv * row_tiles(q.rows) * (key_tiles(q.len()) + p.over);
                 e.first = n < INT32_MAX ? (int)n : INT32_MAX;
             } else if (blockIdx.x == b % gridDim.x) {
                 // arguments that do not hold: zero rows, here and there among the CTAs
@@ -167,14 +168,14 @@ struct Shares {
         Segment g;
         g.q = SeqRows{e.slot_rows & 0xFFFF, e.r0, e.slot_rows >> 16, e.base};
         g.nt = key_tiles(g.q.len());
-        const int rt = row_tiles(g.q.rows), per = g.nt + kOver;
+        const int rt = row_tiles(g.q.rows), per = g.nt + p.over;
         const int local = u - e.first, item = local / per, off = local - item * per;
         g.h = item / rt;
         g.rt = item - g.h * rt;
         g.units = min(end - u, per - off);
-        g.t0 = max(off - kOver, 0);
-        g.t1 = max(off + g.units - kOver, 0);
-        g.first = u - off + kOver;
+        g.t0 = max(off - p.over, 0);
+        g.t1 = max(off + g.units - p.over, 0);
+        g.first = u - off + p.over;
         return g;
     }
 };

@@ -26,12 +26,14 @@
 namespace tfq {
 namespace {
 
-constexpr int kTcThreads = 352;  // eight softmax warps, the producer, an MMA warp for each group
+constexpr int kTcThreads = 384;  // eight softmax warps, the producer, an MMA warp for each group, one idle
+// registers: 168 a thread at launch; the last four warps give 96 of theirs to the softmax warps'
+constexpr int kSoftRegs = 216, kOtherRegs = 72;
+static_assert(kSoftRegs * 256 + kOtherRegs * 128 <= 168 * kTcThreads, "no more registers than the launch has");
 constexpr int kSoftThreads = 256;
 constexpr int kMaxSlots = 12;
 constexpr int KT = 64;                            // keys of a tile
 constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w][buffer] at 128 w + 64 buffer, O[w] at 256 + 128 w
-constexpr int kTcOver = 12;  // a segment's own cost, in key tiles
 constexpr float kGrow = 8.f;
 
 // offsets in shared memory
@@ -219,7 +221,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    Shares<ROWS, KT, kTcOver, 1> shares(p, smem + kTcSched);
+    Shares<ROWS, KT, 1> shares(p, smem + kTcSched);
     tc_fence_before();
     shares.build();  // its barriers publish the tensor-memory address as well
     __syncthreads();
@@ -232,135 +234,139 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // for the one it is after.
     const uint32_t ring_slots = PAIR ? slots : slots / 2;
 
-    if (warp == 8) {
-        // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
-        const int box = min(p.c.page_size, KT), pieces = KT / box;
-        const int z = lane / pieces, piece = lane % pieces;
-        const bool active = lane < pieces * (HD / 64);
-        uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0};
-        bool gone = false;
-        for (int u = u0; u < u1 && !gone;) {
-            const Segment g = shares.segment(u, u1);
-            u += g.units;
-            const SeqRows& q = g.q;
-            const int32_t* table = p.c.table + (int64_t)q.slot * p.c.max_pages;
-            const int len = q.len();
-            auto page_at = [&](int t) {
-                const int row = t * KT + piece * box;
-                return active && t < g.t1 && row < len ? __ldcg(table + (row >> p.c.page_shift)) : -1;
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) {
+            // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
+            const int box = min(p.c.page_size, KT), pieces = KT / box;
+            const int z = lane / pieces, piece = lane % pieces;
+            const bool active = lane < pieces * (HD / 64);
+            uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0};
+            bool gone = false;
+            for (int u = u0; u < u1 && !gone;) {
+                const Segment g = shares.segment(u, u1);
+                u += g.units;
+                const SeqRows& q = g.q;
+                const int32_t* table = p.c.table + (int64_t)q.slot * p.c.max_pages;
+                const int len = q.len();
+                auto page_at = [&](int t) {
+                    const int row = t * KT + piece * box;
+                    return active && t < g.t1 && row < len ? __ldcg(table + (row >> p.c.page_shift)) : -1;
+                };
+                int page = page_at(g.t0);
+                for (int t = g.t0; t < g.t1 && !gone; ++t) {
+                    const int next = page_at(t + 1);
+                    const int row = t * KT + piece * box;
+                    const bool in = active && row < len, good = page >= 0 && page < p.c.n_pages;
+                    if (in && !good)
+                        record_status(p.status, TF_E_INVALID_ARG);
+                    const int r = PAIR ? 0 : (t - g.t0) & 1;
+                    for (int kv = 0; kv < 2; ++kv) {
+                        const uint32_t slot = r * ring_slots + next_slot[r];
+                        const bool ok = pass[r] == 0 || attn_wait(&empty[slot], (pass[r] - 1) & 1, flags, p.status, p.limit_ns);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            gone = true;
+                            break;
+                        }
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
+                        __syncwarp();
+                        if (active) {
+                            const int y = in && good ? (int)p.c.row_of(p.layer, kv, page, g.h) + (row & (p.c.page_size - 1)) : p.total_rows;
+                            tma_box(smem_u32(ring + (size_t)slot * C::kSlotBytes + z * KT * 128 + piece * box * 128), &map, y, z, &full[slot]);
+                        }
+                        if (++next_slot[r] == ring_slots) {
+                            next_slot[r] = 0;
+                            ++pass[r];
+                        }
+                    }
+                    page = next;
+                }
+            }
+            if (gone)  // no copy may be in flight when the CTA leaves: each slot's last one
+                for (int r = 0; r < (PAIR ? 1 : 2); ++r)
+                    for (uint32_t s = 0; s < ring_slots; ++s) {
+                        const uint32_t uses = pass[r] + (s < next_slot[r] ? 1 : 0);
+                        if (uses > 0)
+                            mbar_wait_bounded(&full[r * ring_slots + s], (uses - 1) & 1, p.limit_ns);
+                    }
+        } else if (warp < 11) {
+            // ---- an MMA warp: group w's scores and its products with V (one warp for both groups spent
+            // 1340 cycles a step on its waits, one after the other, for 640 of MMAs)
+            const int w = warp - 9;
+            const bool one = elect_one();
+            constexpr uint32_t kIdS = instr_desc(KT, false), kIdO = instr_desc(HD, true);
+            const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
+            const uint32_t ra = smem_u32(ring) + first_slot * C::kSlotBytes;
+            const uint64_t ad = smem_desc(smem_u32(qbuf) + (PAIR ? w * (128 * HD * 2) : 0), 16, 1024);
+            full += first_slot;
+            empty += first_slot;
+            // the ring's slots of the next K and the next V tile: every second one
+            uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, p_phase = 0 /* a bit a buffer */, seg = 0;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
             };
-            int page = page_at(g.t0);
-            for (int t = g.t0; t < g.t1 && !gone; ++t) {
-                const int next = page_at(t + 1);
-                const int row = t * KT + piece * box;
-                const bool in = active && row < len, good = page >= 0 && page < p.c.n_pages;
-                if (in && !good)
-                    record_status(p.status, TF_E_INVALID_ARG);
-                const int r = PAIR ? 0 : (t - g.t0) & 1;
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t slot = r * ring_slots + next_slot[r];
-                    const bool ok = pass[r] == 0 || attn_wait(&empty[slot], (pass[r] - 1) & 1, flags, p.status, p.limit_ns);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        gone = true;
-                        break;
-                    }
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
-                    __syncwarp();
-                    if (active) {
-                        const int y = in && good ? (int)p.c.row_of(p.layer, kv, page, g.h) + (row & (p.c.page_size - 1)) : p.total_rows;
-                        tma_box(smem_u32(ring + (size_t)slot * C::kSlotBytes + z * KT * 128 + piece * box * 128), &map, y, z, &full[slot]);
-                    }
-                    if (++next_slot[r] == ring_slots) {
-                        next_slot[r] = 0;
-                        ++pass[r];
-                    }
+            auto forward = [&](uint32_t& slot, uint32_t& phase) {
+                slot += 2;
+                if (slot >= ring_slots) {
+                    slot -= ring_slots;
+                    phase ^= 1;
                 }
-                page = next;
-            }
-        }
-        if (gone)  // no copy may be in flight when the CTA leaves: each slot's last one
-            for (int r = 0; r < (PAIR ? 1 : 2); ++r)
-                for (uint32_t s = 0; s < ring_slots; ++s) {
-                    const uint32_t uses = pass[r] + (s < next_slot[r] ? 1 : 0);
-                    if (uses > 0)
-                        mbar_wait_bounded(&full[r * ring_slots + s], (uses - 1) & 1, p.limit_ns);
-                }
-    } else if (warp >= 9) {
-        // ---- an MMA warp: group w's scores and its products with V (one warp for both groups spent
-        // 1340 cycles a step on its waits, one after the other, for 640 of MMAs)
-        const int w = warp - 9;
-        const bool one = elect_one();
-        constexpr uint32_t kIdS = instr_desc(KT, false), kIdO = instr_desc(HD, true);
-        const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
-        const uint32_t ra = smem_u32(ring) + first_slot * C::kSlotBytes;
-        const uint64_t ad = smem_desc(smem_u32(qbuf) + (PAIR ? w * (128 * HD * 2) : 0), 16, 1024);
-        full += first_slot;
-        empty += first_slot;
-        // the ring's slots of the next K and the next V tile: every second one
-        uint32_t k_slot = 0, k_phase = 0, v_slot = 1, v_phase = 0, p_phase = 0 /* a bit a buffer */, seg = 0;
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
-        };
-        auto forward = [&](uint32_t& slot, uint32_t& phase) {
-            slot += 2;
-            if (slot >= ring_slots) {
-                slot -= ring_slots;
-                phase ^= 1;
-            }
-        };
-        auto scores = [&](int buf) {
-            if (!wait(&full[k_slot], k_phase))
-                return false;
-            const uint64_t bd = smem_desc(ra + k_slot * C::kSlotBytes, 16, 1024);
-#pragma unroll
-            for (int ks = 0; ks < HD / 16; ++ks)  // 32 bytes on within 64 columns, then the next 64
-                tc_mma_ss(tmem + 64 * (2 * w + buf), ad + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
-                          bd + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), kIdS, ks > 0, one);
-            tc_commit(&s_full[2 * w + buf], one);
-            tc_commit(&empty[k_slot], one);
-            forward(k_slot, k_phase);
-            return true;
-        };
-        bool ok = true;
-        for (int u = u0; u < u1 && ok;) {
-            const Segment g = shares.segment(u, u1);
-            u += g.units;
-            if (g.t0 == g.t1)
-                continue;
-            const int n = PAIR ? g.t1 - g.t0 : (g.t1 - g.t0 + 1 - w) / 2;  // the group's tiles
-            ok = wait(q_ready, seg & 1);
-            if (!ok)
-                break;
-            tc_fence_after();
-            for (int k = 0; k < 2 && k < n && ok; ++k)
-                ok = scores(k);
-            for (int k = 0; k < n && ok; ++k) {
-                const int buf = k & 1;
-                ok = wait(&p_ready[2 * w + buf], p_phase >> buf & 1) && wait(&full[v_slot], v_phase);
+            };
+            auto scores = [&](int buf) {
+                if (!wait(&full[k_slot], k_phase))
+                    return false;
+                const uint64_t bd = smem_desc(ra + k_slot * C::kSlotBytes, 16, 1024);
+    #pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks)  // 32 bytes on within 64 columns, then the next 64
+                    tc_mma_ss(tmem + 64 * (2 * w + buf), ad + (((ks >> 2) * (128 * 128) + (ks & 3) * 32) >> 4),
+                              bd + (((ks >> 2) * (KT * 128) + (ks & 3) * 32) >> 4), kIdS, ks > 0, one);
+                tc_commit(&s_full[2 * w + buf], one);
+                tc_commit(&empty[k_slot], one);
+                forward(k_slot, k_phase);
+                return true;
+            };
+            bool ok = true;
+            for (int u = u0; u < u1 && ok;) {
+                const Segment g = shares.segment(u, u1);
+                u += g.units;
+                if (g.t0 == g.t1)
+                    continue;
+                const int n = PAIR ? g.t1 - g.t0 : (g.t1 - g.t0 + 1 - w) / 2;  // the group's tiles
+                ok = wait(q_ready, seg & 1);
                 if (!ok)
                     break;
-                p_phase ^= 1u << buf;
                 tc_fence_after();
-                const uint64_t bd = smem_desc(ra + v_slot * C::kSlotBytes, KT * 128, 1024);
-#pragma unroll
-                for (int ks = 0; ks < KT / 16; ++ks)
-                    tc_mma_ts(tmem + kOCol + 128 * w, tmem + 64 * (2 * w + buf) + 8 * ks, bd + (ks * 2048 >> 4), kIdO, k > 0 || ks > 0, one);
-                tc_commit(&o_done[2 * w + buf], one);
-                tc_commit(&empty[v_slot], one);
-                forward(v_slot, v_phase);
-                if (k + 2 < n)
-                    ok = scores(buf);
+                for (int k = 0; k < 2 && k < n && ok; ++k)
+                    ok = scores(k);
+                for (int k = 0; k < n && ok; ++k) {
+                    const int buf = k & 1;
+                    ok = wait(&p_ready[2 * w + buf], p_phase >> buf & 1) && wait(&full[v_slot], v_phase);
+                    if (!ok)
+                        break;
+                    p_phase ^= 1u << buf;
+                    tc_fence_after();
+                    const uint64_t bd = smem_desc(ra + v_slot * C::kSlotBytes, KT * 128, 1024);
+    #pragma unroll
+                    for (int ks = 0; ks < KT / 16; ++ks)
+                        tc_mma_ts(tmem + kOCol + 128 * w, tmem + 64 * (2 * w + buf) + 8 * ks, bd + (ks * 2048 >> 4), kIdO, k > 0 || ks > 0, one);
+                    tc_commit(&o_done[2 * w + buf], one);
+                    tc_commit(&empty[v_slot], one);
+                    forward(v_slot, v_phase);
+                    if (k + 2 < n)
+                        ok = scores(buf);
+                }
+                if (ok)
+                    tc_commit(o_full, one);
+                ++seg;
             }
-            if (ok)
-                tc_commit(o_full, one);
-            ++seg;
+            // no MMA may be under way when the tensor memory is given back
+            tc_commit(fin, one);
+            mbar_wait_bounded(fin, 0, p.limit_ns);
+            __syncwarp();
         }
-        // no MMA may be under way when the tensor memory is given back
-        tc_commit(fin, one);
-        mbar_wait_bounded(fin, 0, p.limit_ns);
-        __syncwarp();
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // ---- softmax: group w, a thread a row
         const int w = warp >> 2, wt = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;

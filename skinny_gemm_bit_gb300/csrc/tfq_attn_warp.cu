@@ -21,7 +21,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kCtaThreads = kWarps * 32;
-constexpr int kOver = 16;     // a segment's own cost, in key tiles
 constexpr float kGrow = 8.f;  // the reference of a row moves when its maximum has grown by 2^8
 
 template <int HD, int RW>
@@ -104,7 +103,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     }
     pdl_wait();
-    Shares<ROWS, KT, kOver, kWarps> shares(p, smem + C::kSchedOff);
+    Shares<ROWS, KT, kWarps> shares(p, smem + C::kSchedOff);
     shares.build();
     pdl_launch_dependents();
     const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
