@@ -494,8 +494,8 @@ size_t tf_kvcache_workspace_bytes(const tf_kvcache* c);
  *   slots     device int32 [M], output: page * page_size + row in the page for each row
  *             (what tf_qk_norm_rope_run stores to); -1 for rows of no sequence
  *   positions device int32 [M], output (may be NULL): the row's position in its sequence,
- *             length before the call + depth in the tree (popcount(mask) - 1; without
- *             masks, the row's index in its block); 0 for rows of no sequence
+ *             length before the call + depth in the tree (popcount(mask) - 1, at least 0;
+ *             without masks, the row's index in its block); 0 for rows of no sequence
  * All or nothing: with too few free pages (TF_E_CACHE_FULL in the status word), a slot out
  * of range or named twice, a length beyond max_pages, a q_start out of order, or a shared
  * unfilled last page (TF_E_INVALID_ARG), the book stays as it was and every slot is -1.
@@ -577,10 +577,12 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
  * over the tokens the row sees; a row that sees none gives zeros. Tokens it does not see take
  * no part, whatever is stored there (NaN and infinities included).
  *   q       bf16 [M], leading dimension ldq >= n_q * head_dim (a multiple of 8), 16-byte aligned
- *   o       bf16 [M][n_q * head_dim], 16-byte aligned; rows of no sequence are left as they were
+ *   o       bf16 [M][n_q * head_dim], 16-byte aligned, not overlapping q; rows of no sequence are
+ *           left as they were
  *   n_q     a multiple of n_kv, at most 64 query heads to a key/value head
  *   B       1..1024; a slot may appear twice
- *   max_rows  1..TF_MAX_DRAFT_ROWS, no T_b above it
+ *   max_rows  1..TF_MAX_DRAFT_ROWS, no T_b above it; it and n_q / n_kv choose the kernel, so it
+ *             should be no larger than it has to be
  *   scale   finite
  *   ws      tf_tree_attn_workspace_bytes(c, n_q, B, max_rows) bytes
  * A sequence whose arguments do not hold (slot out of range, more rows than max_rows or than

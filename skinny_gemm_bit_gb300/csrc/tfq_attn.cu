@@ -120,6 +120,8 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     if (!is_aligned(q, 16) || !is_aligned(o, 16) || ldq % 8 != 0 || ldq < (int64_t)n_q * p.c.head_dim)
         return report_error(TF_E_INVALID_ARG, "%s: q and o must be 16-byte aligned, ldq a multiple of 8 and >= n_q * head_dim",
                             name);
+    if (rows_overlap(q, ldq, (int64_t)n_q * p.c.head_dim, o, (int64_t)n_q * p.c.head_dim, (int64_t)n_q * p.c.head_dim, M))
+        return report_error(TF_E_INVALID_ARG, "%s: o overlaps q", name);
     if (!std::isfinite(scale))
         return report_error(TF_E_INVALID_ARG, "%s: scale must be finite", name);
     if ((rc = check_ws(ws, ws_bytes, tf_tree_attn_workspace_bytes(c, n_q, B, max_rows), name)))

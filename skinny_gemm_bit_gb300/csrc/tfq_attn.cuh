@@ -264,18 +264,20 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
         }
     }
     named_bar_sync(1, THREADS);
-    const int items = s.rows * kQuads, i0 = (int)((int64_t)items * me / n), i1 = (int)((int64_t)items * (me + 1) / n);
+    // item: four columns of a row, whether the sequence has that row or not: no division by a length here
+    constexpr unsigned kItems = ROWS * kQuads;
+    const int i0 = (int)(kItems * (unsigned)me / (unsigned)n), i1 = (int)(kItems * (unsigned)(me + 1) / (unsigned)n);
     int lp = 1;
     while (lp < 8 && (i1 - i0) * lp * 2 <= THREADS && lp < n)
         lp *= 2;
     const int sub = threadIdx.x % lp;
     for (int at = i0; at < i1; at += THREADS / lp) {
         const int item = at + threadIdx.x / lp;
-        const bool in = item < i1;
-        const int quad = in ? item / s.rows : 0, row = in ? item - quad * s.rows : 0, col = quad * 4;
+        const int quad = item / ROWS, row = item % ROWS, col = quad * 4;
+        const bool in = item < i1 && row < s.rows;
         float m = -INFINITY, l = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = s.c0 + sub; c <= s.c1; c += 4 * lp) {
+        for (int c = in ? s.c0 + sub : s.c1 + 1; c <= s.c1; c += 4 * lp) {
             float2 ml[4];
             float4 v[4];
 #pragma unroll

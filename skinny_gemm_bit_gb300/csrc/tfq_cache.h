@@ -31,6 +31,13 @@ int check_ws(const void* ws, size_t ws_bytes, size_t need, const char* name);
 
 inline bool is_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// Whether rows x cols elements of 2 bytes at a (leading dimension lda) and at b share memory.
+inline bool rows_overlap(const void* a, int64_t lda, int64_t cols_a, const void* b, int64_t ldb, int64_t cols_b, int64_t rows)
+{
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    return a0 < b0 + (uintptr_t)((rows - 1) * ldb + cols_b) * 2 && b0 < a0 + (uintptr_t)((rows - 1) * lda + cols_a) * 2;
+}
+
 // Launch with (or without) programmatic dependent launch on the previous kernel.
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,

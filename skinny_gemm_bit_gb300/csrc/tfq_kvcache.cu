@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_kernel(CacheView c, const
             const int at_row = base[lo] + j;
             const int page = c.table[(int64_t)slot_of[lo] * c.max_pages + (at_row >> c.page_shift)];
             slot = page * c.page_size + (at_row & (c.page_size - 1));
-            pos = masks == nullptr ? at_row : base[lo] + __popcll(masks[m]) - 1;
+            pos = masks == nullptr ? at_row : base[lo] + max(__popcll(masks[m]) - 1, 0);
         }
         slots[m] = slot;
         if (positions != nullptr)

@@ -225,6 +225,9 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
         return report_error(TF_E_INVALID_ARG,
                             "%s: qkv and q must be 16-byte aligned, ld a multiple of 8 and >= (n_q + 2 n_kv) * head_dim",
                             name);
+    if (rows_overlap(qkv, ld, (int64_t)(n_q + 2 * p.c.n_kv) * p.c.head_dim, q, (int64_t)n_q * p.c.head_dim,
+                     (int64_t)n_q * p.c.head_dim, M))
+        return report_error(TF_E_INVALID_ARG, "%s: q overlaps qkv", name);
     if ((q_gamma != nullptr && !is_aligned(q_gamma, 16)) || (k_gamma != nullptr && !is_aligned(k_gamma, 16)) || !(eps >= 0.f))
         return report_error(TF_E_INVALID_ARG, "%s: gammas must be 16-byte aligned and eps >= 0", name);
     p.qkv = qkv;

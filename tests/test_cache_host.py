@@ -10,6 +10,7 @@ from skinny_gemm_bit_gb300 import build as tfq_build
 
 FAKE = ctypes.c_void_p(0x10000)  # aligned, never dereferenced: validation fails first
 ODD = ctypes.c_void_p(0x10002)
+OUT = ctypes.c_void_p(0x40000000)
 
 
 @pytest.fixture(scope="module")
@@ -82,13 +83,13 @@ def test_norm_rope_refuses(T):
     L = T.lib()
     _, d = _cache(T)
 
-    def run(qkv=FAKE, ld=1024, M=1, n_q=4, qg=None, kg=None, eps=1e-6, pos=FAKE, turns=FAKE, rot=128, q=FAKE, layer=0,
+    def run(qkv=FAKE, ld=1024, M=1, n_q=4, qg=None, kg=None, eps=1e-6, pos=FAKE, turns=FAKE, rot=128, q=OUT, layer=0,
             slots=FAKE, ws=FAKE, wsb=256, c=d):
         return L.tf_qk_norm_rope_run(qkv, ld, M, n_q, qg, kg, eps, pos, turns, rot, 0, q, ctypes.byref(c), layer, slots, ws,
                                      wsb, 0, None)
 
     for kw in [dict(qkv=None), dict(qkv=ODD), dict(ld=1023), dict(ld=1020), dict(qg=ODD), dict(kg=ODD), dict(eps=-1.0),
-               dict(eps=math.nan), dict(pos=None), dict(turns=None), dict(q=None), dict(q=ODD), dict(layer=2), dict(layer=-1),
+               dict(eps=math.nan), dict(pos=None), dict(turns=None), dict(q=None), dict(q=ODD), dict(q=ctypes.c_void_p(0x10000 + 1008)), dict(layer=2), dict(layer=-1),
                dict(slots=None), dict(ws=None), dict(c=T.tf_kvcache())]:
         assert run(**kw) == T.TF_E_INVALID_ARG, kw
     for kw in [dict(M=0), dict(M=1 << 25), dict(n_q=0), dict(n_q=1025), dict(rot=24), dict(rot=144), dict(rot=-16)]:
@@ -100,12 +101,12 @@ def test_tree_attn_refuses(T):
     L = T.lib()
     _, d = _cache(T)
 
-    def run(q=FAKE, ldq=512, M=1, n_q=4, layer=0, seqs=FAKE, qs=FAKE, B=1, rows=1, scale=0.1, o=FAKE, ws=FAKE, wsb=1 << 30,
+    def run(q=FAKE, ldq=512, M=1, n_q=4, layer=0, seqs=FAKE, qs=FAKE, B=1, rows=1, scale=0.1, o=OUT, ws=FAKE, wsb=1 << 30,
             c=d):
         return L.tf_tree_attn_run(q, ldq, M, n_q, ctypes.byref(c), layer, seqs, qs, B, rows, None, scale, o, ws, wsb, 0, None)
 
     for kw in [dict(q=None), dict(q=ODD), dict(ldq=511), dict(ldq=500), dict(layer=2), dict(seqs=None), dict(qs=None),
-               dict(scale=math.inf), dict(scale=math.nan), dict(o=None), dict(o=ODD), dict(ws=None), dict(c=T.tf_kvcache())]:
+               dict(scale=math.inf), dict(scale=math.nan), dict(o=None), dict(o=ODD), dict(o=FAKE), dict(o=ctypes.c_void_p(0x10000 - 1008)), dict(ws=None), dict(c=T.tf_kvcache())]:
         assert run(**kw) == T.TF_E_INVALID_ARG, kw
     for kw in [dict(M=0), dict(M=1 << 21), dict(n_q=3), dict(n_q=0), dict(n_q=130), dict(B=0), dict(B=1025), dict(rows=0),
                dict(rows=65)]:

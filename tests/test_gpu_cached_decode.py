@@ -193,6 +193,36 @@ def test_tree_attn_many_sequences(T):
     check_attn(T, c, 0, list(range(150)), rows, None, 2, 6)
 
 
+@pytest.mark.parametrize("n_q,hd,rows", [(2, 128, 1), (4, 64, 7), (1, 256, 3), (40, 128, 3)])
+def test_tree_attn_the_most_sequences(T, n_q, hd, rows):
+    """1024 sequences, the kernels' largest schedule; some repeat a slot, some have no row."""
+    lens = [1 + 7 * i % 90 for i in range(40)]
+    c = filled_cache(T, lens, 1, hd, 16, 101)
+    rng = np.random.default_rng(rows)
+    seqs = rng.integers(0, 40, 1024).tolist()
+    rr = [int(min(rng.integers(0, rows + 1), lens[s])) for s in seqs]
+    q, out, start = run_attn(T, c, 1, seqs, rr, None, n_q, 6)
+    for b in rng.permutation(1024)[:60].tolist() + [0, 1023]:
+        qq = R.f64(q[start[b]:start[b + 1]]).reshape(rr[b], n_q, hd)
+        ref, spread = R.tree_attn(qq, tokens(c, 1, 0, seqs[b]), tokens(c, 1, 1, seqs[b]), chain(rr[b]), hd ** -0.5)
+        within(R.f64(out[start[b]:start[b + 1]]).reshape(rr[b], n_q, hd), ref, R.attn_tol(ref, spread))
+
+
+@pytest.mark.parametrize("rows,n_q", [(3, 16), (40, 32)])
+def test_a_cache_past_32_bit_offsets(T, rows, n_q):
+    """5.4 GB of pages: the last layer's values start beyond 2^32 bytes."""
+    c = T.KVCache.create(2, 8, 128, 16, 41000, 1, 60)
+    n = 700
+    c.refs[:40956] = 1  # all pages but the last 44 are somebody's
+    slots = torch.cat([T.tf_kvcache_extend(c, i32([0]), i32([0, r]), r)[0] for r in (n - rows, rows)])
+    at = torch.arange(n, device="cuda")
+    assert torch.equal(slots, (40956 * 16 + at).int())
+    kv = rand((n, (1 + 16) * 128), 7)
+    T.tf_qk_norm_rope_run(kv, c, 1, at.int(), slots, T.RopeTable([]), n_q=1)
+    check_attn(T, c, 1, [0], [rows], None, n_q, 8)
+    np.testing.assert_array_equal(tokens(c, 1, 1, 0), R.f64(kv[:, 9 * 128:]).reshape(n, 8, 128))
+
+
 @pytest.mark.parametrize("hd,rows", [(128, 4), (64, 20), (256, 6), (128, 50)])
 def test_tree_attn_rows_that_see_nothing_are_zero(T, hd, rows):
     c = filled_cache(T, [rows, 100 + rows], 2, hd, 16, 31)
@@ -377,6 +407,27 @@ def test_a_fork_without_enough_free_pages_does_nothing(T):
     assert T.tf_workspace_status(ws) == T.TF_OK and c.len.tolist() == [20, 20, 20, 7]
 
 
+def test_page_operations_of_the_most_slots(T):
+    """1024 slots, all named in one call: extend, a reordering fork, keep."""
+    c = T.KVCache.create(1, 1, 64, 16, 6000, 1024, 9)
+    m = R.Book(1024, 6000, 9, 16)
+    rng = np.random.default_rng(5)
+    for step in range(3):
+        seqs, rows = rng.permutation(1024).tolist(), rng.integers(0, 30, 1024).tolist()
+        start = np.cumsum([0] + rows).tolist()
+        slots, _ = T.tf_kvcache_extend(c, i32(seqs), i32(start), start[-1])
+        assert slots.tolist() == m.extend(seqs, rows)
+        parent = rng.integers(-1, 1024, 1024).tolist()
+        T.tf_kvcache_fork(c, i32(parent))
+        assert m.fork(parent) is not None
+        assert book_of(c) == m.flat()
+    seqs = [s for s in range(1024) if m.len[s] % 16 >= 3]
+    T.tf_kvcache_keep(c, i32(seqs), i32(list(range(0, 3 * len(seqs) + 1, 3))), i32([0, 2, 0] * len(seqs)), i32([2] * len(seqs)))
+    for s in seqs:
+        m.keep(s, 3, [0, 2])
+    assert book_of(c) == m.flat()
+
+
 def test_extend_of_a_tree_gives_the_depths(T):
     c = filled_cache(T, [20, 0], 1, 64, 16, 81)
     masks = [0b1, 0b11, 0b101, 0b1011]  # root, two children, a grandchild of the first
@@ -554,6 +605,8 @@ def test_the_binding_refuses_tensors_that_do_not_fit(T):
             T.tf_tree_attn_run(kw["q"], c, 0, kw["seqs"], kw["q_start"], masks=kw["masks"], max_rows=2, out=kw["out"])
     with pytest.raises(T.TfqError):
         T.tf_tree_attn_run(q, c, 2, s, st, max_rows=2)
+    with pytest.raises(T.TfqError):
+        T.tf_tree_attn_run(q, c, 0, s, st, max_rows=2, out=q)
     with pytest.raises(ValueError):
         T.KVCache(c.data[:, :1], c.book, 1, 3)
     with pytest.raises(T.TfqError):
