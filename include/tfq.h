@@ -496,6 +496,7 @@ size_t tf_kvcache_workspace_bytes(const tf_kvcache* c);
  *   positions device int32 [M], output (may be NULL): the row's position in its sequence,
  *             length before the call + depth in the tree (popcount(mask) - 1, at least 0;
  *             without masks, the row's index in its block); 0 for rows of no sequence
+ * The outputs may not overlap one another or the inputs.
  * All or nothing: with too few free pages (TF_E_CACHE_FULL in the status word), a slot out
  * of range or named twice, a length beyond max_pages, a q_start out of order, or a shared
  * unfilled last page (TF_E_INVALID_ARG), the book stays as it was and every slot is -1.
@@ -554,7 +555,7 @@ int tf_rope_turns(const double* inv_freq, int64_t n, uint64_t* turns);
  *             of one call must not name the same slot.
  *   turns     device uint64 [rot_dim / 2] (tf_rope_turns), may be NULL when rot_dim is 0
  *   rot_dim   0..head_dim, a multiple of 16
- *   q         bf16 [M][n_q * head_dim], 16-byte aligned; may not overlap qkv
+ *   q         bf16 [M][n_q * head_dim], 16-byte aligned; may not overlap qkv, nor either of them the cache
  *   ws        256 zeroed, 256-aligned bytes (status word)
  * 1 <= n_q <= 1024, 1 <= M < 2^31 / 64. TF_RUN_PDL: gammas and turns may be read before the
  * previous kernel on the stream has finished.
@@ -577,8 +578,8 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
  * over the tokens the row sees; a row that sees none gives zeros. Tokens it does not see take
  * no part, whatever is stored there (NaN and infinities included).
  *   q       bf16 [M], leading dimension ldq >= n_q * head_dim (a multiple of 8), 16-byte aligned
- *   o       bf16 [M][n_q * head_dim], 16-byte aligned, not overlapping q; rows of no sequence are
- *           left as they were
+ *   o       bf16 [M][n_q * head_dim], 16-byte aligned, not overlapping q or the cache; rows of no
+ *           sequence are left as they were
  *   n_q     a multiple of n_kv, at most 64 query heads to a key/value head
  *   B       1..1024; a slot may appear twice
  *   max_rows  1..TF_MAX_DRAFT_ROWS, no T_b above it; it and n_q / n_kv choose the kernel, so it
@@ -626,7 +627,7 @@ typedef struct tf_attn_desc {
  *   o   = attention of the M rows over the cache (tf_tree_attn_run)
  *   h1  = h + o . Wo^T, and the MLP and the readout as there
  * on a cache that tf_kvcache_extend has made room in: seqs, q_start, masks, slots and
- * positions are that call's (device). The caches's layers are used from 0; it has at least
+ * positions are that call's (device). The cache's layers are used from 0; it has at least
  * d->n_layers, n_kv * head_dim = d->kv_dim, and M (1..8) rows belong to B sequences.
  * After a verify step tf_kvcache_keep keeps what was accepted. The results are those of the
  * separate calls, bit for bit. ws: tf_decode_step_attn_workspace_bytes(d, c, a) bytes, zeroed
@@ -652,6 +653,7 @@ int tf_decode_step_attn_run(const tf_decoder_desc* d, const tf_kvcache* c, const
  * logp, entropy and top_logp NaN; NaN ranks below every number, as in tf_argmax_rows.
  *   M 1..2^31 / 64, N 1..2^31 - 1; 0 <= top_k <= min(32, N); 0 <= n_targets <= 1024
  *   (targets, logp may be NULL when n_targets is 0, top_idx and top_logp when top_k is 0)
+ * The outputs may not overlap one another, the logits or the targets.
  *   ws  tf_logprobs_workspace_bytes(M, N, top_k) bytes
  */
 size_t tf_logprobs_workspace_bytes(int64_t M, int64_t N, int top_k);

@@ -1276,6 +1276,18 @@ int check_attn_step(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn
     if (a->n_q < 1 || (int64_t)a->n_q * v.head_dim != d->q_dim || (int64_t)v.n_kv * v.head_dim != d->kv_dim ||
         v.n_layers < d->n_layers)
         return fail(TF_E_UNSUPPORTED_SHAPE, "%s: the cache's heads or layers do not match the decoder's dimensions", name);
+    // what tf_qk_norm_rope_run and tf_tree_attn_run would refuse once layers before it have run
+    if (a->n_q % v.n_kv != 0 || a->n_q / v.n_kv > 64 || a->n_q > 1024)
+        return fail(TF_E_UNSUPPORTED_SHAPE, "%s: n_q must be a multiple of n_kv, at most 1024 and 64 query heads to one", name);
+    if (a->rot_dim < 0 || a->rot_dim > v.head_dim || a->rot_dim % 16 != 0)
+        return fail(TF_E_UNSUPPORTED_SHAPE, "%s: rot_dim must be a multiple of 16 within [0, head_dim]", name);
+    if (a->rot_dim > 0 && (a->turns == nullptr || !aligned(a->turns, 8)))
+        return fail(TF_E_INVALID_ARG, "%s: turns NULL or misaligned", name);
+    if (!(a->eps >= 0.f) || !std::isfinite(a->scale))
+        return fail(TF_E_INVALID_ARG, "%s: eps must be >= 0 and scale finite", name);
+    for (int l = 0; l < d->n_layers; ++l)
+        if (!aligned(a->layers[l].q_norm, 16) || !aligned(a->layers[l].k_norm, 16))
+            return fail(TF_E_INVALID_ARG, "%s: layer %d head norms misaligned", name, l);
     return TF_OK;
 }
 

@@ -10,7 +10,10 @@ namespace tfq {
 namespace {
 
 // Query rows of an item, and with them the kernel: up to 32 the warp MMAs, above the tensor-memory
-// MMAs (which need the output of two row groups in tensor memory: head_dim up to 128).
+// MMAs (which need the output of two row groups in tensor memory: head_dim up to 128). Over 64
+// sequences of 8192 tokens, 8 key/value heads of 128, in us, warp and tensor-memory MMAs: 8 rows 320 and
+// 335, 32 rows 335 and 349, 40 rows (two items of the warps') 633 and 351. One sequence of 32,768: 8 rows
+// 32 and 36, 32 rows 39 and 36.5, 40 rows 64 and 39. (Items of 32 rows for 8: 335 and 36.)
 int attn_rows(int max_rows, int group, int head_dim)
 {
     const int r = max_rows * group;
@@ -23,7 +26,7 @@ int attn_rows(int max_rows, int group, int head_dim)
 
 // A segment's own cost in key tiles of its kernel, by which the CTAs' shares are measured. With more
 // items than CTAs it is what evens out those that get several short ones (28 of the warp kernel's 32-key
-// tiles: 64 ragged sequences 176 us, 183 with 16, 199 with 8); with fewer, what a CTA gets should
+// tiles: 64 ragged sequences 176 us, 183 with 16, 199 with 8, side by side); with fewer, what a CTA gets should
 // still be a tile a warp (one token over 4097: 12.0 us with 16, 13.4 with 24).
 int attn_over(int rows, int64_t items)
 {
@@ -122,6 +125,8 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
                             name);
     if (rows_overlap(q, ldq, (int64_t)n_q * p.c.head_dim, o, (int64_t)n_q * p.c.head_dim, (int64_t)n_q * p.c.head_dim, M))
         return report_error(TF_E_INVALID_ARG, "%s: o overlaps q", name);
+    if (in_cache(p.c, o, (int64_t)n_q * p.c.head_dim, (int64_t)n_q * p.c.head_dim, M))
+        return report_error(TF_E_INVALID_ARG, "%s: o overlaps the cache", name);
     if (!std::isfinite(scale))
         return report_error(TF_E_INVALID_ARG, "%s: scale must be finite", name);
     if ((rc = check_ws(ws, ws_bytes, tf_tree_attn_workspace_bytes(c, n_q, B, max_rows), name)))

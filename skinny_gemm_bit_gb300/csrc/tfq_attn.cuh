@@ -7,8 +7,8 @@
 // few rows over a long context still use the whole GPU. A CTA that holds all of an item writes
 // its output; otherwise each writes its part (running maximum, sum and unscaled output) to the
 // workspace, and once all of an item's parts are there each of its CTAs joins a slice of the
-// output, parts in key order. (Joined by the last to arrive, 19 parts of 16 rows by 128 took one CTA
-// 8 us of a 36 us call.) CTAs wait for one another at their very end only, when all their parts are
+// output, parts in key order: 8 rows over 32,771 tokens, some 19 parts to an item, take 32.1 us so and
+// 35.6 when the last CTA to arrive joins them all. CTAs wait for one another at their very end only, when all their parts are
 // written; the launch is cooperative, so all of them run. The lengths are read on the device: a
 // captured call follows them.
 #pragma once
@@ -180,7 +180,7 @@ struct Shares {
     }
 };
 
-// The scaled score of a row and a key in the softmax's running form.
+// 2^x: scores are scaled by log2(e), so that a weight is one instruction
 __device__ __forceinline__ float attn_ex2(float x)
 {
     float y;

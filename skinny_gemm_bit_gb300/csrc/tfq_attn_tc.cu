@@ -10,9 +10,11 @@
 //   O[w] += P V           A from tensor memory, V as it lies in the cache (N-major)
 //
 // Each group has two score buffers: the scores of its next tile are formed while it works on this
-// one's weights, so neither it nor the tensor cores wait for the other's latency (with one buffer
-// and 128-key tiles a group spent 2600 of 6600 cycles a tile waiting: 206 us against 2 x fewer on
-// trees of 64 rows and 8 heads over 8 x 16001 tokens). Up to 128 query rows (PAIR false) both
+// one's weights, so neither it nor the tensor cores wait for the other's latency. Trees of 64 rows
+// by 8 heads to each of 4 key/value heads of 128, over 8 x 16,001 tokens: 143 us, 937 TFLOP/s, against 206
+// with one buffer and 128-key tiles, where a group spent 2600 of 6600 cycles a tile waiting. What
+// is left is the softmax's own work and Q K^T at 64 keys, which reads 128 rows of queries from
+// shared memory for each 64 of keys (some 67 cycles a 128 x 64 x 16 step). Up to 128 query rows (PAIR false) both
 // groups have the same rows and every other tile, and their outputs are joined at the end; that is
 // bound by the cache's bytes. Above (PAIR true) each group has 128 rows of its own and both read
 // every tile, so a tile is fetched once for 256 rows. Tiles are 64 keys: two buffers of them a group

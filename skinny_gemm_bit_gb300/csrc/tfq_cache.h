@@ -38,6 +38,35 @@ inline bool rows_overlap(const void* a, int64_t lda, int64_t cols_a, const void*
     return a0 < b0 + (uintptr_t)((rows - 1) * ldb + cols_b) * 2 && b0 < a0 + (uintptr_t)((rows - 1) * lda + cols_a) * 2;
 }
 
+struct MemRange {
+    const void* p;
+    size_t bytes;
+};
+
+inline bool overlap(const MemRange& a, const MemRange& b)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && a.bytes != 0 && b.bytes != 0 && x < y + b.bytes && y < x + a.bytes;
+}
+
+// Whether one of the first n_out (the outputs) shares memory with another of the n.
+inline bool outputs_overlap(const MemRange* r, int n_out, int n)
+{
+    for (int i = 0; i < n_out; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (overlap(r[i], r[j]))
+                return true;
+    return false;
+}
+
+// Whether rows x cols elements of 2 bytes (leading dimension ld) share memory with the cache's data or book.
+inline bool in_cache(const CacheView& c, const void* a, int64_t ld, int64_t cols, int64_t rows)
+{
+    const MemRange r{a, (size_t)((rows - 1) * ld + cols) * 2};
+    return overlap(r, MemRange{c.data, (size_t)c.row_of(c.n_layers, 0, 0, 0) * c.head_dim * 2}) ||
+           overlap(r, MemRange{c.len, (c.n_seqs + (size_t)c.n_pages + (size_t)c.n_seqs * c.max_pages) * 4});
+}
+
 // Launch with (or without) programmatic dependent launch on the previous kernel.
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool pdl,

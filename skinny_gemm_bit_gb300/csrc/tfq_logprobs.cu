@@ -20,7 +20,7 @@
 // the one batch that their largest came from (they note which, and their second largest batch): those
 // batches are read again (from L2), eight a warp at once, and what reaches the bound is collected
 // and sorted as (value, lower index first) keys, 32 a warp. That costs a row's latency, not its
-// bandwidth: 1000 rows of 151,936 take 54 us without alternatives. A thread whose second batch
+// bandwidth: 1000 rows of 151,936 in bf16 take 67.2 us with 20 alternatives (4.5 TB/s), 54 without (5.6). A thread whose second batch
 // reaches the bound too has all its units read. Rows with more than kMaxCand such elements (ties
 // without end, NaN) take their units through sorted lists instead, one key a lane.
 #include <cmath>
@@ -610,9 +610,18 @@ int tf_logprobs_rows(const void* v, int dtype, int64_t ld, int64_t M, int64_t N,
     int rc = check_ws(ws, ws_bytes, 256, name);
     if (rc)
         return rc;
+    const MemRange ranges[] = {{logp, (size_t)M * n_targets * 4},
+                            {entropy, (size_t)M * 4},
+                            {top_idx, (size_t)M * top_k * 4},
+                            {top_logp, (size_t)M * top_k * 4},
+                            {v, (size_t)((M - 1) * ld + N) * (dtype == TF_DTYPE_F32 ? 4 : 2)},
+                            {targets, (size_t)M * n_targets * 4}};
+    if (outputs_overlap(ranges, 4, 6))
+        return report_error(TF_E_INVALID_ARG, "%s: an output overlaps another argument", name);
     const LpParams p{v, ld, M, N, targets, n_targets, top_k, logp, entropy, top_idx, top_logp, static_cast<int*>(ws)};
     // few rows: as many blocks a row (a power of two up to 8) as the SMs hold, if each still
-    // has a batch of units a thread
+    // has a batch of units a thread. Rows of 151,936 in us, with 1, 2, 4, 8 blocks: one row 13.0,
+    // 11.8, 10.8, 9.4; 24 rows 14.2, 12.9, 11.4, 11.8; 60 rows 14.3, 13.3, 13.4, 15.5.
     int parts = 1;
     const int64_t batch = (int64_t)kLpThreads * kBatch * (dtype == TF_DTYPE_F32 ? 4 : 8);
     while (parts < kMaxCluster && M * parts * 2 <= device_sms() && N >= batch * parts)

@@ -9,6 +9,9 @@
 // one head, chosen so that both ends of each rotated pair are its own: head_dim / 16 lanes take
 // a head (8 at 128, so a warp takes 4 heads at once), the sum of squares is a butterfly over
 // those lanes, and the eight angles a lane needs are made once a row and used for all its heads.
+//
+// 8191 such rows: 25.6 us, 5.2 TB/s of reads and writes (each row's loads run one set of heads ahead of the
+// arithmetic); 8 rows: 2.1 us, of which a launch is most.
 #include <cmath>
 
 #include "tfq_cache.h"
@@ -228,6 +231,9 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
     if (rows_overlap(qkv, ld, (int64_t)(n_q + 2 * p.c.n_kv) * p.c.head_dim, q, (int64_t)n_q * p.c.head_dim,
                      (int64_t)n_q * p.c.head_dim, M))
         return report_error(TF_E_INVALID_ARG, "%s: q overlaps qkv", name);
+    if (in_cache(p.c, q, (int64_t)n_q * p.c.head_dim, (int64_t)n_q * p.c.head_dim, M) ||
+        in_cache(p.c, qkv, ld, (int64_t)(n_q + 2 * p.c.n_kv) * p.c.head_dim, M))
+        return report_error(TF_E_INVALID_ARG, "%s: q or qkv overlaps the cache", name);
     if ((q_gamma != nullptr && !is_aligned(q_gamma, 16)) || (k_gamma != nullptr && !is_aligned(k_gamma, 16)) || !(eps >= 0.f))
         return report_error(TF_E_INVALID_ARG, "%s: gammas must be 16-byte aligned and eps >= 0", name);
     p.qkv = qkv;
@@ -245,7 +251,8 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
     p.layer = layer;
     p.slots = slots;
     p.status = static_cast<int*>(ws);
-    // few rows: a row's heads spread over as many warps as it takes to fill the GPU
+    // few rows: a row's heads spread over as many warps as it takes to fill the GPU. 16 warps an SM:
+    // 2048 rows of 32 heads 7.6 us; 7.8 with 8, 8.4 with 32, 10.2 with 64; 512 rows 3.8 to 4.2 with any.
     const int per_warp = 512 / p.c.head_dim, groups = (n_q + 2 * p.c.n_kv + per_warp - 1) / per_warp;
     const int64_t want = (int64_t)device_sms() * 16;
     p.parts = 1;

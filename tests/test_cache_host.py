@@ -149,3 +149,102 @@ def test_rope_turns(T):
 
 def test_cache_full_has_a_name(T):
     assert T.status_str(T.TF_E_CACHE_FULL) == "TF_E_CACHE_FULL" == T.status_str(8)
+
+
+def _at(a):
+    return ctypes.c_void_p(a)
+
+
+def test_outputs_over_the_cache_or_over_one_another_are_refused(T):
+    L = T.lib()
+    d0, b0, x0, y0 = 0x100000000, 0x200000000, 0x300000000, 0x400000000
+    _, d = _cache(T, data=_at(d0), book=_at(b0))
+    c = ctypes.byref(d)
+    data_end, book_end = d0 + L.tf_kvcache_data_bytes(2, 2, 128, 16, 10), b0 + 4 * L.tf_kvcache_book_elems(10, 4, 8)
+
+    def rope(qkv, q):  # 3 rows of 4 + 2 * 2 heads, 2048 bytes each; q 1024 bytes a row
+        return L.tf_qk_norm_rope_run(_at(qkv), 1024, 3, 4, None, None, 0.0, FAKE, None, 0, 0, _at(q), c, 0, FAKE, FAKE, 256, 0, None)
+
+    def attn(o):
+        ws = L.tf_tree_attn_workspace_bytes(c, 4, 1, 3)
+        return L.tf_tree_attn_run(_at(x0), 512, 3, 4, c, 0, FAKE, FAKE, 1, 3, None, 0.1, _at(o), FAKE, ws, 0, None)
+
+    def extend(slots, pos, seqs=FAKE, qs=FAKE, masks=None):
+        return L.tf_kvcache_extend(c, seqs, qs, 2, 5, masks, slots, pos, FAKE, 1 << 20, None)
+
+    for a in (d0 - 3 * 2048 + 16, d0, data_end - 16, b0 - 3 * 2048 + 16, book_end // 16 * 16 - 16):
+        assert rope(a, y0) == T.TF_E_INVALID_ARG
+    for a in (d0 - 3 * 1024 + 16, d0, data_end - 16, b0 - 3 * 1024 + 16, book_end // 16 * 16 - 16):
+        assert rope(x0, a) == T.TF_E_INVALID_ARG
+        assert attn(a) == T.TF_E_INVALID_ARG
+    assert extend(_at(x0), _at(x0 + 16)) == T.TF_E_INVALID_ARG
+    for out in ((_at(x0), None), (_at(y0), _at(x0))):
+        assert extend(*out, seqs=_at(x0 + 16)) == T.TF_E_INVALID_ARG
+        assert extend(*out, qs=_at(x0 - 8)) == T.TF_E_INVALID_ARG
+        assert extend(*out, masks=_at(x0 - 32)) == T.TF_E_INVALID_ARG
+
+    def logp(v=x0, t=0x500000000, lp=0x600000000, en=0x700000000, ti=0x800000000, tl=0x900000000):
+        return L.tf_logprobs_rows(_at(v), 0, 100, 3, 90, _at(t), 2, 4, _at(lp), _at(en), _at(ti), _at(tl), FAKE, 1 << 20, None)
+
+    last = (2 * 100 + 90) * 2
+    for kw in (dict(lp=x0), dict(en=x0 + last - 4), dict(ti=x0 - 44), dict(tl=x0 + 100), dict(lp=0x500000000),
+               dict(en=0x500000000 + 20), dict(tl=0x800000000 + 44), dict(en=0x600000000 + 20), dict(ti=0x700000000)):
+        assert logp(**kw) == T.TF_E_INVALID_ARG, kw
+
+
+def test_decoder_step_over_a_cache_refuses(T):
+    L = T.lib()
+
+    def qw(N, K):
+        d = T.tf_qweight()
+        d.magic, d.version, d.bits, d.group, d.batch, d.N, d.K = 0x31515446, T.TF_PACK_VERSION, 4, 64, 1, N, K
+        d.code, d.global_scale, d.n_pad, d.tile_bytes, d.data = T.TF_CODE_AFFINE, 1.0, (N + 15) // 16 * 16, 576, 0x20000
+        d.matrix_bytes = d.n_pad // 16 * (K // 64) * d.tile_bytes
+        return d
+
+    D, F, n_q, n_kv, hd, V = 256, 256, 4, 2, 64, 500
+    layers = (T.tf_decoder_layer * 2)()
+    for l in layers:
+        l.qkv, l.o, l.gate, l.up, l.down = qw((n_q + 2 * n_kv) * hd, D), qw(D, n_q * hd), qw(F, D), qw(F, D), qw(D, F)
+        l.attn_norm = l.mlp_norm = FAKE.value
+    dec = T.tf_decoder_desc()
+    dec.n_layers, dec.d_model, dec.d_ff, dec.q_dim, dec.kv_dim, dec.vocab = 2, D, F, n_q * hd, n_kv * hd, V
+    dec.layers, dec.final_norm, dec.readout = ctypes.cast(layers, ctypes.POINTER(T.tf_decoder_layer)), FAKE.value, qw(V, D)
+
+    def attn(**kw):
+        a = dict(n_q=n_q, eps=1e-6, scale=0.1, rot_dim=64, turns=FAKE.value, layers=None, norms=(None, None))
+        a.update(kw)
+        arr = (T.tf_attn_layer * 2)()
+        arr[1].q_norm, arr[1].k_norm = a["norms"]
+        d = T.tf_attn_desc()
+        d.n_q, d.eps, d.scale, d.rot_dim, d.turns = a["n_q"], a["eps"], a["scale"], a["rot_dim"], a["turns"]
+        d.layers = ctypes.cast(arr, ctypes.POINTER(T.tf_attn_layer)) if a["layers"] is None else a["layers"]
+        return d
+
+    def cache(**kw):
+        return _cache(T, hd=hd, **kw)[1]
+
+    def need(a, c=None):
+        return L.tf_decode_step_attn_workspace_bytes(ctypes.byref(dec), ctypes.byref(cache() if c is None else c), ctypes.byref(a))
+
+    good = need(attn())
+    assert good > 0
+
+    def run(a=None, c=None, x=FAKE, M=2, seqs=FAKE, qs=FAKE, B=1, slots=FAKE, pos=FAKE, out=OUT, ws=FAKE, wsb=good):
+        return L.tf_decode_step_attn_run(ctypes.byref(dec), ctypes.byref(cache() if c is None else c),
+                                         ctypes.byref(attn() if a is None else a), x, M, seqs, qs, B, None, slots, pos, out, ws,
+                                         wsb, 0, None)
+
+    shape, arg = T.TF_E_UNSUPPORTED_SHAPE, T.TF_E_INVALID_ARG
+    nowhere = ctypes.POINTER(T.tf_attn_layer)()
+    for kw, rc in [(dict(n_q=2), shape), (dict(n_q=0), shape), (dict(rot_dim=24), shape), (dict(rot_dim=80), shape),
+                   (dict(rot_dim=-16), shape), (dict(turns=None), arg), (dict(turns=0x10004), arg), (dict(eps=-1.0), arg),
+                   (dict(eps=math.nan), arg), (dict(scale=math.inf), arg), (dict(norms=(0x10008, None)), arg),
+                   (dict(norms=(None, 0x10002)), arg), (dict(layers=nowhere), arg)]:
+        assert need(attn(**kw)) == 0, kw
+        assert run(attn(**kw)) == rc, kw
+    for kw, rc in [(dict(c=cache(n_kv=1)), shape), (dict(c=cache(layers=1)), shape), (dict(c=T.tf_kvcache()), arg), (dict(M=0), shape),
+                   (dict(M=9), shape), (dict(B=0), shape), (dict(B=3), shape), (dict(x=None), arg), (dict(x=ODD), arg),
+                   (dict(seqs=None), arg), (dict(qs=None), arg), (dict(slots=None), arg), (dict(pos=None), arg),
+                   (dict(out=None), arg), (dict(ws=None), arg), (dict(wsb=good - 1), T.TF_E_WORKSPACE_TOO_SMALL)]:
+        assert run(**kw) == rc, kw
