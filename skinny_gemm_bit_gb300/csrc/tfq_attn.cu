@@ -12,8 +12,8 @@ namespace {
 // Query rows of an item, and with them the kernel: up to 32 the warp MMAs, above the tensor-memory
 // MMAs (which need the output of two row groups in tensor memory: head_dim up to 128). Over 64
 // sequences of 8192 tokens, 8 key/value heads of 128, in us, warp and tensor-memory MMAs: 8 rows 320 and
-// 335, 32 rows 335 and 349, 40 rows (two items of the warps') 633 and 351. One sequence of 32,768: 8 rows
-// 32 and 36, 32 rows 39 and 36.5, 40 rows 64 and 39. (Items of 32 rows for 8: 335 and 36.)
+// 335, 32 rows 335 and 346, 40 rows (two items of the warps') 633 and 342. One sequence of 32,768: 8 rows
+// 32 and 36, 32 rows 39 and 36.5, 40 rows 64 and 38. (Items of 32 rows for 8: 335 and 36.)
 int attn_rows(int max_rows, int group, int head_dim)
 {
     const int r = max_rows * group;
@@ -30,8 +30,8 @@ int attn_rows(int max_rows, int group, int head_dim)
 // still be a tile a warp (one token over 4097: 12.0 us with 16, 13.4 with 24).
 int attn_over(int rows, int64_t items)
 {
-    if (rows > 32)  // 64-key tiles: 64-row trees 145.5 us, 148.5 with 20 or 40, 151.5 with 12
-        return 32;
+    if (rows > 32)  // 64-key tiles: 64-row trees over 16,001 tokens 131 us, 134 with 32, 135 with 8
+        return 20;
     return items > device_sms() ? 28 : 16;
 }
 

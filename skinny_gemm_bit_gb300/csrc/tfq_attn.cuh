@@ -241,11 +241,76 @@ __device__ __forceinline__ void part_written(const AttnParams& p, const SplitIte
     asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p.counters + 2 * s.c0), "r"(1u) : "memory");
 }
 
+__device__ __forceinline__ const float* part_of(const AttnParams& p, const SplitItem& s, int c, int floats)
+{
+    return p.parts + (int64_t)(c == s.c0 ? 2 * c + 1 : 2 * c) * floats;
+}
+
+// A slice of more items (four columns of a row) than there are threads: i0 .. i1 of few parts. A thread's items
+// are all of one row, so it forms the parts' weights once, and what it will add comes by asynchronous
+// copies of its own into `buf`, all under way at once: loaded into registers item by item, 2 or 3 parts of
+// 256 rows took a CTA 8 us. buf: ROWS * HD * 4 bytes + 1024 for each part and thread, at most.
+template <int ROWS, int HD, int THREADS>
+__device__ __forceinline__ void join_many(const AttnParams& p, const SplitItem& s, int i0, int i1, uint8_t* buf)
+{
+    static_assert(THREADS % ROWS == 0, "a thread keeps its row");
+    constexpr int kFloats = ROWS * (HD + 2);
+    const int n = s.c1 - s.c0 + 1, items = i1 - i0, first = i0 + threadIdx.x, row = first % ROWS;
+    if (row >= s.rows)
+        return;
+    float4* data = reinterpret_cast<float4*>(buf) + threadIdx.x;                       // [n][items]
+    float* weight = reinterpret_cast<float*>(buf + (size_t)n * items * 16) + threadIdx.x;  // [n][THREADS]
+    for (int c = 0; c < n; ++c) {
+        const float* part = part_of(p, s, s.c0 + c, kFloats);
+        for (int i = threadIdx.x; i < items; i += THREADS)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(data + c * items + i - threadIdx.x)),
+                         "l"(part + (size_t)(i0 + i) * 4)
+                         : "memory");
+    }
+    float top = -INFINITY, l = 0.f;
+    for (int c0 = 0; c0 < n; c0 += 4) {
+        float2 ml[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c0 + i < n)
+                ml[i] = __ldcg(reinterpret_cast<const float2*>(part_of(p, s, s.c0 + c0 + i, kFloats) + ROWS * HD + 2 * row));
+        const float was = top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c0 + i < n)
+                top = fmaxf(top, ml[i].x);
+        const float ref = top == -INFINITY ? 0.f : top;
+        l *= attn_ex2(was - ref);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c0 + i < n) {
+                l = fmaf(attn_ex2(ml[i].x - ref), ml[i].y, l);
+                weight[(c0 + i) * THREADS] = ml[i].x;
+            }
+    }
+    const float ref = top == -INFINITY ? 0.f : top, inv = l == 0.f ? 0.f : 1.f / l;
+    for (int c = 0; c < n; ++c)
+        weight[c * THREADS] = attn_ex2(weight[c * THREADS] - ref);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    const int r = s.row0 + row;
+    uint16_t* o = p.o + ((int64_t)(s.q.r0 + p.token_of(r)) * p.n_q + s.h * p.group + p.head_of(r)) * HD;
+    for (int i = 0; i + (int)threadIdx.x < items; i += THREADS) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < n; ++c) {
+            const float w = weight[c * THREADS];
+            const float4 v = data[c * items + i];
+            a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
+        }
+        *reinterpret_cast<uint2*>(o + (first + i) / ROWS * 4) = bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+    }
+}
+
 // Waits for the item's parts and writes this CTA's slice of its output. THREADS threads, which
 // share named barrier 1; several lanes share four columns of a row and take every lp-th part, so
 // that all parts are asked for at once. The order in which they are added depends on the call alone.
+// buf: shared memory that nobody uses any more, as join_many wants it (ROWS >= 128).
 template <int ROWS, int HD, int THREADS>
-__device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem& s, volatile int* abort_flag)
+__device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem& s, volatile int* abort_flag, uint8_t* buf = nullptr)
 {
     constexpr int kFloats = ROWS * (HD + 2), kQuads = HD / 4;
     const int n = s.c1 - s.c0 + 1, me = blockIdx.x - s.c0;
@@ -267,11 +332,17 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
     // item: four columns of a row, whether the sequence has that row or not: no division by a length here
     constexpr unsigned kItems = ROWS * kQuads;
     const int i0 = (int)(kItems * (unsigned)me / (unsigned)n), i1 = (int)(kItems * (unsigned)(me + 1) / (unsigned)n);
+    bool done = false;
+    if constexpr (ROWS >= 128) {
+        done = i1 - i0 > THREADS;
+        if (done)
+            join_many<ROWS, HD, THREADS>(p, s, i0, i1, buf);
+    }
     int lp = 1;
     while (lp < 8 && (i1 - i0) * lp * 2 <= THREADS && lp < n)
         lp *= 2;
     const int sub = threadIdx.x % lp;
-    for (int at = i0; at < i1; at += THREADS / lp) {
+    for (int at = done ? i1 : i0; at < i1; at += THREADS / lp) {
         const int item = at + threadIdx.x / lp;
         const int quad = item / ROWS, row = item % ROWS, col = quad * 4;
         const bool in = item < i1 && row < s.rows;
@@ -284,7 +355,7 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
             for (int i = 0; i < 4; ++i)
                 if (c + i * lp <= s.c1) {
                     const int cc = c + i * lp;
-                    const float* part = p.parts + (int64_t)(cc == s.c0 ? 2 * cc + 1 : 2 * cc) * kFloats;
+                    const float* part = part_of(p, s, cc, kFloats);
                     ml[i] = __ldcg(reinterpret_cast<const float2*>(part + ROWS * HD + 2 * row));
                     v[i] = __ldcg(reinterpret_cast<const float4*>(part + (quad * ROWS + row) * 4));
                 }

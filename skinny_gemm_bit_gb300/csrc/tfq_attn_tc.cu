@@ -11,7 +11,7 @@
 //
 // Each group has two score buffers: the scores of its next tile are formed while it works on this
 // one's weights, so neither it nor the tensor cores wait for the other's latency. Trees of 64 rows
-// by 8 heads to each of 4 key/value heads of 128, over 8 x 16,001 tokens: 143 us, 937 TFLOP/s, against 206
+// by 8 heads to each of 4 key/value heads of 128, over 8 x 16,001 tokens: 131 us, 1030 TFLOP/s, against 206
 // with one buffer and 128-key tiles, where a group spent 2600 of 6600 cycles a tile waiting. What
 // is left is the softmax's own work and Q K^T at 64 keys, which reads 128 rows of queries from
 // shared memory for each 64 of keys (some 67 cycles a 128 x 64 x 16 step). Up to 128 query rows (PAIR false) both
@@ -50,13 +50,13 @@ struct TcCfg {
     static constexpr int ROWS = PAIR ? 256 : 128;
     static constexpr int kSlotBytes = KT * HD * 2;
     static constexpr int kQBytes = ROWS * HD * 2 < 32768 ? 32768 : ROWS * HD * 2;  // also the groups' exchange, 2 x 16 KB
-    static size_t q_off(int B) { return (kTcSched + schedule_bytes(B) + 1023) / 1024 * 1024; }
-    static int slots(int B)
+    static constexpr size_t q_off(int B) { return (kTcSched + schedule_bytes(B) + 1023) / 1024 * 1024; }
+    static constexpr int slots(int B)
     {
         const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes) / kSlotBytes;
         return n < kMaxSlots ? (int)n : kMaxSlots;
     }
-    static size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes; }
+    static constexpr size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes; }
 };
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -443,12 +443,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ok = __all_sync(0xffffffffu, attn_wait(&full[first_slot + pos % ring_slots], (pos / ring_slots) & 1, flags, p.status, p.limit_ns));
                     if (!ok)
                         break;
-                    const int tok = k0 + wt;
-                    if (wt < KT && tok >= q.base) {
-                        uint8_t* v = ring + (size_t)(first_slot + pos % ring_slots) * C::kSlotBytes + wt * 128;
+                    const int tok = k0 + wt % KT;
+                    if (tok >= q.base) {
+                        // two threads a row; each starts at a piece of its own, for the banks' sake
+                        uint8_t* v = ring + (size_t)(first_slot + pos % ring_slots) * C::kSlotBytes + wt % KT * 128;
                         bool bad = false;
-                        for (int c = 0; c < HD / 8; ++c) {
-                            uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + (c & 7) * 16);
+#pragma unroll 4
+                        for (int c = wt / KT * (HD / 16); c < (wt / KT + 1) * (HD / 16); ++c) {
+                            uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + ((c + wt) & 7) * 16);
                             uint32_t x[4];
                             *reinterpret_cast<uint4*>(x) = *at;
                             for (int j = 0; j < 4; ++j) {
@@ -643,7 +645,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < 2; ++i)
             if (split[i].c0 <= split[i].c1)
-                join_slice<ROWS, HD, kSoftThreads>(p, split[i], flags);
+                join_slice<ROWS, HD, kSoftThreads>(p, split[i], flags, qbuf);
     }
     tc_fence_before();
     __syncthreads();
@@ -654,9 +656,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 template <int HD, bool PAIR>
+constexpr int kPartBytes = TcCfg<HD, PAIR>::ROWS * HD * 4;  // of a part's output
+
+template <int HD, bool PAIR>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
 {
     using C = TcCfg<HD, PAIR>;
+    // join_many: fewer parts than ROWS * HD / 4 / kSoftThreads + 1, and a slice's rounding for each
+    static_assert(C::kQBytes + C::slots(kMaxAttnSeqs) * C::kSlotBytes >= kPartBytes<HD, PAIR> + (kPartBytes<HD, PAIR> / 16 / kSoftThreads + 1) * (kSoftThreads * 4 + 16),
+                  "the queries' and the ring's memory takes a slice of the parts");
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(tree_attn_tc_kernel<HD, PAIR>, 227 * 1024, done);
     if (e != cudaSuccess)
