@@ -10,8 +10,8 @@
 // a head (8 at 128, so a warp takes 4 heads at once), the sum of squares is a butterfly over
 // those lanes, and the eight angles a lane needs are made once a row and used for all its heads.
 //
-// 8191 such rows: 25.6 us, 5.2 TB/s of reads and writes (each row's loads run one set of heads ahead of the
-// arithmetic); 8 rows: 2.1 us, of which a launch is most.
+// 8191 such rows: 24.7 us, 5.4 TB/s of reads and writes (each row's loads run one set of heads ahead of the
+// arithmetic); 8 rows: 2.2 us, of which a launch is most.
 #include <cmath>
 
 #include "tfq_cache.h"
@@ -53,8 +53,10 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 }
 
 // LANES lanes take a head (head_dim / 16); a warp takes HEADS = 32 / LANES heads at once.
+// Seven blocks an SM: 72 registers a thread hold everything (8191 rows 24.7 us); with eight some are
+// spilled (26.5), with six the loads in flight are fewer (27.1).
 template <int LANES>
-__global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(kRopeThreads, 7) qk_norm_rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int HD = LANES * 16, HEADS = 32 / LANES;
     const int lane = threadIdx.x & 31, j = lane % LANES, sub = lane / LANES;
@@ -120,53 +122,55 @@ __global__ void __launch_bounds__(kRopeThreads, 8) qk_norm_rope_kernel(const __g
         const bool is_q = h < p.n_q, is_k = !is_q && h < p.n_q + n_kv;
         const uint4* gamma = reinterpret_cast<const uint4*>(is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr);
         const bool norm = gamma != nullptr;
-        float x[8], y[8];
-        unpack8(a, x);
-        unpack8(b, y);
-        float ss = 0.f;
+        if (h0 < p.n_q + n_kv) {  // else the warp has values alone
+            float x[8], y[8];
+            unpack8(a, x);
+            unpack8(b, y);
+            float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+            for (int i = 0; i < 8; ++i)
+                ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
 #pragma unroll
-        for (int o = LANES / 2; o > 0; o >>= 1)
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (norm) {
-            const float r = rsqrtf(ss * (1.f / HD) + p.eps);
-            float g0[8], g1[8];
-            unpack8(__ldg(gamma + c0), g0);
-            unpack8(__ldg(gamma + c1), g1);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[i] = x[i] * r * g0[i];
-                y[i] = y[i] * r * g1[i];
-            }
-        }
-        if (rot && (is_q || is_k)) {
-            if (p.interleaved) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float u = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
-                    x[2 * i + 1] = x[2 * i + 1] * cs[i] + x[2 * i] * sn[i];
-                    x[2 * i] = u;
-                    const float w = y[2 * i] * cs[4 + i] - y[2 * i + 1] * sn[4 + i];
-                    y[2 * i + 1] = y[2 * i + 1] * cs[4 + i] + y[2 * i] * sn[4 + i];
-                    y[2 * i] = w;
-                }
-            } else {
+            for (int o = LANES / 2; o > 0; o >>= 1)
+                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (norm) {
+                const float r = rsqrtf(ss * (1.f / HD) + p.eps);
+                float g0[8], g1[8];
+                unpack8(__ldg(gamma + c0), g0);
+                unpack8(__ldg(gamma + c1), g1);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float u = x[i] * cs[i] - y[i] * sn[i];
-                    y[i] = y[i] * cs[i] + x[i] * sn[i];
-                    x[i] = u;
+                    x[i] = x[i] * r * g0[i];
+                    y[i] = y[i] * r * g1[i];
                 }
+            }
+            if (rot && (is_q || is_k)) {
+                if (p.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float u = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
+                        x[2 * i + 1] = x[2 * i + 1] * cs[i] + x[2 * i] * sn[i];
+                        x[2 * i] = u;
+                        const float w = y[2 * i] * cs[4 + i] - y[2 * i + 1] * sn[4 + i];
+                        y[2 * i + 1] = y[2 * i + 1] * cs[4 + i] + y[2 * i] * sn[4 + i];
+                        y[2 * i] = w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float u = x[i] * cs[i] - y[i] * sn[i];
+                        y[i] = y[i] * cs[i] + x[i] * sn[i];
+                        x[i] = u;
+                    }
+                }
+            }
+            if (norm || (rot && (is_q || is_k))) {
+                a = pack8(x);
+                b = pack8(y);
             }
         }
         if (!live)
             continue;
-        if (norm || (rot && (is_q || is_k))) {
-            a = pack8(x);
-            b = pack8(y);
-        }
         if (is_q) {
             uint4* o = reinterpret_cast<uint4*>(p.q + (m * p.n_q + h) * HD);
             o[c0] = a;
