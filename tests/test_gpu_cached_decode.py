@@ -574,6 +574,43 @@ def test_logprobs_sorted_rows(T):
     np.testing.assert_array_equal(idx.cpu().numpy(), R.logprobs(R.f64(v), np.zeros((3, 0), int), 32)[2])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,k", [(700, 1, 1), (1300, 40, 32), (700, 5001, 7), (613, 33000, 20), (650, 70000, 0)])
+def test_logprobs_of_many_rows(T, dtype, M, N, k):
+    """More rows than the GPU holds blocks at once, of every kind among them."""
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(dtype).min
+    g = torch.Generator(device="cuda").manual_seed(N + k)
+    v = (torch.randn((M, N + 9), generator=g, device="cuda") * 3).to(dtype)[:, 5:5 + N]
+    at = torch.arange(N, device="cuda")
+    for i, rows in enumerate([v[j::50] for j in range(9)]):
+        if i == 0:
+            rows[:] = 1.5
+        elif i == 1:
+            rows[:] = -inf
+        elif i in (2, 3):
+            rows[:, at % 7 != 3] = -inf if i == 2 else low
+        elif i == 4:
+            rows[:, N // 2] = nan
+        elif i == 5:
+            rows[:, N - 1] = inf
+        elif i == 6:
+            rows[:] = rows.round()
+        elif i == 7:
+            rows[:] = (at * 1e-3).to(dtype)
+        else:
+            rows[:] = (at // 1024 % 2 * 5).to(dtype)  # many threads' largest in one batch, or none
+    t = torch.randint(-1, N, (M, 2), generator=g, device="cuda").int()
+    ws = T.workspace(T.tf_logprobs_workspace_bytes(M, N, k))
+    lp, ent, idx, tlp = T.tf_logprobs_rows(v, t, k, ws=ws)
+    assert T.tf_workspace_status(ws) == T.TF_OK
+    ref = R.logprobs(R.f64(v), t.cpu().numpy(), k)
+    lp_close(lp, ref[0], 1.0)
+    lp_close(ent, ref[1], 1.0)
+    if k:
+        np.testing.assert_array_equal(idx.cpu().numpy(), ref[2])
+        lp_close(tlp, ref[3], 1.0)
+
+
 def test_logprobs_agrees_with_argmax_and_repeats_in_a_graph(T):
     v = rand((8, 151936), 5, 3.0)
     t = i32(list(range(8)))
