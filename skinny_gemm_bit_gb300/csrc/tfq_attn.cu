@@ -150,7 +150,9 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     p.total_rows = (int)p.c.row_of(p.c.n_layers, 0, 0, 0);
     p.limit_ns = kDefaultWaitLimitNs;
     const int rows = attn_rows(max_rows, p.group, p.c.head_dim);
-    p.over = attn_over(rows, B * p.c.n_kv * ((max_rows * p.group + rows - 1) / rows));
+    const int64_t items = B * p.c.n_kv * ((max_rows * p.group + rows - 1) / rows);
+    p.over = attn_over(rows, items);
+    p.few = items <= device_sms() && B <= 256;
     const AttnLayout L = attn_layout(p.c.head_dim, rows);
     p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + L.counters);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);

@@ -33,6 +33,7 @@ struct AttnParams {
     const int32_t *seqs, *q_start;
     int B, max_rows;
     int over;  // a segment's own cost, in key tiles
+    bool few;  // no more items than CTAs, and no more sequences than threads
     const uint64_t* masks;
     float scale_log2;  // scale * log2(e)
     uint16_t* o;
@@ -77,7 +78,7 @@ struct SeqEntry {
     int r0, base;   // as in SeqRows
     int slot_rows;  // slot | rows << 16
 };
-constexpr size_t schedule_bytes(int B) { return (size_t)(B + 1) * sizeof(SeqEntry); }
+constexpr size_t schedule_bytes(int B) { return (size_t)(B + 8) * sizeof(SeqEntry); }  // the last 7: build() uses them
 
 struct Segment {
     SeqRows q;       // item: sequence, key/value head, row tile
@@ -90,27 +91,87 @@ struct Segment {
 // An item counts p.over units before its key tiles: what a segment costs apart from them (its
 // queries, joining the warps' parts, the hand-over), so that CTAs with many short items get no more
 // than their share. A CTA has kLeast units or more, so that a short item is not torn apart.
-template <int ROWS, int KEYS, int kLeast>
+//
+// Joining an item's parts costs what kJoin key tiles do (0: not looked at), and more the more CTAs have parts
+// of two. If there are no more items than CTAs, and the longest has no more tiles than an even share and
+// that, each has a CTA: their units are then one number, whatever the lengths, so that shares and items
+// coincide.
+template <int ROWS, int KEYS, int kLeast, int kJoin>
 struct Shares {
     SeqEntry* seq;  // [B + 1]
     const AttnParams& p;
-    int64_t total, ctas;  // units; CTAs that have some: every one of them has at least one
+    unsigned total, ctas;  // units; CTAs that have some: every one of them has at least one
+    unsigned share, rest;  // total = ctas * share + rest
+    int whole;             // units of an item when each has a CTA, else 0
+    static constexpr int kTorn = 64;  // tiles that an item more costs a split call, over all CTAs
 
-    __device__ Shares(const AttnParams& params, void* smem) : seq(static_cast<SeqEntry*>(smem)), p(params), total(0), ctas(0) {}
+    __device__ Shares(const AttnParams& params, void* smem)
+        : seq(static_cast<SeqEntry*>(smem)), p(params), total(0), ctas(0), share(0), rest(0), whole(0)
+    {
+    }
 
     __device__ __forceinline__ int row_tiles(int rows) const { return (rows * p.group + ROWS - 1) / ROWS; }
     __device__ __forceinline__ int key_tiles(int len) const { return (int)(((int64_t)len + KEYS - 1) / KEYS); }
 
+    __device__ __forceinline__ int units_of(int nt) const { return whole ? whole : nt + p.over; }
+
+    template <class Enter, class Items, class Units>
+    __device__ __forceinline__ void sum_up(const SeqRows& first, Enter& enter, Items& items_of, Units& all_units)
+    {
+        if (kJoin > 0 && p.few) {  // a sequence a thread
+            int tiles = 0, items = 0;
+            if (first.base >= 0 && first.rows > 0) {
+                tiles = min(key_tiles(first.len()), 1 << 20);
+                items = items_of(first);
+            }
+            int2* found = reinterpret_cast<int2*>(seq + p.B + 1);  // of each warp: most tiles, their sum and kTorn an item
+            const int most = __reduce_max_sync(0xffffffffu, tiles), sum = __reduce_add_sync(0xffffffffu, (tiles + kTorn) * items);
+            if (threadIdx.x % 32 == 0)
+                found[threadIdx.x / 32] = make_int2(most, sum);
+            __syncthreads();
+            int2 all = make_int2(0, 0);
+            for (int w = 0; w * 32 < p.B; ++w) {
+                all.x = max(all.x, found[w].x);
+                all.y += found[w].y;
+            }
+            if ((int64_t)(all.x - kJoin) * gridDim.x <= all.y)
+                whole = all.x + 1;
+        }
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            const SeqRows q = b < (int)blockDim.x ? first : seq_rows(p, b);
+            enter(b, q, q.base >= 0 ? all_units(q) : 0);
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            unsigned sum = 0;  // sums stop at INT32_MAX, as do their terms
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int b = b0 + threadIdx.x;
+                unsigned x = b < p.B ? seq[b].first : 0;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+                    if ((int)threadIdx.x >= o)
+                        x = min(x + y, (unsigned)INT32_MAX);
+                }
+                const unsigned before = __shfl_up_sync(0xffffffffu, x, 1);
+                if (b < p.B)
+                    seq[b].first = (int)min(threadIdx.x > 0 ? sum + before : sum, (unsigned)INT32_MAX);
+                sum = min(sum + __shfl_sync(0xffffffffu, x, 31), (unsigned)INT32_MAX);
+            }
+            if (threadIdx.x == 0)
+                seq[p.B].first = (int)sum;
+        }
+        __syncthreads();
+        total = seq[p.B].first;
+    }
+
     // All threads of the CTA (a multiple of 32); has barriers.
     __device__ void build()
     {
-        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
-            const SeqRows q = seq_rows(p, b);
+        auto enter = [&](int b, const SeqRows& q, int units) {
             SeqEntry e{0, q.r0, q.base, 0};
             if (q.base >= 0) {
                 e.slot_rows = q.slot | q.rows << 16;
-                const int64_t n = (int64_t)p.c.n_kv * row_tiles(q.rows) * (key_tiles(q.len()) + p.over);
-                e.first = n < INT32_MAX ? (int)n : INT32_MAX;
+                e.first = units;
             } else if (blockIdx.x == b % gridDim.x) {
                 // arguments that do not hold: zero rows, here and there among the CTAs
                 record_status(p.status, TF_E_INVALID_ARG);
@@ -120,39 +181,43 @@ struct Shares {
                     o[i] = make_uint4(0, 0, 0, 0);
             }
             seq[b] = e;
-        }
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            int64_t sum = 0;
-            for (int b0 = 0; b0 < p.B; b0 += 32) {
-                const int b = b0 + threadIdx.x;
-                const int64_t n = b < p.B ? seq[b].first : 0;
-                int64_t x = n;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-                    if ((int)threadIdx.x >= o)
-                        x += y;
-                }
-                if (b < p.B)
-                    seq[b].first = (int)min(sum + x - n, (int64_t)INT32_MAX);
-                sum += __shfl_sync(0xffffffffu, x, 31);
+        };
+        auto items_of = [&](const SeqRows& q) { return p.c.n_kv * row_tiles(q.rows); };
+        auto all_units = [&](const SeqRows& q) {
+            return (int)min((int64_t)items_of(q) * units_of(key_tiles(q.len())), (int64_t)INT32_MAX);
+        };
+        SeqRows first{0, 0, 0, -1};
+        if ((int)threadIdx.x < p.B || p.B == 1)
+            first = seq_rows(p, p.B == 1 ? 0 : threadIdx.x);
+        if (p.B == 1) {  // nothing to be summed up: every thread has the answer
+            if (first.base >= 0) {
+                const int tiles = key_tiles(first.len());
+                if (kJoin > 0 && p.few && (int64_t)(tiles - kJoin) * gridDim.x <= (int64_t)(tiles + kTorn) * items_of(first))
+                    whole = tiles + 1;
+                total = all_units(first);
             }
             if (threadIdx.x == 0)
-                seq[p.B].first = (int)min(sum, (int64_t)INT32_MAX);
+                enter(0, first, 0);
+            __syncthreads();
+        } else {
+            sum_up(first, enter, items_of, all_units);
         }
-        __syncthreads();
-        total = seq[p.B].first;
         if (total == INT32_MAX) {  // more than the units' 31 bits: nothing is done
             if (blockIdx.x == 0 && threadIdx.x == 0)
                 record_status(p.status, TF_E_UNSUPPORTED_SHAPE);
             total = 0;
         }
-        ctas = min((total + kLeast - 1) / kLeast, (int64_t)gridDim.x);
+        ctas = whole ? total / whole : min((total + kLeast - 1) / kLeast, gridDim.x);
+        if (ctas > 0) {
+            share = total / ctas;
+            rest = total - share * ctas;
+        }
     }
 
-    __device__ __forceinline__ int start_of(int cta) const { return cta >= ctas ? (int)total : (int)(total * cta / ctas); }
+    // total * cta / ctas, in 32 bits
+    __device__ __forceinline__ int start_of(unsigned cta) const { return (int)(cta >= ctas ? total : share * cta + rest * cta / ctas); }
     // the CTA that takes unit u
-    __device__ __forceinline__ int cta_of(int u) const { return (int)(((u + 1) * ctas - 1) / total); }
+    __device__ __forceinline__ int cta_of(int u) const { return (int)((((uint64_t)u + 1) * ctas - 1) / total); }
 
     __device__ __forceinline__ Segment segment(int u, int end) const
     {
@@ -168,14 +233,14 @@ struct Shares {
         Segment g;
         g.q = SeqRows{e.slot_rows & 0xFFFF, e.r0, e.slot_rows >> 16, e.base};
         g.nt = key_tiles(g.q.len());
-        const int rt = row_tiles(g.q.rows), per = g.nt + p.over;
+        const int rt = row_tiles(g.q.rows), per = units_of(g.nt), over = per - g.nt;
         const int local = u - e.first, item = local / per, off = local - item * per;
         g.h = item / rt;
         g.rt = item - g.h * rt;
         g.units = min(end - u, per - off);
-        g.t0 = max(off - p.over, 0);
-        g.t1 = max(off + g.units - p.over, 0);
-        g.first = u - off + p.over;
+        g.t0 = max(off - over, 0);
+        g.t1 = max(off + g.units - over, 0);
+        g.first = u - off + over;
         return g;
     }
 };

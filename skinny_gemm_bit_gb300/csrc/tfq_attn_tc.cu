@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    Shares<ROWS, KT, 1> shares(p, smem + kTcSched);
+    Shares<ROWS, KT, 1, 0> shares(p, smem + kTcSched);
     tc_fence_before();
     shares.build();  // its barriers publish the tensor-memory address as well
     __syncthreads();

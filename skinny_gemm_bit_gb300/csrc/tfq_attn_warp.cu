@@ -105,21 +105,24 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     }
     pdl_wait();
-    Shares<ROWS, KT, kWarps> shares(p, smem + C::kSchedOff);
+    // 8 key/value heads of 128, in us, an item a CTA against split and joined: one row over 200 tokens 7.6, 10.8;
+    // over 500 10.2, 11.0, but in a decoder step, its code not in the caches, 28 layers 787, 769; eight
+    // sequences of eight rows over 500 tokens 11.3, 14.7, over 1000 13.9, 18.7, over 3000 27.5, 26.0
+    Shares<ROWS, KT, kWarps, RW == 2 ? 8 : 10> shares(p, smem + C::kSchedOff);
     shares.build();
     pdl_launch_dependents();
     const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
 
     // ---- the warp's loads, in the order it will read them: K, V of its first tile, of its next ...
-    const int box = min(p.c.page_size, KT), boxes = KT / box;
-    const int ahead = 32 / boxes;  // tiles whose pages the lanes hold at once
+    const int box = min(p.c.page_size, KT), bs = KT / box - 1;  // a tile is 1 << bs boxes, one or two
+    const int ahead = 32 >> bs;  // tiles whose pages the lanes hold at once
     int lu = u0;                   // first unit of the segment that the next load belongs to
     Segment lg{};                  // that segment
     int lt = 0, lkv = 0;           // the next load: tile, K or V
-    int lpages = -1, lj = 0;       // the lane's page (tile lane / boxes of those, box lane % boxes); which of them is next
+    int lpages = -1, lj = 0;       // the lane's page (tile lane >> bs of those, box lane & bs); which of them is next
     uint32_t issued = 0, taken = 0;
     auto look = [&]() {
-        const int t = lt + kWarps * (lane / boxes), row = t * KT + lane % boxes * box;
+        const int t = lt + kWarps * (lane >> bs), row = t * KT + (lane & bs) * box;
         lpages = t < lg.t1 && row < lg.q.len() ? p.c.table[(int64_t)lg.q.slot * p.c.max_pages + (row >> p.c.page_shift)] : -1;
         lj = 0;
     };
@@ -139,11 +142,11 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         if (lu >= u1)
             return;
         const uint32_t slot = issued % NS;
-        const int page = __shfl_sync(0xffffffffu, lpages, (lj * boxes + lane) & 31);
+        const int page = __shfl_sync(0xffffffffu, lpages, ((lj << bs) + lane) & 31);
         if (lane == 0)
             mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
         __syncwarp();
-        if (lane < boxes) {
+        if (lane <= bs) {
             const int row = lt * KT + lane * box;
             int y = p.total_rows;  // zeros
             if (row < lg.q.len()) {
@@ -164,8 +167,27 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             settle();
         }
     };
+    // an item's rows of q: a thread's pieces, on their way while the first tiles are asked for
+    constexpr int kPieces = ROWS * (HD / 8), kMine = (kPieces + kCtaThreads - 1) / kCtaThreads;
+    uint4 mine[kMine];
+    auto fetch = [&](const Segment& s) {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int piece = threadIdx.x + i * kCtaThreads, row = s.rt * ROWS + piece / (HD / 8);
+            mine[i] = make_uint4(0, 0, 0, 0);
+            if (piece < kPieces && row < s.q.rows * p.group)
+                mine[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + (s.q.r0 + p.token_of(row)) * p.ldq +
+                                                                (int64_t)(s.h * p.group + p.head_of(row)) * HD + piece % (HD / 8) * 8));
+        }
+    };
+    Segment g{};
     if (u0 < u1) {
-        settle();  // from the empty segment
+        g = lg = shares.segment(u0, u1);
+        fetch(g);
+        lt = lg.t0 + warp;
+        lj = ahead;
+        settle();
+#pragma unroll 1
         for (int i = 0; i < NS; ++i)
             load();
     }
@@ -179,20 +201,21 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     split[0].c1 = split[1].c1 = 0;
     bool alive = true;
     for (int u = u0; u < u1;) {
-        const Segment g = shares.segment(u, u1);
+        if (u != u0) {
+            g = shares.segment(u, u1);
+            fetch(g);
+        }
         u += g.units;
         if (g.t0 == g.t1)
             continue;
         const SeqRows& q = g.q;
         const int len = q.len(), n_rows = q.rows * p.group;
         // the item's rows of q, swizzled as the tiles are
-        for (int i = threadIdx.x; i < ROWS * (HD / 8); i += kCtaThreads) {
-            const int r = i / (HD / 8), c = i % (HD / 8), row = g.rt * ROWS + r;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < n_rows)
-                v = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + p.token_of(row)) * p.ldq +
-                                                          (int64_t)(g.h * p.group + p.head_of(row)) * HD + c * 8));
-            *reinterpret_cast<uint4*>(qbuf + (c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int piece = threadIdx.x + i * kCtaThreads, r = piece / (HD / 8), c = piece % (HD / 8);
+            if (piece < kPieces)
+                *reinterpret_cast<uint4*>(qbuf + (c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = mine[i];
         }
         // the masks of the lane's rows
         uint64_t mask[RW][2];
@@ -454,33 +477,51 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         uint16_t* out = p.o + ((int64_t)(q.r0 + p.token_of(row)) * p.n_q + g.h * p.group + p.head_of(row)) * HD;
         if (sums && !whole && sc == 0 && row < n_rows)
             __stcg(reinterpret_cast<float2*>(part + ROWS * HD + 2 * sr), make_float2(top, all));
+        auto finish = [&](int c0, const float* from) {
+            if (!sums || row >= n_rows)
+                return;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(from + (k * ROWS + sr) * C::kStride + sc);
+                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+            }
+            if (whole)
+                *reinterpret_cast<uint2*>(out + c0 + sc) = bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+            else
+                __stcg(reinterpret_cast<float4*>(part + ((c0 + sc) / 4 * ROWS + sr) * 4), a);
+        };
+        // behind the CTA's last tile the rings are free and take all columns at once: one barrier in the place
+        // of two of each kCols
+        const bool last = u >= u1;
+        constexpr int kRound = kWarps * ROWS * C::kStride;  // floats
+        static_assert(HD / C::kCols * kRound * 4 <= kWarps * NS * C::kSlotBytes, "all columns in the rings");
+        float* rings = reinterpret_cast<float*>(smem + C::ring(p.B));
 #pragma unroll
         for (int c0 = 0; c0 < HD; c0 += C::kCols) {
-            if (c0 > 0)
+            if (c0 > 0 && !last)
                 named_bar_sync(1, kCtaThreads);  // the last columns have been read
+            float* round = last ? rings + c0 / C::kCols * kRound : outbuf;
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
-                float* mine = outbuf + (warp * ROWS + r * 16 + gi) * C::kStride + ti * 2;
+                float* to = round + (warp * ROWS + r * 16 + gi) * C::kStride + ti * 2;
 #pragma unroll
                 for (int i = 0; i < C::kCols / 8; ++i) {
                     const float* v = o[r][c0 / 8 + i];
-                    *reinterpret_cast<float2*>(mine + i * 8) = make_float2(v[0] * f[r][0], v[1] * f[r][0]);
-                    *reinterpret_cast<float2*>(mine + 8 * C::kStride + i * 8) = make_float2(v[2] * f[r][1], v[3] * f[r][1]);
+                    *reinterpret_cast<float2*>(to + i * 8) = make_float2(v[0] * f[r][0], v[1] * f[r][0]);
+                    *reinterpret_cast<float2*>(to + 8 * C::kStride + i * 8) = make_float2(v[2] * f[r][1], v[3] * f[r][1]);
                 }
             }
+            if (!last) {
+                named_bar_sync(1, kCtaThreads);
+                finish(c0, round);
+            }
+        }
+        if (last) {
             named_bar_sync(1, kCtaThreads);
-            if (sums && row < n_rows) {
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int k = 0; k < kWarps; ++k) {
-                    const float4 v = *reinterpret_cast<const float4*>(outbuf + (k * ROWS + sr) * C::kStride + sc);
-                    a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
-                }
-                if (whole)
-                    *reinterpret_cast<uint2*>(out + c0 + sc) = bf16x4(make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
-                else
-                    __stcg(reinterpret_cast<float4*>(part + ((c0 + sc) / 4 * ROWS + sr) * 4), a);
-            }
+#pragma unroll 2
+            for (int c0 = 0; c0 < HD; c0 += C::kCols)
+                finish(c0, rings + c0 / C::kCols * kRound);
         }
         if (threadIdx.x == 0)
             flags[2] = flags[0];
