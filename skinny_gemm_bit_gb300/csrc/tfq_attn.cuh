@@ -7,7 +7,7 @@
 // few rows over a long context still use the whole GPU. A CTA that holds all of an item writes
 // its output; otherwise each writes its part (running maximum, sum and unscaled output) to the
 // workspace, and once all of an item's parts are there each of its CTAs joins a slice of the
-// output, parts in key order: 8 rows over 32,771 tokens, some 19 parts to an item, take 32.1 us so and
+// output, parts in key order: 8 rows over 32,771 tokens, some 19 parts to an item, take 32 us so and
 // 35.6 when the last CTA to arrive joins them all. CTAs wait for one another at their very end only, when all their parts are
 // written; the launch is cooperative, so all of them run. The lengths are read on the device: a
 // captured call follows them.

@@ -10,7 +10,7 @@
 // a head (8 at 128, so a warp takes 4 heads at once), the sum of squares is a butterfly over
 // those lanes, and the eight angles a lane needs are made once a row and used for all its heads.
 //
-// 8191 such rows: 24.7 us, 5.4 TB/s of reads and writes (each row's loads run one set of heads ahead of the
+// 8191 such rows: 24.8 us, 5.4 TB/s of reads and writes (each row's loads run one set of heads ahead of the
 // arithmetic); 8 rows: 2.2 us, of which a launch is most.
 #include <cmath>
 
