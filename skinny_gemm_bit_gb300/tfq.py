@@ -744,7 +744,9 @@ class Attention:
     (bf16 [head_dim] device tensors or None), the rotation, and the head norms' epsilon."""
 
     def __init__(self, norms, n_q: int, head_dim: int, rope: RopeTable, eps: float = 1e-6, scale=None):
-        self.norms, self.rope, self.n_q = norms, rope, n_q
+        self.norms, self.rope, self.n_q, self.head_dim = norms, rope, n_q, head_dim
+        for t in (t for pair in norms for t in pair if t is not None):
+            _want(t, torch.bfloat16, rope.turns.get_device(), head_dim, "a head norm")
         arr = (tf_attn_layer * max(1, len(norms)))()
         for i, (q, k) in enumerate(norms):
             arr[i].q_norm = None if q is None else q.data_ptr()
@@ -770,6 +772,9 @@ def tf_decode_step_attn_run(dec: Decoder, cache: KVCache, attn: Attention, x: to
     M, B = x.shape[0], seqs.numel()
     if len(attn.norms) < dec.desc.n_layers:
         raise ValueError(f"norms of {len(attn.norms)} layers for a decoder of {dec.desc.n_layers}")
+    if attn.head_dim != cache.head_dim or attn.rope.turns.get_device() != at:
+        raise ValueError(f"attention of heads of {attn.head_dim} on {attn.rope.turns.device} for a cache of heads of "
+                         f"{cache.head_dim} on {dev}")
     if out is None or ws is None:
         with _on(stream):
             out = torch.empty((M, dec.readout.N), dtype=torch.bfloat16, device=dev) if out is None else out

@@ -248,3 +248,13 @@ def test_decoder_step_over_a_cache_refuses(T):
                    (dict(seqs=None), arg), (dict(qs=None), arg), (dict(slots=None), arg), (dict(pos=None), arg),
                    (dict(out=None), arg), (dict(ws=None), arg), (dict(wsb=good - 1), T.TF_E_WORKSPACE_TOO_SMALL)]:
         assert run(**kw) == rc, kw
+
+
+def test_the_attention_description_refuses_norms_that_do_not_fit(T):
+    import torch
+    rope = T.RopeTable([1.0, 0.5] * 16, device="cpu")
+    good = torch.ones(64, dtype=torch.bfloat16)
+    T.Attention([(good, None), (None, good)], 2, 64, rope)
+    for bad in (good.float(), good[:32], torch.ones(128, dtype=torch.bfloat16)[::2]):
+        with pytest.raises(ValueError):
+            T.Attention([(good, good), (None, bad)], 2, 64, rope)

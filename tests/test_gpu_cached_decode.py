@@ -185,6 +185,35 @@ def test_tree_attn_long(T, n, rows):
     check_attn(T, c, 1, [0, 1, 2], [rows, 1, min(rows, 700)], None, 4, 5)
 
 
+@pytest.mark.parametrize("lens,rows,n_q,hd", [
+    ([250], 1, 2, 128), ([320], 3, 2, 128), ([380], 8, 8, 128), ([450], 1, 4, 64), ([160], 5, 1, 256), ([330], 2, 2, 256),
+    ([800, 30, 2000], 2, 4, 128), ([1500] * 30, 1, 2, 64), ([10] * 70 + [1200], 4, 2, 128),
+])
+def test_tree_attn_around_the_length_where_items_are_split(T, lens, rows, n_q, hd):
+    """Few short items have a CTA each, longer or uneven ones are split and joined."""
+    c = filled_cache(T, lens, 2, hd, 16, 31 + sum(lens))
+    check_attn(T, c, 1, list(range(len(lens))), [rows] * len(lens), None, 2 * n_q, 8)
+
+
+def test_two_attention_calls_at_once(T):
+    """Two streams, each with a workspace of its own and kernels that wait for their own parts."""
+    c = filled_cache(T, [9001, 2500], 4, 128, 32, 77)
+    q = [rand((8, 8 * 128), 1, 2.0), rand((40, 16 * 128), 2, 2.0)]
+    args = [(i32([0]), i32([0, 8])), (i32([1]), i32([0, 40]))]
+    ws = [T.workspace(T.tf_tree_attn_workspace_bytes(c, n, 1, r)) for n, r in ((8, 8), (16, 40))]
+    want = [T.tf_tree_attn_run(q[i], c, 0, *args[i], max_rows=(8, 40)[i], ws=ws[i]) for i in (0, 1)]
+    out = [[torch.empty_like(x) for _ in range(12)] for x in want]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for n in range(12):
+        for i in (0, 1):
+            T.tf_tree_attn_run(q[i], c, 0, *args[i], max_rows=(8, 40)[i], out=out[i][n], ws=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert T.tf_workspace_status(ws[i]) == T.TF_OK
+        assert all(torch.equal(o, want[i]) for o in out[i])
+
+
 def test_tree_attn_many_sequences(T):
     rng = np.random.default_rng(3)
     lens = rng.integers(1, 200, 150).tolist()

@@ -185,5 +185,10 @@ def test_the_step_refuses_what_does_not_fit(T):
         T.tf_decode_step_attn_run(m.dec, c, m.attn, x, s, st, slots, pos, ws=T.workspace(256))
     with pytest.raises(ValueError):
         T.tf_decode_step_attn_run(m.dec, c, T.Attention([(None, None)], 4, 64, m.rope), x, s, st, slots, pos)
+    with pytest.raises(ValueError):  # described for other heads, or elsewhere
+        T.tf_decode_step_attn_run(m.dec, c, T.Attention([(None, None)] * 2, 4, 128, m.rope), x, s, st, slots, pos)
+    with pytest.raises(ValueError):
+        T.tf_decode_step_attn_run(m.dec, c, T.Attention([(None, None)] * 2, 4, 64, T.RopeTable([1.0], device="cpu")), x, s, st, slots,
+                                  pos)
     with pytest.raises(ValueError):
         T.tf_decode_step_attn_run(m.dec, c, m.attn, x, s, st, slots[:1], pos)
