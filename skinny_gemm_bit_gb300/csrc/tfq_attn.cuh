@@ -245,6 +245,18 @@ struct Shares {
     }
 };
 
+// A row's mask of the block of `rows` tokens, bits behind them taken out.
+__device__ __forceinline__ uint64_t block_mask(const AttnParams& p, const SeqRows& q, int t)
+{
+    return p.masks == nullptr ? ~0ull >> (63 - t) : p.masks[q.r0 + t] & (~0ull >> (64 - q.rows));
+}
+
+// What a row sees of a tile that begins at token d of its block (d > -64: before it), from bit 0.
+__device__ __forceinline__ uint64_t tile_mask(uint64_t mask, int d)
+{
+    return d >= 0 ? (d < 64 ? mask >> d : 0ull) : mask << -d | ((1ull << -d) - 1);
+}
+
 // 2^x: scores are scaled by log2(e), so that a weight is one instruction
 __device__ __forceinline__ float attn_ex2(float x)
 {

@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint64_t mask = 0;
             if (valid) {
                 const int t = p.token_of(row);
-                mask = p.masks == nullptr ? ~0ull >> (63 - t) : p.masks[q.r0 + t];
+                mask = block_mask(p, q, t);
             }
             float m = -INFINITY, l = 0.f;  // the reference, in score units, and the sum against it
             bool had = false, ok = true;
@@ -477,12 +477,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc_wait_ld(s);
                         tc_wait_ld(s + 32);
                         if (edge) {
+                            const uint64_t see = tile_mask(mask, k0 - q.base);
 #pragma unroll
-                            for (int c = 0; c < KT; ++c) {
-                                const int tok = k0 + c, j = tok - q.base;
-                                const bool see = j < 0 || (tok < len && (mask >> (j & 63) & 1));
-                                s[c] = see ? s[c] : 0xFF800000u;  // -inf
-                            }
+                            for (int c = 0; c < KT; ++c)
+                                s[c] = see >> c & 1 ? s[c] : 0xFF800000u;  // -inf
                         }
                     };
                     auto largest = [&]() {

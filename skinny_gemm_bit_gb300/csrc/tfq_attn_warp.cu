@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2 * RW; ++i) {
             const int row = g.rt * ROWS + (i >> 1) * 16 + (i & 1) * 8 + gi, t = p.token_of(row);
-            mask[i >> 1][i & 1] = row >= n_rows ? 0 : p.masks == nullptr ? ~0ull >> (63 - t) : p.masks[q.r0 + t];
+            mask[i >> 1][i & 1] = row >= n_rows ? 0 : block_mask(p, q, t);
         }
         named_bar_sync(1, kCtaThreads);
         const uint32_t q_at = smem_u32(qbuf);
@@ -294,12 +294,11 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                 if (edge) {
                     see[r][0] = see[r][1] = 0u;
 #pragma unroll
-                    for (int i = 0; i < 4 * CH; ++i) {
-                        const int tok = k0 + (i >> 1) * 8 + ti * 2 + (i & 1), j = tok - q.base;
-                        const bool ctx = j < 0, in = tok < len;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t of = (uint32_t)tile_mask(mask[r][h], k0 - q.base) >> (ti * 2);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (ctx || (in && (mask[r][h] >> (j & 63) & 1)))
+                        for (int i = 0; i < 4 * CH; ++i) {
+                            if (of >> ((i >> 1) * 8 + (i & 1)) & 1)
                                 see[r][h] |= 1u << i;
                             else
                                 s[r][i >> 1][2 * h + (i & 1)] = -INFINITY;
