@@ -10,10 +10,10 @@ namespace tfq {
 namespace {
 
 // Query rows of an item, and with them the kernel: up to 32 the warp MMAs, above the tensor-memory
-// MMAs (which need the output of two row groups in tensor memory: head_dim up to 128). Over 64
-// sequences of 8192 tokens, 8 key/value heads of 128, in us, warp and tensor-memory MMAs: 8 rows 320 and
-// 335, 32 rows 335 and 346, 40 rows (two items of the warps') 633 and 342. One sequence of 32,768: 8 rows
-// 32 and 36, 32 rows 39 and 36.5, 40 rows 64 and 38. (Items of 32 rows for 8: 335 and 36.)
+// MMAs (which need the output of two row groups in tensor memory: head_dim up to 128). 8 key/value
+// heads of 128, in us, warp and tensor-memory MMAs: 32 rows over 64 x 8192 tokens in pages of 16 329 and
+// 417, over one sequence of 32,768 35 and 41, over 8 x 4096 43 and 49; 8 rows over 4097 11.6 and 18.9; 40 rows
+// (two items of the warps') over 64 x 8192 633 and 342, over 32,768 64 and 38.
 int attn_rows(int max_rows, int group, int head_dim)
 {
     const int r = max_rows * group;
@@ -30,7 +30,7 @@ int attn_rows(int max_rows, int group, int head_dim)
 // still be a tile a warp (one token over 4097: 12.0 us with 16, 13.4 with 24).
 int attn_over(int rows, int64_t items)
 {
-    if (rows > 32)  // 64-key tiles: 64-row trees over 16,001 tokens 131 us, 134 with 32, 135 with 8
+    if (rows > 32)  // 64-key tiles: 64-row trees over 16,001 tokens 131 us, 134 with 32, 135 with 8, side by side
         return 20;
     return items > device_sms() ? 28 : 16;
 }

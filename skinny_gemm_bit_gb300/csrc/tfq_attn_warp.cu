@@ -12,7 +12,7 @@
 // 64 ragged sequences of up to 8190 tokens, 16 query and 8 key/value heads of 128: 176 us, 6.1 TB/s of
 // K and V; 64 of 8192 tokens 320 us, 6.7 TB/s. A ring shared by the warps, filled by a producer warp, kept a
 // tile 1700 cycles from its release and took 242 us. Few tokens are bound by the chain of latencies
-// (queries, tiles, the warps' join, the CTAs' join): one token over 4097 takes 11.3 us, 8 over 32,771 31.9.
+// (queries, tiles, the warps' join, the CTAs' join): one token over 4097 takes 10.6 us, 8 over 32,771 31.4.
 //
 // Tiles land with the 128-byte swizzle (16-byte piece c of row r at c ^ (r % 8)), so the eight
 // rows of an ldmatrix fall in different banks. A box is one page's rows of a tile.
@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map) : "memory");
     }
     pdl_wait();
-    // 8 key/value heads of 128, in us, an item a CTA against split and joined: one row over 200 tokens 7.6, 10.8;
-    // over 500 10.2, 11.0, but in a decoder step, its code not in the caches, 28 layers 787, 769; eight
+    // 8 key/value heads of 128, in us, an item a CTA against split and joined: one row over 200 tokens 7.1, 10.2;
+    // over 500 9.7, 10.5, but in a decoder step, its code not in the caches, 28 layers 787, 769; eight
     // sequences of eight rows over 500 tokens 11.3, 14.7, over 1000 13.9, 18.7, over 3000 27.5, 26.0
     Shares<ROWS, KT, kWarps, RW == 2 ? 8 : 10> shares(p, smem + C::kSchedOff);
     shares.build();
