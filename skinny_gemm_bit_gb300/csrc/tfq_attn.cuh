@@ -51,7 +51,7 @@ struct AttnParams {
 // Sequence b of the call: its rows and tokens, or why it has none.
 struct SeqRows {
     int slot, r0, rows, base;  // rows r0 .. r0 + rows of q; tokens base .. base + rows of the slot
-    __device__ __forceinline__ int len() const { return base + rows; }
+    __host__ __device__ __forceinline__ int len() const { return base + rows; }
 };
 
 // base < 0: the sequence's arguments do not hold. rows is 0 where the rows themselves do not.
@@ -95,7 +95,7 @@ struct Segment {
 // Joining an item's parts costs what kJoin key tiles do (0: not looked at), and more the more CTAs have parts
 // of two. If there are no more items than CTAs, and the longest has no more tiles than an even share and
 // that, each has a CTA: their units are then one number, whatever the lengths, so that shares and items
-// coincide.
+// coincide. A sequence of kMostTiles or more is always split: counts stop there, so that they fit 32 bits.
 template <int ROWS, int KEYS, int kLeast, int kJoin>
 struct Shares {
     SeqEntry* seq;  // [B + 1]
@@ -104,28 +104,55 @@ struct Shares {
     unsigned share, rest;  // total = ctas * share + rest
     int whole;             // units of an item when each has a CTA, else 0
     static constexpr int kTorn = 64;  // tiles that an item more costs a split call, over all CTAs
+    static constexpr int kMostTiles = 1 << 20;
 
-    __device__ Shares(const AttnParams& params, void* smem)
+    __host__ __device__ Shares(const AttnParams& params, void* smem)
         : seq(static_cast<SeqEntry*>(smem)), p(params), total(0), ctas(0), share(0), rest(0), whole(0)
     {
     }
 
-    __device__ __forceinline__ int row_tiles(int rows) const { return (rows * p.group + ROWS - 1) / ROWS; }
-    __device__ __forceinline__ int key_tiles(int len) const { return (int)(((int64_t)len + KEYS - 1) / KEYS); }
+    __host__ __device__ __forceinline__ int row_tiles(int rows) const { return (rows * p.group + ROWS - 1) / ROWS; }
+    __host__ __device__ __forceinline__ int key_tiles(int len) const { return (int)(((int64_t)len + KEYS - 1) / KEYS); }
 
-    __device__ __forceinline__ int units_of(int nt) const { return whole ? whole : nt + p.over; }
+    __host__ __device__ __forceinline__ int units_of(int nt) const { return whole ? whole : nt + p.over; }
 
-    template <class Enter, class Items, class Units>
-    __device__ __forceinline__ void sum_up(const SeqRows& first, Enter& enter, Items& items_of, Units& all_units)
+    __host__ __device__ __forceinline__ int items_of(const SeqRows& q) const { return p.c.n_kv * row_tiles(q.rows); }
+    __host__ __device__ __forceinline__ int all_units(const SeqRows& q) const
+    {
+        const int64_t n = (int64_t)items_of(q) * units_of(key_tiles(q.len()));
+        return n < INT32_MAX ? (int)n : INT32_MAX;
+    }
+
+    // What a sequence adds to the choice of `whole`: its tiles, and over its items their sum and kTorn each
+    // (at most one item a CTA in all, so 32 bits).
+    __host__ __device__ __forceinline__ int2 counted(const SeqRows& q) const
+    {
+        const int nt = key_tiles(q.len()), tiles = nt < kMostTiles ? nt : kMostTiles;
+        return q.base < 0 || q.rows == 0 ? make_int2(0, 0) : make_int2(tiles, (tiles + kTorn) * items_of(q));
+    }
+    __host__ __device__ __forceinline__ int whole_of(int most, int sum, unsigned grid) const
+    {
+        return most < kMostTiles && (int64_t)(most - kJoin) * grid <= sum ? most + 1 : 0;
+    }
+
+    // The CTAs' shares of `total` units.
+    __host__ __device__ __forceinline__ void deal(unsigned grid)
+    {
+        const unsigned least = (total + kLeast - 1) / kLeast;
+        ctas = whole ? total / whole : least < grid ? least : grid;
+        if (ctas > 0) {
+            share = total / ctas;
+            rest = total - share * ctas;
+        }
+    }
+
+    template <class Enter>
+    __device__ __forceinline__ void sum_up(const SeqRows& first, Enter& enter)
     {
         if (kJoin > 0 && p.few) {  // a sequence a thread
-            int tiles = 0, items = 0;
-            if (first.base >= 0 && first.rows > 0) {
-                tiles = min(key_tiles(first.len()), 1 << 20);
-                items = items_of(first);
-            }
-            int2* found = reinterpret_cast<int2*>(seq + p.B + 1);  // of each warp: most tiles, their sum and kTorn an item
-            const int most = __reduce_max_sync(0xffffffffu, tiles), sum = __reduce_add_sync(0xffffffffu, (tiles + kTorn) * items);
+            const int2 mine = counted(first);
+            int2* found = reinterpret_cast<int2*>(seq + p.B + 1);  // of each warp
+            const int most = __reduce_max_sync(0xffffffffu, mine.x), sum = __reduce_add_sync(0xffffffffu, mine.y);
             if (threadIdx.x % 32 == 0)
                 found[threadIdx.x / 32] = make_int2(most, sum);
             __syncthreads();
@@ -134,8 +161,7 @@ struct Shares {
                 all.x = max(all.x, found[w].x);
                 all.y += found[w].y;
             }
-            if ((int64_t)(all.x - kJoin) * gridDim.x <= all.y)
-                whole = all.x + 1;
+            whole = whole_of(all.x, all.y, gridDim.x);
         }
         for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
             const SeqRows q = b < (int)blockDim.x ? first : seq_rows(p, b);
@@ -182,44 +208,36 @@ struct Shares {
             }
             seq[b] = e;
         };
-        auto items_of = [&](const SeqRows& q) { return p.c.n_kv * row_tiles(q.rows); };
-        auto all_units = [&](const SeqRows& q) {
-            return (int)min((int64_t)items_of(q) * units_of(key_tiles(q.len())), (int64_t)INT32_MAX);
-        };
         SeqRows first{0, 0, 0, -1};
         if ((int)threadIdx.x < p.B || p.B == 1)
             first = seq_rows(p, p.B == 1 ? 0 : threadIdx.x);
         if (p.B == 1) {  // nothing to be summed up: every thread has the answer
             if (first.base >= 0) {
-                const int tiles = key_tiles(first.len());
-                if (kJoin > 0 && p.few && (int64_t)(tiles - kJoin) * gridDim.x <= (int64_t)(tiles + kTorn) * items_of(first))
-                    whole = tiles + 1;
+                const int2 mine = counted(first);
+                if (kJoin > 0 && p.few && mine.y > 0)
+                    whole = whole_of(mine.x, mine.y, gridDim.x);
                 total = all_units(first);
             }
             if (threadIdx.x == 0)
                 enter(0, first, 0);
             __syncthreads();
         } else {
-            sum_up(first, enter, items_of, all_units);
+            sum_up(first, enter);
         }
         if (total == INT32_MAX) {  // more than the units' 31 bits: nothing is done
             if (blockIdx.x == 0 && threadIdx.x == 0)
                 record_status(p.status, TF_E_UNSUPPORTED_SHAPE);
             total = 0;
         }
-        ctas = whole ? total / whole : min((total + kLeast - 1) / kLeast, gridDim.x);
-        if (ctas > 0) {
-            share = total / ctas;
-            rest = total - share * ctas;
-        }
+        deal(gridDim.x);
     }
 
     // total * cta / ctas, in 32 bits
-    __device__ __forceinline__ int start_of(unsigned cta) const { return (int)(cta >= ctas ? total : share * cta + rest * cta / ctas); }
+    __host__ __device__ __forceinline__ int start_of(unsigned cta) const { return (int)(cta >= ctas ? total : share * cta + rest * cta / ctas); }
     // the CTA that takes unit u
-    __device__ __forceinline__ int cta_of(int u) const { return (int)((((uint64_t)u + 1) * ctas - 1) / total); }
+    __host__ __device__ __forceinline__ int cta_of(int u) const { return (int)((((uint64_t)u + 1) * ctas - 1) / total); }
 
-    __device__ __forceinline__ Segment segment(int u, int end) const
+    __host__ __device__ __forceinline__ Segment segment(int u, int end) const
     {
         int lo = 0, hi = p.B - 1;  // the last sequence whose first unit is not behind u
         while (lo < hi) {
