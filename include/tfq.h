@@ -616,6 +616,7 @@ typedef struct tf_attn_desc {
     float eps;                    /* of the head norms */
     float scale;                  /* of the scores */
     int32_t rot_dim, interleaved; /* as for tf_qk_norm_rope_run */
+    int32_t max_rows;             /* most rows of one sequence, 0..8, as for tf_tree_attn_run; 0: the step's M */
     const uint64_t* turns;        /* device uint64 [rot_dim / 2] (tf_rope_turns) */
     const tf_attn_layer* layers;  /* HOST array [n_layers] */
 } tf_attn_desc;
@@ -630,7 +631,9 @@ typedef struct tf_attn_desc {
  * positions are that call's (device). The cache's layers are used from 0; it has at least
  * d->n_layers, n_kv * head_dim = d->kv_dim, and M (1..8) rows belong to B sequences.
  * After a verify step tf_kvcache_keep keeps what was accepted. The results are those of the
- * separate calls, bit for bit. ws: tf_decode_step_attn_workspace_bytes(d, c, a) bytes, zeroed
+ * separate calls, bit for bit, with tf_tree_attn_run's max_rows = min(a->max_rows, M) (M where it is 0).
+ * It chooses the attention's kernel: several sequences of a row or two each want it set (eight of one row
+ * with 8 query heads to a key/value head (16 and 2), over 200 tokens, 28 layers: 744 us, 943 where it is 0). ws: tf_decode_step_attn_workspace_bytes(d, c, a) bytes, zeroed
  * once, for this call alone; device-side errors of all its parts are in its status word.
  */
 size_t tf_decode_step_attn_workspace_bytes(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a);

@@ -1285,6 +1285,8 @@ int check_attn_step(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn
         return fail(TF_E_INVALID_ARG, "%s: turns NULL or misaligned", name);
     if (!(a->eps >= 0.f) || !std::isfinite(a->scale))
         return fail(TF_E_INVALID_ARG, "%s: eps must be >= 0 and scale finite", name);
+    if (a->max_rows < 0 || a->max_rows > kMaxM)
+        return fail(TF_E_UNSUPPORTED_SHAPE, "%s: max_rows must be within [0, %d]", name, kMaxM);
     for (int l = 0; l < d->n_layers; ++l)
         if (!aligned(a->layers[l].q_norm, 16) || !aligned(a->layers[l].k_norm, 16))
             return fail(TF_E_INVALID_ARG, "%s: layer %d head norms misaligned", name, l);
@@ -1295,7 +1297,7 @@ AttnStepLayout attn_step_layout(const tf_decoder_desc* d, const tf_kvcache* c, c
 {
     AttnStepLayout L{};
     L.step = step_layout(d, kMaxM);
-    L.attn = align_up(tf_tree_attn_workspace_bytes(c, a->n_q, kMaxM, kMaxM), 256);
+    L.attn = align_up(tf_tree_attn_workspace_bytes(c, a->n_q, kMaxM, kMaxM), 256);  // enough for fewer rows too
     L.q = L.attn;
     L.o = L.q + align_up((size_t)kMaxM * d->q_dim * sizeof(uint16_t), 256);
     L.base = L.o + align_up((size_t)kMaxM * d->q_dim * sizeof(uint16_t), 256);
@@ -1345,6 +1347,7 @@ int tf_decode_step_attn_run(const tf_decoder_desc* d, const tf_kvcache* c, const
     hp[0] = reinterpret_cast<uint16_t*>(align_up(reinterpret_cast<uintptr_t>(up + L.step.a_e), 256));
     hp[1] = reinterpret_cast<uint16_t*>(align_up(reinterpret_cast<uintptr_t>(hp[0] + L.step.h_e), 256));
     bool pdl = (flags & TF_RUN_PDL) != 0;
+    const int max_rows = a->max_rows > 0 && a->max_rows < M ? a->max_rows : (int)M;
     const uint16_t* h = x;
     for (int l = 0; l < d->n_layers; ++l) {
         const tf_decoder_layer& Ly = d->layers[l];
@@ -1355,7 +1358,7 @@ int tf_decode_step_attn_run(const tf_decoder_desc* d, const tf_kvcache* c, const
         if ((rc = tf_qk_norm_rope_run(qkv, QKV, M, a->n_q, a->layers[l].q_norm, a->layers[l].k_norm, a->eps, positions,
                                       a->turns, a->rot_dim, a->interleaved, qn, c, l, slots, ws, 256, TF_RUN_PDL, stream)))
             return rc;
-        if ((rc = tf_tree_attn_run(qn, Q, M, a->n_q, c, l, seqs, q_start, B, (int)M, masks, a->scale, ao, ws, L.attn, 0, stream)))
+        if ((rc = tf_tree_attn_run(qn, Q, M, a->n_q, c, l, seqs, q_start, B, max_rows, masks, a->scale, ao, ws, L.attn, 0, stream)))
             return rc;
         if ((rc = qlinear_impl(&Ly.o, nullptr, ao, Q, M, nullptr, 0.f, h, h1, D, TF_DTYPE_BF16, ws, red, red_bytes, pdl, s,
                                "tf_decode_step_attn_run: o")))

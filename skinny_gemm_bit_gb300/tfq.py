@@ -77,7 +77,7 @@ class tf_attn_layer(ctypes.Structure):
 
 class tf_attn_desc(ctypes.Structure):
     _fields_ = [("n_q", I32), ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("rot_dim", I32), ("interleaved", I32),
-                ("turns", P), ("layers", ctypes.POINTER(tf_attn_layer))]
+                ("max_rows", I32), ("turns", P), ("layers", ctypes.POINTER(tf_attn_layer))]
 
 
 class TfqError(RuntimeError):
@@ -764,9 +764,10 @@ def tf_decode_step_attn_workspace_bytes(dec: Decoder, cache: KVCache, attn: Atte
 
 
 def tf_decode_step_attn_run(dec: Decoder, cache: KVCache, attn: Attention, x: torch.Tensor, seqs, q_start, slots,
-                            positions, masks=None, out=None, ws=None, flags: int = 0, stream=None) -> torch.Tensor:
+                            positions, masks=None, out=None, ws=None, flags: int = 0, stream=None, max_rows=None) -> torch.Tensor:
     """logits [M, vocab] bf16 of one decoder step with attention over the cache; seqs, q_start, masks, slots and
-    positions as tf_kvcache_extend took and gave them for the step's rows x [M, d_model]."""
+    positions as tf_kvcache_extend took and gave them for the step's rows x [M, d_model]. max_rows: the most rows of
+    one sequence (None: as in `attn`, M unless set there); steps of several short sequences are faster with it."""
     dev = cache.device
     at = _current(dev)
     M, B = x.shape[0], seqs.numel()
@@ -775,12 +776,16 @@ def tf_decode_step_attn_run(dec: Decoder, cache: KVCache, attn: Attention, x: to
     if attn.head_dim != cache.head_dim or attn.rope.turns.get_device() != at:
         raise ValueError(f"attention of heads of {attn.head_dim} on {attn.rope.turns.device} for a cache of heads of "
                          f"{cache.head_dim} on {dev}")
+    desc = attn.desc
+    if max_rows is not None:
+        desc = tf_attn_desc.from_buffer_copy(attn.desc)
+        desc.max_rows = max_rows
     if out is None or ws is None:
         with _on(stream):
             out = torch.empty((M, dec.readout.N), dtype=torch.bfloat16, device=dev) if out is None else out
             ws = workspace(tf_decode_step_attn_workspace_bytes(dec, cache, attn), dev) if ws is None else ws
     _check(lib().tf_decode_step_attn_run(
-        ctypes.byref(dec.desc), cache.ref, ctypes.byref(attn.desc),
+        ctypes.byref(dec.desc), cache.ref, ctypes.byref(desc),
         _want(x, torch.bfloat16, at, M * dec.desc.d_model, "x"), M, _want(seqs, torch.int32, at, 1, "seqs"),
         _want(q_start, torch.int32, at, B + 1, "q_start"), B,
         None if masks is None else _want(masks, torch.int64, at, M, "masks"), _want(slots, torch.int32, at, M, "slots"),

@@ -43,3 +43,47 @@ def test_refused_rows_do_not_hold_up_the_others(T, n_q, hd, good):
                               [(1 << (i + 1)) - 1 for i in range(good)], hd ** -0.5)
     within(R.f64(out[:good]).reshape(good, n_q, hd), ref, R.attn_tol(ref, spread))
     assert min(ms) < 10, ms
+
+
+# ---------------------------------------------------------------- decoder step over a cache
+
+@pytest.mark.parametrize("rows,n_q,n_kv,hd", [([1] * 8, 16, 2, 64), ([1] * 8, 8, 1, 128), ([2, 1, 2, 3], 12, 2, 64), ([4, 0, 4], 5, 1, 64)])
+def test_the_step_takes_the_longest_block_for_its_attention(T, rows, n_q, n_kv, hd):
+    """Several short blocks: bit for bit the separate calls that name the longest block, not the step's rows."""
+    from test_gpu_cached_step import Model
+    m = Model(T, seed=31 + n_q, n_layers=2, d_model=256, d_ff=384, n_q=n_q, n_kv=n_kv, hd=hd, vocab=500)
+    B, M, most = len(rows), sum(rows), max(rows)
+    caches = [m.cache(T, 16, 60, B, 9) for _ in range(2)]
+    seqs, start = i32(list(range(B))), i32(np.cumsum([0] + rows).tolist())
+    lens = [5 + 13 * b for b in range(B)]
+    kv = rand((sum(lens), 2 * n_kv * hd), 3)
+    x, got, ws = m.x[:M].contiguous(), [], None
+    for i, c in enumerate(caches):
+        at, _ = T.tf_kvcache_extend(c, seqs, i32(np.cumsum([0] + lens).tolist()), sum(lens))
+        for l in range(2):
+            c.data[l, 0, (at // 16).long(), :, (at % 16).long()] = kv[:, :n_kv * hd].view(-1, n_kv, hd)
+            c.data[l, 1, (at // 16).long(), :, (at % 16).long()] = kv[:, n_kv * hd:].view(-1, n_kv, hd)
+        slots, pos = T.tf_kvcache_extend(c, seqs, start, M)
+        if i == 0:
+            ws = T.workspace(T.tf_decode_step_attn_workspace_bytes(m.dec, c, m.attn))
+            got.append(T.tf_decode_step_attn_run(m.dec, c, m.attn, x, seqs, start, slots, pos, ws=ws, max_rows=most))
+            again = T.tf_decode_step_attn_run(m.dec, c, m.attn, x, seqs, start, slots, pos, ws=ws, max_rows=8 if M < 8 else None)
+            assert T.tf_workspace_status(ws) == T.TF_OK and again.shape == got[0].shape
+            T.tf_decode_step_attn_run(m.dec, c, m.attn, x, seqs, start, slots, pos, ws=ws, max_rows=most)
+            # a block longer than that is refused by the attention, and said so
+            if most > 1:
+                T.tf_decode_step_attn_run(m.dec, c, m.attn, x, seqs, start, slots, pos, ws=ws, max_rows=most - 1)
+                assert T.tf_workspace_status(ws) == T.TF_E_INVALID_ARG
+                T.tf_decode_step_attn_run(m.dec, c, m.attn, x, seqs, start, slots, pos, ws=ws, max_rows=most)
+            continue
+        h, a = x, m.attn
+        for l, L in enumerate(m.dec.layers):
+            qkv = T.tf_qlinear_run(L["qkv"], h, gamma=L["attn_norm"], eps=m.dec.desc.eps)
+            q = T.tf_qk_norm_rope_run(qkv, c, l, pos, slots, m.rope, q_gamma=a.norms[l][0], k_gamma=a.norms[l][1], eps=a.desc.eps)
+            o = T.tf_tree_attn_run(q, c, l, seqs, start, max_rows=most)
+            h1 = T.tf_qlinear_run(L["o"], o, residual=h)
+            h = T.tf_qlinear_run(L["down"], T.tf_qmlp_gateup_run(L["gate"], L["up"], h1, gamma=L["mlp_norm"], eps=m.dec.desc.eps),
+                                 residual=h1)
+        got.append(T.tf_qlinear_run(m.dec.readout, h, gamma=m.dec.final_norm, eps=m.dec.desc.eps))
+    assert torch.equal(got[0], got[1]) and bool(torch.isfinite(got[0]).all())
+    assert torch.equal(caches[0].data, caches[1].data)
