@@ -511,8 +511,10 @@ int tf_kvcache_extend(const tf_kvcache* c, const int32_t* seqs, const int32_t* q
  * Full pages are shared; of an unfilled last page one slot keeps the original (the parent
  * itself when it stays, else the lowest slot that takes it) and every other gets a fresh
  * page with the filled rows copied, in all layers. Pages that no slot names any more are
- * free after the call; they are not used by the same call. Errors are all or nothing as above
- * (TF_E_CACHE_FULL, or TF_E_INVALID_ARG for a parent or a table entry out of range).
+ * free after the call; they are not used by the same call. Errors are all or nothing as above:
+ * TF_E_CACHE_FULL, or TF_E_INVALID_ARG for a parent out of range, a length beyond max_pages, or a table
+ * entry out of range among the pages of a slot that another one takes. (A slot with such an entry can
+ * still be emptied.)
  */
 int tf_kvcache_fork(const tf_kvcache* c, const int32_t* parent, void* ws, size_t ws_bytes, void* stream);
 
@@ -632,9 +634,10 @@ typedef struct tf_attn_desc {
  * d->n_layers, n_kv * head_dim = d->kv_dim, and M (1..8) rows belong to B sequences.
  * After a verify step tf_kvcache_keep keeps what was accepted. The results are those of the
  * separate calls, bit for bit, with tf_tree_attn_run's max_rows = min(a->max_rows, M) (M where it is 0).
- * It chooses the attention's kernel: several sequences of a row or two each want it set (eight of one row
- * with 8 query heads to a key/value head (16 and 2), over 200 tokens, 28 layers: 744 us, 943 where it is 0). ws: tf_decode_step_attn_workspace_bytes(d, c, a) bytes, zeroed
- * once, for this call alone; device-side errors of all its parts are in its status word.
+ * It chooses the attention's kernel: several sequences of a row or two each want it set (eight of one row,
+ * 16 query and 2 key/value heads of 128, over 200 tokens, 28 layers: 744 us, and 943 where it is 0).
+ * ws: tf_decode_step_attn_workspace_bytes(d, c, a) bytes, zeroed once, for this call alone;
+ * device-side errors of all its parts are in its status word.
  */
 size_t tf_decode_step_attn_workspace_bytes(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a);
 int tf_decode_step_attn_run(const tf_decoder_desc* d, const tf_kvcache* c, const tf_attn_desc* a, const uint16_t* x,

@@ -45,6 +45,47 @@ def test_refused_rows_do_not_hold_up_the_others(T, n_q, hd, good):
     assert min(ms) < 10, ms
 
 
+# ---------------------------------------------------------------- page operations
+
+@pytest.mark.parametrize("entry", [-1, -7, 99, "n_pages", 2 ** 31 - 1])
+@pytest.mark.parametrize("col,parent", [
+    (0, [0, 0, 0, 3]),    # a full page of a slot that stays and is taken
+    (1, [0, 0, 2, 3]),
+    (2, [0, 0, 2, 3]),    # its unfilled page, which is copied
+    (2, [-1, 0, 2, 3]),   # its unfilled page, which the taker keeps
+    (1, [3, 2, 0, 3]),    # a full page that changes hands
+])
+def test_a_fork_over_an_entry_that_is_no_page_does_nothing(T, entry, col, parent):
+    c = filled_cache(T, [40, 33, 5, 7], 1, 64, 16, 94, spare=4)
+    c.table[0, col] = c.n_pages if entry == "n_pages" else entry
+    ws = T.workspace(T.tf_kvcache_workspace_bytes(c))
+    book, data = c.book.clone(), c.data.clone()
+    T.tf_kvcache_fork(c, i32(parent), ws=ws)
+    assert T.tf_workspace_status(ws) == T.TF_E_INVALID_ARG
+    assert torch.equal(c.book, book) and torch.equal(c.data, data)
+    # nobody takes it: the others may be forked, and the slot emptied
+    T.tf_kvcache_fork(c, i32([0, 1, 1, 3]), ws=ws)
+    assert T.tf_workspace_status(ws) == T.TF_OK and c.len.tolist() == [40, 33, 33, 7]
+    T.tf_kvcache_fork(c, i32([-1, 1, 2, 3]), ws=ws)
+    assert T.tf_workspace_status(ws) == T.TF_OK and c.len.tolist() == [0, 33, 33, 7] and (c.table[0] == -1).all()
+
+
+def test_a_fork_of_many_slots_finds_the_one_entry_that_is_no_page(T):
+    c = filled_cache(T, [16 * (1 + s % 90) + s % 16 for s in range(1024)], 1, 64, 16, 95, layers=1, spare=2000)
+    ws = T.workspace(T.tf_kvcache_workspace_bytes(c))
+    rng = np.random.default_rng(1)
+    parent = i32([s if s == 700 else int(rng.integers(1024)) for s in range(1023)] + [700])
+    book = c.book.clone()
+    for col in (0, 33, 69, 70):
+        c.table[700, col] = c.n_pages + 5
+        T.tf_kvcache_fork(c, parent, ws=ws)
+        assert T.tf_workspace_status(ws) == T.TF_E_INVALID_ARG
+        c.table[700, col] = book[1024 + c.n_pages + 700 * c.max_pages + col]
+        assert torch.equal(c.book, book)
+    T.tf_kvcache_fork(c, parent, ws=ws)
+    assert T.tf_workspace_status(ws) == T.TF_OK
+
+
 # ---------------------------------------------------------------- decoder step over a cache
 
 @pytest.mark.parametrize("rows,n_q,n_kv,hd", [([1] * 8, 16, 2, 64), ([1] * 8, 8, 1, 128), ([2, 1, 2, 3], 12, 2, 64), ([4, 0, 4], 5, 1, 64)])
