@@ -8,10 +8,11 @@
 // heads of 128 moves 16 KB), for about six multiply-adds. A lane holds two 16-byte chunks of
 // one head, chosen so that both ends of each rotated pair are its own: head_dim / 16 lanes take
 // a head (8 at 128, so a warp takes 4 heads at once), the sum of squares is a butterfly over
-// those lanes, and the eight angles a lane needs are made once a row and used for all its heads.
+// those lanes, and the eight angles a lane needs are made once a row, by the warp's lanes together, and used
+// for all its heads.
 //
-// 8191 such rows: 24.8 us, 5.4 TB/s of reads and writes (each row's loads run one set of heads ahead of the
-// arithmetic); 8 rows: 2.2 us, of which a launch is most.
+// 8191 such rows: 24.0 us, 5.6 TB/s of reads and writes (each row's loads run one set of heads ahead of the
+// arithmetic); 8 rows: 2.3 us, of which a launch is most.
 #include <cmath>
 
 #include "tfq_cache.h"
@@ -53,12 +54,12 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 }
 
 // LANES lanes take a head (head_dim / 16); a warp takes HEADS = 32 / LANES heads at once.
-// Seven blocks an SM: 72 registers a thread hold everything (8191 rows 24.7 us); with eight some are
-// spilled (26.5), with six the loads in flight are fewer (27.1).
+// Seven blocks an SM: 72 registers a thread hold everything (8191 rows 24.0 us). With every lane making its eight
+// angles itself: 24.7 with seven, 26.5 with eight (spills), 27.1 with six (fewer loads in flight).
 template <int LANES>
 __global__ void __launch_bounds__(kRopeThreads, 7) qk_norm_rope_kernel(const __grid_constant__ RopeParams p)
 {
-    constexpr int HD = LANES * 16, HEADS = 32 / LANES;
+    constexpr int HD = LANES * 16, HEADS = 32 / LANES, OWN = 8 / HEADS;
     const int lane = threadIdx.x & 31, j = lane % LANES, sub = lane / LANES;
     const unsigned wid = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
     const int64_t m = wid / (unsigned)p.parts;
@@ -68,13 +69,14 @@ __global__ void __launch_bounds__(kRopeThreads, 7) qk_norm_rope_kernel(const __g
     const bool rot = j < p.rot16;
     const int c0 = rot ? j : 2 * (j - p.rot16) + 2 * p.rot16;
     const int c1 = rot ? j + p.rot16 : c0 + 1;
-    // what the previous kernel did not write: gammas and frequencies (two registers a frequency)
-    uint2 f[8];
+    // what the previous kernel did not write: gammas and frequencies (two registers a frequency). The lanes
+    // of the warp's heads need the same eight angles: each makes OWN of them
+    uint2 f[OWN];
     if (rot) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int idx = p.interleaved ? (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4) : j * 8 + i;
-            f[i] = __ldg(reinterpret_cast<const uint2*>(p.turns + idx));
+        for (int k = 0; k < OWN; ++k) {
+            const int i = sub * OWN + k, idx = p.interleaved ? (i < 4 ? c0 * 4 + i : c1 * 4 + i - 4) : j * 8 + i;
+            f[k] = __ldg(reinterpret_cast<const uint2*>(p.turns + idx));
         }
     }
     pdl_wait();
@@ -93,19 +95,28 @@ __global__ void __launch_bounds__(kRopeThreads, 7) qk_norm_rope_kernel(const __g
     };
     fetch(part * HEADS);
     const int32_t slot = p.slots[m];
-    // angle = position * turns modulo one turn, from the top 32 bits of the 64-bit product:
-    // exact but for 2^-32 turn, then sine and cosine of an argument within [-pi, pi] by the
-    // fast functions, whose absolute error there (2^-21) is far under a bf16 step of the result
+    // angle = position * turns modulo one turn, exact in 64 bits, then as a signed fraction in fp32 whose
+    // relative error is 2^-23 however small it is. Its sine and cosine keep that: slow pairs turn by 1e-6
+    // a token, where the fast functions' absolute error of 2^-21 is half of the sine (9 % off at one token).
+    // A lane's share of them and sixteen shuffles take no longer than eight fast ones: 8191 rows 24.3 -> 24.0 us;
+    // all eight by every lane 25.7.
     float cs[8], sn[8];
-    if (rot) {
-        const uint32_t pos = (uint32_t)p.positions[m];
-        const uint32_t neg = (int32_t)pos < 0 ? 0xFFFFFFFFu : 0u;  // the sign of the 64-bit position
+    {
+        float mine_c[OWN] = {}, mine_s[OWN] = {};
+        if (rot) {
+            const uint32_t pos = (uint32_t)p.positions[m];
+            const uint32_t neg = (int32_t)pos < 0 ? 0xFFFFFFFFu : 0u;  // the sign of the 64-bit position
+#pragma unroll
+            for (int k = 0; k < OWN; ++k) {
+                // (sign-extended position) * turns modulo 2^64
+                const uint32_t hi = __umulhi(pos, f[k].x) + pos * f[k].y + neg * f[k].x, lo = pos * f[k].x;
+                sincospif(fmaf((float)lo, 0x1p-32f, (float)(int32_t)hi) * 0x1p-31f, &mine_s[k], &mine_c[k]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            // high word of (sign-extended position) * turns modulo 2^64
-            const uint32_t hi = __umulhi(pos, f[i].x) + pos * f[i].y + neg * f[i].x;
-            const float a = (float)(int32_t)hi * 1.4629180792671596e-9f;  // 2 pi / 2^32
-            __sincosf(a, &sn[i], &cs[i]);
+            sn[i] = __shfl_sync(0xffffffffu, mine_s[i % OWN], i / OWN * LANES + j);
+            cs[i] = __shfl_sync(0xffffffffu, mine_c[i % OWN], i / OWN * LANES + j);
         }
     }
     const bool bad = slot >= 0 && slot >= (int64_t)p.c.n_pages * p.c.page_size;

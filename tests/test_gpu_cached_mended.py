@@ -45,6 +45,31 @@ def test_refused_rows_do_not_hold_up_the_others(T, n_q, hd, good):
     assert min(ms) < 10, ms
 
 
+# ---------------------------------------------------------------- norm + rotation
+
+@pytest.mark.parametrize("hd,pairs", [(64, False), (128, False), (128, True), (256, True)])
+def test_small_angles_keep_their_digits(T, hd, pairs):
+    """Pairs (1, 0) become (cos, sin): the sine of a slow pair's small angle within a rounding of itself, not of
+    the pair's length. The fraction of a turn is within 2^-23 of itself (two conversions, a sum: half a step
+    each, rounded up), the sine within 2 steps of 2^-23; a sine's relative error is at most that of its small angle."""
+    M, n = 40, hd // 2
+    inv = 1e6 ** (-np.arange(n) / n)
+    first = slice(0, hd, 2) if pairs else slice(0, n)
+    second = slice(1, hd, 2) if pairs else slice(n, hd)
+    x = torch.zeros((M, 3, hd), device="cuda", dtype=torch.bfloat16)
+    x[:, 0, first] = 1
+    c = T.KVCache.create(1, 1, hd, 16, 4, 1, 4)
+    pos = np.concatenate([np.arange(-20, 0), np.arange(1, 21)])
+    q = T.tf_qk_norm_rope_run(x.view(M, -1), c, 0, i32(pos.tolist()), i32([-1] * M), T.RopeTable(inv, pairs=pairs), n_q=1)
+    angle = pos[:, None] * inv[None]
+    small = np.abs(angle) < 0.5
+    assert small.any(0).sum() > n // 2
+    ref = np.sin(angle)
+    err = np.abs(R.f64(q)[:, second] - ref)
+    tol = (2.0 ** -8 + 2.0 ** -20) * np.abs(ref)
+    assert (err <= tol)[small].all(), float((err / tol)[small].max())
+
+
 # ---------------------------------------------------------------- page operations
 
 @pytest.mark.parametrize("entry", [-1, -7, 99, "n_pages", 2 ** 31 - 1])
