@@ -337,7 +337,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                     l[r][1] += s[r][i][2] + s[r][i][3];
                 }
             }
-            // weights rounded to bf16, the type of V: 2^-8 each, under the output's own rounding
+            // weights rounded to bf16, as the product with V takes them: up to 2^-8 of each, 2^-8 of sum p |v| in
+            // all. Rounding to nearest, independent errors: 8 rows over 32,771 tokens 0.0022 of the output's norm
+            // against 64 bits, 0.0017 of it the output's own rounding. Their sum is of the unrounded ones.
             uint32_t w[RW][CH][4];
 #pragma unroll
             for (int r = 0; r < RW; ++r)
