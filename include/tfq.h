@@ -496,7 +496,7 @@ size_t tf_kvcache_workspace_bytes(const tf_kvcache* c);
  *   positions device int32 [M], output (may be NULL): the row's position in its sequence,
  *             length before the call + depth in the tree (popcount(mask) - 1, at least 0;
  *             without masks, the row's index in its block); 0 for rows of no sequence
- * The outputs may not overlap one another or the inputs.
+ * The outputs may not overlap one another, the inputs or the cache.
  * All or nothing: with too few free pages (TF_E_CACHE_FULL in the status word), a slot out
  * of range or named twice, a length beyond max_pages, a q_start out of order, or a shared
  * unfilled last page (TF_E_INVALID_ARG), the book stays as it was and every slot is -1.
@@ -558,7 +558,7 @@ int tf_rope_turns(const double* inv_freq, int64_t n, uint64_t* turns);
  *             of one call must not name the same slot.
  *   turns     device uint64 [rot_dim / 2] (tf_rope_turns), may be NULL when rot_dim is 0
  *   rot_dim   0..head_dim, a multiple of 16
- *   q         bf16 [M][n_q * head_dim], 16-byte aligned; may not overlap qkv, nor either of them the cache
+ *   q         bf16 [M][n_q * head_dim], 16-byte aligned; may not overlap the inputs, nor it or qkv the cache
  *   ws        256 zeroed, 256-aligned bytes (status word)
  * 1 <= n_q <= 1024, 1 <= M < 2^31 / 64. TF_RUN_PDL: gammas and turns may be read before the
  * previous kernel on the stream has finished.
@@ -581,7 +581,7 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
  * over the tokens the row sees; a row that sees none gives zeros. Tokens it does not see take
  * no part, whatever is stored there (NaN and infinities included).
  *   q       bf16 [M], leading dimension ldq >= n_q * head_dim (a multiple of 8), 16-byte aligned
- *   o       bf16 [M][n_q * head_dim], 16-byte aligned, not overlapping q or the cache; rows of no
+ *   o       bf16 [M][n_q * head_dim], 16-byte aligned, not overlapping the inputs or the cache; rows of no
  *           sequence are left as they were
  *   n_q     a multiple of n_kv, at most 64 query heads to a key/value head
  *   B       1..1024; a slot may appear twice
@@ -634,7 +634,8 @@ typedef struct tf_attn_desc {
  *   h1  = h + o . Wo^T, and the MLP and the readout as there
  * on a cache that tf_kvcache_extend has made room in: seqs, q_start, masks, slots and
  * positions are that call's (device). The cache's layers are used from 0; it has at least
- * d->n_layers, n_kv * head_dim = d->kv_dim, and M (1..8) rows belong to B sequences.
+ * d->n_layers, n_kv * head_dim = d->kv_dim, and M (1..8) rows belong to B sequences. logits do not
+ * overlap it.
  * After a verify step tf_kvcache_keep keeps what was accepted. The results are those of the
  * separate calls, bit for bit, with tf_tree_attn_run's max_rows = min(a->max_rows, M) (M where it is 0).
  * It chooses the attention's kernel: several sequences of a row or two each want it set (eight of one row,

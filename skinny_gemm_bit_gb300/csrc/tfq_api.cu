@@ -1328,6 +1328,10 @@ int tf_decode_step_attn_run(const tf_decoder_desc* d, const tf_kvcache* c, const
         return fail(TF_E_INVALID_ARG, "%s: NULL pointer", name);
     if (B < 1 || B > M)
         return fail(TF_E_UNSUPPORTED_SHAPE, "%s: need 1 <= B <= M", name);
+    CacheView v;
+    check_cache(c, name, &v);
+    if (in_cache(v, logits, d->vocab, d->vocab, M))
+        return fail(TF_E_INVALID_ARG, "%s: logits overlap the cache", name);
     const AttnStepLayout L = attn_step_layout(d, c, a);
     if (L.total == 0)
         return TF_E_UNSUPPORTED_SHAPE;  // the attention's query has set the message

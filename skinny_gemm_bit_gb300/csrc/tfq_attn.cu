@@ -127,6 +127,10 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
         return report_error(TF_E_INVALID_ARG, "%s: o overlaps q", name);
     if (in_cache(p.c, o, (int64_t)n_q * p.c.head_dim, (int64_t)n_q * p.c.head_dim, M))
         return report_error(TF_E_INVALID_ARG, "%s: o overlaps the cache", name);
+    const MemRange ranges[] = {{o, (size_t)M * n_q * p.c.head_dim * 2}, {seqs, (size_t)B * 4}, {q_start, (size_t)(B + 1) * 4},
+                               {masks, (size_t)M * 8}};
+    if (outputs_overlap(ranges, 1, 4))
+        return report_error(TF_E_INVALID_ARG, "%s: o overlaps another argument", name);
     if (!std::isfinite(scale))
         return report_error(TF_E_INVALID_ARG, "%s: scale must be finite", name);
     if ((rc = check_ws(ws, ws_bytes, tf_tree_attn_workspace_bytes(c, n_q, B, max_rows), name)))

@@ -59,12 +59,15 @@ inline bool outputs_overlap(const MemRange* r, int n_out, int n)
     return false;
 }
 
-// Whether rows x cols elements of 2 bytes (leading dimension ld) share memory with the cache's data or book.
-inline bool in_cache(const CacheView& c, const void* a, int64_t ld, int64_t cols, int64_t rows)
+// Whether a range, or rows x cols elements of 2 bytes (leading dimension ld), shares memory with the cache's data or book.
+inline bool in_cache(const CacheView& c, const MemRange& r)
 {
-    const MemRange r{a, (size_t)((rows - 1) * ld + cols) * 2};
     return overlap(r, MemRange{c.data, (size_t)c.row_of(c.n_layers, 0, 0, 0) * c.head_dim * 2}) ||
            overlap(r, MemRange{c.len, (c.n_seqs + (size_t)c.n_pages + (size_t)c.n_seqs * c.max_pages) * 4});
+}
+inline bool in_cache(const CacheView& c, const void* a, int64_t ld, int64_t cols, int64_t rows)
+{
+    return in_cache(c, MemRange{a, (size_t)((rows - 1) * ld + cols) * 2});
 }
 
 // Launch with (or without) programmatic dependent launch on the previous kernel.

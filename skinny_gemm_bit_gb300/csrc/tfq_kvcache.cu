@@ -661,7 +661,7 @@ int tf_kvcache_extend(const tf_kvcache* c, const int32_t* seqs, const int32_t* q
         return report_error(TF_E_INVALID_ARG, "%s: slots is NULL", name);
     const MemRange ranges[] = {{slots, (size_t)M * 4}, {positions, (size_t)M * 4}, {seqs, (size_t)B * 4},
                             {q_start, (size_t)(B + 1) * 4}, {masks, (size_t)M * 8}};
-    if (outputs_overlap(ranges, 2, 5))
+    if (outputs_overlap(ranges, 2, 5) || in_cache(v, ranges[0]) || in_cache(v, ranges[1]))
         return report_error(TF_E_INVALID_ARG, "%s: slots or positions overlaps another argument", name);
     extend_kernel<<<1, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(v, seqs, q_start, (int)B, M, masks, slots,
                                                                              positions, static_cast<int*>(ws));

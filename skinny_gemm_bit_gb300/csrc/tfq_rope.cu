@@ -251,6 +251,11 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
         return report_error(TF_E_INVALID_ARG, "%s: q or qkv overlaps the cache", name);
     if ((q_gamma != nullptr && !is_aligned(q_gamma, 16)) || (k_gamma != nullptr && !is_aligned(k_gamma, 16)) || !(eps >= 0.f))
         return report_error(TF_E_INVALID_ARG, "%s: gammas must be 16-byte aligned and eps >= 0", name);
+    const size_t row = (size_t)p.c.head_dim * 2, rows = (size_t)M * 4;
+    const MemRange ranges[] = {{q, M * n_q * row}, {positions, rows}, {slots, rows}, {rot_dim > 0 ? turns : nullptr, (size_t)rot_dim * 4},
+                               {q_gamma, row}, {k_gamma, row}};
+    if (outputs_overlap(ranges, 1, 6))
+        return report_error(TF_E_INVALID_ARG, "%s: q overlaps another argument", name);
     p.qkv = qkv;
     p.ld = ld;
     p.M = M;

@@ -66,3 +66,33 @@ def test_the_step_refuses_a_max_rows_out_of_range(T):
         s.attn.max_rows = rows
         assert s.need() == 0
         assert s.run() == T.TF_E_UNSUPPORTED_SHAPE
+
+
+def test_outputs_over_the_cache_or_the_inputs_are_refused(T):
+    data, book, x, y, ints = 0x100000000, 0x200000000, 0x300000000, 0x400000000, 0x500000000
+    s = Step(T, data, book)
+    L, c = s.L, ctypes.byref(s.cache)
+    data_end = data + L.tf_kvcache_data_bytes(2, s.n_kv, s.hd, s.page, s.n_pages)
+    book_end = book + 4 * L.tf_kvcache_book_elems(s.n_pages, s.n_seqs, s.max_pages)
+
+    def extend(slots, positions):
+        return L.tf_kvcache_extend(c, ints, ints + 4096, 2, 5, None, slots, positions, FAKE, 1 << 20, None)
+
+    for at in (book - 16, book, book_end - 4, data - 16, data_end - 4):
+        assert extend(at, None) == extend(at, x) == extend(x, at) == T.TF_E_INVALID_ARG
+
+    for at in (data - 4 * s.V + 4, data, data_end - 2, book, book_end - 2, book - 4 * s.V + 2):
+        assert s.run(logits=at) == T.TF_E_INVALID_ARG
+
+    def rope(q, pos=ints, slots=ints + 64, turns=ints + 128, qg=ints + 512, kg=ints + 1024):  # 3 rows of 2 heads of 64
+        return L.tf_qk_norm_rope_run(x, 384, 3, 2, qg, kg, 0.0, pos, turns, 64, 0, q, c, 0, slots, FAKE, 256, 0, None)
+
+    for kw in (dict(pos=y + 764), dict(slots=y - 8), dict(turns=y - 248), dict(turns=y + 760), dict(qg=y + 752), dict(kg=y - 112)):
+        assert rope(y, **kw) == T.TF_E_INVALID_ARG, kw
+
+    def attn(o, seqs=ints, start=ints + 64, masks=None):  # 3 rows of 2 heads of 64, 2 sequences
+        ws = L.tf_tree_attn_workspace_bytes(c, 2, 2, 3)
+        return L.tf_tree_attn_run(x, 128, 3, 2, c, 0, seqs, start, 2, 3, masks, 0.1, o, FAKE, ws, 0, None)
+
+    for kw in (dict(seqs=y - 4), dict(seqs=y + 764), dict(start=y - 8), dict(masks=y - 16), dict(masks=y + 760)):
+        assert attn(y, **kw) == T.TF_E_INVALID_ARG, kw
