@@ -810,7 +810,7 @@ def tf_logprobs_rows(v: torch.Tensor, targets=None, top_k: int = 0, logp=None, e
     M, N = v.shape
     nt = 0
     if targets is not None:
-        if targets.shape[0] != M or targets.dim() > 2:
+        if targets.dim() not in (1, 2) or targets.shape[0] != M:
             raise ValueError("targets must be int32 [M] or [M, n]")
         nt = 1 if targets.dim() == 1 else targets.shape[1]
     if (logp is None and nt > 0) or entropy is None or (top_k > 0 and (top_idx is None or top_logp is None)) or ws is None:

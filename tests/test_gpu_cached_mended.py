@@ -153,3 +153,12 @@ def test_the_step_takes_the_longest_block_for_its_attention(T, rows, n_q, n_kv, 
         got.append(T.tf_qlinear_run(m.dec.readout, h, gamma=m.dec.final_norm, eps=m.dec.desc.eps))
     assert torch.equal(got[0], got[1]) and bool(torch.isfinite(got[0]).all())
     assert torch.equal(caches[0].data, caches[1].data)
+
+
+# ---------------------------------------------------------------- log probabilities
+
+def test_targets_of_no_dimension_are_refused(T):
+    v = rand((1, 100), 1)
+    for bad in (torch.tensor(3, dtype=torch.int32, device="cuda"), i32([1, 2]), i32([[[1]]])):
+        with pytest.raises(ValueError):
+            T.tf_logprobs_rows(v, bad)
