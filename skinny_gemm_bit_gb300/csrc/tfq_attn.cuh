@@ -75,7 +75,7 @@ __device__ __forceinline__ SeqRows seq_rows(const AttnParams& p, int b)
 // A sequence of the call's schedule, in shared memory.
 struct SeqEntry {
     int first;      // units before it
-    int r0, base;   // as in SeqRows; base of a sequence that is refused: -1 - rows
+    int r0, base;   // as in SeqRows
     int slot_rows;  // slot | rows << 16
 };
 constexpr size_t schedule_bytes(int B) { return (size_t)(B + 8) * sizeof(SeqEntry); }  // the last 7: build() uses them
@@ -87,20 +87,6 @@ struct Segment {
     int units;       // units it takes
     int first;       // the item's first key tile, in units
 };
-
-// Zeros for the rows of sequences that are refused, by all threads of all CTAs: they may be any number of
-// rows (20,000 of 16 heads of 128 beside a good sequence: 90 us from the host's view; by one thread, 15,251). Not inlined: rare, and the
-// kernels' registers are all taken.
-__device__ __noinline__ inline void zero_refused(const AttnParams& p, const SeqEntry* seq)
-{
-    const int row = p.n_q * p.c.head_dim / 8;
-    for (int b = 0; b < p.B; ++b) {
-        const int64_t n = seq[b].base < -1 ? (int64_t)(-1 - seq[b].base) * row : 0;
-        uint4* o = reinterpret_cast<uint4*>(p.o) + seq[b].r0 * (int64_t)row;
-        for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
-            o[i] = make_uint4(0, 0, 0, 0);
-    }
-}
 
 // An item counts p.over units before its key tiles: what a segment costs apart from them (its
 // queries, joining the warps' parts, the hand-over), so that CTAs with many short items get no more
@@ -160,9 +146,8 @@ struct Shares {
         }
     }
 
-    // True if a sequence is refused.
     template <class Enter>
-    __device__ __forceinline__ bool sum_up(const SeqRows& first, Enter& enter)
+    __device__ __forceinline__ void sum_up(const SeqRows& first, Enter& enter)
     {
         if (kJoin > 0 && p.few) {  // a sequence a thread
             const int2 mine = counted(first);
@@ -178,13 +163,11 @@ struct Shares {
             }
             whole = whole_of(all.x, all.y, gridDim.x);
         }
-        bool refused = false;
         for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
             const SeqRows q = b < (int)blockDim.x ? first : seq_rows(p, b);
             enter(b, q, q.base >= 0 ? all_units(q) : 0);
-            refused |= q.base < 0;
         }
-        refused = __syncthreads_or(refused);
+        __syncthreads();
         if (threadIdx.x < 32) {
             unsigned sum = 0;  // sums stop at INT32_MAX, as do their terms
             for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -205,7 +188,6 @@ struct Shares {
         }
         __syncthreads();
         total = seq[p.B].first;
-        return refused;
     }
 
     // All threads of the CTA (a multiple of 32); has barriers.
@@ -217,16 +199,21 @@ struct Shares {
                 e.slot_rows = q.slot | q.rows << 16;
                 e.first = units;
             } else {
-                e.base = -1 - q.rows;
-                if (blockIdx.x == b % gridDim.x)
+                // arguments that do not hold: zero rows, a share of them a CTA (20,000 of 16 heads of 128 beside a
+                // good sequence: 168 us from the host's view; by one thread, 15,251)
+                if (blockIdx.x == 0)
                     record_status(p.status, TF_E_INVALID_ARG);
+                const int64_t n = (int64_t)q.rows * p.n_q * p.c.head_dim / 8;
+                uint4* o = reinterpret_cast<uint4*>(p.o + (int64_t)q.r0 * p.n_q * p.c.head_dim);
+                const uint4* end = o + n * (blockIdx.x + 1) / gridDim.x;
+                for (o += n * blockIdx.x / gridDim.x; o < end; ++o)
+                    *o = make_uint4(0, 0, 0, 0);
             }
             seq[b] = e;
         };
         SeqRows first{0, 0, 0, -1};
         if ((int)threadIdx.x < p.B || p.B == 1)
             first = seq_rows(p, p.B == 1 ? 0 : threadIdx.x);
-        bool refused = first.base < 0;
         if (p.B == 1) {  // nothing to be summed up: every thread has the answer
             if (first.base >= 0) {
                 const int2 mine = counted(first);
@@ -238,10 +225,8 @@ struct Shares {
                 enter(0, first, 0);
             __syncthreads();
         } else {
-            refused = sum_up(first, enter);
+            sum_up(first, enter);
         }
-        if (refused)
-            zero_refused(p, seq);
         if (total == INT32_MAX) {  // more than the units' 31 bits: nothing is done
             if (blockIdx.x == 0 && threadIdx.x == 0)
                 record_status(p.status, TF_E_UNSUPPORTED_SHAPE);
