@@ -549,8 +549,8 @@ int tf_rope_turns(const double* inv_freq, int64_t n, uint64_t* turns);
  *     (a, b) -> (a cos - b sin, b cos + a sin), pairs (i, i + rot_dim / 2), or (2i, 2i + 1)
  *     with `interleaved` non-zero;
  *   q heads go to q [M][n_q * head_dim]; k and v heads (v as they are) to the cache's layer
- *   at slots[m]. fp32 inside, one rounding to bf16 at the end; before it the rotation is within 2^-20 of
- *   the pair's length, and cosine and sine of an angle below a radian within 2^-20 of their own values.
+ *   at slots[m]. fp32 inside, one rounding to bf16 at the end; before it cosine and sine are
+ *   within 2^-20 of their own values, whatever the angle.
  *   qkv       bf16 [M], leading dimension ld >= (n_q + 2 n_kv) * head_dim, 16-byte aligned rows
  *   positions device int32 [M], any sign
  *   slots     device int32 [M] (tf_kvcache_extend); negative: nothing is stored for the row;

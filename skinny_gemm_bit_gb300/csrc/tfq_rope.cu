@@ -53,6 +53,21 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
                       f32x2_to_bf16x2(f[6], f[7]));
 }
 
+// Sine and cosine of hi + lo / 2^32 units of 2^-32 turn: less the nearest quarter turn, exactly, x is within
+// [-pi / 4, pi / 4] and as near as fp32 has it however small it is; there the Taylor polynomials' own error is
+// x^8 / 9! and x^10 / 10! at most (2^-21, 2^-25), so both are within 2^-20 of their own values at every angle.
+__device__ __forceinline__ void turn_sincos(uint32_t hi, uint32_t lo, float& sn, float& cs)
+{
+    const uint32_t quarter = (hi + 0x20000000u) >> 30;
+    const float x = fmaf((float)lo, 0x1p-32f, (float)(int32_t)(hi - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const float y = x * x;
+    const float s = fmaf(x * y, fmaf(y, fmaf(y, -1.f / 5040.f, 1.f / 120.f), -1.f / 6.f), x);
+    const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+    const bool odd = quarter & 1;
+    sn = __uint_as_float(__float_as_uint(odd ? c : s) ^ (quarter & 2) << 30);
+    cs = __uint_as_float(__float_as_uint(odd ? s : c) ^ (quarter + 1 & 2) << 30);
+}
+
 // LANES lanes take a head (head_dim / 16); a warp takes HEADS = 32 / LANES heads at once.
 // Seven blocks an SM: 72 registers a thread hold everything (8191 rows 24.0 us). With every lane making its eight
 // angles itself: 24.7 with seven, 26.5 with eight (spills), 27.1 with six (fewer loads in flight).
@@ -95,11 +110,10 @@ __global__ void __launch_bounds__(kRopeThreads, 7) qk_norm_rope_kernel(const __g
     };
     fetch(part * HEADS);
     const int32_t slot = p.slots[m];
-    // angle = position * turns modulo one turn, exact in 64 bits, then as a signed fraction in fp32 whose
-    // relative error is 2^-23 however small it is. Its sine and cosine keep that: slow pairs turn by 1e-6
-    // a token, where the fast functions' absolute error of 2^-21 is half of the sine (9 % off at one token).
-    // A lane's share of them and sixteen shuffles take no longer than eight fast ones: 8191 rows 24.3 -> 24.0 us;
-    // all eight by every lane 25.7.
+    // angle = position * turns modulo one turn, exact in 64 bits. Its sine and cosine keep their digits however
+    // small they are: slow pairs turn by 1e-6 a token, where the fast functions' absolute error of 2^-21 is half
+    // of the sine (9 % off at one token). A lane's share of them and sixteen shuffles take no longer than eight
+    // fast ones: 8191 rows 24.0 us, 24.3 with those; CUDA's sincospif, all eight by every lane 25.7.
     float cs[8], sn[8];
     {
         float mine_c[OWN] = {}, mine_s[OWN] = {};
@@ -110,7 +124,7 @@ __global__ void __launch_bounds__(kRopeThreads, 7) qk_norm_rope_kernel(const __g
             for (int k = 0; k < OWN; ++k) {
                 // (sign-extended position) * turns modulo 2^64
                 const uint32_t hi = __umulhi(pos, f[k].x) + pos * f[k].y + neg * f[k].x, lo = pos * f[k].x;
-                sincospif(fmaf((float)lo, 0x1p-32f, (float)(int32_t)hi) * 0x1p-31f, &mine_s[k], &mine_c[k]);
+                turn_sincos(hi, lo, mine_s[k], mine_c[k]);
             }
         }
 #pragma unroll
