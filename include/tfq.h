@@ -499,7 +499,9 @@ size_t tf_kvcache_workspace_bytes(const tf_kvcache* c);
  * The outputs may not overlap one another, the inputs or the cache.
  * All or nothing: with too few free pages (TF_E_CACHE_FULL in the status word), a slot out
  * of range or named twice, a length beyond max_pages, a q_start out of order, or a shared
- * unfilled last page (TF_E_INVALID_ARG), the book stays as it was and every slot is -1.
+ * unfilled last page (TF_E_INVALID_ARG), the book stays as it was and every slot is -1. What follows on
+ * the stream does not know: an attention then takes each sequence's last tokens for the rows, so the status
+ * (tf_workspace_status), or a slot of -1, is looked at before a result is used.
  */
 int tf_kvcache_extend(const tf_kvcache* c, const int32_t* seqs, const int32_t* q_start, int64_t B, int64_t M,
                       const uint64_t* masks, int32_t* slots, int32_t* positions, void* ws, size_t ws_bytes,

@@ -547,6 +547,10 @@ def tf_generate_greedy(dec: Decoder, prompt, max_new: int, max_draft: int = 7, m
 
 
 # ---------------------------------------------------------------- K/V cache
+#
+# What a kernel finds wrong (no free page, a slot out of range, an argument that does not hold) is recorded in the
+# call's workspace: pass `ws` and ask tf_workspace_status(ws) before a result is relied on. A call without `ws` makes
+# one for itself, and its status is lost with it.
 
 def _raw_stream(stream, device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
