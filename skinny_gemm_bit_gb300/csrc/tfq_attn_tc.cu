@@ -11,7 +11,7 @@
 //
 // Each group has two score buffers: the scores of its next tile are formed while it works on this
 // one's weights, so neither it nor the tensor cores wait for the other's latency. Trees of 64 rows
-// by 8 heads to each of 4 key/value heads of 128, over 8 x 16,001 tokens: 130 us, 1040 TFLOP/s, against 206
+// by 8 heads to each of 4 key/value heads of 128, over 8 x 16,001 tokens: 125 us, 1080 TFLOP/s, against 206
 // with one buffer and 128-key tiles, where a group spent 2600 of 6600 cycles a tile waiting. What
 // is left is the softmax's own work and Q K^T at 64 keys, which reads 128 rows of queries from
 // shared memory for each 64 of keys (some 67 cycles a 128 x 64 x 16 step). Up to 128 query rows (PAIR false) both

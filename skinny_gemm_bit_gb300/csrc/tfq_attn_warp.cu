@@ -9,10 +9,10 @@
 // warp keeps its own running maximum, sum and output; they meet in shared memory once a
 // segment.
 //
-// 64 ragged sequences of up to 8190 tokens, 16 query and 8 key/value heads of 128: 176 us, 6.1 TB/s of
+// 64 ragged sequences of up to 8190 tokens, 16 query and 8 key/value heads of 128: 174 us, 6.2 TB/s of
 // K and V; 64 of 8192 tokens 320 us, 6.7 TB/s. A ring shared by the warps, filled by a producer warp, kept a
 // tile 1700 cycles from its release and took 242 us. Few tokens are bound by the chain of latencies
-// (queries, tiles, the warps' join, the CTAs' join): one token over 4097 takes 10.6 us, 8 over 32,771 31.4.
+// (queries, tiles, the warps' join, the CTAs' join): one token over 4097 takes 10.7 us, 8 over 32,771 31.6.
 //
 // Tiles land with the 128-byte swizzle (16-byte piece c of row r at c ^ (r % 8)), so the eight
 // rows of an ldmatrix fall in different banks. A box is one page's rows of a tile.
