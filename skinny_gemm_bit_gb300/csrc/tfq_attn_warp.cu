@@ -339,7 +339,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             }
             // weights rounded to bf16, as the product with V takes them: up to 2^-8 of each, 2^-8 of sum p |v| in
             // all. Rounding to nearest, independent errors: 8 rows over 32,771 tokens 0.0022 of the output's norm
-            // against 64 bits, 0.0017 of it the output's own rounding. Their sum is of the unrounded ones.
+            // against 64 bits, 0.0017 of it the output's own rounding. Their sum is of the unrounded ones. A second
+            // product with what the rounding left took 64 ragged sequences from 174 to 176 us, one token over 4097
+            // from 10.6 to 10.8 and 8 x 8 rows over 2000 from 20.0 to 21.8.
             uint32_t w[RW][CH][4];
 #pragma unroll
             for (int r = 0; r < RW; ++r)
