@@ -445,6 +445,15 @@ int tf_generate_greedy(const tf_decoder_desc* d, const int32_t* prompt, int64_t 
  * other slot (so that appending to it changes nobody else's tokens).
  * tf_kvcache describes it on the host and is read during a call only.
  *
+ * A cache of 8 bits (tf_kvcache_init_e4m3) holds e4m3 codes in the same layout, and beside them a power of two
+ * for each block of 16 rows of a page and head, as its biased exponent:
+ *   data    uint8 [n_layers][2][n_pages][n_kv][page_size][head_dim], e4m3 (bit 7 sign, bits 6-3 exponent with bias 7,
+ *           bits 2-0 mantissa, S.1111.111 NaN)
+ *   scales  uint8 [n_layers][2][n_pages][n_kv][page_size / 16]: value = code * 2^(scale - 127), scales 95 .. 159
+ *           (2^-32 .. 2^32); one below counts as 95, one above as 159
+ * Every call below takes either kind, and the attentions and the decoder step too: what they store to such a cache
+ * is described at tf_qk_norm_rope_run and tf_kvcache_keep.
+ *
  * Free pages are taken lowest index first, in slot order of the call's list, so the
  * book after a call depends on nothing but the book before it and the arguments.
  */
@@ -459,7 +468,12 @@ typedef struct tf_kvcache {
     int32_t max_pages;  /* page-table columns of a slot */
     void* data;         /* 16-byte aligned */
     int32_t* book;      /* 4-byte aligned */
+    int32_t code;       /* TF_KV_BF16 or TF_KV_E4M3 */
+    uint8_t* scales;    /* TF_KV_E4M3: the blocks' scales, 4-byte aligned; else NULL */
 } tf_kvcache;
+#define TF_KV_BF16 0
+#define TF_KV_E4M3 1
+#define TF_KV_BLOCK 16 /* rows of a page that share a scale */
 #define TF_KVCACHE_MAGIC 0x314B5654u /* "TVK1" */
 #define TF_MAX_DRAFT_ROWS 64 /* rows of a sequence that one attention or keep call takes */
 
@@ -476,6 +490,17 @@ size_t tf_kvcache_book_elems(int64_t n_pages, int n_seqs, int64_t max_pages);
 int tf_kvcache_init(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages, int n_seqs,
                     int64_t max_pages, void* data, size_t data_bytes, int32_t* book, size_t book_elems,
                     tf_kvcache* desc);
+
+/*
+ * The same for a cache of 8 bits. `scales`: tf_kvcache_scale_bytes bytes (the layout above, its end rounded up to
+ * a multiple of 4: they are read as aligned words of four). tf_kvcache_e4m3_bytes is half of tf_kvcache_data_bytes.
+ * Codes and scales need no clearing: a block's scale is written with its first row.
+ */
+size_t tf_kvcache_e4m3_bytes(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages);
+size_t tf_kvcache_scale_bytes(int n_layers, int n_kv, int page_size, int64_t n_pages);
+int tf_kvcache_init_e4m3(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages, int n_seqs,
+                         int64_t max_pages, void* data, size_t data_bytes, uint8_t* scales, size_t scale_bytes,
+                         int32_t* book, size_t book_elems, tf_kvcache* desc);
 
 /* Empty every slot and free every page (the data stays as it is). */
 int tf_kvcache_reset(const tf_kvcache* c, void* stream);
@@ -530,6 +555,9 @@ int tf_kvcache_fork(const tf_kvcache* c, const int32_t* parent, void* ws, size_t
  * not increasing or out of range, a slot out of range, a page of the block that is shared)
  * is left as it was and TF_E_INVALID_ARG recorded; the others are done. A slot named twice
  * leaves every sequence as it was.
+ * In a cache of 8 bits a block that rows move into takes the largest scale of its own and of the blocks they come
+ * from (its own not counted where its first row moves in), and codes that meet a larger scale than theirs are rounded
+ * to it, to nearest even: exact but where they become subnormal.
  */
 int tf_kvcache_keep(const tf_kvcache* c, const int32_t* seqs, const int32_t* q_start, const int32_t* keep,
                     const int32_t* n_keep, int64_t B, int64_t M, void* ws, size_t ws_bytes, void* stream);
@@ -564,6 +592,15 @@ int tf_rope_turns(const double* inv_freq, int64_t n, uint64_t* turns);
  *   ws        256 zeroed, 256-aligned bytes (status word)
  * 1 <= n_q <= 1024, 1 <= M < 2^31 / 64. TF_RUN_PDL: gammas and turns may be read before the
  * previous kernel on the stream has finished.
+ *
+ * Into a cache of 8 bits k and v go as e4m3 codes, rounded once, to nearest even, from fp32. For each block of 16
+ * rows of a page and head that the call stores rows to, K and V apart:
+ *   need = the least power of two with |x| <= 448 need for every finite x stored there, within 2^-32 .. 2^32
+ *   scale = need where the block's first row is stored (what the block held is dropped), else max(scale, need);
+ *   where it grows, the codes of the block's other rows are rounded to it (exact but where they become subnormal)
+ *   code = e4m3(x / scale), +-448 for what is larger (infinities among them), NaN for NaN
+ * Rows that go to one block are neighbours in the call, in the order of their slots, as tf_kvcache_extend gives
+ * them, and a block's rows are stored in order over the calls. The same call again changes nothing.
  */
 int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, const uint16_t* q_gamma,
                         const uint16_t* k_gamma, float eps, const int32_t* positions, const uint64_t* turns,
@@ -604,11 +641,32 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
  * status word, after which the workspace has to be zeroed again). TF_RUN_PDL has no effect.
  * A call has fewer than 2^31 key tiles (tokens * n_kv * query-row tiles / 32): beyond that it
  * records TF_E_UNSUPPORTED_SHAPE and writes nothing.
+ * Over a cache of 8 bits the codes are multiplied as they are, in fp16, which holds every e4m3 value, and the blocks'
+ * scales enter the scores and the weights. A query row is scaled by a power of two into fp16's range (its values
+ * below 2^-38 of its largest are lost), and the weights are rounded to fp16: 2^-11 of each, those
+ * below 2^-31 of the row's largest lost.
  */
 size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int max_rows);
 int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
                      const int32_t* seqs, const int32_t* q_start, int64_t B, int max_rows, const uint64_t* masks,
                      float scale, uint16_t* o, void* ws, size_t ws_bytes, unsigned flags, void* stream);
+
+/*
+ * Attention of prompts over the cache: as tf_tree_attn_run with causal rows and no limit to a sequence's number of
+ * them. Sequence b's rows q_start[b] .. q_start[b + 1) are the last T_b tokens of slot seqs[b], T_b >= 0, whose keys
+ * and values are in the cache already; row i of them sees the tokens up to its own, len[seqs[b]] - T_b + i.
+ * A whole prompt has T_b = len; a chunk of one has a context before it. A token's keys and values are read
+ * once for 256 query rows (query heads that share a key/value head times rows) instead of for 64 rows of each head.
+ *   head_dim 64 or 128; n_q a multiple of n_kv, at most 64 query heads to a key/value head; 1 <= B <= 1024;
+ *   1 <= M < 2^21
+ *   ws  tf_prompt_attn_workspace_bytes(c, n_q, B) bytes
+ * Everything else (q, ldq, o, scale, refusals, errors in the status word, both kinds of cache, a workspace of its own)
+ * is as for tf_tree_attn_run. A call has fewer than 2^31 key tiles of 64 tokens, each row tile's counted apart.
+ */
+size_t tf_prompt_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B);
+int tf_prompt_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
+                       const int32_t* seqs, const int32_t* q_start, int64_t B, float scale, uint16_t* o, void* ws,
+                       size_t ws_bytes, unsigned flags, void* stream);
 
 /* ---------------------------------------------------------------- decoder step over a cache */
 

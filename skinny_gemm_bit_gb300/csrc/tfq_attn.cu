@@ -35,6 +35,9 @@ int attn_over(int rows, int64_t items)
     return items > device_sms() ? 28 : 16;
 }
 
+// Query rows of a prompt's item, and a segment's own cost in 64-key tiles.
+constexpr int kPromptRows = 256, kPromptOver = 8;
+
 struct AttnLayout {
     size_t counters, parts, total;
 };
@@ -70,16 +73,89 @@ EncodeTiled encode_tiled()
 
 // The pool as {64 columns, rows, head_dim / 64}: a box is `rows` rows of `halves` times 64 columns
 // (128 bytes a row, swizzled), one 64 after the other.
+// Of 8 bits, {128 bytes or head_dim if that is less, rows, head_dim / 128}.
 bool encode_rows(const CacheView& c, int total_rows, int rows, int halves, CUtensorMap* map)
 {
     const EncodeTiled fn = encode_tiled();
     if (fn == nullptr)
         return false;
+    if (c.code == TF_KV_E4M3) {
+        const cuuint32_t line = c.head_dim < 128 ? 64 : 128, lines = c.head_dim / line;
+        const cuuint64_t dims[3] = {line, (cuuint64_t)total_rows, lines}, strides[2] = {(cuuint64_t)c.head_dim, 128};
+        const cuuint32_t box[3] = {line, (cuuint32_t)rows, lines}, one[3] = {1, 1, 1};
+        return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, c.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    }
     const cuuint64_t dims[3] = {64, (cuuint64_t)total_rows, (cuuint64_t)c.head_dim / 64};
     const cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * 2, 128};
     const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)halves}, one[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The checks that both calls make of their arguments, and the parameters that follow from them.
+int fill_params(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer, const int32_t* seqs,
+                const int32_t* q_start, int64_t B, int max_rows, int most_rows, const uint64_t* masks, float scale,
+                uint16_t* o, const char* name, AttnParams* p)
+{
+    int rc = check_cache(c, name, &p->c);
+    if (rc)
+        return rc;
+    if (q == nullptr || o == nullptr || seqs == nullptr || q_start == nullptr)
+        return report_error(TF_E_INVALID_ARG, "%s: NULL pointer", name);
+    if (n_q < 1 || n_q % p->c.n_kv != 0 || n_q / p->c.n_kv > 64)
+        return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q must be a multiple of n_kv, at most 64 query heads to one", name);
+    if (B < 1 || B > 1024 || M < 1 || M > INT32_MAX / 1024 || max_rows < 1 || max_rows > most_rows)
+        return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: need 1 <= B <= 1024, 1 <= M < 2^21 and 1 <= max_rows <= %d", name,
+                            most_rows);
+    if (layer < 0 || layer >= p->c.n_layers)
+        return report_error(TF_E_INVALID_ARG, "%s: layer %d outside the cache's %d", name, layer, p->c.n_layers);
+    if (!is_aligned(q, 16) || !is_aligned(o, 16) || ldq % 8 != 0 || ldq < (int64_t)n_q * p->c.head_dim)
+        return report_error(TF_E_INVALID_ARG, "%s: q and o must be 16-byte aligned, ldq a multiple of 8 and >= n_q * head_dim",
+                            name);
+    if (rows_overlap(q, ldq, (int64_t)n_q * p->c.head_dim, o, (int64_t)n_q * p->c.head_dim, (int64_t)n_q * p->c.head_dim, M))
+        return report_error(TF_E_INVALID_ARG, "%s: o overlaps q", name);
+    if (in_cache(p->c, o, (int64_t)n_q * p->c.head_dim, (int64_t)n_q * p->c.head_dim, M))
+        return report_error(TF_E_INVALID_ARG, "%s: o overlaps the cache", name);
+    const MemRange ranges[] = {{o, (size_t)M * n_q * p->c.head_dim * 2}, {seqs, (size_t)B * 4}, {q_start, (size_t)(B + 1) * 4},
+                               {masks, (size_t)M * 8}};
+    if (outputs_overlap(ranges, 1, 4))
+        return report_error(TF_E_INVALID_ARG, "%s: o overlaps another argument", name);
+    if (!std::isfinite(scale))
+        return report_error(TF_E_INVALID_ARG, "%s: scale must be finite", name);
+    p->q = q;
+    p->ldq = ldq;
+    p->M = M;
+    p->n_q = n_q;
+    p->group = n_q / p->c.n_kv;
+    p->group_inv = ((1u << 31) + p->group - 1) / p->group;
+    p->layer = layer;
+    p->seqs = seqs;
+    p->q_start = q_start;
+    p->B = (int)B;
+    p->max_rows = max_rows;
+    p->masks = masks;
+    p->scale_log2 = scale * 1.4426950408889634f;
+    p->o = o;
+    p->total_rows = (int)p->c.row_of(p->c.n_layers, 0, 0, 0);
+    p->limit_ns = kDefaultWaitLimitNs;
+    return TF_OK;
+}
+
+int launch_attn(AttnParams& p, int rows, bool causal, void* ws, cudaStream_t stream, const char* name)
+{
+    const AttnLayout L = attn_layout(p.c.head_dim, rows);
+    p.status = static_cast<int*>(ws);
+    p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + L.counters);
+    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
+    CUtensorMap map;
+    const bool tc = rows > 64;
+    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(p.c.page_size) : attn_warp_box(p.c.head_dim, p.c.page_size),
+                     tc ? 1 : p.c.head_dim / 64, &map))
+        return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
+    const cudaError_t e = tc ? launch_attn_tc(p, rows, causal, map, stream) : launch_attn_warp(p, rows, map, stream);
+    return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }
 
 }  // namespace
@@ -108,65 +184,48 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
 {
     const char* name = "tf_tree_attn_run";
     AttnParams p{};
-    int rc = check_cache(c, name, &p.c);
-    if (rc)
+    int rc = fill_params(q, ldq, M, n_q, c, layer, seqs, q_start, B, max_rows, kMaxDraftRows, masks, scale, o, name, &p);
+    if (rc || (rc = check_ws(ws, ws_bytes, tf_tree_attn_workspace_bytes(c, n_q, B, max_rows), name)))
         return rc;
-    if (q == nullptr || o == nullptr || seqs == nullptr || q_start == nullptr)
-        return report_error(TF_E_INVALID_ARG, "%s: NULL pointer", name);
-    if (n_q < 1 || n_q % p.c.n_kv != 0 || n_q / p.c.n_kv > 64)
-        return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q must be a multiple of n_kv, at most 64 query heads to one", name);
-    if (B < 1 || B > 1024 || M < 1 || M > INT32_MAX / 1024 || max_rows < 1 || max_rows > kMaxDraftRows)
-        return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: need 1 <= B <= 1024, 1 <= M < 2^21 and 1 <= max_rows <= %d", name,
-                            kMaxDraftRows);
-    if (layer < 0 || layer >= p.c.n_layers)
-        return report_error(TF_E_INVALID_ARG, "%s: layer %d outside the cache's %d", name, layer, p.c.n_layers);
-    if (!is_aligned(q, 16) || !is_aligned(o, 16) || ldq % 8 != 0 || ldq < (int64_t)n_q * p.c.head_dim)
-        return report_error(TF_E_INVALID_ARG, "%s: q and o must be 16-byte aligned, ldq a multiple of 8 and >= n_q * head_dim",
-                            name);
-    if (rows_overlap(q, ldq, (int64_t)n_q * p.c.head_dim, o, (int64_t)n_q * p.c.head_dim, (int64_t)n_q * p.c.head_dim, M))
-        return report_error(TF_E_INVALID_ARG, "%s: o overlaps q", name);
-    if (in_cache(p.c, o, (int64_t)n_q * p.c.head_dim, (int64_t)n_q * p.c.head_dim, M))
-        return report_error(TF_E_INVALID_ARG, "%s: o overlaps the cache", name);
-    const MemRange ranges[] = {{o, (size_t)M * n_q * p.c.head_dim * 2}, {seqs, (size_t)B * 4}, {q_start, (size_t)(B + 1) * 4},
-                               {masks, (size_t)M * 8}};
-    if (outputs_overlap(ranges, 1, 4))
-        return report_error(TF_E_INVALID_ARG, "%s: o overlaps another argument", name);
-    if (!std::isfinite(scale))
-        return report_error(TF_E_INVALID_ARG, "%s: scale must be finite", name);
-    if ((rc = check_ws(ws, ws_bytes, tf_tree_attn_workspace_bytes(c, n_q, B, max_rows), name)))
-        return rc;
-    p.q = q;
-    p.ldq = ldq;
-    p.M = M;
-    p.n_q = n_q;
-    p.group = n_q / p.c.n_kv;
-    p.group_inv = ((1u << 20) + p.group - 1) / p.group;
-    p.layer = layer;
-    p.seqs = seqs;
-    p.q_start = q_start;
-    p.B = (int)B;
-    p.max_rows = max_rows;
-    p.masks = masks;
-    p.scale_log2 = scale * 1.4426950408889634f;
-    p.o = o;
-    p.status = static_cast<int*>(ws);
     (void)flags;  // the launch is cooperative, which excludes a programmatic dependent one
-    p.total_rows = (int)p.c.row_of(p.c.n_layers, 0, 0, 0);
-    p.limit_ns = kDefaultWaitLimitNs;
     const int rows = attn_rows(max_rows, p.group, p.c.head_dim);
     const int64_t items = B * p.c.n_kv * ((max_rows * p.group + rows - 1) / rows);
     p.over = attn_over(rows, items);
     p.few = items <= device_sms() && B <= 256;
-    const AttnLayout L = attn_layout(p.c.head_dim, rows);
-    p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + L.counters);
-    p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
-    CUtensorMap map;
-    const bool tc = rows > 64;
-    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(p.c.page_size) : attn_warp_box(p.c.head_dim, p.c.page_size),
-                     tc ? 1 : p.c.head_dim / 64, &map))
-        return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
-    const cudaError_t e = (tc ? launch_attn_tc : launch_attn_warp)(p, rows, map, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
+    return launch_attn(p, rows, false, ws, static_cast<cudaStream_t>(stream), name);
+}
+
+size_t tf_prompt_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B)
+{
+    const char* name = "tf_prompt_attn_workspace_bytes";
+    CacheView v;
+    if (check_cache(c, name, &v))
+        return 0;
+    if (n_q < 1 || n_q % v.n_kv != 0 || n_q / v.n_kv > 64 || B < 1 || B > 1024 || v.head_dim > 128) {
+        report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q, B or head_dim out of range", name);
+        return 0;
+    }
+    return attn_layout(v.head_dim, kPromptRows).total;
+}
+
+int tf_prompt_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
+                       const int32_t* seqs, const int32_t* q_start, int64_t B, float scale, uint16_t* o, void* ws,
+                       size_t ws_bytes, unsigned flags, void* stream)
+{
+    const char* name = "tf_prompt_attn_run";
+    AttnParams p{};
+    int rc = fill_params(q, ldq, M, n_q, c, layer, seqs, q_start, B, INT32_MAX, INT32_MAX, nullptr, scale, o, name, &p);
+    if (rc)
+        return rc;
+    if (p.c.head_dim > 128)
+        return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: head_dim must be 64 or 128", name);
+    if (M * p.group >= 1 << 25)
+        return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: need M * n_q / n_kv < 2^25", name);
+    if ((rc = check_ws(ws, ws_bytes, tf_prompt_attn_workspace_bytes(c, n_q, B), name)))
+        return rc;
+    (void)flags;
+    p.over = kPromptOver;
+    return launch_attn(p, kPromptRows, true, ws, static_cast<cudaStream_t>(stream), name);
 }
 
 }  // extern "C"

@@ -26,7 +26,7 @@ struct AttnParams {
     const uint16_t* q;
     int64_t ldq, M;
     int n_q, group;  // query heads; query heads of a key/value head
-    unsigned group_inv;  // 2^20 / group, rounded up
+    unsigned group_inv;  // 2^31 / group, rounded up
     CacheView c;
     int layer;
     int total_rows;  // rows of the pool: a row coordinate that the tensor map fills with zeros
@@ -42,9 +42,9 @@ struct AttnParams {
     float* parts;        // [2 * CTAs] of a part: [head_dim / 4][ROWS] float4, then [ROWS] (m, l)
     uint64_t limit_ns;
 
-    // Query row r of a key/value head is head r % group of its sequence's row r / group. The product
-    // is exact for r < 64 * 64 and group <= 64: it is over by less than r / 2^20 < 1 / group.
-    __device__ __forceinline__ int token_of(int r) const { return (int)((unsigned)r * group_inv >> 20); }
+    // Query row r of a key/value head is head r % group of its sequence's row r / group. The quotient
+    // is exact for r < 2^25 and group <= 64: it is over by less than r * 63 / 2^31 / group < 1 / group.
+    __device__ __forceinline__ int token_of(int r) const { return (int)__umulhi((unsigned)r << 1, group_inv); }
     __device__ __forceinline__ int head_of(int r) const { return r - token_of(r) * group; }
 };
 
@@ -262,6 +262,142 @@ struct Shares {
         g.t0 = max(off - over, 0);
         g.t1 = max(off + g.units - over, 0);
         g.first = u - off + over;
+        return g;
+    }
+};
+
+// The same for causal rows without a limit to their number, where a row tile sees the tokens up to its last row's: its
+// key tiles grow with the rows before it. The units before row tile rt of a head are
+//   P(rt) = rt * (over + 1) + floor((rt * base + A * rt * (rt + 1) / 2) / KEYS),   A = ROWS / group, rounded up, tokens,
+// in closed form, so an item is found without a list of them. Its own P(rt + 1) - P(rt) is over - 1 at least above its
+// key tiles ceil((base + last row's token + 1) / KEYS), since A (rt + 1) >= that token + 1; over >= 2.
+template <int ROWS, int KEYS>
+struct PromptShares {
+    struct Entry {
+        int first, r0, base, rows;
+    };
+    Entry* seq;  // [B + 1], base < 0: none
+    const AttnParams& p;
+    unsigned total, ctas, share, rest;
+    static_assert(sizeof(Entry) == sizeof(SeqEntry), "schedule_bytes");
+
+    __host__ __device__ PromptShares(const AttnParams& params, void* smem)
+        : seq(static_cast<Entry*>(smem)), p(params), total(0), ctas(0), share(0), rest(0)
+    {
+    }
+
+    __host__ __device__ __forceinline__ int row_tiles(int rows) const { return (rows * p.group + ROWS - 1) / ROWS; }
+    __host__ __device__ __forceinline__ int64_t before(int base, int rt) const
+    {
+        const int64_t a = (ROWS + p.group - 1) / p.group;
+        return (int64_t)rt * (p.over + 1) + ((int64_t)rt * base + a * rt * (rt + 1) / 2) / KEYS;
+    }
+    // tokens that row tile rt's last row, the last of them, sees
+    __host__ __device__ __forceinline__ int seen_by(int base, int rows, int rt) const
+    {
+        const int last = ((rt + 1) * ROWS + p.group - 1) / p.group;
+        return base + (last < rows ? last : rows);
+    }
+    __host__ __device__ __forceinline__ int all_units(int base, int rows) const
+    {
+        const int64_t n = p.c.n_kv * before(base, row_tiles(rows));  // below 2^8 * 2^43
+        return n < INT32_MAX ? (int)n : INT32_MAX;
+    }
+    __host__ __device__ __forceinline__ void deal(unsigned grid)
+    {
+        ctas = total < grid ? total : grid;
+        if (ctas > 0) {
+            share = total / ctas;
+            rest = total - share * ctas;
+        }
+    }
+
+    // All threads of the CTA (a multiple of 32); has barriers.
+    __device__ void build()
+    {
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            const SeqRows q = seq_rows(p, b);
+            seq[b] = Entry{q.base >= 0 ? all_units(q.base, q.rows) : 0, q.r0, q.base, q.rows};
+            if (q.base < 0 && blockIdx.x == 0)
+                record_status(p.status, TF_E_INVALID_ARG);
+        }
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            unsigned sum = 0;  // sums stop at INT32_MAX, as do their terms
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int b = b0 + threadIdx.x;
+                const unsigned own = b < p.B ? seq[b].first : 0;
+                unsigned x = own;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+                    if ((int)threadIdx.x >= o)
+                        x = min(x + y, (unsigned)INT32_MAX);
+                }
+                const unsigned upto = __shfl_up_sync(0xffffffffu, x, 1);
+                if (b < p.B)
+                    seq[b].first = (int)min(threadIdx.x > 0 ? sum + upto : sum, (unsigned)INT32_MAX);
+                sum = min(sum + __shfl_sync(0xffffffffu, x, 31), (unsigned)INT32_MAX);
+            }
+            if (threadIdx.x == 0)
+                seq[p.B].first = (int)sum;
+        }
+        __syncthreads();
+        total = seq[p.B].first;
+        // rows of a sequence whose arguments do not hold become zeros, a share of them a CTA
+        for (int b = 0; b < p.B; ++b) {
+            if (seq[b].base >= 0)
+                continue;
+            const int64_t row = (int64_t)p.n_q * p.c.head_dim / 8, n = seq[b].rows * row;
+            uint4* o = reinterpret_cast<uint4*>(p.o) + seq[b].r0 * row;
+            for (int64_t i = n * blockIdx.x / gridDim.x + threadIdx.x; i < n * (blockIdx.x + 1) / gridDim.x; i += blockDim.x)
+                o[i] = make_uint4(0, 0, 0, 0);
+        }
+        if (total == INT32_MAX) {  // more than the units' 31 bits: nothing is done
+            if (blockIdx.x == 0 && threadIdx.x == 0)
+                record_status(p.status, TF_E_UNSUPPORTED_SHAPE);
+            total = 0;
+        }
+        deal(gridDim.x);
+    }
+
+    __host__ __device__ __forceinline__ int start_of(unsigned cta) const { return (int)(cta >= ctas ? total : share * cta + rest * cta / ctas); }
+    __host__ __device__ __forceinline__ int cta_of(int u) const { return (int)((((uint64_t)u + 1) * ctas - 1) / total); }
+
+    __host__ __device__ __forceinline__ Segment segment(int u, int end) const
+    {
+        int lo = 0, hi = p.B - 1;  // the last sequence whose first unit is not behind u
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (seq[mid].first <= u)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const Entry e = seq[lo];
+        const int tiles = row_tiles(e.rows), head = (int)before(e.base, tiles), local = u - e.first;
+        Segment g;
+        g.h = local / head;
+        const int off = local - g.h * head;
+        // the last rt with P(rt) <= off: the root of the parabola, then the step or so that it is off
+        const float b = (ROWS + p.group - 1) / p.group * (0.5f / KEYS), a = p.over + 1 + (float)e.base / KEYS + b;
+        int rt = (int)((sqrtf(a * a + 4.f * b * off) - a) / (2.f * b));
+        rt = rt < 0 ? 0 : rt > tiles - 1 ? tiles - 1 : rt;
+        while (rt > 0 && before(e.base, rt) > off)
+            --rt;
+        while (rt < tiles - 1 && before(e.base, rt + 1) <= off)
+            ++rt;
+        const int at = (int)before(e.base, rt), per = (int)before(e.base, rt + 1) - at;
+        g.rt = rt;
+        g.q = SeqRows{0, e.r0, e.rows, e.base};
+#ifdef __CUDA_ARCH__
+        g.q.slot = p.seqs[lo];
+#endif
+        g.nt = (seen_by(e.base, e.rows, rt) + KEYS - 1) / KEYS;
+        const int over = per - g.nt;
+        g.units = end - u < per - (off - at) ? end - u : per - (off - at);
+        g.t0 = off - at - over > 0 ? off - at - over : 0;
+        g.t1 = off - at + g.units - over > 0 ? off - at + g.units - over : 0;
+        g.first = u - (off - at) + over;
         return g;
     }
 };
@@ -500,9 +636,9 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
 }
 
 // rows: query rows of an item. tfq_attn_warp.cu: 16, and up to head_dim 128 also 32;
-// tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128. *_box: cache rows of a tensor-map box.
+// tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128; causal: the rows of prompts. *_box: cache rows of a tensor-map box.
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
-cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream);
 int attn_warp_box(int head_dim, int page_size);
 int attn_tc_box(int page_size);
 

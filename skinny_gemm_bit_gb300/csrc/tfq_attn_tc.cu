@@ -23,16 +23,30 @@
 // The reference m of a row moves only when its maximum has grown by more than 2^8: until then
 // the weights stay below 256 and the sums are exact enough, and the output in tensor memory
 // needs no rescaling; when it does, the group first waits for its last product with V.
+//
+// Prompts (CAUSAL) are the same with a limit in the place of a mask: an item is 256 rows of a prompt, and its key
+// tiles end with its last row's.
+//
+// Over a cache of 8 bits (E8) the TMA brings the tiles as they are into a ring of their own, and four more warps turn
+// them into fp16 in the ring that the MMAs read (exactly: fp16 has every e4m3 value), so the MMAs and the
+// rest stay as they are; Q and the weights are fp16 too. The blocks' scales enter the scores and the weights, as in
+// tfq_attn_warp.cu: with the products' own constants for each 16 keys they cost nothing an element. The
+// converting warps also zero what lies behind a sequence's end and take out NaN.
 #include "tfq_attn.cuh"
 
 namespace tfq {
 namespace {
 
-constexpr int kTcThreads = 384;  // eight softmax warps, the producer, an MMA warp for each group, one idle
-// registers: 168 a thread at launch; the last four warps give 96 of theirs to the softmax warps'
-constexpr int kSoftRegs = 216, kOtherRegs = 72;
-static_assert(kSoftRegs * 256 + kOtherRegs * 128 <= 168 * kTcThreads, "no more registers than the launch has");
+// eight softmax warps, the producer, an MMA warp for each group, one idle; 8 bits: and four converting warps
+constexpr int tc_threads(bool e8) { return e8 ? 512 : 384; }
+// registers: 168 a thread at launch; the last four warps give 96 of theirs to the softmax warps'. 8 bits: 128 a thread
+constexpr int kOtherRegs = 72, kConvertRegs = 80;
+constexpr int soft_regs(bool e8) { return e8 ? 176 : 216; }
+static_assert(soft_regs(false) * 256 + kOtherRegs * 128 <= 168 * tc_threads(false), "no more registers than the launch has");
+static_assert(soft_regs(true) * 256 + (kOtherRegs + kConvertRegs) * 128 <= 128 * tc_threads(true), "no more registers than the launch has");
 constexpr int kSoftThreads = 256;
+constexpr int kConvertThreads = 128;
+constexpr float kHead = 7.f;  // fp16 weights reach 2^(kGrow + kHead) = 2^15
 constexpr int kMaxSlots = 12;
 constexpr int KT = 64;                            // keys of a tile
 constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w][buffer] at 128 w + 64 buffer, O[w] at 256 + 128 w
@@ -41,22 +55,39 @@ constexpr float kGrow = 8.f;
 // offsets in shared memory
 constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 288, kTcODone = 320, kTcQReady = 352, kTcOFull = 360, kTcFin = 368;
 constexpr int kTcTmem = 384, kTcFlags = 400 /* [0] abort [2] abort as of a segment's end */, kTcOdd = 416;
+// tokens taken out of V, bits from the item's first: [8] words (trees: 2); 8 bits: [kOddItems][8], as
+// the converting warps may be some items ahead
+constexpr int kOddItems = 8, kTcOdd8 = 512;
+constexpr int kOddTokens = 256;  // behind them no row of the item sees a token
+constexpr int kTcFull8 = 768, kTcEmpty8 = 896;  // 8 bits: the ring of codes
 constexpr int kTcMl = 1024;  // [2][128] (m, l)
 constexpr int kTcSched = 3 * 1024;
-static_assert(kMaxSlots * 8 <= 128, "slots");
+// 8 bits: the rows' factors of the scores; by slot, 3 x [4] of a tile's blocks: 2^ks, log2 vs, 1 / vs; by slot of codes
+// and box, the words with K's and V's scales and their places in them
+constexpr int kMaxCodeSlots = 8;
+constexpr int kTcFactor = 3 * 1024, kTcScales = 4 * 1024, kTcWords = kTcScales + kMaxSlots * 48, kTcSched8 = 6 * 1024;
+static_assert(kTcWords + kMaxCodeSlots * 48 <= kTcSched8, "scales");
+static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 128 && kTcOdd + 32 <= kTcOdd8 && kTcOdd8 + kOddItems * 32 <= kTcFull8, "slots");
 
-template <int HD, bool PAIR>
+template <int HD, bool PAIR, bool E8>
 struct TcCfg {
     static constexpr int ROWS = PAIR ? 256 : 128;
     static constexpr int kSlotBytes = KT * HD * 2;
+    static constexpr int kCodeBytes = KT * HD;  // 8 bits: of a tile of codes
     static constexpr int kQBytes = ROWS * HD * 2 < 32768 ? 32768 : ROWS * HD * 2;  // also the groups' exchange, 2 x 16 KB
-    static constexpr size_t q_off(int B) { return (kTcSched + schedule_bytes(B) + 1023) / 1024 * 1024; }
+    static constexpr size_t q_off(int B) { return ((E8 ? kTcSched8 : kTcSched) + schedule_bytes(B) + 1023) / 1024 * 1024; }
     static constexpr int slots(int B)
     {
-        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes) / kSlotBytes;
-        return n < kMaxSlots ? (int)n : kMaxSlots;
+        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (E8 ? 4 * kCodeBytes : 0)) / kSlotBytes;
+        return E8 && n >= 8 ? 8 : n < kMaxSlots ? (int)n : kMaxSlots;
     }
-    static constexpr size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes; }
+    // an even number: K's tiles lie in the even ones
+    static constexpr int code_slots(int B)
+    {
+        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (size_t)slots(B) * kSlotBytes) / kCodeBytes / 2 * 2;
+        return !E8 ? 0 : n < kMaxCodeSlots ? (int)n : kMaxCodeSlots;
+    }
+    static constexpr size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes + (size_t)code_slots(B) * kCodeBytes; }
 };
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -135,10 +166,10 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint3
     return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
 }
-// Instruction descriptor: fp32 accumulator, bf16 A (K-major) and B, M = 128
-__host__ __device__ constexpr uint32_t instr_desc(int n, bool b_n_major)
+// Instruction descriptor: fp32 accumulator, bf16 (or fp16) A (K-major) and B, M = 128
+__host__ __device__ constexpr uint32_t instr_desc(int n, bool b_n_major, bool f16)
 {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+    return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int y, int z, uint64_t* bar)
@@ -152,19 +183,34 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
 
 __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
-// Infinities and NaN among the block's values were taken out of the product with V: what they add
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Infinities and NaN among the values from token `from` on were taken out of the product with V: what they add
 // to columns c0 .. c0 + 31 of a row that sees their tokens. Rare, so the scores are formed anew.
-template <int HD>
-__device__ __forceinline__ void add_odd(const AttnParams& p, const SeqRows& q, int head, int row, uint64_t odd, uint64_t mask,
+template <int HD, bool E8>
+__device__ __forceinline__ void add_odd(const AttnParams& p, const SeqRows& q, int head, int row, int from, uint64_t odd, uint64_t mask,
                                         float sc, float sign, float ref, int c0, float (&acc)[32])
 {
     const uint16_t* qr = p.q + (q.r0 + p.token_of(row)) * p.ldq + (int64_t)(head * p.group + row % p.group) * HD;
     for (odd &= mask; odd != 0; odd &= odd - 1) {
-        const int tok = q.base + __ffsll((long long)odd) - 1;
+        const int tok = from + __ffsll((long long)odd) - 1;
         const int page = p.c.table[(int64_t)q.slot * p.c.max_pages + (tok >> p.c.page_shift)];
         if (page < 0 || page >= p.c.n_pages)
             continue;
         const int off = tok & (p.c.page_size - 1);
+        if constexpr (E8) {  // e4m3 has no infinities
+            const uint8_t* codes = p.c.codes() + (p.c.row_of(p.layer, 1, page, head) + off) * HD + c0;
+#pragma unroll
+            for (int d = 0; d < 32; ++d)
+                if ((codes[d] & 0x7F) == 0x7F)
+                    acc[d] = NAN;
+            continue;
+        }
         const uint16_t* k = p.c.data + (p.c.row_of(p.layer, 0, page, head) + off) * HD;
         const uint16_t* v = p.c.data + (p.c.row_of(p.layer, 1, page, head) + off) * HD;
         float s = 0.f;
@@ -178,11 +224,22 @@ __device__ __forceinline__ void add_odd(const AttnParams& p, const SeqRows& q, i
     }
 }
 
-template <int HD, bool PAIR>
-__global__ void __launch_bounds__(kTcThreads, 1)
-    tree_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map, uint32_t slots, int q_off)
+// The last key tile of an item, and the shares, by kind of call
+template <int ROWS, bool CAUSAL>
+struct SharesOf {
+    using type = Shares<ROWS, KT, 1, 0>;
+};
+template <int ROWS>
+struct SharesOf<ROWS, true> {
+    using type = PromptShares<ROWS, KT>;
+};
+
+template <int HD, bool PAIR, bool E8, bool CAUSAL>
+__global__ void __launch_bounds__(tc_threads(E8), 1)
+    tree_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map, uint32_t slots, uint32_t code_slots,
+                        int q_off)
 {
-    using C = TcCfg<HD, PAIR>;
+    using C = TcCfg<HD, PAIR, E8>;
     constexpr int ROWS = C::ROWS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
@@ -200,13 +257,29 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     float* ml = reinterpret_cast<float*>(smem + kTcMl);
     uint8_t* qbuf = smem + q_off;
     uint8_t* ring = qbuf + C::kQBytes;
+    // 8 bits: the ring of codes and its barriers, and where the scales lie
+    [[maybe_unused]] uint8_t* code_ring = ring + (size_t)slots * C::kSlotBytes;
+    [[maybe_unused]] uint64_t* full8 = reinterpret_cast<uint64_t*>(smem + kTcFull8);
+    [[maybe_unused]] uint64_t* empty8 = reinterpret_cast<uint64_t*>(smem + kTcEmpty8);
+    [[maybe_unused]] float* factor = reinterpret_cast<float*>(smem + kTcFactor);
+    [[maybe_unused]] float* scales = reinterpret_cast<float*>(smem + kTcScales);
+    [[maybe_unused]] uint32_t* words = reinterpret_cast<uint32_t*>(smem + kTcWords);
+    [[maybe_unused]] unsigned* odd8 = reinterpret_cast<unsigned*>(smem + kTcOdd8);
+    const int box = min(p.c.page_size, KT), pieces = KT / box;  // boxes of a tile
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < slots; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], E8 ? kConvertThreads / 32 : 1);
             mbar_init(&empty[i], PAIR ? 2 : 1);
         }
+        for (uint32_t i = 0; E8 && i < code_slots; ++i) {
+            // each box's lane, and again in V's slots where it has fetched scales
+            mbar_init(&full8[i], 1 + pieces + (i & 1 ? pieces : 0));
+            mbar_init(&empty8[i], kConvertThreads / 32);
+        }
+        for (int i = 0; E8 && i < kOddItems * 8; ++i)
+            odd8[i] = 0;
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 4);
@@ -223,7 +296,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     pdl_wait();
-    Shares<ROWS, KT, 1, 0> shares(p, smem + kTcSched);
+    typename SharesOf<ROWS, CAUSAL>::type shares(p, smem + (E8 ? kTcSched8 : kTcSched));
     tc_fence_before();
     shares.build();  // its barriers publish the tensor-memory address as well
     __syncthreads();
@@ -235,14 +308,102 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // order, by each MMA warp that its ring serves: a wait can then not take the phase before last
     // for the one it is after.
     const uint32_t ring_slots = PAIR ? slots : slots / 2;
+    // The first token that not every row of an item sees
+    auto hidden_from = [&](const Segment& g) { return g.q.base + (CAUSAL ? p.token_of(g.rt * ROWS) : 0); };
 
-    if (warp >= 8) {
+    if (E8 && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+        // ---- codes to fp16: a thread 16 codes of a row. Eight lanes take the same piece of eight rows, so that
+        // neither their reads nor their writes meet in a bank
+        const int ct = threadIdx.x & (kConvertThreads - 1);
+        const int r8 = ct & 7, c = (ct >> 3) % (HD / 16), first_row = (ct >> 3) / (HD / 16) * 8 + r8;
+        constexpr int kStep = kConvertThreads / (HD / 16);  // rows that the threads take at once
+        uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0}, from = 0, from_phase = 0, seg = 0;
+        bool gone = false;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
+        };
+        for (int u = u0; u < u1 && !gone;) {
+            const Segment g = shares.segment(u, u1);
+            u += g.units;
+            if (g.t0 == g.t1)
+                continue;
+            const int hidden = hidden_from(g), len = g.q.len();
+            unsigned* odd_bits = odd8 + seg % kOddItems * 8;
+            for (int t = g.t0; t < g.t1 && !gone; ++t) {
+                const int r = PAIR ? 0 : (t - g.t0) & 1, k0 = t * KT;
+                const bool edge = k0 + KT > hidden;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t slot = r * ring_slots + next_slot[r];
+                    if (!wait(&full8[from], from_phase) || (pass[r] > 0 && !wait(&empty[slot], (pass[r] - 1) & 1))) {
+                        gone = true;
+                        break;
+                    }
+                    const uint8_t* in = code_ring + (size_t)from * C::kCodeBytes;
+                    uint8_t* out = ring + (size_t)slot * C::kSlotBytes;
+#pragma unroll
+                    for (int i = 0; i < KT / kStep; ++i) {
+                        const int row = first_row + i * kStep;
+                        uint4 v = *reinterpret_cast<const uint4*>(in + (HD == 64 ? row * 64 + ((c ^ (row >> 1 & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4)));
+                        if (edge && kv == 1) {
+                            const int tok = k0 + row;
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool bad = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (tok >= len)
+                                    w[k] = 0;
+                                const uint32_t nan = __vcmpeq4(w[k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+                                if (tok >= hidden) {
+                                    bad |= nan != 0;
+                                    w[k] &= ~nan;
+                                }
+                            }
+                            if (bad && tok - hidden < kOddTokens)
+                                atomicOr(&odd_bits[(tok - hidden) >> 5], 1u << ((tok - hidden) & 31));
+                            v = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        uint8_t* line = out + (c >> 2) * (KT * 128) + row * 128;
+                        const int at = 2 * c & 7;
+                        *reinterpret_cast<uint4*>(line + ((at ^ (row & 7)) << 4)) =
+                            make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
+                        *reinterpret_cast<uint4*>(line + ((at + 1 ^ (row & 7)) << 4)) =
+                            make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+                    }
+                    if (kv == 1 && ct < KT / 16) {
+                        const uint32_t* w = words + (from * 4 + ct * 16 / box) * 3;
+                        const uint32_t within = ct * 16 % box / 2;
+                        const int ks = min(max((int)(w[0] >> ((w[2] & 0xFFu) + within) & 0xFFu), 127 - 32), 127 + 32);
+                        const int vs = min(max((int)(w[1] >> ((w[2] >> 8) + within) & 0xFFu), 127 - 32), 127 + 32);
+                        float* to = scales + slot * 12 + ct;
+                        to[0] = __uint_as_float((uint32_t)ks << 23);
+                        to[4] = (float)(vs - 127);
+                        to[8] = __uint_as_float((uint32_t)(254 - vs) << 23);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&full[slot]);
+                        mbar_arrive(&empty8[from]);
+                    }
+                    if (++next_slot[r] == ring_slots) {
+                        next_slot[r] = 0;
+                        ++pass[r];
+                    }
+                    if (++from == code_slots) {
+                        from = 0;
+                        from_phase ^= 1;
+                    }
+                }
+            }
+            ++seg;
+        }
+    } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) {
             // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
-            const int box = min(p.c.page_size, KT), pieces = KT / box;
             const int z = lane / pieces, piece = lane % pieces;
-            const bool active = lane < pieces * (HD / 64);
+            const bool active = lane < pieces * (E8 ? 1 : HD / 64);
             uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0};
             bool gone = false;
             for (int u = u0; u < u1 && !gone;) {
@@ -262,8 +423,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const bool in = active && row < len, good = page >= 0 && page < p.c.n_pages;
                     if (in && !good)
                         record_status(p.status, TF_E_INVALID_ARG);
-                    const int r = PAIR ? 0 : (t - g.t0) & 1;
+                    const int r = PAIR || E8 ? 0 : (t - g.t0) & 1;
                     for (int kv = 0; kv < 2; ++kv) {
+                        if constexpr (E8) {
+                            const uint32_t slot = next_slot[0];
+                            const bool ok = pass[0] == 0 || attn_wait(&empty8[slot], (pass[0] - 1) & 1, flags, p.status, p.limit_ns);
+                            if (!__all_sync(0xffffffffu, ok)) {
+                                gone = true;
+                                break;
+                            }
+                            if (lane == 0)
+                                mbar_arrive_expect_tx(&full8[slot], C::kCodeBytes);
+                            __syncwarp();
+                            if (active) {
+                                const bool there = in && good;
+                                const int y = there ? (int)p.c.row_of(p.layer, kv, page, g.h) + (row & (p.c.page_size - 1)) : p.total_rows;
+                                tma_box(smem_u32(code_ring + (size_t)slot * C::kCodeBytes + piece * box * HD), &map, y, 0, &full8[slot]);
+                                if (kv == 1) {
+                                    // the tile's scales, as the aligned words that hold them
+                                    uint32_t* w = words + (slot * 4 + piece) * 3;
+                                    if (there) {
+                                        const int64_t v = y >> 4, k = v - (((int64_t)p.c.n_pages * p.c.n_kv) << (p.c.page_shift - 4));
+                                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(w)), "l"(p.c.scales + (k & ~3ll)) : "memory");
+                                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(w + 1)), "l"(p.c.scales + (v & ~3ll)) : "memory");
+                                        w[2] = (uint32_t)(k & 3) * 8 | (uint32_t)(v & 3) * 8 << 8;
+                                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full8[slot])) : "memory");
+                                    } else {
+                                        w[0] = w[1] = 0x7F7F7F7Fu;
+                                        w[2] = 0;
+                                        mbar_arrive(&full8[slot]);
+                                    }
+                                }
+                                mbar_arrive(&full8[slot]);
+                            }
+                            if (++next_slot[0] == code_slots) {
+                                next_slot[0] = 0;
+                                ++pass[0];
+                            }
+                            continue;
+                        }
                         const uint32_t slot = r * ring_slots + next_slot[r];
                         const bool ok = pass[r] == 0 || attn_wait(&empty[slot], (pass[r] - 1) & 1, flags, p.status, p.limit_ns);
                         if (!__all_sync(0xffffffffu, ok)) {
@@ -286,18 +484,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
             }
             if (gone)  // no copy may be in flight when the CTA leaves: each slot's last one
-                for (int r = 0; r < (PAIR ? 1 : 2); ++r)
-                    for (uint32_t s = 0; s < ring_slots; ++s) {
+                for (int r = 0; r < (PAIR || E8 ? 1 : 2); ++r)
+                    for (uint32_t s = 0; s < (E8 ? code_slots : ring_slots); ++s) {
                         const uint32_t uses = pass[r] + (s < next_slot[r] ? 1 : 0);
                         if (uses > 0)
-                            mbar_wait_bounded(&full[r * ring_slots + s], (uses - 1) & 1, p.limit_ns);
+                            mbar_wait_bounded(E8 ? &full8[s] : &full[r * ring_slots + s], (uses - 1) & 1, p.limit_ns);
                     }
         } else if (warp < 11) {
             // ---- an MMA warp: group w's scores and its products with V (one warp for both groups spent
             // 1340 cycles a step on its waits, one after the other, for 640 of MMAs)
             const int w = warp - 9;
             const bool one = elect_one();
-            constexpr uint32_t kIdS = instr_desc(KT, false), kIdO = instr_desc(HD, true);
+            constexpr uint32_t kIdS = instr_desc(KT, false, E8), kIdO = instr_desc(HD, true, E8);
             const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
             const uint32_t ra = smem_u32(ring) + first_slot * C::kSlotBytes;
             const uint64_t ad = smem_desc(smem_u32(qbuf) + (PAIR ? w * (128 * HD * 2) : 0), 16, 1024);
@@ -368,7 +566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(E8)));
         // ---- softmax: group w, a thread a row
         const int w = warp >> 2, wt = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -406,24 +604,50 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = r0 + i * kRowsAtOnce;
+                    if constexpr (E8) {
+                        // fp16, the row's largest value moved to 2^14 .. 2^15 by a power of two (tfq_attn_warp.cu)
+                        uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu), __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+                        top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+                        for (int o = HD / 16; o > 0; o >>= 1)
+                            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int up = min(127 + 14 - (int)(top >> 7), 60);
+                        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                        auto pair = [&](uint32_t x) { return f32x2_to_f16x2(bf16lo_f32(x) * f, bf16hi_f32(x) * f); };
+                        v[i] = make_uint4(pair(v[i].x), pair(v[i].y), pair(v[i].z), pair(v[i].w));
+                        if (qc == 0)
+                            factor[r] = sc * __uint_as_float((uint32_t)(127 - up) << 23);
+                    }
                     *reinterpret_cast<uint4*>(qbuf + (r >> 7) * (128 * HD * 2) + (qc >> 3) * (128 * 128) + (r & 127) * 128 + (((qc & 7) ^ (r & 7)) << 4)) =
                         make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
                 }
             }
-            if (threadIdx.x == 0)
-                odd[0] = odd[1] = 0;
+            if (!E8 && threadIdx.x < (CAUSAL ? 8 : 2))
+                odd[threadIdx.x] = 0;
             fence_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(q_ready);
             const int row = g.rt * ROWS + (PAIR ? w * 128 : 0) + wt;
             const bool valid = row < n_rows, busy = __any_sync(0xffffffffu, valid);
+            const int hidden = hidden_from(g);
             uint64_t mask = 0;
+            [[maybe_unused]] int sees = 0;  // causal: tokens that the row sees
             if (valid) {
                 const int t = p.token_of(row);
-                mask = block_mask(p, q, t);
+                if constexpr (CAUSAL)
+                    sees = q.base + t + 1;
+                else
+                    mask = block_mask(p, q, t);
             }
-            float m = -INFINITY, l = 0.f;  // the reference, in score units, and the sum against it
+            // causal: the row's view of 64 tokens from `at` on
+            auto view = [&](int at) -> uint64_t { return sees - at >= 64 ? ~0ull : sees - at <= 0 ? 0ull : ~0ull >> (64 - (sees - at)); };
+            float m = -INFINITY, l = 0.f;  // the reference, in score units (8 bits: times its factor), and the sum against it
+            [[maybe_unused]] float row_factor = 0.f;
+            if constexpr (E8) {
+                named_bar_sync(1, kSoftThreads);  // the rows' factors are there
+                row_factor = factor[(PAIR ? w * 128 : 0) + wt];
+            }
             bool had = false, ok = true;
             int buf = 0;
             for (int t = g.t0 + (PAIR ? 0 : w); t < g.t1; t += PAIR ? 1 : 2, buf ^= 1) {
@@ -433,8 +657,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const uint32_t s_at = tmem + lanes + 128 * w + 64 * buf;
                 tc_fence_after();
                 const int k0 = t * KT;
-                const bool edge = k0 + KT > q.base;
-                if (edge) {
+                const bool edge = k0 + KT > hidden;
+                [[maybe_unused]] const float* blocks = nullptr;
+                if constexpr (E8) {
+                    // the converting warps have seen to V, and left the tile's scales beside it
+                    const uint32_t pos = 2 * tiles + 1;
+                    ok = __all_sync(0xffffffffu, attn_wait(&full[first_slot + pos % ring_slots], (pos / ring_slots) & 1, flags, p.status, p.limit_ns));
+                    if (!ok)
+                        break;
+                    blocks = scales + (first_slot + pos % ring_slots) * 12;
+                } else if (edge) {
                     // values behind the sequence's end become zeros, and infinities and NaN among the
                     // block's own are noted and taken out: a row that does not see them may not meet
                     // them, not even as 0 times NaN. (Of a pair each group does it: what the other has
@@ -444,7 +676,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (!ok)
                         break;
                     const int tok = k0 + wt % KT;
-                    if (tok >= q.base) {
+                    if (tok >= hidden) {
                         // two threads a row; each starts at a piece of its own, for the banks' sake
                         uint8_t* v = ring + (size_t)(first_slot + pos % ring_slots) * C::kSlotBytes + wt % KT * 128;
                         bool bad = false;
@@ -464,8 +696,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             }
                             *at = *reinterpret_cast<uint4*>(x);
                         }
-                        if (bad)
-                            atomicOr(&odd[(tok - q.base) >> 5], 1u << ((tok - q.base) & 31));
+                        if (bad && tok - hidden < kOddTokens)
+                            atomicOr(&odd[(tok - hidden) >> 5], 1u << ((tok - hidden) & 31));
                     }
                     fence_async_smem();
                 }
@@ -477,13 +709,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc_wait_ld(s);
                         tc_wait_ld(s + 32);
                         if (edge) {
-                            const uint64_t see = tile_mask(mask, k0 - q.base);
+                            const uint64_t see = CAUSAL ? view(k0) : tile_mask(mask, k0 - q.base);
 #pragma unroll
                             for (int c = 0; c < KT; ++c)
                                 s[c] = see >> c & 1 ? s[c] : 0xFF800000u;  // -inf
                         }
                     };
+                    [[maybe_unused]] float ks[4], lvs[4];  // 8 bits: factors of the blocks' scores, log2 of their V scales
+                    if constexpr (E8) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            ks[i] = fmaxf(row_factor * blocks[i], 1.2e-38f);  // not 0, which -inf times would be NaN
+                            lvs[i] = blocks[4 + i];
+                        }
+                    }
                     auto largest = [&]() {
+                        if constexpr (E8) {
+                            float x = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    y[c & 1] = fmaxf(y[c & 1], __uint_as_float(s[16 * i + c]));
+                                x = fmaxf(x, fmaf(fmaxf(y[0], y[1]), ks[i], lvs[i]));
+                            }
+                            return x;
+                        }
                         float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int c = 0; c < KT; ++c)
@@ -494,6 +746,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // they add 2^-8 of sum p |v| at most; 64-row trees over 16,001 tokens: 0.0023 of the output's
                     // norm against 64 bits, 0.0017 of it the output's own rounding
                     auto weigh = [&]() {
+                        if constexpr (E8) {  // fp16: 2^-11 of each, below 2^-29 of the row's reference 2^-40 of it
+                            const float ref = (m == -INFINITY ? 0.f : m) - kHead;
+                            float added = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 k2 = make_float2(ks[i], ks[i]), off = make_float2(lvs[i] - ref, lvs[i] - ref);
+                                float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                                for (int c = 16 * i; c < 16 * i + 16; c += 2) {
+                                    float2 e = __ffma2_rn(make_float2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k2, off);
+                                    e.x = attn_ex2(e.x);
+                                    e.y = attn_ex2(e.y);
+                                    sum = __fadd2_rn(sum, e);
+                                    s[c / 2] = f32x2_to_f16x2(e.x, e.y);
+                                }
+                                added = fmaf(sum.x + sum.y, blocks[8 + i], added);
+                            }
+                            return added;
+                        }
                         const float ref = m == -INFINITY ? 0.f : m * sc;
                         const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
                         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -515,12 +786,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // the last reference serves nearly always, so the weights do not wait for the
                     // tile's maximum; when it has grown they are formed again
                     float added = weigh();
-                    const bool grown = had && (top - m) * sc > kGrow;
+                    const float units = E8 ? 1.f : sc;
+                    const bool grown = had && (top - m) * units > kGrow;
                     if (__any_sync(0xffffffffu, grown)) {
                         // the last product with V: the other buffer's, whose phase has moved on since
                         ok = __all_sync(0xffffffffu, attn_wait(&o_done[2 * w + (buf ^ 1)], (phase >> (buf ^ 1) & 1) ^ 1, flags, p.status, p.limit_ns));
                         tc_fence_after();
-                        const float f = grown ? attn_ex2((m - top) * sc) : 1.f;
+                        const float f = grown ? attn_ex2((m - top) * units) : 1.f;
                         if (grown)
                             m = top;
                         l *= f;
@@ -556,7 +828,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool whole = g.t0 == 0 && g.t1 == g.nt;
             float* part = p.parts + (int64_t)(g.t0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * (ROWS * (HD + 2));
             const int prow = (PAIR ? w * 128 : 0) + wt;  // the row within the tile
-            float mine = m == -INFINITY ? -INFINITY : m * sc, top = mine, all = l;
+            float mine = m == -INFINITY ? -INFINITY : E8 ? m : m * sc, top = mine, all = l;
             if (!PAIR) {
                 ml[(w * 128 + wt) * 2] = mine;
                 ml[(w * 128 + wt) * 2 + 1] = l;
@@ -570,12 +842,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             const float ref = top == -INFINITY ? 0.f : top, scale = PAIR ? 1.f : attn_ex2(mine - ref);
             const float inv = all == 0.f ? 0.f : 1.f / all;
-            const uint64_t odd_bits = (uint64_t)odd[1] << 32 | odd[0];
+            [[maybe_unused]] const unsigned* odd_words = E8 ? odd8 + seg % kOddItems * 8 : odd;
+            auto odd_bits = [&](int i) { return (uint64_t)odd_words[2 * i + 1] << 32 | odd_words[2 * i]; };  // tokens hidden + 64 i ..
+            bool any_odd = odd_bits(0) != 0;
+            for (int i = 1; CAUSAL && i < 4; ++i)
+                any_odd |= odd_bits(i) != 0;
             auto put = [&](float (&a)[32], int c0) {  // columns c0 .. c0 + 31 of the row, unscaled
                 if (!valid)
                     return;
-                if (odd_bits != 0)
-                    add_odd<HD>(p, q, g.h, row, odd_bits, mask, sc, sign, ref, c0, a);
+                if (any_odd)
+                    for (int i = 0; i < (CAUSAL ? 4 : 1); ++i)
+                        add_odd<HD, E8>(p, q, g.h, row, hidden + 64 * i, odd_bits(i), CAUSAL ? view(hidden + 64 * i) : mask, sc, sign, ref, c0, a);
                 if (whole) {
                     uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)(q.r0 + p.token_of(row)) * p.n_q + g.h * p.group + p.head_of(row)) * HD + c0);
 #pragma unroll
@@ -635,6 +912,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             named_bar_sync(1, kSoftThreads);  // the Q buffer may be written again; the part is written
             if (flags[2])                     // one answer for all warps
                 break;
+            if (E8 && threadIdx.x < 8)        // for the item kOddItems on, whose tiles wait for those in between
+                odd8[seg % kOddItems * 8 + threadIdx.x] = 0;
             if (!whole) {
                 SplitItem& s = split[g.t0 > 0 ? 0 : 1];
                 s = SplitItem{q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), shares.cta_of(g.first), shares.cta_of(g.first + g.nt - 1)};
@@ -655,33 +934,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 }
 
-template <int HD, bool PAIR>
-constexpr int kPartBytes = TcCfg<HD, PAIR>::ROWS * HD * 4;  // of a part's output
-
-template <int HD, bool PAIR>
+template <int HD, bool PAIR, bool E8, bool CAUSAL>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
 {
-    using C = TcCfg<HD, PAIR>;
+    using C = TcCfg<HD, PAIR, E8>;
     // join_many: fewer parts than ROWS * HD / 4 / kSoftThreads + 1, and a slice's rounding for each
-    static_assert(C::kQBytes + C::slots(kMaxAttnSeqs) * C::kSlotBytes >= kPartBytes<HD, PAIR> + (kPartBytes<HD, PAIR> / 16 / kSoftThreads + 1) * (kSoftThreads * 4 + 16),
-                  "the queries' and the ring's memory takes a slice of the parts");
+    constexpr int kPartBytes = C::ROWS * HD * 4;  // of a part's output
+    static_assert(C::smem(kMaxAttnSeqs) - 1024 - C::q_off(kMaxAttnSeqs) >= kPartBytes + (kPartBytes / 16 / kSoftThreads + 1) * (kSoftThreads * 4 + 16),
+                  "the queries' and the rings' memory takes a slice of the parts");
+    static_assert(!E8 || (C::slots(kMaxAttnSeqs) >= (PAIR ? 3 : 6) && C::code_slots(kMaxAttnSeqs) >= 4), "rings");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(tree_attn_tc_kernel<HD, PAIR>, 227 * 1024, done);
+    const cudaError_t e = allow_smem(tree_attn_tc_kernel<HD, PAIR, E8, CAUSAL>, 227 * 1024, done);
     if (e != cudaSuccess)
         return e;
-    return launch_coop(tree_attn_tc_kernel<HD, PAIR>, dim3(device_sms()), dim3(kTcThreads), C::smem(p.B), stream, p, map,
-                       (uint32_t)C::slots(p.B), (int)C::q_off(p.B));
+    return launch_coop(tree_attn_tc_kernel<HD, PAIR, E8, CAUSAL>, dim3(device_sms()), dim3(tc_threads(E8)), C::smem(p.B), stream, p, map,
+                       (uint32_t)C::slots(p.B), (uint32_t)C::code_slots(p.B), (int)C::q_off(p.B));
+}
+
+template <int HD, bool E8>
+cudaError_t launch_any(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream)
+{
+    if (causal)
+        return launch<HD, true, E8, true>(p, map, stream);
+    return rows == 128 ? launch<HD, false, E8, false>(p, map, stream) : launch<HD, true, E8, false>(p, map, stream);
 }
 
 }  // namespace
 
 int attn_tc_box(int page_size) { return page_size < KT ? page_size : KT; }
 
-cudaError_t launch_attn_tc(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream)
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream)
 {
-    if (p.c.head_dim == 64)
-        return rows == 128 ? launch<64, false>(p, map, stream) : launch<64, true>(p, map, stream);
-    return rows == 128 ? launch<128, false>(p, map, stream) : launch<128, true>(p, map, stream);
+    if (p.c.code == TF_KV_E4M3)
+        return p.c.head_dim == 64 ? launch_any<64, true>(p, rows, causal, map, stream) : launch_any<128, true>(p, rows, causal, map, stream);
+    return p.c.head_dim == 64 ? launch_any<64, false>(p, rows, causal, map, stream) : launch_any<128, false>(p, rows, causal, map, stream);
 }
 
 }  // namespace tfq

@@ -16,6 +16,13 @@
 //
 // Tiles land with the 128-byte swizzle (16-byte piece c of row r at c ^ (r % 8)), so the eight
 // rows of an ldmatrix fall in different banks. A box is one page's rows of a tile.
+//
+// Over a cache of 8 bits (E4M3) the same warps read half the bytes. e4m3 codes become fp16 between ldmatrix and the
+// MMA, two by one conversion: K's four codes of a lane are two fragments' worth of 16 columns in an order of their own,
+// which Q is stored in, and V's come by transposed 16-bit units, whose byte pairs belong to neighbouring columns:
+// each 16 columns make an even and an odd tile of the output. The scales cost nothing an element: with K's
+// in the factor of a block's scores and V's exponent added to them, x_j = score + log2 vs_j, weights are
+// w_j = 2^(x_j - m), and o = sum w_j code_j / sum w_j / vs_j.
 #include "tfq_attn.cuh"
 
 namespace tfq {
@@ -25,20 +32,25 @@ constexpr int kWarps = 8;
 constexpr int kCtaThreads = kWarps * 32;
 constexpr float kGrow = 8.f;  // the reference of a row moves when its maximum has grown by 2^8
 
-template <int HD, int RW>
+template <int HD, int RW, bool E8>
 struct Cfg {
     static constexpr int CH = HD == 256 ? 1 : 2;          // 16-key pieces of a tile
     static constexpr int KT = 16 * CH;
     static constexpr int ROWS = 16 * RW;
-    static constexpr int kSlotBytes = KT * HD * 2;        // K or V of a tile
-    static constexpr int kSlots = 24576 / kSlotBytes;     // of a warp: 3, or 6 at head_dim 64
-    static constexpr int kCols = RW == 2 ? 8 : 16;         // output columns joined at once, as shared memory allows
+    static constexpr int kSlotBytes = KT * HD * (E8 ? 1 : 2);  // K or V of a tile
+    // slots of a warp: 3, or 6 at head_dim 64; of 8 bits 5 to 12
+    static constexpr int kSlots = (E8 && RW == 2 ? 20480 : 24576) / kSlotBytes;
+    static constexpr int kCols = RW == 2 && !E8 ? 8 : 16;  // output columns joined at once, as shared memory allows
     static constexpr int kStride = kCols + 4;             // floats
     static constexpr int kMlOff = 0;                      // [kWarps][ROWS][2] floats
     static constexpr int kBarOff = kMlOff + kWarps * ROWS * 2 * 4;
     static constexpr int kFlagOff = kBarOff + kWarps * kSlots * 8;  // [0] abort [2] abort, as of a segment's end
+    // 8 bits: the rows' factors of the scores; by K slot and box, the words with K's and V's scales and their places
+    static constexpr int kRowOff = kFlagOff + 16;
+    static constexpr int kScaleOff = kRowOff + (E8 ? ROWS * 4 : 0);
+    static constexpr int kScaleWords = E8 ? kSlots * 2 * 3 : 0;  // of a warp
     // the item's queries, and after its last tile what the warps hand over
-    static constexpr int kQOff = (kFlagOff + 16 + 1023) / 1024 * 1024;
+    static constexpr int kQOff = (kScaleOff + kWarps * kScaleWords * 4 + 1023) / 1024 * 1024;
     static constexpr int kOutBytes = kWarps * ROWS * kStride * 4;
     static constexpr int kSchedOff = kQOff + (ROWS * HD * 2 > kOutBytes ? ROWS * HD * 2 : kOutBytes);
     static constexpr __host__ __device__ size_t ring(int B) { return (kSchedOff + schedule_bytes(B) + 1023) / 1024 * 1024; }
@@ -77,12 +89,37 @@ __device__ __forceinline__ uint32_t nonfinite2(uint32_t x)
     return ((x & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 
-// RW row tiles of 16 (16 RW query rows an item).
-template <int HD, int RW>
+// The same of an fp16 pair.
+__device__ __forceinline__ uint32_t nonfinite2_f16(uint32_t x)
+{
+    return ((x & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) | ((x & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
+}
+
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Where 16-byte piece c of row r of a box lies: rows of 128 bytes (64 at head_dim 64), swizzled by the TMA.
+template <int HD>
+__device__ __forceinline__ uint32_t piece8(int r, int c, int half)
+{
+    return HD == 64 ? r * 64 + ((c ^ (r >> 1 & 3)) << 4) : (c >> 3) * half + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// 2^(scale byte - 127), the byte within its bounds
+__device__ __forceinline__ int scale_bits(uint32_t word, uint32_t at) { return min(max((int)(word >> at & 0xFFu), 127 - 32), 127 + 32); }
+
+constexpr float kHead = 7.f;  // fp16 weights reach 2^(kGrow + kHead) = 2^15, and 2^-24 is 2^-31 of a row's reference
+
+// Tile scores of 8 bits: the rows' weights in fp16, RW row tiles of 16 (16 RW query rows an item).
+template <int HD, int RW, bool E8>
 __global__ void __launch_bounds__(kCtaThreads, 1)
     tree_attn_warp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map)
 {
-    using C = Cfg<HD, RW>;
+    using C = Cfg<HD, RW, E8>;
     constexpr int ROWS = C::ROWS, KT = C::KT, CH = C::CH, NC = HD / 8, KS = HD / 16, NS = C::kSlots;
     constexpr bool kQRegs = RW == 1 && HD <= 128;  // the rows' A fragments in registers
     extern __shared__ uint8_t smem_raw[];
@@ -95,9 +132,14 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     float* outbuf = reinterpret_cast<float*>(qbuf);
     uint8_t* ring = smem + C::ring(p.B) + (size_t)warp * NS * C::kSlotBytes;
 
+    [[maybe_unused]] float* row_factor = reinterpret_cast<float*>(smem + C::kRowOff);
+    // of slot s, box b, at 3 (2 s + b): K's word, V's word, their scales' places in them (bits)
+    [[maybe_unused]] uint32_t* scale_words = reinterpret_cast<uint32_t*>(smem + C::kScaleOff) + warp * C::kScaleWords;
+    const int box = min(p.c.page_size, KT), bs = KT / box - 1;  // a tile is 1 << bs boxes, one or two
+
     if (lane == 0) {
         for (int i = 0; i < NS; ++i)
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], E8 ? bs + 2 : 1);  // 8 bits: and one for each lane that fetches scales
         fence_mbar_init();
     }
     if (threadIdx.x == 0) {
@@ -114,7 +156,6 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
 
     // ---- the warp's loads, in the order it will read them: K, V of its first tile, of its next ...
-    const int box = min(p.c.page_size, KT), bs = KT / box - 1;  // a tile is 1 << bs boxes, one or two
     const int ahead = 32 >> bs;  // tiles whose pages the lanes hold at once
     int lu = u0;                   // first unit of the segment that the next load belongs to
     Segment lg{};                  // that segment
@@ -155,7 +196,26 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                 else
                     record_status(p.status, TF_E_INVALID_ARG);
             }
-            tma_rows(smem_u32(ring + slot * C::kSlotBytes + lane * box * HD * 2), &map, y, &full[slot]);
+            tma_rows(smem_u32(ring + slot * C::kSlotBytes + lane * box * HD * (E8 ? 1 : 2)), &map, y, &full[slot]);
+            if constexpr (E8) {
+                if (lkv == 0) {
+                    // the tile's scales, K's and V's, as the aligned words that hold them
+                    uint32_t* words = scale_words + 3 * (2 * slot + lane);
+                    if (y < p.total_rows) {
+                        const int64_t k = y >> 4, v = k + (((int64_t)p.c.n_pages * p.c.n_kv) << (p.c.page_shift - 4));
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(words)), "l"(p.c.scales + (k & ~3ll)) : "memory");
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(words + 1)), "l"(p.c.scales + (v & ~3ll)) : "memory");
+                        words[2] = (uint32_t)(k & 3) * 8 | (uint32_t)(v & 3) * 8 << 8;
+                        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full[slot])) : "memory");
+                    } else {
+                        words[0] = words[1] = 0x7F7F7F7Fu;
+                        words[2] = 0;
+                        mbar_arrive(&full[slot]);
+                    }
+                } else {
+                    mbar_arrive(&full[slot]);
+                }
+            }
         }
         ++issued;
         if (lkv == 0) {
@@ -214,7 +274,28 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             const int piece = threadIdx.x + i * kCtaThreads, r = piece / (HD / 8), c = piece % (HD / 8);
-            if (piece < kPieces)
+            if constexpr (E8) {
+                // fp16, the row's largest value moved to 2^14 .. 2^15 by a power of two: what is below 2^-38 of it is
+                // lost, 2^-39 of it at most (an fp32 sum of the products rounds off more)
+                uint32_t top = __vmaxu2(__vmaxu2(mine[i].x & 0x7FFF7FFFu, mine[i].y & 0x7FFF7FFFu),
+                                        __vmaxu2(mine[i].z & 0x7FFF7FFFu, mine[i].w & 0x7FFF7FFFu));
+                top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+                for (int o = HD / 16; o > 0; o >>= 1)
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const int up = min(127 + 14 - (int)(top >> 7), 60);
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                if (piece < kPieces) {
+                    auto pair = [&](uint32_t w) { return f32x2_to_f16x2(bf16lo_f32(w) * f, bf16hi_f32(w) * f); };
+                    // K's four codes of a lane are columns 4 ti .. 4 ti + 3 of 16; the MMA's places for them are
+                    // 2 ti, 2 ti + 1, 2 ti + 8 and 2 ti + 9
+                    auto at = [&](int piece) { return qbuf + (piece >> 3) * (ROWS * 128) + r * 128 + (((piece & 7) ^ (r & 7)) << 4) + (c & 1) * 8; };
+                    *reinterpret_cast<uint2*>(at(c & ~1)) = make_uint2(pair(mine[i].x), pair(mine[i].z));
+                    *reinterpret_cast<uint2*>(at(c | 1)) = make_uint2(pair(mine[i].y), pair(mine[i].w));
+                    if (c == 0)
+                        row_factor[r] = p.scale_log2 * __uint_as_float((uint32_t)(127 - up) << 23);
+                }
+            } else if (piece < kPieces)
                 *reinterpret_cast<uint4*>(qbuf + (c >> 3) * (ROWS * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = mine[i];
         }
         // the masks of the lane's rows
@@ -226,6 +307,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         }
         named_bar_sync(1, kCtaThreads);
         const uint32_t q_at = smem_u32(qbuf);
+        [[maybe_unused]] float factor[RW][2];
+        if constexpr (E8) {
+#pragma unroll
+            for (int i = 0; i < 2 * RW; ++i)
+                factor[i >> 1][i & 1] = row_factor[(i >> 1) * 16 + (i & 1) * 8 + gi];
+        }
         auto q_frag = [&](uint32_t (&a)[4], int rw, int ks) {
             ldsm4(a, q_at + (ks >> 2) * (ROWS * 128) + (rw * 16 + v_row) * 128 + ((((ks & 3) * 2 + v_bit) ^ (v_row & 7)) << 4));
         };
@@ -255,6 +342,42 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             // S = Q K^T
             const uint32_t k_at = smem_u32(ring + ks_slot * C::kSlotBytes);
             float s[RW][2 * CH][4] = {};
+            [[maybe_unused]] int ks_bits[CH], vs_bits[CH];  // scale bytes of the tile's blocks
+            if constexpr (E8) {
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) {
+                    const uint32_t* words = scale_words + 3 * (2 * ks_slot + ch * 16 / box);
+                    const uint32_t places = words[2], within = (ch * 16 % box) / 2;
+                    ks_bits[ch] = scale_bits(words[0], (places & 0xFFu) + within);
+                    vs_bits[ch] = scale_bits(words[1], (places >> 8) + within);
+                }
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) {
+                    const uint32_t at = k_at + (ch * 16 / box) * (box * HD) + (ch * 16 % box) * (HD == 64 ? 64 : 128);
+#pragma unroll
+                    for (int kq = 0; kq < KS; kq += 4) {
+                        uint32_t b[2][4];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            ldsm4(b[j], at + piece8<HD>(k_row, kq + j * 2 + k_bit, half));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo = b[j >> 1][j & 1], hi = b[j >> 1][2 + (j & 1)];
+                            const uint32_t l0 = e4m3x2_to_f16x2(lo), l1 = e4m3x2_to_f16x2(lo >> 16), h0 = e4m3x2_to_f16x2(hi), h1 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+                            for (int r = 0; r < RW; ++r) {
+                                uint32_t a[4];
+                                if (kQRegs)
+                                    a[0] = qa[kQRegs ? kq + j : 0][0], a[1] = qa[kQRegs ? kq + j : 0][1], a[2] = qa[kQRegs ? kq + j : 0][2], a[3] = qa[kQRegs ? kq + j : 0][3];
+                                else
+                                    q_frag(a, r, kq + j);
+                                mma_f16_16816(s[r][2 * ch], a[0], a[1], a[2], a[3], l0, l1);
+                                mma_f16_16816(s[r][2 * ch + 1], a[0], a[1], a[2], a[3], h0, h1);
+                            }
+                        }
+                    }
+                }
+            } else
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
                 const uint32_t at = k_at + (ch * 16 / box) * (box * HD * 2) + (ch * 16 % box) * 128 + k_row * 128;
@@ -289,8 +412,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 2 * CH; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        s[r][i][j] *= p.scale_log2;
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (E8)
+                            s[r][i][j] = fmaf(s[r][i][j], factor[r][j >> 1] * __uint_as_float((uint32_t)ks_bits[i >> 1] << 23), (float)(vs_bits[i >> 1] - 127));
+                        else
+                            s[r][i][j] *= p.scale_log2;
+                    }
                 if (edge) {
                     see[r][0] = see[r][1] = 0u;
 #pragma unroll
@@ -328,13 +455,20 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                             o[r][i][2 * h] *= f, o[r][i][2 * h + 1] *= f;
                     }
                 }
-                const float ref0 = m[r][0] == -INFINITY ? 0.f : m[r][0], ref1 = m[r][1] == -INFINITY ? 0.f : m[r][1];
+                const float head = E8 ? kHead : 0.f;
+                const float ref0 = (m[r][0] == -INFINITY ? 0.f : m[r][0]) - head, ref1 = (m[r][1] == -INFINITY ? 0.f : m[r][1]) - head;
 #pragma unroll
                 for (int i = 0; i < 2 * CH; ++i) {
                     s[r][i][0] = attn_ex2(s[r][i][0] - ref0), s[r][i][1] = attn_ex2(s[r][i][1] - ref0);
                     s[r][i][2] = attn_ex2(s[r][i][2] - ref1), s[r][i][3] = attn_ex2(s[r][i][3] - ref1);
-                    l[r][0] += s[r][i][0] + s[r][i][1];
-                    l[r][1] += s[r][i][2] + s[r][i][3];
+                    if constexpr (E8) {
+                        const float inv_vs = __uint_as_float((uint32_t)(254 - vs_bits[i >> 1]) << 23);
+                        l[r][0] = fmaf(s[r][i][0] + s[r][i][1], inv_vs, l[r][0]);
+                        l[r][1] = fmaf(s[r][i][2] + s[r][i][3], inv_vs, l[r][1]);
+                    } else {
+                        l[r][0] += s[r][i][0] + s[r][i][1];
+                        l[r][1] += s[r][i][2] + s[r][i][3];
+                    }
                 }
             }
             // weights rounded to bf16, as the product with V takes them: up to 2^-8 of each, 2^-8 of sum p |v| in
@@ -342,15 +476,17 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             // against 64 bits, 0.0017 of it the output's own rounding. Their sum is of the unrounded ones. A second
             // product with what the rounding left took 64 ragged sequences from 174 to 176 us, one token over 4097
             // from 10.6 to 10.8 and 8 x 8 rows over 2000 from 20.0 to 21.8.
+            // Over 8 bits they are rounded to fp16: 2^-11 of each, below 2^-29 of the row's reference 2^-40 of it.
             uint32_t w[RW][CH][4];
+            auto pair = [](float lo, float hi) { return E8 ? f32x2_to_f16x2(lo, hi) : f32x2_to_bf16x2(lo, hi); };
 #pragma unroll
             for (int r = 0; r < RW; ++r)
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    w[r][ch][0] = f32x2_to_bf16x2(s[r][2 * ch][0], s[r][2 * ch][1]);
-                    w[r][ch][1] = f32x2_to_bf16x2(s[r][2 * ch][2], s[r][2 * ch][3]);
-                    w[r][ch][2] = f32x2_to_bf16x2(s[r][2 * ch + 1][0], s[r][2 * ch + 1][1]);
-                    w[r][ch][3] = f32x2_to_bf16x2(s[r][2 * ch + 1][2], s[r][2 * ch + 1][3]);
+                    w[r][ch][0] = pair(s[r][2 * ch][0], s[r][2 * ch][1]);
+                    w[r][ch][1] = pair(s[r][2 * ch][2], s[r][2 * ch][3]);
+                    w[r][ch][2] = pair(s[r][2 * ch + 1][0], s[r][2 * ch + 1][1]);
+                    w[r][ch][3] = pair(s[r][2 * ch + 1][2], s[r][2 * ch + 1][3]);
                 }
 
             // O += P V
@@ -359,6 +495,66 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             if (!alive)
                 break;
             const uint32_t v_at = smem_u32(ring + vs * C::kSlotBytes);
+            if constexpr (E8) {
+#pragma unroll
+                for (int ch = 0; ch < CH; ++ch) {
+                    const uint32_t at = v_at + (ch * 16 / box) * (box * HD) + (ch * 16 % box) * (HD == 64 ? 64 : 128);
+                    const int left = edge ? len - (k0 + ch * 16) : 16;  // keys of the piece that exist
+                    if (left <= 0)
+                        continue;
+                    // nothing behind the sequence's end takes part: not even as 0 times NaN
+                    const uint32_t in_lo = (2 * ti < left ? 0xFFFFu : 0u) | (2 * ti + 1 < left ? 0xFFFF0000u : 0u);
+                    const uint32_t in_hi = (2 * ti + 8 < left ? 0xFFFFu : 0u) | (2 * ti + 9 < left ? 0xFFFF0000u : 0u);
+                    uint32_t odd = 0;
+#pragma unroll
+                    for (int c = 0; c < HD / 16; c += 2) {
+                        uint32_t b[4];
+                        ldsm4_trans(b, at + piece8<HD>(v_row, c + v_bit, half));
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            // keys 2 ti, 2 ti + 1 and 2 ti + 8, 2 ti + 9 of an even column and of the next
+                            const uint32_t even = __byte_perm(b[2 * j], b[2 * j + 1], 0x6420), next = __byte_perm(b[2 * j], b[2 * j + 1], 0x7531);
+                            uint32_t v[4] = {e4m3x2_to_f16x2(even), e4m3x2_to_f16x2(even >> 16), e4m3x2_to_f16x2(next), e4m3x2_to_f16x2(next >> 16)};
+                            if (edge) {
+                                v[0] &= in_lo, v[1] &= in_hi, v[2] &= in_lo, v[3] &= in_hi;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t x = nonfinite2_f16(v[k]);
+                                    odd |= x;
+                                    v[k] &= ~x;
+                                }
+                            }
+#pragma unroll
+                            for (int r = 0; r < RW; ++r) {
+                                mma_f16_16816(o[r][2 * (c + j)], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], v[0], v[1]);
+                                mma_f16_16816(o[r][2 * (c + j) + 1], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], v[2], v[3]);
+                            }
+                        }
+                    }
+                    if (edge && __any_sync(0xffffffffu, odd != 0)) {
+                        // NaN among the values: it reaches the rows that see its key alone
+#pragma unroll 1
+                        for (int k = 0; k < 16 && k < left; ++k) {
+                            const int src = (lane & ~3) | ((k & 7) >> 1), bit = ch * 4 + (k >> 3) * 2 + (k & 1);
+#pragma unroll
+                            for (int r = 0; r < RW; ++r) {
+                                const bool s0 = __shfl_sync(0xffffffffu, see[r][0], src) >> bit & 1, s1 = __shfl_sync(0xffffffffu, see[r][1], src) >> bit & 1;
+#pragma unroll
+                                for (int c = 0; c < HD / 16; ++c) {
+                                    uint32_t v;
+                                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + piece8<HD>(k, c, half) + ti * 4) : "memory");
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)  // columns 4 ti + i of the piece
+                                        if ((v >> (8 * i) & 0x7Fu) == 0x7Fu) {
+                                            if (s0) o[r][2 * c + (i & 1)][i >> 1] = NAN;
+                                            if (s1) o[r][2 * c + (i & 1)][2 + (i >> 1)] = NAN;
+                                        }
+                                }
+                            }
+                        }
+                    }
+                }
+            } else
 #pragma unroll
             for (int ch = 0; ch < CH; ++ch) {
                 const uint32_t at = v_at + (ch * 16 / box) * (box * HD * 2) + (ch * 16 % box) * 128;
@@ -507,6 +703,13 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             float* round = last ? rings + c0 / C::kCols * kRound : outbuf;
 #pragma unroll
             for (int r = 0; r < RW; ++r) {
+                if constexpr (E8) {  // an even and an odd tile: columns 4 ti .. 4 ti + 3
+                    float* to = round + (warp * ROWS + r * 16 + gi) * C::kStride + ti * 4;
+                    const float *a = o[r][c0 / 8], *b = o[r][c0 / 8 + 1];
+                    *reinterpret_cast<float4*>(to) = make_float4(a[0] * f[r][0], b[0] * f[r][0], a[1] * f[r][0], b[1] * f[r][0]);
+                    *reinterpret_cast<float4*>(to + 8 * C::kStride) = make_float4(a[2] * f[r][1], b[2] * f[r][1], a[3] * f[r][1], b[3] * f[r][1]);
+                    continue;
+                }
                 float* to = round + (warp * ROWS + r * 16 + gi) * C::kStride + ti * 2;
 #pragma unroll
                 for (int i = 0; i < C::kCols / 8; ++i) {
@@ -546,15 +749,26 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         mbar_wait_bounded(&full[taken % NS], (taken / NS) & 1, p.limit_ns);
 }
 
-template <int HD, int RW>
+template <int HD, int RW, bool E8>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
 {
-    static_assert(Cfg<HD, RW>::smem(kMaxAttnSeqs) <= 227 * 1024, "shared memory");
+    using C = Cfg<HD, RW, E8>;
+    static_assert(C::smem(kMaxAttnSeqs) <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(tree_attn_warp_kernel<HD, RW>, (int)Cfg<HD, RW>::smem(kMaxAttnSeqs), done);
+    const cudaError_t e = allow_smem(tree_attn_warp_kernel<HD, RW, E8>, (int)C::smem(kMaxAttnSeqs), done);
     if (e != cudaSuccess)
         return e;
-    return launch_coop(tree_attn_warp_kernel<HD, RW>, dim3(device_sms()), dim3(kCtaThreads), Cfg<HD, RW>::smem(p.B), stream, p, map);
+    return launch_coop(tree_attn_warp_kernel<HD, RW, E8>, dim3(device_sms()), dim3(kCtaThreads), C::smem(p.B), stream, p, map);
+}
+
+template <bool E8>
+cudaError_t launch_any(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream)
+{
+    if (p.c.head_dim == 64)
+        return rows == 16 ? launch<64, 1, E8>(p, map, stream) : launch<64, 2, E8>(p, map, stream);
+    if (p.c.head_dim == 128)
+        return rows == 16 ? launch<128, 1, E8>(p, map, stream) : launch<128, 2, E8>(p, map, stream);
+    return launch<256, 1, E8>(p, map, stream);
 }
 
 }  // namespace
@@ -563,11 +777,7 @@ int attn_warp_box(int head_dim, int page_size) { return head_dim == 256 ? 16 : p
 
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream)
 {
-    if (p.c.head_dim == 64)
-        return rows == 16 ? launch<64, 1>(p, map, stream) : launch<64, 2>(p, map, stream);
-    if (p.c.head_dim == 128)
-        return rows == 16 ? launch<128, 1>(p, map, stream) : launch<128, 2>(p, map, stream);
-    return launch<256, 1>(p, map, stream);
+    return p.c.code == TF_KV_E4M3 ? launch_any<true>(p, rows, map, stream) : launch_any<false>(p, rows, map, stream);
 }
 
 }  // namespace tfq

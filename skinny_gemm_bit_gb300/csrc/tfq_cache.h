@@ -12,11 +12,16 @@ constexpr int kMaxDraftRows = TF_MAX_DRAFT_ROWS;
 
 // Passed by value. Row r of page p of head h (K: kv = 0, V: 1) of a layer starts at element
 //   ((((layer * 2 + kv) * n_pages + p) * n_kv + h) * page_size + r) * head_dim   (64 bits)
+// Of an 8-bit cache `data` holds bytes, and pool row i (row_of + r) belongs to the block with scale byte i / 16.
 struct CacheView {
     uint16_t* data;
     int32_t *len, *refs, *table;
     int n_layers, n_kv, head_dim, page_size, page_shift;
     int n_seqs, n_pages, max_pages;
+    int code;         // TF_KV_*
+    uint8_t* scales;  // of an 8-bit cache
+    __host__ __device__ uint8_t* codes() const { return reinterpret_cast<uint8_t*>(data); }
+    __host__ __device__ int elem_bytes() const { return code == TF_KV_E4M3 ? 1 : 2; }
 
     __host__ __device__ int64_t row_of(int layer, int kv, int page, int head) const
     {
@@ -62,7 +67,8 @@ inline bool outputs_overlap(const MemRange* r, int n_out, int n)
 // Whether a range, or rows x cols elements of 2 bytes (leading dimension ld), shares memory with the cache's data or book.
 inline bool in_cache(const CacheView& c, const MemRange& r)
 {
-    return overlap(r, MemRange{c.data, (size_t)c.row_of(c.n_layers, 0, 0, 0) * c.head_dim * 2}) ||
+    return overlap(r, MemRange{c.data, (size_t)c.row_of(c.n_layers, 0, 0, 0) * c.head_dim * c.elem_bytes()}) ||
+           overlap(r, MemRange{c.scales, (size_t)c.row_of(c.n_layers, 0, 0, 0) / TF_KV_BLOCK}) ||
            overlap(r, MemRange{c.len, (c.n_seqs + (size_t)c.n_pages + (size_t)c.n_seqs * c.max_pages) * 4});
 }
 inline bool in_cache(const CacheView& c, const void* a, int64_t ld, int64_t cols, int64_t rows)

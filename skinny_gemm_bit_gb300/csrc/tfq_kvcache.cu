@@ -315,18 +315,21 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(CacheView c, co
 }
 
 // Copies `rows` rows of every head of a page, in all layers, K and V. A unit is one
-// (copy, layer, kv, head): rows * head_dim elements in a row on both sides.
+// (copy, layer, kv, head): rows * head_dim elements in a row on both sides, and in 8 bits their blocks' scales.
 __device__ void copy_pages(const CacheView& c, const CopyItem* items, int n_items, int block, int n_blocks)
 {
     const int units_per = c.n_layers * 2 * c.n_kv;
     const int64_t units = (int64_t)n_items * units_per;
-    const int row16 = c.head_dim / 8;
+    const int row_bytes = c.head_dim * c.elem_bytes(), row16 = row_bytes / 16;
     for (int64_t u = block; u < units; u += n_blocks) {
         const CopyItem it = items[u / units_per];
         const int lkh = (int)(u % units_per), head = lkh % c.n_kv, lk = lkh / c.n_kv;
-        const uint4* src = reinterpret_cast<const uint4*>(c.data + c.row_of(lk >> 1, lk & 1, it.src, head) * c.head_dim);
-        uint4* dst = reinterpret_cast<uint4*>(c.data + c.row_of(lk >> 1, lk & 1, it.dst, head) * c.head_dim);
+        const int64_t from = c.row_of(lk >> 1, lk & 1, it.src, head), to = c.row_of(lk >> 1, lk & 1, it.dst, head);
+        const uint4* src = reinterpret_cast<const uint4*>(c.codes() + from * row_bytes);
+        uint4* dst = reinterpret_cast<uint4*>(c.codes() + to * row_bytes);
         const int n = it.rows * row16;
+        if (c.code == TF_KV_E4M3 && (int)threadIdx.x < (it.rows + 15) / 16)
+            c.scales[to / 16 + threadIdx.x] = c.scales[from / 16 + threadIdx.x];
         for (int i = threadIdx.x; i < n; i += 4 * kCopyThreads) {
             uint4 v[4];
 #pragma unroll
@@ -502,6 +505,138 @@ __global__ void __launch_bounds__(kCopyThreads) keep_move_kernel(CacheView c, co
     }
 }
 
+// The same for a cache of 8 bits: a thread moves 16 codes of a row. The lanes of one head (head_dim / 16 of a warp)
+// read the scales of the sequence's last blocks (five at most), all before one of them writes the new ones. Behind the
+// first row that moves every kept row moves, so one block at most holds rows that stay beside rows that join it.
+constexpr int kKeepBlocks = kMaxDraftRows / TF_KV_BLOCK + 1;
+
+// e4m3 codes rounded to a scale 2^d times theirs (d <= 0), four in w
+__device__ __forceinline__ uint32_t rescaled4(uint32_t w, float f)
+{
+    uint32_t out = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t h = e4m3x2_to_f16x2(w >> (16 * i));
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        out |= f32x2_to_e4m3x2(v.x * f, v.y * f) << (16 * i);
+    }
+    return out;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) keep_move8_kernel(CacheView c, const int32_t* __restrict__ q_start,
+                                                                  const int32_t* __restrict__ keep, int64_t M, void* ws)
+{
+    __shared__ SlotPlan pl;
+    __shared__ int64_t src[kMaxDraftRows], dst[kMaxDraftRows];  // rows of head 0 of page 0; src < 0: stays
+    __shared__ int src_block[kMaxDraftRows], dst_block[kMaxDraftRows];
+    __shared__ int64_t block_row[kKeepBlocks];  // first row of each block; < 0: the sequence has no such block
+    const int64_t at = (int64_t)q_start[blockIdx.y] + threadIdx.x;
+    const int from = threadIdx.x < kMaxDraftRows && at >= 0 && at < M ? keep[at] : 0;
+    const int row16 = c.head_dim / 16, cols = c.n_layers * 2 * c.n_kv * row16;
+    const int col = blockIdx.x * kCopyThreads + threadIdx.x;
+    const int lkh = col / row16, head = lkh % c.n_kv, lk = lkh / c.n_kv;
+    pdl_wait();
+    if (threadIdx.x < sizeof(SlotPlan) / 4)
+        reinterpret_cast<int32_t*>(&pl)[threadIdx.x] = __ldcg(reinterpret_cast<const int32_t*>(plan_slots(ws) + blockIdx.y) + threadIdx.x);
+    __syncthreads();
+    const int n = pl.new_len;
+    if (n <= 0)
+        return;
+    const int first = pl.old_len >> c.page_shift, block0 = pl.old_len / TF_KV_BLOCK;
+    auto place = [&](int row) {
+        return (int64_t)pl.pages[(row >> c.page_shift) - first] * c.n_kv * c.page_size + (row & (c.page_size - 1));
+    };
+    // the rows that are read end at the last kept one
+    const int last = at - threadIdx.x + n - 1 < M && n - 1 < kMaxDraftRows ? keep[q_start[blockIdx.y] + n - 1] : 0;
+    if ((int)threadIdx.x < n) {
+        const int j = threadIdx.x;
+        src[j] = from == j ? -1 : place(pl.old_len + from);
+        dst[j] = place(pl.old_len + j);
+        src_block[j] = (pl.old_len + from) / TF_KV_BLOCK - block0;
+        dst_block[j] = (pl.old_len + j) / TF_KV_BLOCK - block0;
+    }
+    if (threadIdx.x < kKeepBlocks) {
+        const int row = max((block0 + (int)threadIdx.x) * TF_KV_BLOCK, first << c.page_shift);
+        block_row[threadIdx.x] = row <= pl.old_len + last ? place(row) : -1;
+    }
+    __syncthreads();
+    const bool live = col < cols;  // whole groups of lanes: cols and the block are multiples of row16
+    const int64_t base = live ? c.row_of(lk >> 1, lk & 1, 0, head) : 0;
+    uint8_t* codes = c.codes() + (live ? (col - lkh * row16) * 16 : 0);
+    int old[kKeepBlocks], now[kKeepBlocks];
+    unsigned joined = 0;  // blocks that rows join
+#pragma unroll
+    for (int b = 0; b < kKeepBlocks; ++b) {
+        old[b] = live && block_row[b] >= 0 ? min(max((int)c.scales[(base + block_row[b]) / TF_KV_BLOCK], 127 - 32), 127 + 32) : 0;
+        now[b] = old[b];
+    }
+    int stay = -1, stay_rows = 0;  // the block that keeps rows and takes others; how many it keeps
+    for (int j = 0; j < n; ++j) {
+        if (src[j] < 0)
+            continue;
+        const int b = dst_block[j], row = (pl.old_len + j) % TF_KV_BLOCK;
+        int theirs = 0;
+#pragma unroll
+        for (int k = 0; k < kKeepBlocks; ++k)
+            theirs = k == src_block[j] ? old[k] : theirs;
+#pragma unroll
+        for (int k = 0; k < kKeepBlocks; ++k)
+            if (k == b)
+                now[k] = max(row == 0 && !(joined >> b & 1) ? 0 : now[k], theirs);
+        if (joined == 0 && row > 0) {
+            stay = b;
+            stay_rows = row;
+        }
+        joined |= 1u << b;
+    }
+    __syncwarp();  // every lane of the head has read the scales
+    if (!live)
+        return;
+    if (col % row16 == 0) {
+#pragma unroll
+        for (int b = 0; b < kKeepBlocks; ++b)
+            if (joined >> b & 1)
+                c.scales[(base + block_row[b]) / TF_KV_BLOCK] = (uint8_t)now[b];
+    }
+    auto two_to = [](int e) { return __uint_as_float((uint32_t)(e + 127) << 23); };
+    for (int j0 = 0; j0 < n; j0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < n && src[j0 + j] >= 0)
+                v[j] = *reinterpret_cast<const uint4*>(codes + (base + src[j0 + j]) * c.head_dim);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j0 + j < n && src[j0 + j] >= 0) {
+                int d = 0;
+#pragma unroll
+                for (int k = 0; k < kKeepBlocks; ++k)
+                    d += (k == src_block[j0 + j] ? old[k] : 0) - (k == dst_block[j0 + j] ? now[k] : 0);
+                if (d != 0) {
+                    const float f = two_to(d);
+                    v[j] = make_uint4(rescaled4(v[j].x, f), rescaled4(v[j].y, f), rescaled4(v[j].z, f), rescaled4(v[j].w, f));
+                }
+                *reinterpret_cast<uint4*>(codes + (base + dst[j0 + j]) * c.head_dim) = v[j];
+            }
+    }
+    int d = 0;
+    int64_t row0 = -1;
+#pragma unroll
+    for (int k = 0; k < kKeepBlocks; ++k)
+        if (k == stay) {
+            d = old[k] - now[k];
+            row0 = base + block_row[k];
+        }
+    if (d == 0)
+        return;
+    const float f = two_to(d);
+    for (int r = 0; r < stay_rows; ++r) {
+        uint4* w = reinterpret_cast<uint4*>(codes + (row0 + r) * c.head_dim);
+        const uint4 v = *w;
+        *w = make_uint4(rescaled4(v.x, f), rescaled4(v.y, f), rescaled4(v.z, f), rescaled4(v.w, f));
+    }
+}
+
 __global__ void reset_kernel(CacheView c, int64_t n)
 {
     const int64_t zeros = (int64_t)c.n_seqs + c.n_pages;
@@ -536,7 +671,11 @@ int check_cache(const tf_kvcache* c, const char* name, CacheView* v)
         return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: cache shape out of range", name);
     if (c->data == nullptr || c->book == nullptr || !is_aligned(c->data, 16) || !is_aligned(c->book, 4))
         return report_error(TF_E_INVALID_ARG, "%s: cache data or book NULL or misaligned", name);
+    if ((c->code != TF_KV_BF16 && c->code != TF_KV_E4M3) || (c->code == TF_KV_E4M3) != (c->scales != nullptr) || !is_aligned(c->scales, 4))
+        return report_error(TF_E_INVALID_ARG, "%s: cache code unknown, or its scales NULL, misaligned or not asked for", name);
     v->data = static_cast<uint16_t*>(c->data);
+    v->code = c->code;
+    v->scales = c->scales;
     v->len = c->book;
     v->refs = c->book + c->n_seqs;
     v->table = v->refs + c->n_pages;
@@ -598,11 +737,22 @@ size_t tf_kvcache_book_elems(int64_t n_pages, int n_seqs, int64_t max_pages)
     return (size_t)n_seqs + n_pages + (size_t)n_seqs * max_pages;
 }
 
-int tf_kvcache_init(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages, int n_seqs,
-                    int64_t max_pages, void* data, size_t data_bytes, int32_t* book, size_t book_elems,
-                    tf_kvcache* desc)
+size_t tf_kvcache_e4m3_bytes(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages)
 {
-    const char* name = "tf_kvcache_init";
+    return tf_kvcache_data_bytes(n_layers, n_kv, head_dim, page_size, n_pages) / sizeof(uint16_t);
+}
+
+size_t tf_kvcache_scale_bytes(int n_layers, int n_kv, int page_size, int64_t n_pages)
+{
+    if (!shape_ok(n_layers, n_kv, 64, page_size, n_pages))
+        return 0;
+    return ((size_t)n_layers * 2 * n_pages * n_kv * (page_size / TF_KV_BLOCK) + 3) / 4 * 4;
+}
+
+static int init_cache(const char* name, int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages, int n_seqs,
+                      int64_t max_pages, int elem, void* data, size_t data_bytes, int32_t* book, size_t book_elems,
+                      tf_kvcache* desc)
+{
     if (desc == nullptr)
         return report_error(TF_E_INVALID_ARG, "%s: desc is NULL", name);
     if (!shape_ok(n_layers, n_kv, head_dim, page_size, n_pages))
@@ -615,7 +765,7 @@ int tf_kvcache_init(int n_layers, int n_kv, int head_dim, int page_size, int64_t
                             name, kMaxSeqs);
     if (data == nullptr || book == nullptr || !is_aligned(data, 16) || !is_aligned(book, 4))
         return report_error(TF_E_INVALID_ARG, "%s: data (16-byte) or book (4-byte) NULL or misaligned", name);
-    if (data_bytes < tf_kvcache_data_bytes(n_layers, n_kv, head_dim, page_size, n_pages) ||
+    if (data_bytes < tf_kvcache_data_bytes(n_layers, n_kv, head_dim, page_size, n_pages) / sizeof(uint16_t) * elem ||
         book_elems < tf_kvcache_book_elems(n_pages, n_seqs, max_pages))
         return report_error(TF_E_WORKSPACE_TOO_SMALL, "%s: data or book too small for the shape", name);
     desc->magic = TF_KVCACHE_MAGIC;
@@ -628,6 +778,35 @@ int tf_kvcache_init(int n_layers, int n_kv, int head_dim, int page_size, int64_t
     desc->max_pages = (int32_t)max_pages;
     desc->data = data;
     desc->book = book;
+    desc->code = elem == 1 ? TF_KV_E4M3 : TF_KV_BF16;
+    desc->scales = nullptr;
+    return TF_OK;
+}
+
+int tf_kvcache_init(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages, int n_seqs,
+                    int64_t max_pages, void* data, size_t data_bytes, int32_t* book, size_t book_elems,
+                    tf_kvcache* desc)
+{
+    return init_cache("tf_kvcache_init", n_layers, n_kv, head_dim, page_size, n_pages, n_seqs, max_pages, 2, data, data_bytes,
+                      book, book_elems, desc);
+}
+
+int tf_kvcache_init_e4m3(int n_layers, int n_kv, int head_dim, int page_size, int64_t n_pages, int n_seqs,
+                         int64_t max_pages, void* data, size_t data_bytes, uint8_t* scales, size_t scale_bytes,
+                         int32_t* book, size_t book_elems, tf_kvcache* desc)
+{
+    const char* name = "tf_kvcache_init_e4m3";
+    if (desc == nullptr || scales == nullptr || !is_aligned(scales, 4))
+        return report_error(TF_E_INVALID_ARG, "%s: desc NULL, or scales NULL or not 4-byte aligned", name);
+    tf_kvcache made{};
+    const int rc = init_cache(name, n_layers, n_kv, head_dim, page_size, n_pages, n_seqs, max_pages, 1, data, data_bytes, book,
+                              book_elems, &made);
+    if (rc)
+        return rc;
+    if (scale_bytes < tf_kvcache_scale_bytes(n_layers, n_kv, page_size, n_pages))
+        return report_error(TF_E_WORKSPACE_TOO_SMALL, "%s: scales too small for the shape", name);
+    made.scales = scales;
+    *desc = made;
     return TF_OK;
 }
 
@@ -709,8 +888,8 @@ int tf_kvcache_keep(const tf_kvcache* c, const int32_t* seqs, const int32_t* q_s
     keep_plan_kernel<<<1, kPlanThreads, 0, s>>>(v, seqs, q_start, keep, n_keep, (int)B, M, ws);
     if ((rc = launched(cudaGetLastError(), name)))
         return rc;
-    const int64_t cols = (int64_t)v.n_layers * 2 * v.n_kv * (v.head_dim / 8), per = kCopyThreads;
-    return launched(launch_pdl(keep_move_kernel, dim3((unsigned)((cols + per - 1) / per), (unsigned)B), dim3(kCopyThreads), 0, s,
+    const int64_t cols = (int64_t)v.n_layers * 2 * v.n_kv * (v.head_dim * v.elem_bytes() / 16), per = kCopyThreads;
+    return launched(launch_pdl(v.code == TF_KV_E4M3 ? keep_move8_kernel : keep_move_kernel, dim3((unsigned)((cols + per - 1) / per), (unsigned)B), dim3(kCopyThreads), 0, s,
                                true, v, q_start, keep, M, ws),
                     name);
 }

@@ -15,58 +15,12 @@
 // arithmetic); 8 rows: 2.3 us, of which a launch is most.
 #include <cmath>
 
-#include "tfq_cache.h"
-#include "tfq_ptx.cuh"
+#include "tfq_rope.cuh"
 
 namespace tfq {
 namespace {
 
 constexpr int kRopeThreads = 128;
-
-struct RopeParams {
-    const uint16_t* qkv;
-    int64_t ld, M;
-    int n_q;
-    const uint16_t *q_gamma, *k_gamma;
-    float eps;
-    const int32_t* positions;
-    const uint64_t* turns;
-    int rot16;  // rot_dim / 16: lanes of a head whose chunks are rotated
-    int interleaved;
-    uint16_t* q;
-    CacheView c;
-    int layer;
-    const int32_t* slots;
-    int* status;
-    int parts;  // warps that share a row
-};
-
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8])
-{
-    f[0] = bf16lo_f32(v.x), f[1] = bf16hi_f32(v.x), f[2] = bf16lo_f32(v.y), f[3] = bf16hi_f32(v.y);
-    f[4] = bf16lo_f32(v.z), f[5] = bf16hi_f32(v.z), f[6] = bf16lo_f32(v.w), f[7] = bf16hi_f32(v.w);
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8])
-{
-    return make_uint4(f32x2_to_bf16x2(f[0], f[1]), f32x2_to_bf16x2(f[2], f[3]), f32x2_to_bf16x2(f[4], f[5]),
-                      f32x2_to_bf16x2(f[6], f[7]));
-}
-
-// Sine and cosine of hi + lo / 2^32 units of 2^-32 turn: less the nearest quarter turn, exactly, x is within
-// [-pi / 4, pi / 4] and as near as fp32 has it however small it is; there the Taylor polynomials' own error is
-// x^8 / 9! and x^10 / 10! at most (2^-21, 2^-25), so both are within 2^-20 of their own values at every angle.
-__device__ __forceinline__ void turn_sincos(uint32_t hi, uint32_t lo, float& sn, float& cs)
-{
-    const uint32_t quarter = (hi + 0x20000000u) >> 30;
-    const float x = fmaf((float)lo, 0x1p-32f, (float)(int32_t)(hi - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
-    const float y = x * x;
-    const float s = fmaf(x * y, fmaf(y, fmaf(y, -1.f / 5040.f, 1.f / 120.f), -1.f / 6.f), x);
-    const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
-    const bool odd = quarter & 1;
-    sn = __uint_as_float(__float_as_uint(odd ? c : s) ^ (quarter & 2) << 30);
-    cs = __uint_as_float(__float_as_uint(odd ? s : c) ^ (quarter + 1 & 2) << 30);
-}
 
 // LANES lanes take a head (head_dim / 16); a warp takes HEADS = 32 / LANES heads at once.
 // Seven blocks an SM: 72 registers a thread hold everything (8191 rows 24.0 us). With every lane making its eight
@@ -285,6 +239,13 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
     p.layer = layer;
     p.slots = slots;
     p.status = static_cast<int*>(ws);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool pdl = (flags & TF_RUN_PDL) != 0;
+    cudaError_t e;
+    if (p.c.code == TF_KV_E4M3) {
+        e = launch_rope8(p, pdl, s);
+        return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
+    }
     // few rows: a row's heads spread over as many warps as it takes to fill the GPU. 16 warps an SM:
     // 2048 rows of 32 heads 7.6 us; 7.8 with 8, 8.4 with 32, 10.2 with 64; 512 rows 3.8 to 4.2 with any.
     const int per_warp = 512 / p.c.head_dim, groups = (n_q + 2 * p.c.n_kv + per_warp - 1) / per_warp;
@@ -295,9 +256,6 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
     if (p.parts > groups)
         p.parts = groups;
     const unsigned grid = (unsigned)((M * p.parts + kRopeThreads / 32 - 1) / (kRopeThreads / 32));
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const bool pdl = (flags & TF_RUN_PDL) != 0;
-    cudaError_t e;
     if (p.c.head_dim == 64)
         e = launch_pdl(qk_norm_rope_kernel<4>, dim3(grid), dim3(kRopeThreads), 0, s, pdl, p);
     else if (p.c.head_dim == 128)

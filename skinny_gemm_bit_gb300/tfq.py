@@ -41,6 +41,9 @@ TF_TUNE_WARPS = 4
 TF_TUNE_MODE = 5
 TF_TUNE_CHAIN = 6
 TF_KVCACHE_MAGIC = 0x314B5654
+TF_KV_BF16 = 0
+TF_KV_E4M3 = 1
+TF_KV_BLOCK = 16
 TF_MAX_DRAFT_ROWS = 64
 
 P = ctypes.c_void_p
@@ -68,7 +71,8 @@ class tf_decoder_desc(ctypes.Structure):
 
 class tf_kvcache(ctypes.Structure):
     _fields_ = [("magic", ctypes.c_uint32), ("n_layers", I32), ("n_kv", I32), ("head_dim", I32), ("page_size", I32),
-                ("n_seqs", I32), ("n_pages", I32), ("max_pages", I32), ("data", P), ("book", P)]
+                ("n_seqs", I32), ("n_pages", I32), ("max_pages", I32), ("data", P), ("book", P),
+                ("code", I32), ("scales", P)]
 
 
 class tf_attn_layer(ctypes.Structure):
@@ -128,6 +132,10 @@ _SIGS = {
     "tf_kvcache_book_elems": (SZ, [I64, ctypes.c_int, I64]),
     "tf_kvcache_init": (ctypes.c_int, [ctypes.c_int] * 4 + [I64, ctypes.c_int, I64, P, SZ, P, SZ,
                                                            ctypes.POINTER(tf_kvcache)]),
+    "tf_kvcache_e4m3_bytes": (SZ, [ctypes.c_int] * 4 + [I64]),
+    "tf_kvcache_scale_bytes": (SZ, [ctypes.c_int] * 3 + [I64]),
+    "tf_kvcache_init_e4m3": (ctypes.c_int, [ctypes.c_int] * 4 + [I64, ctypes.c_int, I64, P, SZ, P, SZ, P, SZ,
+                                                                ctypes.POINTER(tf_kvcache)]),
     "tf_kvcache_reset": (ctypes.c_int, [ctypes.POINTER(tf_kvcache), P]),
     "tf_kvcache_workspace_bytes": (SZ, [ctypes.POINTER(tf_kvcache)]),
     "tf_kvcache_extend": (ctypes.c_int, [ctypes.POINTER(tf_kvcache), P, P, I64, I64, P, P, P, P, SZ, P]),
@@ -140,6 +148,9 @@ _SIGS = {
     "tf_tree_attn_workspace_bytes": (SZ, [ctypes.POINTER(tf_kvcache), ctypes.c_int, I64, ctypes.c_int]),
     "tf_tree_attn_run": (ctypes.c_int, [P, I64, I64, ctypes.c_int, ctypes.POINTER(tf_kvcache), ctypes.c_int, P, P, I64,
                                         ctypes.c_int, P, ctypes.c_float, P, P, SZ, ctypes.c_uint, P]),
+    "tf_prompt_attn_workspace_bytes": (SZ, [ctypes.POINTER(tf_kvcache), ctypes.c_int, I64]),
+    "tf_prompt_attn_run": (ctypes.c_int, [P, I64, I64, ctypes.c_int, ctypes.POINTER(tf_kvcache), ctypes.c_int, P, P, I64,
+                                          ctypes.c_float, P, P, SZ, ctypes.c_uint, P]),
     "tf_decode_step_attn_workspace_bytes": (SZ, [ctypes.POINTER(tf_decoder_desc), ctypes.POINTER(tf_kvcache),
                                                  ctypes.POINTER(tf_attn_desc)]),
     "tf_decode_step_attn_run": (ctypes.c_int, [ctypes.POINTER(tf_decoder_desc), ctypes.POINTER(tf_kvcache),
@@ -578,31 +589,49 @@ def _current(device) -> int:
 
 
 class KVCache:
-    """A paged K/V cache: bf16 data [layers, 2, pages, kv heads, page rows, head dim] and an int32
-    book [n_seqs lengths | pages' reference counts | n_seqs x max_pages page table]."""
+    """A paged K/V cache: data [layers, 2, pages, kv heads, page rows, head dim] and an int32 book
+    [n_seqs lengths | pages' reference counts | n_seqs x max_pages page table]. The data is bfloat16, or
+    float8_e4m3fn with `scales`, float8_e8m0fnu [layers, 2, pages, kv heads, page rows / 16]: a value is
+    its code times its block's scale."""
 
-    def __init__(self, data: torch.Tensor, book: torch.Tensor, n_seqs: int, max_pages: int):
-        if data.dim() != 6 or data.shape[1] != 2 or data.dtype != torch.bfloat16 or not data.is_contiguous():
-            raise ValueError("data must be a contiguous bfloat16 tensor [layers, 2, pages, kv heads, page rows, head dim]")
+    def __init__(self, data: torch.Tensor, book: torch.Tensor, n_seqs: int, max_pages: int, scales=None):
+        kind = torch.bfloat16 if scales is None else torch.float8_e4m3fn
+        if data.dim() != 6 or data.shape[1] != 2 or data.dtype != kind or not data.is_contiguous():
+            raise ValueError(f"data must be a contiguous {kind} tensor [layers, 2, pages, kv heads, page rows, head dim]"
+                             + (" (float8_e4m3fn takes `scales`)" if scales is None else ""))
         if book.dim() != 1 or book.dtype != torch.int32 or not book.is_contiguous() or book.device != data.device:
             raise ValueError("book must be a contiguous 1-D int32 tensor on the data's device")
         L, _, n_pages, n_kv, page, hd = data.shape
-        self.data, self.book, self.device = data, book, data.device
+        self.data, self.book, self.scales, self.device = data, book, scales, data.device
         self.n_seqs, self.max_pages, self.n_pages = n_seqs, max_pages, n_pages
         self.n_layers, self.n_kv, self.page_size, self.head_dim = L, n_kv, page, hd
         self.desc = tf_kvcache()
-        _check(lib().tf_kvcache_init(L, n_kv, hd, page, n_pages, n_seqs, max_pages, data.data_ptr(),
-                                     data.numel() * 2, book.data_ptr(), book.numel(), ctypes.byref(self.desc)))
+        if scales is None:
+            _check(lib().tf_kvcache_init(L, n_kv, hd, page, n_pages, n_seqs, max_pages, data.data_ptr(),
+                                         data.numel() * 2, book.data_ptr(), book.numel(), ctypes.byref(self.desc)))
+        else:
+            shape = (L, 2, n_pages, n_kv, page // TF_KV_BLOCK)
+            if tuple(scales.shape) != shape or scales.dtype != torch.float8_e8m0fnu or not scales.is_contiguous() or scales.device != data.device:
+                raise ValueError(f"scales must be a contiguous float8_e8m0fnu tensor {shape} on the data's device")
+            # read as words of four: their end is rounded up, and the storage has to go as far
+            held = scales.untyped_storage().nbytes() - scales.storage_offset()
+            _check(lib().tf_kvcache_init_e4m3(L, n_kv, hd, page, n_pages, n_seqs, max_pages, data.data_ptr(), data.numel(),
+                                              scales.data_ptr(), held, book.data_ptr(), book.numel(), ctypes.byref(self.desc)))
         self.ref = ctypes.byref(self.desc)
 
     @classmethod
     def create(cls, n_layers: int, n_kv: int, head_dim: int, page_size: int, n_pages: int, n_seqs: int, max_pages: int,
-               device="cuda") -> "KVCache":
-        """An empty cache in tensors of its own."""
-        data = torch.zeros((n_layers, 2, n_pages, n_kv, page_size, head_dim), dtype=torch.bfloat16, device=device)
+               device="cuda", dtype=torch.bfloat16) -> "KVCache":
+        """An empty cache in tensors of its own, of bfloat16 or float8_e4m3fn."""
+        data = torch.zeros((n_layers, 2, n_pages, n_kv, page_size, head_dim), dtype=dtype, device=device)
         book = torch.zeros(n_seqs + n_pages + n_seqs * max_pages, dtype=torch.int32, device=device)
         book[n_seqs + n_pages:] = -1
-        return cls(data, book, n_seqs, max_pages)
+        if dtype != torch.float8_e4m3fn:
+            return cls(data, book, n_seqs, max_pages)
+        shape = (n_layers, 2, n_pages, n_kv, page_size // TF_KV_BLOCK)
+        n = int(np.prod(shape))
+        scales = torch.full(((n + 3) // 4 * 4,), 127, dtype=torch.uint8, device=device)  # 1
+        return cls(data, book, n_seqs, max_pages, scales[:n].view(torch.float8_e8m0fnu).view(shape))
 
     @property
     def len(self) -> torch.Tensor:
@@ -738,6 +767,31 @@ def tf_tree_attn_run(q: torch.Tensor, cache: KVCache, layer: int, seqs, q_start,
         None if masks is None else _want(masks, torch.int64, at, M, "masks"), hd ** -0.5 if scale is None else scale,
         _want(out, torch.bfloat16, at, M * n_q * hd, "out"), _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), flags,
         _raw_stream(stream, dev)))
+    return out
+
+
+def tf_prompt_attn_workspace_bytes(cache: KVCache, n_q: int, B: int) -> int:
+    return lib().tf_prompt_attn_workspace_bytes(cache.ref, n_q, B)
+
+
+def tf_prompt_attn_run(q: torch.Tensor, cache: KVCache, layer: int, seqs, q_start, scale=None, out=None, ws=None,
+                       flags: int = 0, stream=None) -> torch.Tensor:
+    """o [M, n_q * head_dim]: causal attention of prompts' rows q, each sequence's the last tokens of its slot, over the
+    cache (scale: head_dim ** -0.5)."""
+    dev, hd = cache.device, cache.head_dim
+    at = _current(dev)
+    if q.dim() != 2 or q.stride(1) != 1 or q.dtype is not torch.bfloat16 or q.get_device() != at or q.shape[1] % hd != 0:
+        raise ValueError(f"q must be bfloat16 [M, n_q * {hd}] on {dev} with unit column stride")
+    M, n_q, B = q.shape[0], q.shape[1] // hd, seqs.numel()
+    if out is None or ws is None:
+        with _on(stream):
+            out = torch.empty((M, n_q * hd), dtype=torch.bfloat16, device=dev) if out is None else out
+            ws = workspace(tf_prompt_attn_workspace_bytes(cache, n_q, B), dev) if ws is None else ws
+    _check(lib().tf_prompt_attn_run(
+        q.data_ptr(), q.stride(0) if M > 1 else q.shape[1], M, n_q, cache.ref, layer,
+        _want(seqs, torch.int32, at, 1, "seqs"), _want(q_start, torch.int32, at, B + 1, "q_start"), B,
+        hd ** -0.5 if scale is None else scale, _want(out, torch.bfloat16, at, M * n_q * hd, "out"),
+        _want(ws, torch.uint8, at, 1, "ws"), ws.numel(), flags, _raw_stream(stream, dev)))
     return out
 
 
