@@ -22,7 +22,7 @@ struct RopeParams {
     const int32_t* slots;
     int* status;
     int parts;  // warps (8 bits: CTAs) that share a row's heads
-    int step, pair_shift;  // 8 bits: rows that a CTA begins at; a row's angles are made by 1 << pair_shift threads
+    int step;   // 8 bits: rows that a CTA begins at
 };
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8])
