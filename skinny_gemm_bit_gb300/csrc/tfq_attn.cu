@@ -42,12 +42,13 @@ struct AttnLayout {
     size_t counters, parts, total;
 };
 
-AttnLayout attn_layout(int head_dim, int rows)
+AttnLayout attn_layout(const CacheView& c, int rows)
 {
+    const size_t ctas = (size_t)device_sms() * (rows > 64 ? 1 : attn_warp_ctas(c, rows));
     AttnLayout L{};
     L.counters = 256;
-    L.parts = L.counters + ((size_t)device_sms() * 2 * sizeof(unsigned) + 255) / 256 * 256;
-    L.total = L.parts + (size_t)2 * device_sms() * rows * (head_dim + 2) * sizeof(float);  // two parts a CTA
+    L.parts = L.counters + (ctas * 2 * sizeof(unsigned) + 255) / 256 * 256;
+    L.total = L.parts + 2 * ctas * rows * (c.head_dim + 2) * sizeof(float);  // two parts a CTA
     return L;
 }
 
@@ -145,14 +146,14 @@ int fill_params(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvc
 
 int launch_attn(AttnParams& p, int rows, bool causal, void* ws, cudaStream_t stream, const char* name)
 {
-    const AttnLayout L = attn_layout(p.c.head_dim, rows);
+    const AttnLayout L = attn_layout(p.c, rows);
     p.status = static_cast<int*>(ws);
     p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + L.counters);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
     CUtensorMap map;
     const bool tc = rows > 64;
-    if (!encode_rows(p.c, p.total_rows, tc ? attn_tc_box(p.c.page_size) : attn_warp_box(p.c.head_dim, p.c.page_size),
-                     tc ? 1 : p.c.head_dim / 64, &map))
+    const int tile = tc ? kTcTile : attn_warp_tile(p.c);
+    if (!encode_rows(p.c, p.total_rows, p.c.page_size < tile ? p.c.page_size : tile, tc ? 1 : p.c.head_dim / 64, &map))
         return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
     const cudaError_t e = tc ? launch_attn_tc(p, rows, causal, map, stream) : launch_attn_warp(p, rows, map, stream);
     return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
@@ -175,7 +176,7 @@ size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int
         report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q, B or max_rows out of range", name);
         return 0;
     }
-    return attn_layout(v.head_dim, attn_rows(max_rows, n_q / v.n_kv, v.head_dim)).total;
+    return attn_layout(v, attn_rows(max_rows, n_q / v.n_kv, v.head_dim)).total;
 }
 
 int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
@@ -191,7 +192,7 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
     const int rows = attn_rows(max_rows, p.group, p.c.head_dim);
     const int64_t items = B * p.c.n_kv * ((max_rows * p.group + rows - 1) / rows);
     p.over = attn_over(rows, items);
-    p.few = items <= device_sms() && B <= 256;
+    p.few = items <= device_sms() && B <= (rows > 64 ? 256 : attn_warp_threads(p.c, rows));
     return launch_attn(p, rows, false, ws, static_cast<cudaStream_t>(stream), name);
 }
 
@@ -205,7 +206,7 @@ size_t tf_prompt_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B)
         report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q, B or head_dim out of range", name);
         return 0;
     }
-    return attn_layout(v.head_dim, kPromptRows).total;
+    return attn_layout(v, kPromptRows).total;
 }
 
 int tf_prompt_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,

@@ -636,10 +636,12 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
 }
 
 // rows: query rows of an item. tfq_attn_warp.cu: 16, and up to head_dim 128 also 32;
-// tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128; causal: the rows of prompts. *_box: cache rows of a tensor-map box.
+// tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128; causal: the rows of prompts. *Tile: keys of a tile.
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
 cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream);
-int attn_warp_box(int head_dim, int page_size);
-int attn_tc_box(int page_size);
+int attn_warp_tile(const CacheView& c);
+int attn_warp_ctas(const CacheView& c, int rows);  // an SM
+int attn_warp_threads(const CacheView& c, int rows);
+constexpr int kTcTile = 64;
 
 }  // namespace tfq

@@ -48,7 +48,7 @@ constexpr int kSoftThreads = 256;
 constexpr int kConvertThreads = 128;
 constexpr float kHead = 7.f;  // fp16 weights reach 2^(kGrow + kHead) = 2^15
 constexpr int kMaxSlots = 12;
-constexpr int KT = 64;                            // keys of a tile
+constexpr int KT = kTcTile;                       // keys of a tile
 constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w][buffer] at 128 w + 64 buffer, O[w] at 256 + 128 w
 constexpr float kGrow = 8.f;
 
@@ -365,10 +365,13 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         }
                         uint8_t* line = out + (c >> 2) * (KT * 128) + row * 128;
                         const int at = 2 * c & 7;
-                        *reinterpret_cast<uint4*>(line + ((at ^ (row & 7)) << 4)) =
-                            make_uint4(e4m3x2_to_f16x2(v.x), e4m3x2_to_f16x2(v.x >> 16), e4m3x2_to_f16x2(v.y), e4m3x2_to_f16x2(v.y >> 16));
-                        *reinterpret_cast<uint4*>(line + ((at + 1 ^ (row & 7)) << 4)) =
-                            make_uint4(e4m3x2_to_f16x2(v.z), e4m3x2_to_f16x2(v.z >> 16), e4m3x2_to_f16x2(v.w), e4m3x2_to_f16x2(v.w >> 16));
+                        uint4 lo, hi;
+                        e4m3x4_to_f16x2(v.x, lo.x, lo.y);
+                        e4m3x4_to_f16x2(v.y, lo.z, lo.w);
+                        e4m3x4_to_f16x2(v.z, hi.x, hi.y);
+                        e4m3x4_to_f16x2(v.w, hi.z, hi.w);
+                        *reinterpret_cast<uint4*>(line + ((at ^ (row & 7)) << 4)) = lo;
+                        *reinterpret_cast<uint4*>(line + ((at + 1 ^ (row & 7)) << 4)) = hi;
                     }
                     if (kv == 1 && ct < KT / 16) {
                         const uint32_t* w = words + (from * 4 + ct * 16 / box) * 3;
@@ -960,8 +963,6 @@ cudaError_t launch_any(const AttnParams& p, int rows, bool causal, const CUtenso
 }
 
 }  // namespace
-
-int attn_tc_box(int page_size) { return page_size < KT ? page_size : KT; }
 
 cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream)
 {

@@ -28,19 +28,22 @@
 namespace tfq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kCtaThreads = kWarps * 32;
 constexpr float kGrow = 8.f;  // the reference of a row moves when its maximum has grown by 2^8
 
 template <int HD, int RW, bool E8>
 struct Cfg {
-    static constexpr int CH = HD == 256 ? 1 : 2;          // 16-key pieces of a tile
+    // of 8 bits, where registers allow, two CTAs an SM with six warps each: half a tile's bytes for the same
+    // instructions need more warps, and one CTA works while the other joins its warps' parts
+    static constexpr int kCtas = E8 && RW == 1 && HD <= 128 ? 2 : 1;
+    static constexpr int kWarps = kCtas == 2 ? 6 : 8;
+    static constexpr int kCtaThreads = kWarps * 32;
+    static constexpr int CH = HD == 256 ? 1 : 2;  // 16-key pieces of a tile
     static constexpr int KT = 16 * CH;
     static constexpr int ROWS = 16 * RW;
     static constexpr int kSlotBytes = KT * HD * (E8 ? 1 : 2);  // K or V of a tile
     // slots of a warp: 3, or 6 at head_dim 64; of 8 bits 5 to 12
-    static constexpr int kSlots = (E8 && RW == 2 ? 20480 : 24576) / kSlotBytes;
-    static constexpr int kCols = RW == 2 && !E8 ? 8 : 16;  // output columns joined at once, as shared memory allows
+    static constexpr int kSlots = (kCtas == 2 ? 12288 : E8 ? 20480 : 24576) / kSlotBytes;
+    static constexpr int kCols = E8 ? (RW == 2 || kCtas == 2 ? 32 : 64) : RW == 2 ? 8 : 16;  // output columns joined at once, as shared memory allows
     static constexpr int kStride = kCols + 4;             // floats
     static constexpr int kMlOff = 0;                      // [kWarps][ROWS][2] floats
     static constexpr int kBarOff = kMlOff + kWarps * ROWS * 2 * 4;
@@ -48,7 +51,7 @@ struct Cfg {
     // 8 bits: the rows' factors of the scores; by K slot and box, the words with K's and V's scales and their places
     static constexpr int kRowOff = kFlagOff + 16;
     static constexpr int kScaleOff = kRowOff + (E8 ? ROWS * 4 : 0);
-    static constexpr int kScaleWords = E8 ? kSlots * 2 * 3 : 0;  // of a warp
+    static constexpr int kScaleWords = E8 ? kSlots * CH * 3 : 0;  // of a warp
     // the item's queries, and after its last tile what the warps hand over
     static constexpr int kQOff = (kScaleOff + kWarps * kScaleWords * 4 + 1023) / 1024 * 1024;
     static constexpr int kOutBytes = kWarps * ROWS * kStride * 4;
@@ -116,12 +119,12 @@ constexpr float kHead = 7.f;  // fp16 weights reach 2^(kGrow + kHead) = 2^15, an
 
 // Tile scores of 8 bits: the rows' weights in fp16, RW row tiles of 16 (16 RW query rows an item).
 template <int HD, int RW, bool E8>
-__global__ void __launch_bounds__(kCtaThreads, 1)
+__global__ void __launch_bounds__(Cfg<HD, RW, E8>::kCtaThreads, Cfg<HD, RW, E8>::kCtas)
     tree_attn_warp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map)
 {
     using C = Cfg<HD, RW, E8>;
-    constexpr int ROWS = C::ROWS, KT = C::KT, CH = C::CH, NC = HD / 8, KS = HD / 16, NS = C::kSlots;
-    constexpr bool kQRegs = RW == 1 && HD <= 128;  // the rows' A fragments in registers
+    constexpr int kWarps = C::kWarps, kCtaThreads = C::kCtaThreads, ROWS = C::ROWS, KT = C::KT, CH = C::CH, NC = HD / 8, KS = HD / 16, NS = C::kSlots;
+    constexpr bool kQRegs = RW == 1 && HD <= 128 && C::kCtas == 1;  // the rows' A fragments in registers
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -133,13 +136,13 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     uint8_t* ring = smem + C::ring(p.B) + (size_t)warp * NS * C::kSlotBytes;
 
     [[maybe_unused]] float* row_factor = reinterpret_cast<float*>(smem + C::kRowOff);
-    // of slot s, box b, at 3 (2 s + b): K's word, V's word, their scales' places in them (bits)
+    // of slot s, box b, at 3 (CH s + b): K's word, V's word, their scales' places in them (bits)
     [[maybe_unused]] uint32_t* scale_words = reinterpret_cast<uint32_t*>(smem + C::kScaleOff) + warp * C::kScaleWords;
-    const int box = min(p.c.page_size, KT), bs = KT / box - 1;  // a tile is 1 << bs boxes, one or two
+    const int box = min(p.c.page_size, KT), boxes = KT / box, bs = boxes >> 1;  // a tile is boxes = 1 << bs: 1, 2 or 4
 
     if (lane == 0) {
         for (int i = 0; i < NS; ++i)
-            mbar_init(&full[i], E8 ? bs + 2 : 1);  // 8 bits: and one for each lane that fetches scales
+            mbar_init(&full[i], E8 ? boxes + 1 : 1);  // 8 bits: and one for each lane that fetches scales
         fence_mbar_init();
     }
     if (threadIdx.x == 0) {
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     // 8 key/value heads of 128, in us, an item a CTA against split and joined: one row over 200 tokens 7.1, 10.2;
     // over 500 9.7, 10.5, but in a decoder step, its code not in the caches, 28 layers 787, 769; eight
     // sequences of eight rows over 500 tokens 11.3, 14.7, over 1000 13.9, 18.7, over 3000 27.5, 26.0
-    Shares<ROWS, KT, kWarps, RW == 2 ? 8 : 10> shares(p, smem + C::kSchedOff);
+    Shares<ROWS, KT, 8, KT == 64 ? 5 : RW == 2 ? 8 : 10> shares(p, smem + C::kSchedOff);
     shares.build();
     pdl_launch_dependents();
     const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
     int lpages = -1, lj = 0;       // the lane's page (tile lane >> bs of those, box lane & bs); which of them is next
     uint32_t issued = 0, taken = 0;
     auto look = [&]() {
-        const int t = lt + kWarps * (lane >> bs), row = t * KT + (lane & bs) * box;
+        const int t = lt + kWarps * (lane >> bs), row = t * KT + (lane & (boxes - 1)) * box;
         lpages = t < lg.t1 && row < lg.q.len() ? p.c.table[(int64_t)lg.q.slot * p.c.max_pages + (row >> p.c.page_shift)] : -1;
         lj = 0;
     };
@@ -179,6 +182,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         if (lj == ahead)
             look();
     };
+    const int layer_pages = p.layer * 2 * p.c.n_pages;
     auto load = [&]() {
         if (lu >= u1)
             return;
@@ -187,12 +191,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
         if (lane == 0)
             mbar_arrive_expect_tx(&full[slot], C::kSlotBytes);
         __syncwarp();
-        if (lane <= bs) {
+        if (lane < boxes) {
             const int row = lt * KT + lane * box;
             int y = p.total_rows;  // zeros
             if (row < lg.q.len()) {
                 if (page >= 0 && page < p.c.n_pages)
-                    y = (int)p.c.row_of(p.layer, lkv, page, lg.h) + (row & (p.c.page_size - 1));
+                    y = ((layer_pages + lkv * p.c.n_pages + page) * p.c.n_kv + lg.h) * p.c.page_size + (row & (p.c.page_size - 1));  // fewer than 2^31 rows
                 else
                     record_status(p.status, TF_E_INVALID_ARG);
             }
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             if constexpr (E8) {
                 if (lkv == 0) {
                     // the tile's scales, K's and V's, as the aligned words that hold them
-                    uint32_t* words = scale_words + 3 * (2 * slot + lane);
+                    uint32_t* words = scale_words + 3 * (CH * slot + lane);
                     if (y < p.total_rows) {
                         const int64_t k = y >> 4, v = k + (((int64_t)p.c.n_pages * p.c.n_kv) << (p.c.page_shift - 4));
                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(words)), "l"(p.c.scales + (k & ~3ll)) : "memory");
@@ -346,7 +350,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             if constexpr (E8) {
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
-                    const uint32_t* words = scale_words + 3 * (2 * ks_slot + ch * 16 / box);
+                    const uint32_t* words = scale_words + 3 * (CH * ks_slot + ch * 16 / box);
                     const uint32_t places = words[2], within = (ch * 16 % box) / 2;
                     ks_bits[ch] = scale_bits(words[0], (places & 0xFFu) + within);
                     vs_bits[ch] = scale_bits(words[1], (places >> 8) + within);
@@ -363,7 +367,9 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t lo = b[j >> 1][j & 1], hi = b[j >> 1][2 + (j & 1)];
-                            const uint32_t l0 = e4m3x2_to_f16x2(lo), l1 = e4m3x2_to_f16x2(lo >> 16), h0 = e4m3x2_to_f16x2(hi), h1 = e4m3x2_to_f16x2(hi >> 16);
+                            uint32_t l0, l1, h0, h1;
+                            e4m3x4_to_f16x2(lo, l0, l1);
+                            e4m3x4_to_f16x2(hi, h0, h1);
 #pragma unroll
                             for (int r = 0; r < RW; ++r) {
                                 uint32_t a[4];
@@ -422,10 +428,10 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                     see[r][0] = see[r][1] = 0u;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t of = (uint32_t)tile_mask(mask[r][h], k0 - q.base) >> (ti * 2);
+                        const uint64_t view = tile_mask(mask[r][h], k0 - q.base) >> (ti * 2);
 #pragma unroll
                         for (int i = 0; i < 4 * CH; ++i) {
-                            if (of >> ((i >> 1) * 8 + (i & 1)) & 1)
+                            if ((KT == 64 ? view : (uint32_t)view) >> ((i >> 1) * 8 + (i & 1)) & 1)
                                 see[r][h] |= 1u << i;
                             else
                                 s[r][i >> 1][2 * h + (i & 1)] = -INFINITY;
@@ -496,10 +502,33 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                 break;
             const uint32_t v_at = smem_u32(ring + vs * C::kSlotBytes);
             if constexpr (E8) {
+                if (!edge) {
+#pragma unroll
+                    for (int ch = 0; ch < CH; ++ch) {
+                        const uint32_t at = v_at + (ch * 16 / box) * (box * HD) + (ch * 16 % box) * (HD == 64 ? 64 : 128);
+#pragma unroll
+                        for (int c = 0; c < HD / 16; c += 2) {
+                            uint32_t b[4];
+                            ldsm4_trans(b, at + piece8<HD>(v_row, c + v_bit, half));
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                // keys 2 ti, 2 ti + 1 and 2 ti + 8, 2 ti + 9 of an even column and of the next
+                                uint32_t v[4];
+                                e4m3x4_to_f16x2(__byte_perm(b[2 * j], b[2 * j + 1], 0x6420), v[0], v[1]);
+                                e4m3x4_to_f16x2(__byte_perm(b[2 * j], b[2 * j + 1], 0x7531), v[2], v[3]);
+#pragma unroll
+                                for (int r = 0; r < RW; ++r) {
+                                    mma_f16_16816(o[r][2 * (c + j)], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], v[0], v[1]);
+                                    mma_f16_16816(o[r][2 * (c + j) + 1], w[r][ch][0], w[r][ch][1], w[r][ch][2], w[r][ch][3], v[2], v[3]);
+                                }
+                            }
+                        }
+                    }
+                } else
 #pragma unroll
                 for (int ch = 0; ch < CH; ++ch) {
                     const uint32_t at = v_at + (ch * 16 / box) * (box * HD) + (ch * 16 % box) * (HD == 64 ? 64 : 128);
-                    const int left = edge ? len - (k0 + ch * 16) : 16;  // keys of the piece that exist
+                    const int left = len - (k0 + ch * 16);  // keys of the piece that exist
                     if (left <= 0)
                         continue;
                     // nothing behind the sequence's end takes part: not even as 0 times NaN
@@ -514,15 +543,15 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                         for (int j = 0; j < 2; ++j) {
                             // keys 2 ti, 2 ti + 1 and 2 ti + 8, 2 ti + 9 of an even column and of the next
                             const uint32_t even = __byte_perm(b[2 * j], b[2 * j + 1], 0x6420), next = __byte_perm(b[2 * j], b[2 * j + 1], 0x7531);
-                            uint32_t v[4] = {e4m3x2_to_f16x2(even), e4m3x2_to_f16x2(even >> 16), e4m3x2_to_f16x2(next), e4m3x2_to_f16x2(next >> 16)};
-                            if (edge) {
-                                v[0] &= in_lo, v[1] &= in_hi, v[2] &= in_lo, v[3] &= in_hi;
+                            uint32_t v[4];
+                            e4m3x4_to_f16x2(even, v[0], v[1]);
+                            e4m3x4_to_f16x2(next, v[2], v[3]);
+                            v[0] &= in_lo, v[1] &= in_hi, v[2] &= in_lo, v[3] &= in_hi;
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const uint32_t x = nonfinite2_f16(v[k]);
-                                    odd |= x;
-                                    v[k] &= ~x;
-                                }
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t x = nonfinite2_f16(v[k]);
+                                odd |= x;
+                                v[k] &= ~x;
                             }
 #pragma unroll
                             for (int r = 0; r < RW; ++r) {
@@ -531,7 +560,7 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
                             }
                         }
                     }
-                    if (edge && __any_sync(0xffffffffu, odd != 0)) {
+                    if (__any_sync(0xffffffffu, odd != 0)) {
                         // NaN among the values: it reaches the rows that see its key alone
 #pragma unroll 1
                         for (int k = 0; k < 16 && k < left; ++k) {
@@ -705,9 +734,12 @@ __global__ void __launch_bounds__(kCtaThreads, 1)
             for (int r = 0; r < RW; ++r) {
                 if constexpr (E8) {  // an even and an odd tile: columns 4 ti .. 4 ti + 3
                     float* to = round + (warp * ROWS + r * 16 + gi) * C::kStride + ti * 4;
-                    const float *a = o[r][c0 / 8], *b = o[r][c0 / 8 + 1];
-                    *reinterpret_cast<float4*>(to) = make_float4(a[0] * f[r][0], b[0] * f[r][0], a[1] * f[r][0], b[1] * f[r][0]);
-                    *reinterpret_cast<float4*>(to + 8 * C::kStride) = make_float4(a[2] * f[r][1], b[2] * f[r][1], a[3] * f[r][1], b[3] * f[r][1]);
+#pragma unroll
+                    for (int i = 0; i < C::kCols / 8; i += 2) {
+                        const float *a = o[r][c0 / 8 + i], *b = o[r][c0 / 8 + i + 1];
+                        *reinterpret_cast<float4*>(to + i * 8) = make_float4(a[0] * f[r][0], b[0] * f[r][0], a[1] * f[r][0], b[1] * f[r][0]);
+                        *reinterpret_cast<float4*>(to + 8 * C::kStride + i * 8) = make_float4(a[2] * f[r][1], b[2] * f[r][1], a[3] * f[r][1], b[3] * f[r][1]);
+                    }
                     continue;
                 }
                 float* to = round + (warp * ROWS + r * 16 + gi) * C::kStride + ti * 2;
@@ -753,12 +785,12 @@ template <int HD, int RW, bool E8>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
 {
     using C = Cfg<HD, RW, E8>;
-    static_assert(C::smem(kMaxAttnSeqs) <= 227 * 1024, "shared memory");
+    static_assert(C::smem(kMaxAttnSeqs) <= (C::kCtas == 2 ? 113 : 227) * 1024, "shared memory");
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(tree_attn_warp_kernel<HD, RW, E8>, (int)C::smem(kMaxAttnSeqs), done);
     if (e != cudaSuccess)
         return e;
-    return launch_coop(tree_attn_warp_kernel<HD, RW, E8>, dim3(device_sms()), dim3(kCtaThreads), C::smem(p.B), stream, p, map);
+    return launch_coop(tree_attn_warp_kernel<HD, RW, E8>, dim3(device_sms() * C::kCtas), dim3(C::kCtaThreads), C::smem(p.B), stream, p, map);
 }
 
 template <bool E8>
@@ -773,7 +805,10 @@ cudaError_t launch_any(const AttnParams& p, int rows, const CUtensorMap& map, cu
 
 }  // namespace
 
-int attn_warp_box(int head_dim, int page_size) { return head_dim == 256 ? 16 : page_size < 32 ? page_size : 32; }
+int attn_warp_tile(const CacheView& c) { return c.head_dim == 256 ? 16 : 32; }
+int attn_warp_ctas(const CacheView& c, int rows) { return c.code == TF_KV_E4M3 && rows == 16 && c.head_dim <= 128 ? Cfg<128, 1, true>::kCtas : 1; }
+int attn_warp_threads(const CacheView& c, int rows) { return attn_warp_ctas(c, rows) == 2 ? Cfg<128, 1, true>::kCtaThreads : 256; }
+
 
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream)
 {
