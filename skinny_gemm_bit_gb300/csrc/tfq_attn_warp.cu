@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(Cfg<HD, RW, E8>::kCtaThreads, Cfg<HD, RW, E8>:
     // 8 key/value heads of 128, in us, an item a CTA against split and joined: one row over 200 tokens 7.1, 10.2;
     // over 500 9.7, 10.5, but in a decoder step, its code not in the caches, 28 layers 787, 769; eight
     // sequences of eight rows over 500 tokens 11.3, 14.7, over 1000 13.9, 18.7, over 3000 27.5, 26.0
-    Shares<ROWS, KT, 8, KT == 64 ? 5 : RW == 2 ? 8 : 10> shares(p, smem + C::kSchedOff);
+    Shares<ROWS, KT, C::kCtas == 2 ? kWarps : 8, RW == 2 ? 8 : 10> shares(p, smem + C::kSchedOff);
     shares.build();
     pdl_launch_dependents();
     const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
