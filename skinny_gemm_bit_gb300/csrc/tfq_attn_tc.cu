@@ -335,19 +335,27 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 const bool edge = k0 + KT > hidden;
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t slot = r * ring_slots + next_slot[r];
-                    if (!wait(&full8[from], from_phase) || (pass[r] > 0 && !wait(&empty[slot], (pass[r] - 1) & 1))) {
+                    if (!wait(&full8[from], from_phase)) {
                         gone = true;
                         break;
                     }
+                    constexpr int kTimes = KT / kStep;
                     const uint8_t* in = code_ring + (size_t)from * C::kCodeBytes;
-                    uint8_t* out = ring + (size_t)slot * C::kSlotBytes;
+                    uint4 v[kTimes];  // all under way at once, and while the slot is waited for
 #pragma unroll
-                    for (int i = 0; i < KT / kStep; ++i) {
+                    for (int i = 0; i < kTimes; ++i) {
                         const int row = first_row + i * kStep;
-                        uint4 v = *reinterpret_cast<const uint4*>(in + (HD == 64 ? row * 64 + ((c ^ (row >> 1 & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4)));
-                        if (edge && kv == 1) {
-                            const int tok = k0 + row;
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        v[i] = *reinterpret_cast<const uint4*>(in + (HD == 64 ? row * 64 + ((c ^ (row >> 1 & 3)) << 4) : row * 128 + ((c ^ (row & 7)) << 4)));
+                    }
+                    if (pass[r] > 0 && !wait(&empty[slot], (pass[r] - 1) & 1)) {
+                        gone = true;
+                        break;
+                    }
+                    if (edge && kv == 1) {
+#pragma unroll
+                        for (int i = 0; i < kTimes; ++i) {
+                            const int tok = k0 + first_row + i * kStep;
+                            uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                             bool bad = false;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
@@ -361,17 +369,19 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                             }
                             if (bad && tok - hidden < kOddTokens)
                                 atomicOr(&odd_bits[(tok - hidden) >> 5], 1u << ((tok - hidden) & 31));
-                            v = make_uint4(w[0], w[1], w[2], w[3]);
+                            v[i] = make_uint4(w[0], w[1], w[2], w[3]);
                         }
-                        uint8_t* line = out + (c >> 2) * (KT * 128) + row * 128;
-                        const int at = 2 * c & 7;
+                    }
+                    uint8_t* out = ring + (size_t)slot * C::kSlotBytes + (c >> 2) * (KT * 128) + first_row * 128;
+#pragma unroll
+                    for (int i = 0; i < kTimes; ++i) {  // kStep is a multiple of 8: the same swizzle every time
                         uint4 lo, hi;
-                        e4m3x4_to_f16x2(v.x, lo.x, lo.y);
-                        e4m3x4_to_f16x2(v.y, lo.z, lo.w);
-                        e4m3x4_to_f16x2(v.z, hi.x, hi.y);
-                        e4m3x4_to_f16x2(v.w, hi.z, hi.w);
-                        *reinterpret_cast<uint4*>(line + ((at ^ (row & 7)) << 4)) = lo;
-                        *reinterpret_cast<uint4*>(line + ((at + 1 ^ (row & 7)) << 4)) = hi;
+                        e4m3x4_to_f16x2(v[i].x, lo.x, lo.y);
+                        e4m3x4_to_f16x2(v[i].y, lo.z, lo.w);
+                        e4m3x4_to_f16x2(v[i].z, hi.x, hi.y);
+                        e4m3x4_to_f16x2(v[i].w, hi.z, hi.w);
+                        *reinterpret_cast<uint4*>(out + i * (kStep * 128) + (((2 * c & 7) ^ r8) << 4)) = lo;
+                        *reinterpret_cast<uint4*>(out + i * (kStep * 128) + (((2 * c & 7) + 1 ^ r8) << 4)) = hi;
                     }
                     if (kv == 1 && ct < KT / 16) {
                         const uint32_t* w = words + (from * 4 + ct * 16 / box) * 3;
