@@ -36,15 +36,17 @@ int attn_over(int rows, int64_t items)
 }
 
 // Query rows of a prompt's item, and a segment's own cost in 64-key tiles.
-constexpr int kPromptRows = 256, kPromptOver = 8;
+int prompt_rows(const CacheView& c) { return c.code == TF_KV_E4M3 ? 256 : 128; }
+constexpr int kPromptOver = 8;
 
 struct AttnLayout {
     size_t counters, parts, total;
 };
 
-AttnLayout attn_layout(const CacheView& c, int rows)
+AttnLayout attn_layout(const CacheView& c, int rows, bool causal)
 {
-    const size_t ctas = (size_t)device_sms() * (rows > 64 ? 1 : attn_warp_ctas(c, rows));
+    // those that take shares: CTAs, and of a prompt's groups of them
+    const size_t ctas = (size_t)device_sms() * (causal && rows == 128 ? 2 : rows > 64 ? 1 : attn_warp_ctas(c, rows));
     AttnLayout L{};
     L.counters = 256;
     L.parts = L.counters + (ctas * 2 * sizeof(unsigned) + 255) / 256 * 256;
@@ -146,7 +148,7 @@ int fill_params(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvc
 
 int launch_attn(AttnParams& p, int rows, bool causal, void* ws, cudaStream_t stream, const char* name)
 {
-    const AttnLayout L = attn_layout(p.c, rows);
+    const AttnLayout L = attn_layout(p.c, rows, causal);
     p.status = static_cast<int*>(ws);
     p.counters = reinterpret_cast<unsigned*>(static_cast<uint8_t*>(ws) + L.counters);
     p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.parts);
@@ -176,7 +178,7 @@ size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int
         report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q, B or max_rows out of range", name);
         return 0;
     }
-    return attn_layout(v, attn_rows(max_rows, n_q / v.n_kv, v.head_dim)).total;
+    return attn_layout(v, attn_rows(max_rows, n_q / v.n_kv, v.head_dim), false).total;
 }
 
 int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
@@ -206,7 +208,7 @@ size_t tf_prompt_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B)
         report_error(TF_E_UNSUPPORTED_SHAPE, "%s: n_q, B or head_dim out of range", name);
         return 0;
     }
-    return attn_layout(v, kPromptRows).total;
+    return attn_layout(v, prompt_rows(v), true).total;
 }
 
 int tf_prompt_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
@@ -226,7 +228,7 @@ int tf_prompt_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const
         return rc;
     (void)flags;
     p.over = kPromptOver;
-    return launch_attn(p, kPromptRows, true, ws, static_cast<cudaStream_t>(stream), name);
+    return launch_attn(p, prompt_rows(p.c), true, ws, static_cast<cudaStream_t>(stream), name);
 }
 
 }  // extern "C"

@@ -271,7 +271,7 @@ struct Shares {
 //   P(rt) = rt * (over + 1) + floor((rt * base + A * rt * (rt + 1) / 2) / KEYS),   A = ROWS / group, rounded up, tokens,
 // in closed form, so an item is found without a list of them. Its own P(rt + 1) - P(rt) is over - 1 at least above its
 // key tiles ceil((base + last row's token + 1) / KEYS), since A (rt + 1) >= that token + 1; over >= 2.
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int PER = 1>  // PER: shares a CTA
 struct PromptShares {
     struct Entry {
         int first, r0, base, rows;
@@ -357,7 +357,7 @@ struct PromptShares {
                 record_status(p.status, TF_E_UNSUPPORTED_SHAPE);
             total = 0;
         }
-        deal(gridDim.x);
+        deal(gridDim.x * PER);
     }
 
     __host__ __device__ __forceinline__ int start_of(unsigned cta) const { return (int)(cta >= ctas ? total : share * cta + rest * cta / ctas); }
@@ -485,19 +485,19 @@ __device__ __forceinline__ const float* part_of(const AttnParams& p, const Split
 // copies of its own into `buf`, all under way at once: loaded into registers item by item, 2 or 3 parts of
 // 256 rows took a CTA 8 us. buf: ROWS * HD * 4 bytes + 1024 for each part and thread, at most.
 template <int ROWS, int HD, int THREADS>
-__device__ __forceinline__ void join_many(const AttnParams& p, const SplitItem& s, int i0, int i1, uint8_t* buf)
+__device__ __forceinline__ void join_many(const AttnParams& p, const SplitItem& s, int i0, int i1, uint8_t* buf, int tid)
 {
     static_assert(THREADS % ROWS == 0, "a thread keeps its row");
     constexpr int kFloats = ROWS * (HD + 2);
-    const int n = s.c1 - s.c0 + 1, items = i1 - i0, first = i0 + threadIdx.x, row = first % ROWS;
+    const int n = s.c1 - s.c0 + 1, items = i1 - i0, first = i0 + tid, row = first % ROWS;
     if (row >= s.rows)
         return;
-    float4* data = reinterpret_cast<float4*>(buf) + threadIdx.x;                       // [n][items]
-    float* weight = reinterpret_cast<float*>(buf + (size_t)n * items * 16) + threadIdx.x;  // [n][THREADS]
+    float4* data = reinterpret_cast<float4*>(buf) + tid;                       // [n][items]
+    float* weight = reinterpret_cast<float*>(buf + (size_t)n * items * 16) + tid;  // [n][THREADS]
     for (int c = 0; c < n; ++c) {
         const float* part = part_of(p, s, s.c0 + c, kFloats);
-        for (int i = threadIdx.x; i < items; i += THREADS)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(data + c * items + i - threadIdx.x)),
+        for (int i = tid; i < items; i += THREADS)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(data + c * items + i - tid)),
                          "l"(part + (size_t)(i0 + i) * 4)
                          : "memory");
     }
@@ -528,7 +528,7 @@ __device__ __forceinline__ void join_many(const AttnParams& p, const SplitItem& 
     asm volatile("cp.async.wait_all;" ::: "memory");
     const int r = s.row0 + row;
     uint16_t* o = p.o + ((int64_t)(s.q.r0 + p.token_of(r)) * p.n_q + s.h * p.group + p.head_of(r)) * HD;
-    for (int i = 0; i + (int)threadIdx.x < items; i += THREADS) {
+    for (int i = 0; i + tid < items; i += THREADS) {
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int c = 0; c < n; ++c) {
             const float w = weight[c * THREADS];
@@ -539,16 +539,16 @@ __device__ __forceinline__ void join_many(const AttnParams& p, const SplitItem& 
     }
 }
 
-// Waits for the item's parts and writes this CTA's slice of its output. THREADS threads, which
-// share named barrier 1; several lanes share four columns of a row and take every lp-th part, so
+// Waits for the item's parts and writes this CTA's (or group's) slice of its output. THREADS threads, which
+// share named barrier `bar`; several lanes share four columns of a row and take every lp-th part, so
 // that all parts are asked for at once. The order in which they are added depends on the call alone.
 // buf: shared memory that nobody uses any more, as join_many wants it (ROWS >= 128).
 template <int ROWS, int HD, int THREADS>
-__device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem& s, volatile int* abort_flag, uint8_t* buf = nullptr)
+__device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem& s, volatile int* abort_flag, uint8_t* buf, int tid, int cta, int bar)
 {
     constexpr int kFloats = ROWS * (HD + 2), kQuads = HD / 4;
-    const int n = s.c1 - s.c0 + 1, me = blockIdx.x - s.c0;
-    if (threadIdx.x == 0) {
+    const int n = s.c1 - s.c0 + 1, me = cta - s.c0;
+    if (tid == 0) {
         const long long start = clock64(), limit = (long long)(p.limit_ns * 2);
         unsigned there = 0;
         while (true) {
@@ -562,7 +562,7 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
             }
         }
     }
-    named_bar_sync(1, THREADS);
+    named_bar_sync(bar, THREADS);
     // item: four columns of a row, whether the sequence has that row or not: no division by a length here
     constexpr unsigned kItems = ROWS * kQuads;
     const int i0 = (int)(kItems * (unsigned)me / (unsigned)n), i1 = (int)(kItems * (unsigned)(me + 1) / (unsigned)n);
@@ -570,14 +570,14 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
     if constexpr (ROWS >= 128) {
         done = i1 - i0 > THREADS;
         if (done)
-            join_many<ROWS, HD, THREADS>(p, s, i0, i1, buf);
+            join_many<ROWS, HD, THREADS>(p, s, i0, i1, buf, tid);
     }
     int lp = 1;
     while (lp < 8 && (i1 - i0) * lp * 2 <= THREADS && lp < n)
         lp *= 2;
-    const int sub = threadIdx.x % lp;
+    const int sub = tid % lp;
     for (int at = done ? i1 : i0; at < i1; at += THREADS / lp) {
-        const int item = at + threadIdx.x / lp;
+        const int item = at + tid / lp;
         const int quad = item / ROWS, row = item % ROWS, col = quad * 4;
         const bool in = item < i1 && row < s.rows;
         float m = -INFINITY, l = 0.f;
@@ -628,8 +628,8 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
         }
     }
     // the last CTA to have read the parts leaves the counters as the next call wants them
-    named_bar_sync(1, THREADS);
-    if (threadIdx.x == 0 && !*abort_flag && atom_add_acq_rel_gpu(p.counters + 2 * s.c0 + 1, 1u) == (unsigned)(n - 1)) {
+    named_bar_sync(bar, THREADS);
+    if (tid == 0 && !*abort_flag && atom_add_acq_rel_gpu(p.counters + 2 * s.c0 + 1, 1u) == (unsigned)(n - 1)) {
         p.counters[2 * s.c0] = 0;
         p.counters[2 * s.c0 + 1] = 0;
     }

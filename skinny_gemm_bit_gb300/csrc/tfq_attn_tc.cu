@@ -24,8 +24,10 @@
 // the weights stay below 256 and the sums are exact enough, and the output in tensor memory
 // needs no rescaling; when it does, the group first waits for its last product with V.
 //
-// Prompts (CAUSAL) are the same with a limit in the place of a mask: an item is 256 rows of a prompt, and its key
-// tiles end with its last row's.
+// Prompts (CAUSAL) have a limit in the place of a mask, and an item's key tiles end with its last row's. Over a bf16 cache
+// an item is 128 rows and each group works for itself (DUAL), with a producer warp, an MMA warp and half the ring of its
+// own, as two CTAs would (the runtime places one CTA with tcgen05 on an SM): while one begins or ends an item the
+// other computes. Over 8 bits a pair shares its tiles, since each is converted but once then.
 //
 // Over a cache of 8 bits (E8) the TMA brings the tiles as they are into a ring of their own, and four more warps turn
 // them into fp16 in the ring that the MMAs read (exactly: fp16 has every e4m3 value), so the MMAs and the
@@ -53,11 +55,11 @@ constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w][buffer] at 128 w + 64 
 constexpr float kGrow = 8.f;
 
 // offsets in shared memory
-constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 288, kTcODone = 320, kTcQReady = 352, kTcOFull = 360, kTcFin = 368;
-constexpr int kTcTmem = 384, kTcFlags = 400 /* [0] abort [2] abort as of a segment's end */, kTcOdd = 416;
-// tokens taken out of V, bits from the item's first: [8] words (trees: 2); 8 bits: [kOddItems][8], as
-// the converting warps may be some items ahead
-constexpr int kOddItems = 8, kTcOdd8 = 512;
+constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 288, kTcODone = 320, kTcQReady = 352, kTcOFull = 368, kTcFin = 480;
+constexpr int kTcTmem = 384, kTcFlags = 400 /* [0] abort [2 + w] abort as of a segment's end */, kTcOdd = 416;
+// tokens taken out of V, bits from the item's first: [groups][8] words (trees: 2); 8 bits: [groups][4][8], or [8][8] where the
+// groups share items, as the converting warps may be some items ahead
+constexpr int kTcOdd8 = 512;
 constexpr int kOddTokens = 256;  // behind them no row of the item sees a token
 constexpr int kTcFull8 = 768, kTcEmpty8 = 896;  // 8 bits: the ring of codes
 constexpr int kTcMl = 1024;  // [2][128] (m, l)
@@ -67,24 +69,27 @@ constexpr int kTcSched = 3 * 1024;
 constexpr int kMaxCodeSlots = 8;
 constexpr int kTcFactor = 3 * 1024, kTcScales = 4 * 1024, kTcWords = kTcScales + kMaxSlots * 48, kTcSched8 = 6 * 1024;
 static_assert(kTcWords + kMaxCodeSlots * 48 <= kTcSched8, "scales");
-static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 128 && kTcOdd + 32 <= kTcOdd8 && kTcOdd8 + kOddItems * 32 <= kTcFull8, "slots");
+static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 128 && kTcOdd + 64 <= kTcFin && kTcFin + 16 <= kTcOdd8 && kTcOdd8 + 256 <= kTcFull8, "slots");
 
-template <int HD, bool PAIR, bool E8>
+template <int HD, bool PAIR, bool E8, bool DUAL>
 struct TcCfg {
     static constexpr int ROWS = PAIR ? 256 : 128;
+    static constexpr int kConvertThreads = DUAL ? 64 : 128;  // that convert a tile together
+    static constexpr int kOddItems = DUAL ? 4 : 8;
     static constexpr int kSlotBytes = KT * HD * 2;
     static constexpr int kCodeBytes = KT * HD;  // 8 bits: of a tile of codes
-    static constexpr int kQBytes = ROWS * HD * 2 < 32768 ? 32768 : ROWS * HD * 2;  // also the groups' exchange, 2 x 16 KB
+    // also the groups' exchange, 2 x 16 KB
+    static constexpr int kQBytes = (DUAL ? 2 : 1) * ROWS * HD * 2 < 32768 ? 32768 : (DUAL ? 2 : 1) * ROWS * HD * 2;
     static constexpr size_t q_off(int B) { return ((E8 ? kTcSched8 : kTcSched) + schedule_bytes(B) + 1023) / 1024 * 1024; }
     static constexpr int slots(int B)
     {
         const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (E8 ? 4 * kCodeBytes : 0)) / kSlotBytes;
-        return E8 && n >= 8 ? 8 : n < kMaxSlots ? (int)n : kMaxSlots;
+        return (int)(E8 && n >= 8 ? 8 : n < kMaxSlots ? n : kMaxSlots) / (DUAL ? 2 : 1) * (DUAL ? 2 : 1);
     }
-    // an even number: K's tiles lie in the even ones
+    // an even number (for each group that has its own): K's tiles lie in the even ones
     static constexpr int code_slots(int B)
     {
-        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (size_t)slots(B) * kSlotBytes) / kCodeBytes / 2 * 2;
+        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (size_t)slots(B) * kSlotBytes) / kCodeBytes / (DUAL ? 4 : 2) * (DUAL ? 4 : 2);
         return !E8 ? 0 : n < kMaxCodeSlots ? (int)n : kMaxCodeSlots;
     }
     static constexpr size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes + (size_t)code_slots(B) * kCodeBytes; }
@@ -231,7 +236,7 @@ struct SharesOf {
 };
 template <int ROWS>
 struct SharesOf<ROWS, true> {
-    using type = PromptShares<ROWS, KT>;
+    using type = PromptShares<ROWS, KT, ROWS == 128 ? 2 : 1>;
 };
 
 template <int HD, bool PAIR, bool E8, bool CAUSAL>
@@ -239,8 +244,10 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
     tree_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map, uint32_t slots, uint32_t code_slots,
                         int q_off)
 {
-    using C = TcCfg<HD, PAIR, E8>;
-    constexpr int ROWS = C::ROWS;
+    constexpr bool DUAL = CAUSAL && !PAIR;  // the groups apart
+    using C = TcCfg<HD, PAIR, E8, DUAL>;
+    constexpr int ROWS = C::ROWS, kConvertThreads = C::kConvertThreads, kOddItems = C::kOddItems;
+    constexpr bool ALT = !PAIR && !DUAL;  // the groups take every other tile of the same rows
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTcFull);
@@ -256,9 +263,12 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
     unsigned* odd = reinterpret_cast<unsigned*>(smem + kTcOdd);
     float* ml = reinterpret_cast<float*>(smem + kTcMl);
     uint8_t* qbuf = smem + q_off;
-    uint8_t* ring = qbuf + C::kQBytes;
+    // Groups apart: each has its queries, ring and codes in one piece, which at the end takes a slice of the parts
+    constexpr int kOwnQ = DUAL ? C::kQBytes / 2 : C::kQBytes;
+    const uint32_t own_bytes = kOwnQ + slots / 2 * C::kSlotBytes + code_slots / 2 * C::kCodeBytes;
+    uint8_t* ring = qbuf + kOwnQ;
     // 8 bits: the ring of codes and its barriers, and where the scales lie
-    [[maybe_unused]] uint8_t* code_ring = ring + (size_t)slots * C::kSlotBytes;
+    [[maybe_unused]] uint8_t* code_ring = ring + (size_t)(DUAL ? slots / 2 : slots) * C::kSlotBytes;
     [[maybe_unused]] uint64_t* full8 = reinterpret_cast<uint64_t*>(smem + kTcFull8);
     [[maybe_unused]] uint64_t* empty8 = reinterpret_cast<uint64_t*>(smem + kTcEmpty8);
     [[maybe_unused]] float* factor = reinterpret_cast<float*>(smem + kTcFactor);
@@ -275,19 +285,21 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         }
         for (uint32_t i = 0; E8 && i < code_slots; ++i) {
             // each box's lane, and again in V's slots where it has fetched scales
-            mbar_init(&full8[i], 1 + pieces + (i & 1 ? pieces : 0));
+            mbar_init(&full8[i], 1 + pieces + (i & 1 ? pieces : 0));  // a group's first slot is even
             mbar_init(&empty8[i], kConvertThreads / 32);
         }
-        for (int i = 0; E8 && i < kOddItems * 8; ++i)
+        for (int i = 0; E8 && i < 64; ++i)
             odd8[i] = 0;
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 4);
             mbar_init(&o_done[i], 1);
         }
-        mbar_init(q_ready, 8);
-        mbar_init(o_full, 2);
-        mbar_init(fin, 2);
+        for (int i = 0; i < 2; ++i) {  // of each group; else the first alone counts
+            mbar_init(&q_ready[i], DUAL ? 4 : 8);
+            mbar_init(&o_full[i], DUAL ? 1 : 2);
+            mbar_init(&fin[i], DUAL ? 1 : 2);
+        }
         flags[0] = 0;
         fence_mbar_init();
     }
@@ -303,11 +315,28 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kTcTmem);
-    const int u0 = shares.start_of(blockIdx.x), u1 = shares.start_of(blockIdx.x + 1);
     // Slots: one ring for both groups, or half of them for each. Every use of a slot is waited for, in
     // order, by each MMA warp that its ring serves: a wait can then not take the phase before last
     // for the one it is after.
     const uint32_t ring_slots = PAIR ? slots : slots / 2;
+    // a CTA's units, or a group's
+    auto cta_of_group = [&](int w) { return DUAL ? 2 * blockIdx.x + w : blockIdx.x; };
+    auto first_unit = [&](int w) { return shares.start_of(cta_of_group(w)); };
+    auto end_unit = [&](int w) { return shares.start_of(cta_of_group(w) + 1); };
+    // slots are counted over both groups' rings
+    auto to_group = [&](int w) {
+        if (!DUAL)
+            return;
+        qbuf += w * own_bytes;
+        ring += w * (own_bytes - ring_slots * C::kSlotBytes);
+        if (E8) {
+            const uint32_t first = w * (code_slots / 2);
+            full8 += first;
+            empty8 += first;
+            code_ring += w * own_bytes;
+            words += first * 12;
+        }
+    };
     // The first token that not every row of an item sees
     auto hidden_from = [&](const Segment& g) { return g.q.base + (CAUSAL ? p.token_of(g.rt * ROWS) : 0); };
 
@@ -315,6 +344,9 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
         // ---- codes to fp16: a thread 16 codes of a row. Eight lanes take the same piece of eight rows, so that
         // neither their reads nor their writes meet in a bank
+        const int w = DUAL ? (warp - 12) >> 1 : 0, u0 = first_unit(w), u1 = end_unit(w);
+        const uint32_t my_codes = DUAL ? code_slots / 2 : code_slots;
+        to_group(w);
         const int ct = threadIdx.x & (kConvertThreads - 1);
         const int r8 = ct & 7, c = (ct >> 3) % (HD / 16), first_row = (ct >> 3) / (HD / 16) * 8 + r8;
         constexpr int kStep = kConvertThreads / (HD / 16);  // rows that the threads take at once
@@ -329,9 +361,9 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             if (g.t0 == g.t1)
                 continue;
             const int hidden = hidden_from(g), len = g.q.len();
-            unsigned* odd_bits = odd8 + seg % kOddItems * 8;
+            unsigned* odd_bits = odd8 + (w * kOddItems + seg % kOddItems) * 8;
             for (int t = g.t0; t < g.t1 && !gone; ++t) {
-                const int r = PAIR ? 0 : (t - g.t0) & 1, k0 = t * KT;
+                const int r = DUAL ? w : PAIR ? 0 : (t - g.t0) & 1, k0 = t * KT;
                 const bool edge = k0 + KT > hidden;
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t slot = r * ring_slots + next_slot[r];
@@ -403,7 +435,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         next_slot[r] = 0;
                         ++pass[r];
                     }
-                    if (++from == code_slots) {
+                    if (++from == my_codes) {
                         from = 0;
                         from_phase ^= 1;
                     }
@@ -413,8 +445,11 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8) {
+        if (warp == 8 || (DUAL && warp == 11)) {
             // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
+            const int w = DUAL && warp == 11 ? 1 : 0, u0 = first_unit(w), u1 = end_unit(w);
+            const uint32_t my_codes = DUAL ? code_slots / 2 : code_slots;
+            to_group(w);
             const int z = lane / pieces, piece = lane % pieces;
             const bool active = lane < pieces * (E8 ? 1 : HD / 64);
             uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0};
@@ -436,7 +471,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                     const bool in = active && row < len, good = page >= 0 && page < p.c.n_pages;
                     if (in && !good)
                         record_status(p.status, TF_E_INVALID_ARG);
-                    const int r = PAIR || E8 ? 0 : (t - g.t0) & 1;
+                    const int r = DUAL && !E8 ? w : PAIR || E8 ? 0 : (t - g.t0) & 1;
                     for (int kv = 0; kv < 2; ++kv) {
                         if constexpr (E8) {
                             const uint32_t slot = next_slot[0];
@@ -469,7 +504,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                                 }
                                 mbar_arrive(&full8[slot]);
                             }
-                            if (++next_slot[0] == code_slots) {
+                            if (++next_slot[0] == my_codes) {
                                 next_slot[0] = 0;
                                 ++pass[0];
                             }
@@ -498,7 +533,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             }
             if (gone)  // no copy may be in flight when the CTA leaves: each slot's last one
                 for (int r = 0; r < (PAIR || E8 ? 1 : 2); ++r)
-                    for (uint32_t s = 0; s < (E8 ? code_slots : ring_slots); ++s) {
+                    for (uint32_t s = 0; s < (E8 ? my_codes : ring_slots); ++s) {
                         const uint32_t uses = pass[r] + (s < next_slot[r] ? 1 : 0);
                         if (uses > 0)
                             mbar_wait_bounded(E8 ? &full8[s] : &full[r * ring_slots + s], (uses - 1) & 1, p.limit_ns);
@@ -506,12 +541,14 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         } else if (warp < 11) {
             // ---- an MMA warp: group w's scores and its products with V (one warp for both groups spent
             // 1340 cycles a step on its waits, one after the other, for 640 of MMAs)
-            const int w = warp - 9;
+            const int w = warp - 9, u0 = first_unit(w), u1 = end_unit(w);
+            to_group(w);
             const bool one = elect_one();
             constexpr uint32_t kIdS = instr_desc(KT, false, E8), kIdO = instr_desc(HD, true, E8);
             const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
             const uint32_t ra = smem_u32(ring) + first_slot * C::kSlotBytes;
             const uint64_t ad = smem_desc(smem_u32(qbuf) + (PAIR ? w * (128 * HD * 2) : 0), 16, 1024);
+            const int own = DUAL ? w : 0;
             full += first_slot;
             empty += first_slot;
             // the ring's slots of the next K and the next V tile: every second one
@@ -545,8 +582,8 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 u += g.units;
                 if (g.t0 == g.t1)
                     continue;
-                const int n = PAIR ? g.t1 - g.t0 : (g.t1 - g.t0 + 1 - w) / 2;  // the group's tiles
-                ok = wait(q_ready, seg & 1);
+                const int n = !ALT ? g.t1 - g.t0 : (g.t1 - g.t0 + 1 - w) / 2;  // the group's tiles
+                ok = wait(&q_ready[own], seg & 1);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -570,18 +607,25 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         ok = scores(buf);
                 }
                 if (ok)
-                    tc_commit(o_full, one);
+                    tc_commit(&o_full[own], one);
                 ++seg;
             }
             // no MMA may be under way when the tensor memory is given back
-            tc_commit(fin, one);
-            mbar_wait_bounded(fin, 0, p.limit_ns);
+            tc_commit(&fin[own], one);
+            mbar_wait_bounded(&fin[own], 0, p.limit_ns);
             __syncwarp();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(soft_regs(E8)));
         // ---- softmax: group w, a thread a row
-        const int w = warp >> 2, wt = threadIdx.x & 127;
+        const int w = warp >> 2, wt = threadIdx.x & 127, own = DUAL ? w : 0, u0 = first_unit(w), u1 = end_unit(w);
+        // the threads that have items in common: both groups', or one's
+        constexpr int kMates = DUAL ? 128 : kSoftThreads;
+        const int mate = DUAL ? wt : threadIdx.x, bar = 1 + own, cta = cta_of_group(w);
+        to_group(w);
+        odd += own * 8;
+        odd8 += own * kOddItems * 8;
+        factor += own * 128;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_at = tmem + lanes + kOCol + 128 * w;
         const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale goes into Q
@@ -601,10 +645,10 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             const SeqRows& q = g.q;
             const int len = q.len(), n_rows = q.rows * p.group;
             // the item's queries, swizzled as the tiles are; a thread loads eight pieces before it stores one
-            constexpr int kRowsAtOnce = kSoftThreads / (HD / 8);  // rows that the threads hold a piece each of
-            const int qc = threadIdx.x % (HD / 8);
+            constexpr int kRowsAtOnce = kMates / (HD / 8);  // rows that the threads hold a piece each of
+            const int qc = mate % (HD / 8);
 #pragma unroll 1
-            for (int r0 = threadIdx.x / (HD / 8); r0 < ROWS; r0 += 8 * kRowsAtOnce) {
+            for (int r0 = mate / (HD / 8); r0 < ROWS; r0 += 8 * kRowsAtOnce) {
                 uint4 v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -635,12 +679,12 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
                 }
             }
-            if (!E8 && threadIdx.x < (CAUSAL ? 8 : 2))
-                odd[threadIdx.x] = 0;
+            if (!E8 && mate < (CAUSAL ? 8 : 2))
+                odd[mate] = 0;
             fence_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(q_ready);
+                mbar_arrive(&q_ready[own]);
             const int row = g.rt * ROWS + (PAIR ? w * 128 : 0) + wt;
             const bool valid = row < n_rows, busy = __any_sync(0xffffffffu, valid);
             const int hidden = hidden_from(g);
@@ -658,12 +702,12 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             float m = -INFINITY, l = 0.f;  // the reference, in score units (8 bits: times its factor), and the sum against it
             [[maybe_unused]] float row_factor = 0.f;
             if constexpr (E8) {
-                named_bar_sync(1, kSoftThreads);  // the rows' factors are there
+                named_bar_sync(bar, kMates);  // the rows' factors are there
                 row_factor = factor[(PAIR ? w * 128 : 0) + wt];
             }
             bool had = false, ok = true;
             int buf = 0;
-            for (int t = g.t0 + (PAIR ? 0 : w); t < g.t1; t += PAIR ? 1 : 2, buf ^= 1) {
+            for (int t = g.t0 + (ALT ? w : 0); t < g.t1; t += ALT ? 2 : 1, buf ^= 1) {
                 ok = __all_sync(0xffffffffu, attn_wait(&s_full[2 * w + buf], phase >> buf & 1, flags, p.status, p.limit_ns));
                 if (!ok)
                     break;
@@ -834,26 +878,26 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 if (lane == 0)
                     mbar_arrive(&p_ready[2 * w + buf]);
             }
-            ok = ok && __all_sync(0xffffffffu, attn_wait(o_full, seg & 1, flags, p.status, p.limit_ns));
+            ok = ok && __all_sync(0xffffffffu, attn_wait(&o_full[own], seg & 1, flags, p.status, p.limit_ns));
             tc_fence_after();
 
             // ---- the segment's end
             const bool whole = g.t0 == 0 && g.t1 == g.nt;
-            float* part = p.parts + (int64_t)(g.t0 > 0 ? 2 * blockIdx.x : 2 * blockIdx.x + 1) * (ROWS * (HD + 2));
+            float* part = p.parts + (int64_t)(g.t0 > 0 ? 2 * cta : 2 * cta + 1) * (ROWS * (HD + 2));
             const int prow = (PAIR ? w * 128 : 0) + wt;  // the row within the tile
             float mine = m == -INFINITY ? -INFINITY : E8 ? m : m * sc, top = mine, all = l;
-            if (!PAIR) {
+            if (ALT) {
                 ml[(w * 128 + wt) * 2] = mine;
                 ml[(w * 128 + wt) * 2 + 1] = l;
             }
-            named_bar_sync(1, kSoftThreads);  // also: nobody reads Q or marks odd values any more
-            if (!PAIR) {
+            named_bar_sync(bar, kMates);  // also: nobody reads Q or marks odd values any more
+            if (ALT) {
                 const float other = ml[((w ^ 1) * 128 + wt) * 2];
                 top = fmaxf(mine, other);
                 const float r = top == -INFINITY ? 0.f : top;
                 all = l * attn_ex2(mine - r) + ml[((w ^ 1) * 128 + wt) * 2 + 1] * attn_ex2(other - r);
             }
-            const float ref = top == -INFINITY ? 0.f : top, scale = PAIR ? 1.f : attn_ex2(mine - ref);
+            const float ref = top == -INFINITY ? 0.f : top, scale = ALT ? attn_ex2(mine - ref) : 1.f;
             const float inv = all == 0.f ? 0.f : 1.f / all;
             [[maybe_unused]] const unsigned* odd_words = E8 ? odd8 + seg % kOddItems * 8 : odd;
             auto odd_bits = [&](int i) { return (uint64_t)odd_words[2 * i + 1] << 32 | odd_words[2 * i]; };  // tokens hidden + 64 i ..
@@ -890,7 +934,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 for (int i = 0; i < 32; ++i)
                     a[i] = had ? __uint_as_float(o[i]) * scale : 0.f;
             };
-            if (PAIR) {
+            if (!ALT) {
                 if (busy)
 #pragma unroll 1
                     for (int c0 = 0; c0 < HD; c0 += 32) {
@@ -919,25 +963,25 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                     named_bar_sync(1, kSoftThreads);
                 }
             }
-            if (threadIdx.x == 0)
-                flags[2] = flags[0];
-            tc_fence_before();                // the output has been read
-            named_bar_sync(1, kSoftThreads);  // the Q buffer may be written again; the part is written
-            if (flags[2])                     // one answer for all warps
+            if (mate == 0)
+                flags[2 + own] = flags[0];
+            tc_fence_before();            // the output has been read
+            named_bar_sync(bar, kMates);  // the Q buffer may be written again; the part is written
+            if (flags[2 + own])           // one answer for all warps
                 break;
-            if (E8 && threadIdx.x < 8)        // for the item kOddItems on, whose tiles wait for those in between
-                odd8[seg % kOddItems * 8 + threadIdx.x] = 0;
+            if (E8 && mate < 8)           // for the item kOddItems on, whose tiles wait for those in between
+                odd8[seg % kOddItems * 8 + mate] = 0;
             if (!whole) {
                 SplitItem& s = split[g.t0 > 0 ? 0 : 1];
                 s = SplitItem{q, g.h, g.rt * ROWS, min(ROWS, n_rows - g.rt * ROWS), shares.cta_of(g.first), shares.cta_of(g.first + g.nt - 1)};
-                if (threadIdx.x == 0)  // the barrier above and this release cover every thread's part
+                if (mate == 0)  // the barrier above and this release cover every thread's part
                     part_written(p, s);
             }
             ++seg;
         }
         for (int i = 0; i < 2; ++i)
             if (split[i].c0 <= split[i].c1)
-                join_slice<ROWS, HD, kSoftThreads>(p, split[i], flags, qbuf);
+                join_slice<ROWS, HD, kMates>(p, split[i], flags, qbuf, mate, cta, bar);
     }
     tc_fence_before();
     __syncthreads();
@@ -950,12 +994,13 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
 template <int HD, bool PAIR, bool E8, bool CAUSAL>
 cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
 {
-    using C = TcCfg<HD, PAIR, E8>;
-    // join_many: fewer parts than ROWS * HD / 4 / kSoftThreads + 1, and a slice's rounding for each
-    constexpr int kPartBytes = C::ROWS * HD * 4;  // of a part's output
-    static_assert(C::smem(kMaxAttnSeqs) - 1024 - C::q_off(kMaxAttnSeqs) >= kPartBytes + (kPartBytes / 16 / kSoftThreads + 1) * (kSoftThreads * 4 + 16),
+    constexpr bool DUAL = CAUSAL && !PAIR;
+    using C = TcCfg<HD, PAIR, E8, DUAL>;
+    // join_many: fewer parts than ROWS * HD / 4 / threads + 1, and a slice's rounding for each
+    constexpr int kPartBytes = C::ROWS * HD * 4, kThreads = DUAL ? 128 : kSoftThreads;  // of a part's output; that join it
+    static_assert((C::smem(kMaxAttnSeqs) - 1024 - C::q_off(kMaxAttnSeqs)) / (DUAL ? 2 : 1) >= kPartBytes + (kPartBytes / 16 / kThreads + 1) * (kThreads * 4 + 16),
                   "the queries' and the rings' memory takes a slice of the parts");
-    static_assert(!E8 || (C::slots(kMaxAttnSeqs) >= (PAIR ? 3 : 6) && C::code_slots(kMaxAttnSeqs) >= 4), "rings");
+    static_assert(C::slots(kMaxAttnSeqs) >= (PAIR ? 3 : 6) && (!E8 || C::code_slots(kMaxAttnSeqs) >= 4), "rings");
     static std::atomic<uint64_t> done{0};
     const cudaError_t e = allow_smem(tree_attn_tc_kernel<HD, PAIR, E8, CAUSAL>, 227 * 1024, done);
     if (e != cudaSuccess)
@@ -968,7 +1013,7 @@ template <int HD, bool E8>
 cudaError_t launch_any(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream)
 {
     if (causal)
-        return launch<HD, true, E8, true>(p, map, stream);
+        return launch<HD, E8, E8, true>(p, map, stream);  // 8 bits: a pair
     return rows == 128 ? launch<HD, false, E8, false>(p, map, stream) : launch<HD, true, E8, false>(p, map, stream);
 }
 

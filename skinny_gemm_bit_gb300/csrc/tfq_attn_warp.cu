@@ -775,7 +775,7 @@ __global__ void __launch_bounds__(Cfg<HD, RW, E8>::kCtaThreads, Cfg<HD, RW, E8>:
     }
     for (int i = 0; i < 2; ++i)
         if (split[i].c0 <= split[i].c1)
-            join_slice<ROWS, HD, kCtaThreads>(p, split[i], flags);
+            join_slice<ROWS, HD, kCtaThreads>(p, split[i], flags, nullptr, threadIdx.x, blockIdx.x, 1);
     // no copy may be in flight when the CTA leaves (after a wait that gave up)
     for (; taken < issued; ++taken)
         mbar_wait_bounded(&full[taken % NS], (taken / NS) & 1, p.limit_ns);

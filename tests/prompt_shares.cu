@@ -20,7 +20,7 @@ using namespace tfq;
 
 int main()
 {
-    using S = PromptShares<256, 64>;
+    using S = PromptShares<128, 64, 2>;
     int number = 0, grid, n_kv, group, over, B;
     while (std::scanf("%d %d %d %d %d", &grid, &n_kv, &group, &over, &B) == 5) {
         AttnParams p{};
@@ -76,7 +76,7 @@ int main()
             for (int h = 0; h < n_kv; ++h)
                 for (int rt = 0; rt < s.row_tiles(entries[b].rows); ++rt) {
                     Item& it = items[{entries[b].r0, h, rt}];
-                    const int last = ((rt + 1) * 256 - 1) / group;  // the tile's last row's token
+                    const int last = ((rt + 1) * 128 - 1) / group;  // the tile's last row's token
                     const int len = entries[b].base + (last + 1 < entries[b].rows ? last + 1 : entries[b].rows);
                     CHECK(it.next == (len + 63) / 64);
                     CHECK(it.c0 < 0 || (int)it.written.size() == it.c1 - it.c0 + 1);

@@ -7,7 +7,7 @@ import pytest
 
 from skinny_gemm_bit_gb300 import build as tfq_build
 
-SMS = 152
+SMS = 2 * 152  # two groups a CTA, each with a share
 
 
 @pytest.fixture(scope="module")
