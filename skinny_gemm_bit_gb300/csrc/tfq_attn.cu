@@ -37,7 +37,7 @@ int attn_over(int rows, int64_t items)
 
 // Query rows of a prompt's item, and a segment's own cost in 64-key tiles.
 int prompt_rows(const CacheView& c) { return c.code == TF_KV_E4M3 ? 256 : 128; }
-constexpr int kPromptOver = 8;
+constexpr int kPromptOver = 4;
 
 struct AttnLayout {
     size_t counters, parts, total;
@@ -95,6 +95,16 @@ bool encode_rows(const CacheView& c, int total_rows, int rows, int halves, CUten
     const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)halves}, one[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, c.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The queries as {64 columns, head_dim / 64, heads, tokens}: a box is the group's heads of 128 / group tokens, 128 rows.
+bool encode_queries(const AttnParams& p, CUtensorMap* map)
+{
+    const EncodeTiled fn = encode_tiled();
+    const cuuint64_t hd = p.c.head_dim, dims[4] = {64, hd / 64, (cuuint64_t)p.n_q, (cuuint64_t)p.M}, strides[3] = {128, hd * 2, (cuuint64_t)p.ldq * 2};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)p.group, 128u / p.group}, one[4] = {1, 1, 1, 1};
+    return fn != nullptr && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(p.q), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The checks that both calls make of their arguments, and the parameters that follow from them.
@@ -157,7 +167,10 @@ int launch_attn(AttnParams& p, int rows, bool causal, void* ws, cudaStream_t str
     const int tile = tc ? kTcTile : attn_warp_tile(p.c);
     if (!encode_rows(p.c, p.total_rows, p.c.page_size < tile ? p.c.page_size : tile, tc ? 1 : p.c.head_dim / 64, &map))
         return report_error(TF_E_CUDA, "%s: the cache's tensor map could not be made", name);
-    const cudaError_t e = tc ? launch_attn_tc(p, rows, causal, map, stream) : launch_attn_warp(p, rows, map, stream);
+    // the boxes of a prompt's queries, where a group's heads of whole tokens are 128 rows (a negative scale goes into Q)
+    CUtensorMap q_map = map;
+    p.q_boxes = causal && rows == 128 && 128 % p.group == 0 && p.scale_log2 >= 0.f && encode_queries(p, &q_map);
+    const cudaError_t e = tc ? launch_attn_tc(p, rows, causal, map, q_map, stream) : launch_attn_warp(p, rows, map, stream);
     return e == cudaSuccess ? TF_OK : report_error(TF_E_CUDA, "%s: %s", name, cudaGetErrorString(e));
 }
 

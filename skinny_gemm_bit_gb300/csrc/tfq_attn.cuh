@@ -37,6 +37,7 @@ struct AttnParams {
     const uint64_t* masks;
     float scale_log2;  // scale * log2(e)
     uint16_t* o;
+    bool q_boxes;  // prompts: an item's queries are a tensor map's box
     int* status;
     unsigned* counters;  // [CTAs][2], zero between calls: parts written, CTAs done with them
     float* parts;        // [2 * CTAs] of a part: [head_dim / 4][ROWS] float4, then [ROWS] (m, l)
@@ -638,7 +639,7 @@ __device__ __forceinline__ void join_slice(const AttnParams& p, const SplitItem&
 // rows: query rows of an item. tfq_attn_warp.cu: 16, and up to head_dim 128 also 32;
 // tfq_attn_tc.cu: 128 or 256, head_dim 64 or 128; causal: the rows of prompts. *Tile: keys of a tile.
 cudaError_t launch_attn_warp(const AttnParams& p, int rows, const CUtensorMap& map, cudaStream_t stream);
-cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream);
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, const CUtensorMap& q_map, cudaStream_t stream);
 int attn_warp_tile(const CacheView& c);
 int attn_warp_ctas(const CacheView& c, int rows);  // an SM
 int attn_warp_threads(const CacheView& c, int rows);

@@ -55,7 +55,7 @@ constexpr uint32_t kTmemCols = 512, kOCol = 256;  // S[w][buffer] at 128 w + 64 
 constexpr float kGrow = 8.f;
 
 // offsets in shared memory
-constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 288, kTcODone = 320, kTcQReady = 352, kTcOFull = 368, kTcFin = 480;
+constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 288, kTcODone = 320, kTcQReady = 352, kTcOFull = 368, kTcFin = 480, kTcQFree = 496;
 constexpr int kTcTmem = 384, kTcFlags = 400 /* [0] abort [2 + w] abort as of a segment's end */, kTcOdd = 416;
 // tokens taken out of V, bits from the item's first: [groups][8] words (trees: 2); 8 bits: [groups][4][8], or [8][8] where the
 // groups share items, as the converting warps may be some items ahead
@@ -69,7 +69,7 @@ constexpr int kTcSched = 3 * 1024;
 constexpr int kMaxCodeSlots = 8;
 constexpr int kTcFactor = 3 * 1024, kTcScales = 4 * 1024, kTcWords = kTcScales + kMaxSlots * 48, kTcSched8 = 6 * 1024;
 static_assert(kTcWords + kMaxCodeSlots * 48 <= kTcSched8, "scales");
-static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 128 && kTcOdd + 64 <= kTcFin && kTcFin + 16 <= kTcOdd8 && kTcOdd8 + 256 <= kTcFull8, "slots");
+static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 128 && kTcOdd + 64 <= kTcFin && kTcQFree + 16 <= kTcOdd8 && kTcOdd8 + 256 <= kTcFull8, "slots");
 
 template <int HD, bool PAIR, bool E8, bool DUAL>
 struct TcCfg {
@@ -186,6 +186,16 @@ __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, in
         : "memory");
 }
 
+// A box {64 columns, 1, heads of a group, tokens} of the queries: the 128 rows of an item, as they lie in a tile.
+__device__ __forceinline__ void tma_queries(uint32_t dst, const CUtensorMap* map, int half, int head, int token, uint64_t* bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(map), "r"(0), "r"(half), "r"(head), "r"(token), "r"(smem_u32(bar))
+        : "memory");
+}
+
 __device__ __forceinline__ bool nonfinite16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }
 
 __device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi)
@@ -241,8 +251,8 @@ struct SharesOf<ROWS, true> {
 
 template <int HD, bool PAIR, bool E8, bool CAUSAL>
 __global__ void __launch_bounds__(tc_threads(E8), 1)
-    tree_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map, uint32_t slots, uint32_t code_slots,
-                        int q_off)
+    tree_attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map,
+                        uint32_t slots, uint32_t code_slots, int q_off)
 {
     constexpr bool DUAL = CAUSAL && !PAIR;  // the groups apart
     using C = TcCfg<HD, PAIR, E8, DUAL>;
@@ -259,6 +269,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
     uint64_t* q_ready = reinterpret_cast<uint64_t*>(smem + kTcQReady);
     uint64_t* o_full = reinterpret_cast<uint64_t*>(smem + kTcOFull);
     uint64_t* fin = reinterpret_cast<uint64_t*>(smem + kTcFin);
+    [[maybe_unused]] uint64_t* q_free = reinterpret_cast<uint64_t*>(smem + kTcQFree);  // groups apart: the item's scores are all formed
     volatile int* flags = reinterpret_cast<volatile int*>(smem + kTcFlags);
     unsigned* odd = reinterpret_cast<unsigned*>(smem + kTcOdd);
     float* ml = reinterpret_cast<float*>(smem + kTcMl);
@@ -296,7 +307,8 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             mbar_init(&o_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {  // of each group; else the first alone counts
-            mbar_init(&q_ready[i], DUAL ? 4 : 8);
+            mbar_init(&q_ready[i], DUAL ? (p.q_boxes ? 1 : 4) : 8);
+            mbar_init(&q_free[i], 1);
             mbar_init(&o_full[i], DUAL ? 1 : 2);
             mbar_init(&fin[i], DUAL ? 1 : 2);
         }
@@ -453,11 +465,25 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             const int z = lane / pieces, piece = lane % pieces;
             const bool active = lane < pieces * (E8 ? 1 : HD / 64);
             uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0};
+            [[maybe_unused]] uint32_t items = 0;
             bool gone = false;
             for (int u = u0; u < u1 && !gone;) {
                 const Segment g = shares.segment(u, u1);
                 u += g.units;
                 const SeqRows& q = g.q;
+                if (DUAL && p.q_boxes && g.t0 < g.t1) {
+                    // the item's queries, while the group is still busy with the end of the one before
+                    if (items > 0 && !__all_sync(0xffffffffu, attn_wait(&q_free[w], (items - 1) & 1, flags, p.status, p.limit_ns))) {
+                        gone = true;
+                        break;
+                    }
+                    ++items;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&q_ready[w], 128 * HD * 2);
+                    __syncwarp();
+                    if (lane < HD / 64)
+                        tma_queries(smem_u32(qbuf + lane * (128 * 128)), &q_map, lane, g.h * p.group, q.r0 + p.token_of(g.rt * 128), &q_ready[w]);
+                }
                 const int32_t* table = p.c.table + (int64_t)q.slot * p.c.max_pages;
                 const int len = q.len();
                 auto page_at = [&](int t) {
@@ -531,7 +557,9 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                     page = next;
                 }
             }
-            if (gone)  // no copy may be in flight when the CTA leaves: each slot's last one
+            if (DUAL && p.q_boxes && items > 0)  // no copy may be in flight when the CTA leaves
+                mbar_wait_bounded(&q_ready[w], (items - 1) & 1, p.limit_ns);
+            if (gone)  // each slot's last one
                 for (int r = 0; r < (PAIR || E8 ? 1 : 2); ++r)
                     for (uint32_t s = 0; s < (E8 ? my_codes : ring_slots); ++s) {
                         const uint32_t uses = pass[r] + (s < next_slot[r] ? 1 : 0);
@@ -589,6 +617,8 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 tc_fence_after();
                 for (int k = 0; k < 2 && k < n && ok; ++k)
                     ok = scores(k);
+                if (DUAL && ok && n <= 2)
+                    tc_commit(&q_free[w], one);
                 for (int k = 0; k < n && ok; ++k) {
                     const int buf = k & 1;
                     ok = wait(&p_ready[2 * w + buf], p_phase >> buf & 1) && wait(&full[v_slot], v_phase);
@@ -603,8 +633,11 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                     tc_commit(&o_done[2 * w + buf], one);
                     tc_commit(&empty[v_slot], one);
                     forward(v_slot, v_phase);
-                    if (k + 2 < n)
+                    if (k + 2 < n) {
                         ok = scores(buf);
+                        if (DUAL && ok && k + 3 == n)
+                            tc_commit(&q_free[w], one);
+                    }
                 }
                 if (ok)
                     tc_commit(&o_full[own], one);
@@ -637,54 +670,65 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         split[0].c1 = split[1].c1 = 0;
         const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
         uint32_t tiles = 0;  // the group's tiles so far
+        const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+        Segment upcoming{};
+        if (DUAL && u0 < u1)
+            upcoming = shares.segment(u0, u1);
         for (int u = u0; u < u1;) {
-            const Segment g = shares.segment(u, u1);
+            const Segment g = DUAL ? upcoming : shares.segment(u, u1);
             u += g.units;
-            if (g.t0 == g.t1)
+            if (g.t0 == g.t1) {
+                if (DUAL && u < u1)
+                    upcoming = shares.segment(u, u1);
                 continue;
+            }
             const SeqRows& q = g.q;
             const int len = q.len(), n_rows = q.rows * p.group;
-            // the item's queries, swizzled as the tiles are; a thread loads eight pieces before it stores one
-            constexpr int kRowsAtOnce = kMates / (HD / 8);  // rows that the threads hold a piece each of
-            const int qc = mate % (HD / 8);
-#pragma unroll 1
-            for (int r0 = mate / (HD / 8); r0 < ROWS; r0 += 8 * kRowsAtOnce) {
-                uint4 v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int row = g.rt * ROWS + r0 + i * kRowsAtOnce;
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (row < n_rows)
-                        v[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + p.token_of(row)) * p.ldq +
-                                                                     (int64_t)(g.h * p.group + p.head_of(row)) * HD + qc * 8));
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = r0 + i * kRowsAtOnce;
-                    if constexpr (E8) {
-                        // fp16, the row's largest value moved to 2^14 .. 2^15 by a power of two (tfq_attn_warp.cu)
-                        uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu), __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
-                        top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-                        for (int o = HD / 16; o > 0; o >>= 1)
-                            top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int up = min(127 + 14 - (int)(top >> 7), 60);
-                        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-                        auto pair = [&](uint32_t x) { return f32x2_to_f16x2(bf16lo_f32(x) * f, bf16hi_f32(x) * f); };
-                        v[i] = make_uint4(pair(v[i].x), pair(v[i].y), pair(v[i].z), pair(v[i].w));
-                        if (qc == 0)
-                            factor[r] = sc * __uint_as_float((uint32_t)(127 - up) << 23);
-                    }
-                    *reinterpret_cast<uint4*>(qbuf + (r >> 7) * (128 * HD * 2) + (qc >> 3) * (128 * 128) + (r & 127) * 128 + (((qc & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
-                }
-            }
             if (!E8 && mate < (CAUSAL ? 8 : 2))
                 odd[mate] = 0;
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&q_ready[own]);
+            if (DUAL && p.q_boxes)
+                named_bar_sync(bar, kMates);  // before anybody notes a token
+            // the item's queries, swizzled as the tiles are; a thread loads eight pieces before it stores one
+            if (!DUAL || !p.q_boxes) {
+                constexpr int kRowsAtOnce = kMates / (HD / 8);  // rows that the threads hold a piece each of
+                const int qc = mate % (HD / 8);
+#pragma unroll 1
+                for (int r0 = mate / (HD / 8); r0 < ROWS; r0 += 8 * kRowsAtOnce) {
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = g.rt * ROWS + r0 + i * kRowsAtOnce;
+                        v[i] = make_uint4(0, 0, 0, 0);
+                        if (row < n_rows)
+                            v[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + (q.r0 + p.token_of(row)) * p.ldq +
+                                                                         (int64_t)(g.h * p.group + p.head_of(row)) * HD + qc * 8));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = r0 + i * kRowsAtOnce;
+                        if constexpr (E8) {
+                            // fp16, the row's largest value moved to 2^14 .. 2^15 by a power of two (tfq_attn_warp.cu)
+                            uint32_t top = __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu), __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu));
+                            top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+                            for (int o = HD / 16; o > 0; o >>= 1)
+                                top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            const int up = min(127 + 14 - (int)(top >> 7), 60);
+                            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+                            auto pair = [&](uint32_t x) { return f32x2_to_f16x2(bf16lo_f32(x) * f, bf16hi_f32(x) * f); };
+                            v[i] = make_uint4(pair(v[i].x), pair(v[i].y), pair(v[i].z), pair(v[i].w));
+                            if (qc == 0)
+                                factor[r] = sc * __uint_as_float((uint32_t)(127 - up) << 23);
+                        }
+                        *reinterpret_cast<uint4*>(qbuf + (r >> 7) * (128 * HD * 2) + (qc >> 3) * (128 * 128) + (r & 127) * 128 + (((qc & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip);
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&q_ready[own]);
+            }
             const int row = g.rt * ROWS + (PAIR ? w * 128 : 0) + wt;
             const bool valid = row < n_rows, busy = __any_sync(0xffffffffu, valid);
             const int hidden = hidden_from(g);
@@ -734,29 +778,32 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         break;
                     const int tok = k0 + wt % KT;
                     if (tok >= hidden) {
-                        // two threads a row; each starts at a piece of its own, for the banks' sake
+                        // two threads a row; each starts at a piece of its own, for the banks' sake. Rows are
+                        // rarely written: an exponent of all ones, or nothing else, carries into the bit above it
                         uint8_t* v = ring + (size_t)(first_slot + pos % ring_slots) * C::kSlotBytes + wt % KT * 128;
-                        bool bad = false;
-#pragma unroll 4
-                        for (int c = wt / KT * (HD / 16); c < (wt / KT + 1) * (HD / 16); ++c) {
-                            uint4* at = reinterpret_cast<uint4*>(v + (c >> 3) * (KT * 128) + ((c + wt) & 7) * 16);
-                            uint32_t x[4];
-                            *reinterpret_cast<uint4*>(x) = *at;
-                            for (int j = 0; j < 4; ++j) {
-                                if (tok >= len) {
-                                    x[j] = 0;
-                                    continue;
-                                }
-                                const bool lo = nonfinite16(x[j]), hi = nonfinite16(x[j] >> 16);
-                                bad |= lo | hi;
-                                x[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                        auto at = [&](int i) { return reinterpret_cast<uint4*>(v + ((wt / KT * (HD / 16) + i) >> 3) * (KT * 128) + ((wt / KT * (HD / 16) + i + wt) & 7) * 16); };
+                        uint32_t sum = 0;
+#pragma unroll
+                        for (int i = 0; i < HD / 16; ++i) {
+                            const uint4 x = *at(i);
+                            sum |= (x.x & 0x7F807F80u) + 0x00800080u | (x.y & 0x7F807F80u) + 0x00800080u;
+                            sum |= (x.z & 0x7F807F80u) + 0x00800080u | (x.w & 0x7F807F80u) + 0x00800080u;
+                        }
+                        const bool bad = tok < len && (sum & 0x80008000u) != 0;
+                        if (PAIR || bad || tok >= len) {  // (of a pair each makes its own product safe)
+#pragma unroll 1
+                            for (int i = 0; i < HD / 16; ++i) {
+                                uint32_t x[4];
+                                *reinterpret_cast<uint4*>(x) = *at(i);
+                                for (int j = 0; j < 4; ++j)
+                                    x[j] &= tok >= len ? 0u : (nonfinite16(x[j]) ? 0u : 0xFFFFu) | (nonfinite16(x[j] >> 16) ? 0u : 0xFFFF0000u);
+                                *at(i) = *reinterpret_cast<uint4*>(x);
                             }
-                            *at = *reinterpret_cast<uint4*>(x);
+                            fence_async_smem();
                         }
                         if (bad && tok - hidden < kOddTokens)
                             atomicOr(&odd[(tok - hidden) >> 5], 1u << ((tok - hidden) & 31));
                     }
-                    fence_async_smem();
                 }
                 if (busy) {
                     uint32_t s[KT];
@@ -878,6 +925,8 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 if (lane == 0)
                     mbar_arrive(&p_ready[2 * w + buf]);
             }
+            if (DUAL && u < u1)  // while the last product with V is under way
+                upcoming = shares.segment(u, u1);
             ok = ok && __all_sync(0xffffffffu, attn_wait(&o_full[own], seg & 1, flags, p.status, p.limit_ns));
             tc_fence_after();
 
@@ -911,11 +960,22 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                     for (int i = 0; i < (CAUSAL ? 4 : 1); ++i)
                         add_odd<HD, E8>(p, q, g.h, row, hidden + 64 * i, odd_bits(i), CAUSAL ? view(hidden + 64 * i) : mask, sc, sign, ref, c0, a);
                 if (whole) {
-                    uint4* o = reinterpret_cast<uint4*>(p.o + ((int64_t)(q.r0 + p.token_of(row)) * p.n_q + g.h * p.group + p.head_of(row)) * HD + c0);
+                    uint16_t* o = p.o + ((int64_t)(q.r0 + p.token_of(row)) * p.n_q + g.h * p.group + p.head_of(row)) * HD + c0;
+                    uint32_t x[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[i] = make_uint4(f32x2_to_bf16x2(a[8 * i] * inv, a[8 * i + 1] * inv), f32x2_to_bf16x2(a[8 * i + 2] * inv, a[8 * i + 3] * inv),
-                                          f32x2_to_bf16x2(a[8 * i + 4] * inv, a[8 * i + 5] * inv), f32x2_to_bf16x2(a[8 * i + 6] * inv, a[8 * i + 7] * inv));
+                    for (int i = 0; i < 16; ++i)
+                        x[i] = f32x2_to_bf16x2(a[2 * i] * inv, a[2 * i + 1] * inv);
+                    if (wide) {  // a sector a store
+#pragma unroll
+                        for (int i = 0; i < 16; i += 8)
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 2 * i), "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]),
+                                         "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+                                         : "memory");
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            reinterpret_cast<uint4*>(o)[i] = make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    }
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
@@ -992,7 +1052,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
 }
 
 template <int HD, bool PAIR, bool E8, bool CAUSAL>
-cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t stream)
+cudaError_t launch(const AttnParams& p, const CUtensorMap& map, const CUtensorMap& q_map, cudaStream_t stream)
 {
     constexpr bool DUAL = CAUSAL && !PAIR;
     using C = TcCfg<HD, PAIR, E8, DUAL>;
@@ -1005,25 +1065,25 @@ cudaError_t launch(const AttnParams& p, const CUtensorMap& map, cudaStream_t str
     const cudaError_t e = allow_smem(tree_attn_tc_kernel<HD, PAIR, E8, CAUSAL>, 227 * 1024, done);
     if (e != cudaSuccess)
         return e;
-    return launch_coop(tree_attn_tc_kernel<HD, PAIR, E8, CAUSAL>, dim3(device_sms()), dim3(tc_threads(E8)), C::smem(p.B), stream, p, map,
+    return launch_coop(tree_attn_tc_kernel<HD, PAIR, E8, CAUSAL>, dim3(device_sms()), dim3(tc_threads(E8)), C::smem(p.B), stream, p, map, q_map,
                        (uint32_t)C::slots(p.B), (uint32_t)C::code_slots(p.B), (int)C::q_off(p.B));
 }
 
 template <int HD, bool E8>
-cudaError_t launch_any(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream)
+cudaError_t launch_any(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, const CUtensorMap& q_map, cudaStream_t stream)
 {
     if (causal)
-        return launch<HD, E8, E8, true>(p, map, stream);  // 8 bits: a pair
-    return rows == 128 ? launch<HD, false, E8, false>(p, map, stream) : launch<HD, true, E8, false>(p, map, stream);
+        return launch<HD, E8, E8, true>(p, map, q_map, stream);  // 8 bits: a pair
+    return rows == 128 ? launch<HD, false, E8, false>(p, map, q_map, stream) : launch<HD, true, E8, false>(p, map, q_map, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, cudaStream_t stream)
+cudaError_t launch_attn_tc(const AttnParams& p, int rows, bool causal, const CUtensorMap& map, const CUtensorMap& q_map, cudaStream_t stream)
 {
     if (p.c.code == TF_KV_E4M3)
-        return p.c.head_dim == 64 ? launch_any<64, true>(p, rows, causal, map, stream) : launch_any<128, true>(p, rows, causal, map, stream);
-    return p.c.head_dim == 64 ? launch_any<64, false>(p, rows, causal, map, stream) : launch_any<128, false>(p, rows, causal, map, stream);
+        return p.c.head_dim == 64 ? launch_any<64, true>(p, rows, causal, map, q_map, stream) : launch_any<128, true>(p, rows, causal, map, q_map, stream);
+    return p.c.head_dim == 64 ? launch_any<64, false>(p, rows, causal, map, q_map, stream) : launch_any<128, false>(p, rows, causal, map, q_map, stream);
 }
 
 }  // namespace tfq
