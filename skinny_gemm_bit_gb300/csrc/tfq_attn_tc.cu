@@ -61,15 +61,15 @@ constexpr int kTcTmem = 384, kTcFlags = 400 /* [0] abort [2 + w] abort as of a s
 // groups share items, as the converting warps may be some items ahead
 constexpr int kTcOdd8 = 512;
 constexpr int kOddTokens = 256;  // behind them no row of the item sees a token
-constexpr int kTcFull8 = 768, kTcEmpty8 = 896;  // 8 bits: the ring of codes
+constexpr int kTcFull8 = 768, kTcEmpty8 = 832, kTcScaleFull = 896;  // 8 bits: the ring of codes; the rings' tiles' scales
 constexpr int kTcMl = 1024;  // [2][128] (m, l)
 constexpr int kTcSched = 3 * 1024;
-// 8 bits: the rows' factors of the scores; by slot, 3 x [4] of a tile's blocks: 2^ks, log2 vs, 1 / vs; by slot of codes
-// and box, the words with K's and V's scales and their places in them
-constexpr int kMaxCodeSlots = 8;
-constexpr int kTcFactor = 3 * 1024, kTcScales = 4 * 1024, kTcWords = kTcScales + kMaxSlots * 48, kTcSched8 = 6 * 1024;
+// 8 bits: the rows' factors of the scores; by ring, the last 8 tiles' 3 x [4] of their blocks: 2^ks, log2 vs, 1 / vs; by slot
+// of codes and box, the words with K's and V's scales and their places in them
+constexpr int kMaxCodeSlots = 8, kScaleTiles = 8;
+constexpr int kTcFactor = 3 * 1024, kTcScales = 4 * 1024, kTcWords = kTcScales + 2 * kScaleTiles * 48, kTcSched8 = 6 * 1024;
 static_assert(kTcWords + kMaxCodeSlots * 48 <= kTcSched8, "scales");
-static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 128 && kTcOdd + 64 <= kTcFin && kTcQFree + 16 <= kTcOdd8 && kTcOdd8 + 256 <= kTcFull8, "slots");
+static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 64 && kTcScaleFull + 2 * kScaleTiles * 8 <= kTcMl && kTcOdd + 64 <= kTcFin && kTcQFree + 16 <= kTcOdd8 && kTcOdd8 + 256 <= kTcFull8, "slots");
 
 template <int HD, bool PAIR, bool E8, bool DUAL>
 struct TcCfg {
@@ -282,6 +282,9 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
     [[maybe_unused]] uint8_t* code_ring = ring + (size_t)(DUAL ? slots / 2 : slots) * C::kSlotBytes;
     [[maybe_unused]] uint64_t* full8 = reinterpret_cast<uint64_t*>(smem + kTcFull8);
     [[maybe_unused]] uint64_t* empty8 = reinterpret_cast<uint64_t*>(smem + kTcEmpty8);
+    // [ring][tile % 8]. A tile's K is converted when the products of tiles after the eighth before it are done, so nobody
+    // reads that one's scales any more
+    [[maybe_unused]] uint64_t* scale_full = reinterpret_cast<uint64_t*>(smem + kTcScaleFull);
     [[maybe_unused]] float* factor = reinterpret_cast<float*>(smem + kTcFactor);
     [[maybe_unused]] float* scales = reinterpret_cast<float*>(smem + kTcScales);
     [[maybe_unused]] uint32_t* words = reinterpret_cast<uint32_t*>(smem + kTcWords);
@@ -295,10 +298,12 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             mbar_init(&empty[i], PAIR ? 2 : 1);
         }
         for (uint32_t i = 0; E8 && i < code_slots; ++i) {
-            // each box's lane, and again in V's slots where it has fetched scales
-            mbar_init(&full8[i], 1 + pieces + (i & 1 ? pieces : 0));  // a group's first slot is even
+            // each box's lane, and again in K's slots where it has fetched scales
+            mbar_init(&full8[i], 1 + pieces + (i & 1 ? 0 : pieces));  // a group's first slot is even
             mbar_init(&empty8[i], kConvertThreads / 32);
         }
+        for (int i = 0; E8 && i < 2 * kScaleTiles; ++i)
+            mbar_init(&scale_full[i], 1);
         for (int i = 0; E8 && i < 64; ++i)
             odd8[i] = 0;
         for (int i = 0; i < 4; ++i) {
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         const int ct = threadIdx.x & (kConvertThreads - 1);
         const int r8 = ct & 7, c = (ct >> 3) % (HD / 16), first_row = (ct >> 3) / (HD / 16) * 8 + r8;
         constexpr int kStep = kConvertThreads / (HD / 16);  // rows that the threads take at once
-        uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0}, from = 0, from_phase = 0, seg = 0;
+        uint32_t next_slot[2] = {0, 0}, pass[2] = {0, 0}, tiles[2] = {0, 0}, from = 0, from_phase = 0, seg = 0;
         bool gone = false;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
@@ -395,6 +400,22 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         gone = true;
                         break;
                     }
+                    if (kv == 0 && ct < 32) {  // the tile's scales
+                        if (ct < KT / 16) {
+                            const uint32_t* w = words + (from * 4 + ct * 16 / box) * 3;
+                            const uint32_t within = ct * 16 % box / 2;
+                            const int ks = min(max((int)(w[0] >> ((w[2] & 0xFFu) + within) & 0xFFu), 127 - 32), 127 + 32);
+                            const int vs = min(max((int)(w[1] >> ((w[2] >> 8) + within) & 0xFFu), 127 - 32), 127 + 32);
+                            float* to = scales + (r * kScaleTiles + tiles[r] % kScaleTiles) * 12 + ct;
+                            to[0] = __uint_as_float((uint32_t)ks << 23);
+                            to[4] = (float)(vs - 127);
+                            to[8] = __uint_as_float((uint32_t)(254 - vs) << 23);
+                        }
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&scale_full[r * kScaleTiles + tiles[r] % kScaleTiles]);
+                        ++tiles[r];
+                    }
                     if (edge && kv == 1) {
 #pragma unroll
                         for (int i = 0; i < kTimes; ++i) {
@@ -426,16 +447,6 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         e4m3x4_to_f16x2(v[i].w, hi.z, hi.w);
                         *reinterpret_cast<uint4*>(out + i * (kStep * 128) + (((2 * c & 7) ^ r8) << 4)) = lo;
                         *reinterpret_cast<uint4*>(out + i * (kStep * 128) + (((2 * c & 7) + 1 ^ r8) << 4)) = hi;
-                    }
-                    if (kv == 1 && ct < KT / 16) {
-                        const uint32_t* w = words + (from * 4 + ct * 16 / box) * 3;
-                        const uint32_t within = ct * 16 % box / 2;
-                        const int ks = min(max((int)(w[0] >> ((w[2] & 0xFFu) + within) & 0xFFu), 127 - 32), 127 + 32);
-                        const int vs = min(max((int)(w[1] >> ((w[2] >> 8) + within) & 0xFFu), 127 - 32), 127 + 32);
-                        float* to = scales + slot * 12 + ct;
-                        to[0] = __uint_as_float((uint32_t)ks << 23);
-                        to[4] = (float)(vs - 127);
-                        to[8] = __uint_as_float((uint32_t)(254 - vs) << 23);
                     }
                     fence_async_smem();
                     __syncwarp();
@@ -513,11 +524,11 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                                 const bool there = in && good;
                                 const int y = there ? (int)p.c.row_of(p.layer, kv, page, g.h) + (row & (p.c.page_size - 1)) : p.total_rows;
                                 tma_box(smem_u32(code_ring + (size_t)slot * C::kCodeBytes + piece * box * HD), &map, y, 0, &full8[slot]);
-                                if (kv == 1) {
+                                if (kv == 0) {
                                     // the tile's scales, as the aligned words that hold them
                                     uint32_t* w = words + (slot * 4 + piece) * 3;
                                     if (there) {
-                                        const int64_t v = y >> 4, k = v - (((int64_t)p.c.n_pages * p.c.n_kv) << (p.c.page_shift - 4));
+                                        const int64_t k = y >> 4, v = k + (((int64_t)p.c.n_pages * p.c.n_kv) << (p.c.page_shift - 4));
                                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(w)), "l"(p.c.scales + (k & ~3ll)) : "memory");
                                         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(w + 1)), "l"(p.c.scales + (v & ~3ll)) : "memory");
                                         w[2] = (uint32_t)(k & 3) * 8 | (uint32_t)(v & 3) * 8 << 8;
@@ -761,12 +772,12 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 const bool edge = k0 + KT > hidden;
                 [[maybe_unused]] const float* blocks = nullptr;
                 if constexpr (E8) {
-                    // the converting warps have seen to V, and left the tile's scales beside it
-                    const uint32_t pos = 2 * tiles + 1;
-                    ok = __all_sync(0xffffffffu, attn_wait(&full[first_slot + pos % ring_slots], (pos / ring_slots) & 1, flags, p.status, p.limit_ns));
+                    // the converting warps see to V, and have left the tile's scales
+                    const int at = (PAIR ? 0 : w) * kScaleTiles + tiles % kScaleTiles;
+                    ok = __all_sync(0xffffffffu, attn_wait(&scale_full[at], (tiles / kScaleTiles) & 1, flags, p.status, p.limit_ns));
                     if (!ok)
                         break;
-                    blocks = scales + (first_slot + pos % ring_slots) * 12;
+                    blocks = scales + at * 12;
                 } else if (edge) {
                     // values behind the sequence's end become zeros, and infinities and NaN among the
                     // block's own are noted and taken out: a row that does not see them may not meet
