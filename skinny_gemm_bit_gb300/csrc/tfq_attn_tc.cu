@@ -338,8 +338,9 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
     const uint32_t ring_slots = PAIR ? slots : slots / 2;
     // a CTA's units, or a group's
     auto cta_of_group = [&](int w) { return DUAL ? 2 * blockIdx.x + w : blockIdx.x; };
-    auto first_unit = [&](int w) { return shares.start_of(cta_of_group(w)); };
-    auto end_unit = [&](int w) { return shares.start_of(cta_of_group(w) + 1); };
+    const int cta_u0 = DUAL ? 0 : shares.start_of(blockIdx.x), cta_u1 = DUAL ? 0 : shares.start_of(blockIdx.x + 1);
+    auto first_unit = [&](int w) { return DUAL ? shares.start_of(cta_of_group(w)) : cta_u0; };
+    auto end_unit = [&](int w) { return DUAL ? shares.start_of(cta_of_group(w) + 1) : cta_u1; };
     // slots are counted over both groups' rings
     auto to_group = [&](int w) {
         if (!DUAL)
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         split[0].c1 = split[1].c1 = 0;
         const uint32_t first_slot = PAIR ? 0 : w * ring_slots;
         uint32_t tiles = 0;  // the group's tiles so far
-        const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
+        const bool wide = !PAIR && (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
         Segment upcoming{};
         if (DUAL && u0 < u1)
             upcoming = shares.segment(u0, u1);
@@ -793,28 +794,43 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         // rarely written: an exponent of all ones, or nothing else, carries into the bit above it
                         uint8_t* v = ring + (size_t)(first_slot + pos % ring_slots) * C::kSlotBytes + wt % KT * 128;
                         auto at = [&](int i) { return reinterpret_cast<uint4*>(v + ((wt / KT * (HD / 16) + i) >> 3) * (KT * 128) + ((wt / KT * (HD / 16) + i + wt) & 7) * 16); };
+                        bool bad = false;
+                        auto clean = [&](int i) {
+                            uint32_t x[4];
+                            *reinterpret_cast<uint4*>(x) = *at(i);
+                            for (int j = 0; j < 4; ++j) {
+                                if (tok >= len) {
+                                    x[j] = 0;
+                                    continue;
+                                }
+                                const bool lo = nonfinite16(x[j]), hi = nonfinite16(x[j] >> 16);
+                                bad |= lo | hi;
+                                x[j] &= (lo ? 0u : 0xFFFFu) | (hi ? 0u : 0xFFFF0000u);
+                            }
+                            *at(i) = *reinterpret_cast<uint4*>(x);
+                        };
                         uint32_t sum = 0;
 #pragma unroll
-                        for (int i = 0; i < HD / 16; ++i) {
+                        for (int i = 0; !PAIR && i < HD / 16; ++i) {
                             const uint4 x = *at(i);
                             sum |= (x.x & 0x7F807F80u) + 0x00800080u | (x.y & 0x7F807F80u) + 0x00800080u;
                             sum |= (x.z & 0x7F807F80u) + 0x00800080u | (x.w & 0x7F807F80u) + 0x00800080u;
                         }
-                        const bool bad = tok < len && (sum & 0x80008000u) != 0;
-                        if (PAIR || bad || tok >= len) {  // (of a pair each makes its own product safe)
+                        if (PAIR) {  // each makes its own product safe
+#pragma unroll 4
+                            for (int i = 0; i < HD / 16; ++i)
+                                clean(i);
+                        } else if (tok >= len || (sum & 0x80008000u) != 0) {
 #pragma unroll 1
-                            for (int i = 0; i < HD / 16; ++i) {
-                                uint32_t x[4];
-                                *reinterpret_cast<uint4*>(x) = *at(i);
-                                for (int j = 0; j < 4; ++j)
-                                    x[j] &= tok >= len ? 0u : (nonfinite16(x[j]) ? 0u : 0xFFFFu) | (nonfinite16(x[j] >> 16) ? 0u : 0xFFFF0000u);
-                                *at(i) = *reinterpret_cast<uint4*>(x);
-                            }
+                            for (int i = 0; i < HD / 16; ++i)
+                                clean(i);
                             fence_async_smem();
                         }
                         if (bad && tok - hidden < kOddTokens)
                             atomicOr(&odd[(tok - hidden) >> 5], 1u << ((tok - hidden) & 31));
                     }
+                    if (PAIR)
+                        fence_async_smem();
                 }
                 if (busy) {
                     uint32_t s[KT];
