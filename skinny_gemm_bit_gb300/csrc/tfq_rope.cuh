@@ -22,7 +22,7 @@ struct RopeParams {
     const int32_t* slots;
     int* status;
     int parts;  // warps (8 bits: CTAs) that share a row's heads
-    int step;   // 8 bits: rows that a CTA begins at
+    int step;   // 8 bits: a CTA's rows begin at or behind every step-th
 };
 
 __device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8])

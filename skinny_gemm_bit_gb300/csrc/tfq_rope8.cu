@@ -50,6 +50,10 @@ __device__ __forceinline__ void turn_sincos_near(uint32_t hi, uint32_t lo, float
     cs = __uint_as_float(__float_as_uint(odd ? s : c) ^ (quarter + 1 & 2) << 30);
 }
 
+// Apart: packed they are no faster, and take more registers
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+
 __device__ __forceinline__ void unpack8(const uint4& v, float2 (&f)[4])
 {
     f[0] = make_float2(bf16lo_f32(v.x), bf16hi_f32(v.x)), f[1] = make_float2(bf16lo_f32(v.y), bf16hi_f32(v.y));
@@ -61,7 +65,7 @@ __device__ __forceinline__ uint4 pack8(const float2 (&f)[4], float by)
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float2 t = __fmul2_rn(f[k], s);
+        const float2 t = mul2(f[k], s);
         w[k] = f32x2_to_bf16x2(t.x, t.y);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -72,7 +76,7 @@ __device__ __forceinline__ uint2 codes8(const float2 (&f)[4], float by)
     uint32_t c[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float2 t = __fmul2_rn(f[k], s);
+        const float2 t = mul2(f[k], s);
         c[k] = f32x2_to_e4m3x2(t.x, t.y);
     }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
@@ -187,7 +191,7 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
                 float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    ss = __ffma2_rn(x[k], x[k], __ffma2_rn(y[k], y[k], ss));
+                    ss = fma2(x[k], x[k], fma2(y[k], y[k], ss));
                 float sum = ss.x + ss.y;
 #pragma unroll
                 for (int o = LANES / 2; o > 0; o >>= 1)
@@ -199,11 +203,11 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
                     unpack8(__ldg(gamma + c0), g);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        x[k] = __fmul2_rn(x[k], g[k]);
+                        x[k] = mul2(x[k], g[k]);
                     unpack8(__ldg(gamma + c1), g);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        y[k] = __fmul2_rn(y[k], g[k]);
+                        y[k] = mul2(y[k], g[k]);
                 }
                 if (rot && (is_q || is_k)) {
                     if (p.interleaved) {
@@ -217,8 +221,8 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float2 u = x[k], c2 = make_float2(cs[2 * k], cs[2 * k + 1]), s2 = make_float2(sn[2 * k], sn[2 * k + 1]);
-                            x[k] = __ffma2_rn(y[k], make_float2(-s2.x, -s2.y), __fmul2_rn(u, c2));
-                            y[k] = __ffma2_rn(y[k], c2, __fmul2_rn(u, s2));
+                            x[k] = fma2(y[k], make_float2(-s2.x, -s2.y), mul2(u, c2));
+                            y[k] = fma2(y[k], c2, mul2(u, s2));
                         }
                     }
                 }
