@@ -537,7 +537,7 @@ int tf_kvcache_extend(const tf_kvcache* c, const int32_t* seqs, const int32_t* q
  * s holds what slot parent[s] held before the call (parent[s] = s: unchanged; -1: empty).
  * Full pages are shared; of an unfilled last page one slot keeps the original (the parent
  * itself when it stays, else the lowest slot that takes it) and every other gets a fresh
- * page with the filled rows copied, in all layers. Pages that no slot names any more are
+ * page with the filled rows copied (and their blocks' scales), in all layers. Pages that no slot names any more are
  * free after the call; they are not used by the same call. Errors are all or nothing as above:
  * TF_E_CACHE_FULL, or TF_E_INVALID_ARG for a parent out of range, a length beyond max_pages, or a table
  * entry out of range among the pages of a slot that another one takes. (A slot with such an entry can
@@ -642,9 +642,9 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
  * A call has fewer than 2^31 key tiles (tokens * n_kv * query-row tiles / 32): beyond that it
  * records TF_E_UNSUPPORTED_SHAPE and writes nothing.
  * Over a cache of 8 bits the codes are multiplied as they are, in fp16, which holds every e4m3 value, and the blocks'
- * scales enter the scores and the weights. A query row is scaled by a power of two into fp16's range (its values
- * below 2^-38 of its largest are lost), and the weights are rounded to fp16: 2^-11 of each, those
- * below 2^-31 of the row's largest lost.
+ * scales enter the scores and the weights. A query row is scaled by a power of two into fp16's range (2^60 at most; its
+ * values below 2^-38 of its largest are lost), and the weights are rounded to fp16: 2^-11 of each, those
+ * below 2^-32 of the row's largest lost. Its outputs are as near to 64 bits as their own rounding.
  */
 size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int max_rows);
 int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
@@ -655,13 +655,14 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
  * Attention of prompts over the cache: as tf_tree_attn_run with causal rows and no limit to a sequence's number of
  * them. Sequence b's rows q_start[b] .. q_start[b + 1) are the last T_b tokens of slot seqs[b], T_b >= 0, whose keys
  * and values are in the cache already; row i of them sees the tokens up to its own, len[seqs[b]] - T_b + i.
- * A whole prompt has T_b = len; a chunk of one has a context before it. A token's keys and values are read
- * once for 256 query rows (query heads that share a key/value head times rows) instead of for 64 rows of each head.
+ * A whole prompt has T_b = len; a chunk of one has a context before it. A token's keys and values are read once for
+ * each 128 query rows (256 over 8 bits), the query heads that share a key/value head times the sequence's rows.
  *   head_dim 64 or 128; n_q a multiple of n_kv, at most 64 query heads to a key/value head; 1 <= B <= 1024;
- *   1 <= M < 2^21
+ *   1 <= M < 2^21, M * n_q / n_kv < 2^25
  *   ws  tf_prompt_attn_workspace_bytes(c, n_q, B) bytes
  * Everything else (q, ldq, o, scale, refusals, errors in the status word, both kinds of cache, a workspace of its own)
- * is as for tf_tree_attn_run. A call has fewer than 2^31 key tiles of 64 tokens, each row tile's counted apart.
+ * is as for tf_tree_attn_run. A call has fewer than 2^31 key tiles of 64 tokens, each row tile's counted apart. Over a
+ * bf16 cache the weights are rounded to bf16: 8191 rows of one prompt 0.0022 of the output's norm against 64 bits.
  */
 size_t tf_prompt_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B);
 int tf_prompt_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,
@@ -692,7 +693,7 @@ typedef struct tf_attn_desc {
  *   q, k normalised and rotated, k and v stored to the cache's layer (tf_qk_norm_rope_run)
  *   o   = attention of the M rows over the cache (tf_tree_attn_run)
  *   h1  = h + o . Wo^T, and the MLP and the readout as there
- * on a cache that tf_kvcache_extend has made room in: seqs, q_start, masks, slots and
+ * on a cache (of either kind) that tf_kvcache_extend has made room in: seqs, q_start, masks, slots and
  * positions are that call's (device). The cache's layers are used from 0; it has at least
  * d->n_layers, n_kv * head_dim = d->kv_dim, and M (1..8) rows belong to B sequences. logits do not
  * overlap it.

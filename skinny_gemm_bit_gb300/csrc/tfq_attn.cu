@@ -36,6 +36,7 @@ int attn_over(int rows, int64_t items)
 }
 
 // Query rows of a prompt's item, and a segment's own cost in 64-key tiles.
+// Side by side with 8: 24 packed prompts 214 and 228 us, one of 8191 rows 226 and 231; 333 rows 18.8 with either.
 int prompt_rows(const CacheView& c) { return c.code == TF_KV_E4M3 ? 256 : 128; }
 constexpr int kPromptOver = 4;
 

@@ -104,7 +104,7 @@ struct Shares {
     unsigned total, ctas;  // units; CTAs that have some: every one of them has at least one
     unsigned share, rest;  // total = ctas * share + rest
     int whole;             // units of an item when each has a CTA, else 0
-    static constexpr int kTorn = kLeast == 6 ? 24 : 64;  // tiles that an item more costs a split call, over all CTAs
+    static constexpr int kTorn = kLeast == 6 ? 24 : 64;  // tiles that an item more costs a split call, over all CTAs (6: two an SM)
     static constexpr int kMostTiles = 1 << 20;
 
     __host__ __device__ Shares(const AttnParams& params, void* smem)

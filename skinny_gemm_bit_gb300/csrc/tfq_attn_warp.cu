@@ -22,7 +22,10 @@
 // which Q is stored in, and V's come by transposed 16-bit units, whose byte pairs belong to neighbouring columns:
 // each 16 columns make an even and an odd tile of the output. The scales cost nothing an element: with K's
 // in the factor of a block's scores and V's exponent added to them, x_j = score + log2 vs_j, weights are
-// w_j = 2^(x_j - m), and o = sum w_j code_j / sum w_j / vs_j.
+// w_j = 2^(x_j - m), and o = sum w_j code_j / sum w_j / vs_j. The same instructions a key for half the bytes: with eight
+// warps an SM the 64 ragged sequences took 166 us, bound by each warp's own chain of latencies; with two CTAs of six
+// 113, of which 33 are the items' beginnings and ends (7 us an item of one tile), and 80 us for each 537 MB
+// beyond that, 6.7 TB/s. 8 rows over 32,771 tokens 23 us, one token over 4097 11.7.
 #include "tfq_attn.cuh"
 
 namespace tfq {
