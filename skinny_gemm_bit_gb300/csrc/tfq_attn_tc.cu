@@ -53,7 +53,7 @@ constexpr int soft_regs(bool e8) { return e8 ? 176 : 216; }
 static_assert(soft_regs(false) * 256 + kOtherRegs * 128 <= 168 * tc_threads(false), "no more registers than the launch has");
 static_assert(soft_regs(true) * 256 + (kOtherRegs + kConvertRegs) * 128 <= 128 * tc_threads(true), "no more registers than the launch has");
 constexpr int kSoftThreads = 256;
-constexpr int kConvertThreads = 128;
+constexpr int kConvertThreads = 128;              // that convert a tile together
 constexpr float kHead = 7.f;  // fp16 weights reach 2^(kGrow + kHead) = 2^15
 constexpr int kMaxSlots = 12;
 constexpr int KT = kTcTile;                       // keys of a tile
@@ -63,9 +63,9 @@ constexpr float kGrow = 8.f;
 // offsets in shared memory
 constexpr int kTcFull = 0, kTcEmpty = 128, kTcSFull = 256, kTcPReady = 288, kTcODone = 320, kTcQReady = 352, kTcOFull = 368, kTcFin = 480, kTcQFree = 496;
 constexpr int kTcTmem = 384, kTcFlags = 400 /* [0] abort [2 + w] abort as of a segment's end */, kTcOdd = 416;
-// tokens taken out of V, bits from the item's first: [groups][8] words (trees: 2); 8 bits: [groups][4][8], or [8][8] where the
-// groups share items, as the converting warps may be some items ahead
-constexpr int kTcOdd8 = 512;
+// tokens taken out of V, bits from the item's first: [groups][8] words (trees: 2); 8 bits: [items][8], as the
+// converting warps may be some items ahead
+constexpr int kTcOdd8 = 512, kOddItems = 8;
 constexpr int kOddTokens = 256;  // behind them no row of the item sees a token
 constexpr int kTcFull8 = 768, kTcEmpty8 = 832, kTcScaleFull = 896;  // 8 bits: the ring of codes; the rings' tiles' scales
 constexpr int kTcMl = 1024;  // [2][128] (m, l)
@@ -75,13 +75,12 @@ constexpr int kTcSched = 3 * 1024;
 constexpr int kMaxCodeSlots = 8, kScaleTiles = 8;
 constexpr int kTcFactor = 3 * 1024, kTcScales = 4 * 1024, kTcWords = kTcScales + 2 * kScaleTiles * 48, kTcSched8 = 6 * 1024;
 static_assert(kTcWords + kMaxCodeSlots * 48 <= kTcSched8, "scales");
-static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 64 && kTcScaleFull + 2 * kScaleTiles * 8 <= kTcMl && kTcOdd + 64 <= kTcFin && kTcQFree + 16 <= kTcOdd8 && kTcOdd8 + 256 <= kTcFull8, "slots");
+static_assert(kMaxSlots * 8 <= 128 && kMaxCodeSlots * 8 <= 64 && kTcScaleFull + 2 * kScaleTiles * 8 <= kTcMl && kTcOdd + 64 <= kTcFin && kTcQFree + 16 <= kTcOdd8 && kTcOdd8 + kOddItems * 32 <= kTcFull8, "slots");
 
 template <int HD, bool PAIR, bool E8, bool DUAL>
 struct TcCfg {
+    static_assert(!E8 || !DUAL, "groups apart would convert every tile twice");
     static constexpr int ROWS = PAIR ? 256 : 128;
-    static constexpr int kConvertThreads = DUAL ? 64 : 128;  // that convert a tile together
-    static constexpr int kOddItems = DUAL ? 4 : 8;
     static constexpr int kSlotBytes = KT * HD * 2;
     static constexpr int kCodeBytes = KT * HD;  // 8 bits: of a tile of codes
     // also the groups' exchange, 2 x 16 KB
@@ -92,10 +91,10 @@ struct TcCfg {
         const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (E8 ? 4 * kCodeBytes : 0)) / kSlotBytes;
         return (int)(E8 && n >= 8 ? 8 : n < kMaxSlots ? n : kMaxSlots) / (DUAL ? 2 : 1) * (DUAL ? 2 : 1);
     }
-    // an even number (for each group that has its own): K's tiles lie in the even ones
+    // an even number: K's tiles lie in the even ones
     static constexpr int code_slots(int B)
     {
-        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (size_t)slots(B) * kSlotBytes) / kCodeBytes / (DUAL ? 4 : 2) * (DUAL ? 4 : 2);
+        const size_t n = (227 * 1024 - 1024 - q_off(B) - kQBytes - (size_t)slots(B) * kSlotBytes) / kCodeBytes / 2 * 2;
         return !E8 ? 0 : n < kMaxCodeSlots ? (int)n : kMaxCodeSlots;
     }
     static constexpr size_t smem(int B) { return 1024 + q_off(B) + kQBytes + (size_t)slots(B) * kSlotBytes + (size_t)code_slots(B) * kCodeBytes; }
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
 {
     constexpr bool DUAL = CAUSAL && !PAIR;  // the groups apart
     using C = TcCfg<HD, PAIR, E8, DUAL>;
-    constexpr int ROWS = C::ROWS, kConvertThreads = C::kConvertThreads, kOddItems = C::kOddItems;
+    constexpr int ROWS = C::ROWS;
     constexpr bool ALT = !PAIR && !DUAL;  // the groups take every other tile of the same rows
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
@@ -280,12 +279,12 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
     unsigned* odd = reinterpret_cast<unsigned*>(smem + kTcOdd);
     float* ml = reinterpret_cast<float*>(smem + kTcMl);
     uint8_t* qbuf = smem + q_off;
-    // Groups apart: each has its queries, ring and codes in one piece, which at the end takes a slice of the parts
+    // Groups apart: each has its queries and ring in one piece, which at the end takes a slice of the parts
     constexpr int kOwnQ = DUAL ? C::kQBytes / 2 : C::kQBytes;
-    const uint32_t own_bytes = kOwnQ + slots / 2 * C::kSlotBytes + code_slots / 2 * C::kCodeBytes;
+    const uint32_t own_bytes = kOwnQ + slots / 2 * C::kSlotBytes;
     uint8_t* ring = qbuf + kOwnQ;
     // 8 bits: the ring of codes and its barriers, and where the scales lie
-    [[maybe_unused]] uint8_t* code_ring = ring + (size_t)(DUAL ? slots / 2 : slots) * C::kSlotBytes;
+    [[maybe_unused]] uint8_t* code_ring = ring + (size_t)slots * C::kSlotBytes;
     [[maybe_unused]] uint64_t* full8 = reinterpret_cast<uint64_t*>(smem + kTcFull8);
     [[maybe_unused]] uint64_t* empty8 = reinterpret_cast<uint64_t*>(smem + kTcEmpty8);
     // [ring][tile % 8]. A tile's K is converted when the products of tiles after the eighth before it are done, so nobody
@@ -305,12 +304,12 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         }
         for (uint32_t i = 0; E8 && i < code_slots; ++i) {
             // each box's lane, and again in K's slots where it has fetched scales
-            mbar_init(&full8[i], 1 + pieces + (i & 1 ? 0 : pieces));  // a group's first slot is even
+            mbar_init(&full8[i], 1 + pieces + (i & 1 ? 0 : pieces));
             mbar_init(&empty8[i], kConvertThreads / 32);
         }
         for (int i = 0; E8 && i < 2 * kScaleTiles; ++i)
             mbar_init(&scale_full[i], 1);
-        for (int i = 0; E8 && i < 64; ++i)
+        for (int i = 0; E8 && i < kOddItems * 8; ++i)
             odd8[i] = 0;
         for (int i = 0; i < 4; ++i) {
             mbar_init(&s_full[i], 1);
@@ -353,13 +352,6 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
             return;
         qbuf += w * own_bytes;
         ring += w * (own_bytes - ring_slots * C::kSlotBytes);
-        if (E8) {
-            const uint32_t first = w * (code_slots / 2);
-            full8 += first;
-            empty8 += first;
-            code_ring += w * own_bytes;
-            words += first * 12;
-        }
     };
     // The first token that not every row of an item sees
     auto hidden_from = [&](const Segment& g) { return g.q.base + (CAUSAL ? p.token_of(g.rt * ROWS) : 0); };
@@ -368,9 +360,6 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
         // ---- codes to fp16: a thread 16 codes of a row. Eight lanes take the same piece of eight rows, so that
         // neither their reads nor their writes meet in a bank
-        const int w = DUAL ? (warp - 12) >> 1 : 0, u0 = first_unit(w), u1 = end_unit(w);
-        const uint32_t my_codes = DUAL ? code_slots / 2 : code_slots;
-        to_group(w);
         const int ct = threadIdx.x & (kConvertThreads - 1);
         const int r8 = ct & 7, c = (ct >> 3) % (HD / 16), first_row = (ct >> 3) / (HD / 16) * 8 + r8;
         constexpr int kStep = kConvertThreads / (HD / 16);  // rows that the threads take at once
@@ -379,15 +368,15 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             return __all_sync(0xffffffffu, attn_wait(bar, parity, flags, p.status, p.limit_ns)) != 0;
         };
-        for (int u = u0; u < u1 && !gone;) {
-            const Segment g = shares.segment(u, u1);
+        for (int u = cta_u0; u < cta_u1 && !gone;) {
+            const Segment g = shares.segment(u, cta_u1);
             u += g.units;
             if (g.t0 == g.t1)
                 continue;
             const int hidden = hidden_from(g), len = g.q.len();
-            unsigned* odd_bits = odd8 + (w * kOddItems + seg % kOddItems) * 8;
+            unsigned* odd_bits = odd8 + seg % kOddItems * 8;
             for (int t = g.t0; t < g.t1 && !gone; ++t) {
-                const int r = DUAL ? w : PAIR ? 0 : (t - g.t0) & 1, k0 = t * KT;
+                const int r = PAIR ? 0 : (t - g.t0) & 1, k0 = t * KT;
                 const bool edge = k0 + KT > hidden;
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t slot = r * ring_slots + next_slot[r];
@@ -465,7 +454,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                         next_slot[r] = 0;
                         ++pass[r];
                     }
-                    if (++from == my_codes) {
+                    if (++from == code_slots) {
                         from = 0;
                         from_phase ^= 1;
                     }
@@ -478,7 +467,6 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
         if (warp == 8 || (DUAL && warp == 11)) {
             // ---- producer: a lane a box (64 columns of one page's rows of the tile); K then V of each tile
             const int w = DUAL && warp == 11 ? 1 : 0, u0 = first_unit(w), u1 = end_unit(w);
-            const uint32_t my_codes = DUAL ? code_slots / 2 : code_slots;
             to_group(w);
             const int z = lane / pieces, piece = lane % pieces;
             const bool active = lane < pieces * (E8 ? 1 : HD / 64);
@@ -515,7 +503,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                     const bool in = active && row < len, good = page >= 0 && page < p.c.n_pages;
                     if (in && !good)
                         record_status(p.status, TF_E_INVALID_ARG);
-                    const int r = DUAL && !E8 ? w : PAIR || E8 ? 0 : (t - g.t0) & 1;
+                    const int r = DUAL ? w : PAIR || E8 ? 0 : (t - g.t0) & 1;
                     for (int kv = 0; kv < 2; ++kv) {
                         if constexpr (E8) {
                             const uint32_t slot = next_slot[0];
@@ -548,7 +536,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                                 }
                                 mbar_arrive(&full8[slot]);
                             }
-                            if (++next_slot[0] == my_codes) {
+                            if (++next_slot[0] == code_slots) {
                                 next_slot[0] = 0;
                                 ++pass[0];
                             }
@@ -579,7 +567,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                 mbar_wait_bounded(&q_ready[w], (items - 1) & 1, p.limit_ns);
             if (gone)  // each slot's last one
                 for (int r = 0; r < (PAIR || E8 ? 1 : 2); ++r)
-                    for (uint32_t s = 0; s < (E8 ? my_codes : ring_slots); ++s) {
+                    for (uint32_t s = 0; s < (E8 ? code_slots : ring_slots); ++s) {
                         const uint32_t uses = pass[r] + (s < next_slot[r] ? 1 : 0);
                         if (uses > 0)
                             mbar_wait_bounded(E8 ? &full8[s] : &full[r * ring_slots + s], (uses - 1) & 1, p.limit_ns);

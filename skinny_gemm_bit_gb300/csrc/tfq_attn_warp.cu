@@ -120,7 +120,7 @@ __device__ __forceinline__ int scale_bits(uint32_t word, uint32_t at) { return m
 
 constexpr float kHead = 7.f;  // fp16 weights reach 2^(kGrow + kHead) = 2^15, and 2^-24 is 2^-31 of a row's reference
 
-// Tile scores of 8 bits: the rows' weights in fp16, RW row tiles of 16 (16 RW query rows an item).
+// RW row tiles of 16: 16 RW query rows an item.
 template <int HD, int RW, bool E8>
 __global__ void __launch_bounds__(Cfg<HD, RW, E8>::kCtaThreads, Cfg<HD, RW, E8>::kCtas)
     tree_attn_warp_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map)
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(Cfg<HD, RW, E8>::kCtaThreads, Cfg<HD, RW, E8>:
     [[maybe_unused]] float* row_factor = reinterpret_cast<float*>(smem + C::kRowOff);
     // of slot s, box b, at 3 (CH s + b): K's word, V's word, their scales' places in them (bits)
     [[maybe_unused]] uint32_t* scale_words = reinterpret_cast<uint32_t*>(smem + C::kScaleOff) + warp * C::kScaleWords;
-    const int box = min(p.c.page_size, KT), boxes = KT / box, bs = boxes >> 1;  // a tile is boxes = 1 << bs: 1, 2 or 4
+    const int box = min(p.c.page_size, KT), boxes = KT / box, bs = boxes >> 1;  // a tile is boxes = 1 << bs: 1 or 2
 
     if (lane == 0) {
         for (int i = 0; i < NS; ++i)
@@ -431,10 +431,10 @@ __global__ void __launch_bounds__(Cfg<HD, RW, E8>::kCtaThreads, Cfg<HD, RW, E8>:
                     see[r][0] = see[r][1] = 0u;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint64_t view = tile_mask(mask[r][h], k0 - q.base) >> (ti * 2);
+                        const uint32_t view = (uint32_t)(tile_mask(mask[r][h], k0 - q.base) >> (ti * 2));
 #pragma unroll
                         for (int i = 0; i < 4 * CH; ++i) {
-                            if ((KT == 64 ? view : (uint32_t)view) >> ((i >> 1) * 8 + (i & 1)) & 1)
+                            if (view >> ((i >> 1) * 8 + (i & 1)) & 1)
                                 see[r][h] |= 1u << i;
                             else
                                 s[r][i >> 1][2 * h + (i & 1)] = -INFINITY;
