@@ -204,6 +204,12 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
                 if (gamma != nullptr) {
                     const float mean = sum * (1.f / HD) + p.eps, near = rsqrtf(mean);
                     inv = fmaf(near * 0.5f, fmaf(-mean * near, near, 1.f), near);  // a Newton step: the last bit counts too
+                    if (!(mean < INFINITY)) {  // rare: as in a cache of bf16, finite values give 0 and infinite ones NaN
+                        inv = 1.f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            x[k] = mul2(x[k], make_float2(near, near)), y[k] = mul2(y[k], make_float2(near, near));
+                    }
                     float2 g[4];
                     unpack8(__ldg(gamma + c0), g);
 #pragma unroll

@@ -254,6 +254,29 @@ def test_store_repeats_in_a_graph_on_another_stream_and_reports(T):
     assert T.tf_workspace_status(ws) == T.TF_E_INVALID_ARG
 
 
+def test_sums_of_squares_past_fp32_give_what_a_bf16_cache_gets(T):
+    """Finite rows whose squares overflow: 0; with an infinity among them, NaN where it is and where it is turned to."""
+    qkv = rand((6, 4 * 64), 40, 2.0)
+    qkv[1] *= 2.0 ** 100
+    qkv[2, 5] = 2.0 ** 90
+    qkv[3, 64 + 7] = float("inf")
+    qkv[4, 128 + 9] = float("inf")
+    gamma = rand((64,), 41) * 2.0 ** 40
+    rope = T.RopeTable(1e4 ** (-np.arange(32) / 32))
+    got = []
+    for dtype in (E4M3, torch.bfloat16):
+        c = T.KVCache.create(1, 1, 64, 16, 1, 1, 1, dtype=dtype)
+        q = T.tf_qk_norm_rope_run(qkv, c, 0, i32([0] * 6), i32(list(range(6))), rope, q_gamma=gamma, k_gamma=gamma)
+        k = c.data[0, 0, 0, 0, :6].float()
+        got.append((q.float().cpu(), k.cpu()))
+    (q8, k8), (q16, k16) = got
+    assert torch.equal(q8.isnan(), q16.isnan()) and torch.equal(k8.isnan(), k16.isnan())
+    assert q8[3].isnan().any() and k8[4].isnan().any() and not q8[:3].isnan().any()
+    for i in (1, 2):  # row 2's first head alone
+        assert (q8[i, :64] == 0).all() and (q16[i, :64] == 0).all()
+    assert (k8[1] == 0).all() and (k16[1] == 0).all()
+
+
 # ---------------------------------------------------------------- attention
 
 def chain(rows):
