@@ -40,6 +40,8 @@ int attn_over(int rows, int64_t items)
 int prompt_rows(const CacheView& c) { return c.code == TF_KV_E4M3 ? 256 : 128; }
 constexpr int kPromptOver = 4;
 
+constexpr int kMostShares = 2;  // shares an SM: two CTAs of few rows over 8 bits, two groups of a prompt's
+
 struct AttnLayout {
     size_t counters, parts, total;
 };
@@ -50,7 +52,8 @@ AttnLayout attn_layout(const CacheView& c, int rows, bool causal)
     const size_t ctas = (size_t)device_sms() * (causal && rows == 128 ? 2 : rows > 64 ? 1 : attn_warp_ctas(c, rows));
     AttnLayout L{};
     L.counters = 256;
-    L.parts = L.counters + (ctas * 2 * sizeof(unsigned) + 255) / 256 * 256;
+    // as many counters for every shape: no call's parts lie where another's counters have to be zero
+    L.parts = L.counters + ((size_t)device_sms() * kMostShares * 2 * sizeof(unsigned) + 255) / 256 * 256;
     L.total = L.parts + 2 * ctas * rows * (c.head_dim + 2) * sizeof(float);  // two parts a CTA
     return L;
 }

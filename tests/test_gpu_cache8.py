@@ -610,3 +610,28 @@ def test_reset_and_the_binding(T):
             T.KVCache(d, c.book, 2, c.max_pages, scales=s)
     with pytest.raises(T.TfqError):  # an odd number of scales, and no room for the word's end
         T.KVCache(data[:1, :, :1, :1].contiguous(), c.book, 2, 1, scales=scales[:1, :, :1, :1].clone().contiguous())
+
+
+def test_one_workspace_for_calls_of_all_shapes(T):
+    """The largest of them, over both kinds of cache: each finds it as the others left it."""
+    cs = [paged(T, [4000, 900], 2, 64, 16, 77, dtype=dtype) for dtype in (E4M3, torch.bfloat16)]
+    calls = [(c, rows) for c in cs for rows in (1, 16, 64, 5, 2)]
+    need = max(T.tf_tree_attn_workspace_bytes(c, 16, 2, rows) for c, rows in calls)
+    prompt_need = max(T.tf_prompt_attn_workspace_bytes(c, 16, 2) for c in cs)
+    ws, prompt_ws = T.workspace(need), T.workspace(prompt_need)
+    q = rand((128, 16 * 64), 79)
+
+    def run(c, rows, w):
+        return T.tf_tree_attn_run(q[: 2 * rows], c, 0, i32([0, 1]), i32([0, rows, 2 * rows]), max_rows=rows, ws=w)
+
+    def prompt(c, w):
+        return T.tf_prompt_attn_run(q, c, 0, i32([0, 1]), i32([0, 90, 128]), ws=w)
+
+    want = [run(c, rows, T.workspace(need)) for c, rows in calls]
+    want_prompt = [prompt(c, T.workspace(prompt_need)) for c in cs]
+    for _ in range(2):
+        for (c, rows), w in zip(calls, want):
+            assert torch.equal(run(c, rows, ws), w)
+        for c, w in zip(cs, want_prompt):
+            assert torch.equal(prompt(c, prompt_ws), w)
+    assert T.tf_workspace_status(ws) == T.TF_OK and T.tf_workspace_status(prompt_ws) == T.TF_OK
