@@ -154,7 +154,7 @@ struct Shares {
             const int2 mine = counted(first);
             int2* found = reinterpret_cast<int2*>(seq + p.B + 1);  // of each warp
             const int most = __reduce_max_sync(0xffffffffu, mine.x), sum = __reduce_add_sync(0xffffffffu, mine.y);
-            if (threadIdx.x % 32 == 0)
+            if (threadIdx.x % 32 == 0 && (int)threadIdx.x < p.B)  // 8 warps at most: the call looks at 256 sequences or fewer
                 found[threadIdx.x / 32] = make_int2(most, sum);
             __syncthreads();
             int2 all = make_int2(0, 0);
