@@ -11,7 +11,7 @@
 // of two: the division, and the raising of a scale that the block has, are exact but for e4m3's subnormals, and an
 // attention adds exponents to its scores.
 //
-// 8191 rows of 16 + 2 * 8 heads of 128: 30.6 us, 3.8 TB/s of reads and writes, three quarters of the issue slots: what a row
+// 8191 rows of 16 + 2 * 8 heads of 128: 29.6 us, 4.0 TB/s of reads and writes, three quarters of the issue slots: what a row
 // costs before its first head and the meetings at half of the sets bound it (without norm and rotation 30.1). One warp to
 // 16 rows of a head, which needs no meeting but 128 registers for the values: 46 us; a pair of warps 35. CTAs that
 // take equal runs of sets of heads in the place of halves of them: 31.0. One row 3.6 us, 64 rows of 64 sequences 5.0.
@@ -108,6 +108,14 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
             f[k] = __ldg(reinterpret_cast<const uint2*>(p.turns + idx));
         }
     }
+    // the norms' weights in fp32, as the lanes take them: unpacked once and not for every head (8191 rows 30.9 us)
+    __shared__ float4 gammas[2][4][LANES];
+    uint4 ga = {}, gb = {};
+    const uint4* gamma = reinterpret_cast<const uint4*>(warp == 0 ? p.q_gamma : warp == 1 ? p.k_gamma : nullptr);
+    if (gamma != nullptr && lane < LANES) {
+        ga = __ldg(gamma + c0);
+        gb = __ldg(gamma + c1);
+    }
     pdl_wait();
     pdl_launch_dependents();
 
@@ -121,6 +129,15 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
         if (lane == 0)
             before = g0 > 0 ? p.slots[g0 - 1] : -1;
         first = __ballot_sync(0xffffffffu, g0 + lane >= p.M || mine < 0 || before < 0 || mine >> 4 != before >> 4 || mine <= before);
+    }
+    if (warp < 2 && lane < LANES) {
+        float2 g[4];
+        unpack8(ga, g);
+        gammas[warp][0][lane] = make_float4(g[0].x, g[0].y, g[1].x, g[1].y);
+        gammas[warp][1][lane] = make_float4(g[2].x, g[2].y, g[3].x, g[3].y);
+        unpack8(gb, g);
+        gammas[warp][2][lane] = make_float4(g[0].x, g[0].y, g[1].x, g[1].y);
+        gammas[warp][3][lane] = make_float4(g[2].x, g[2].y, g[3].x, g[3].y);
     }
     const unsigned ours = first & ((1u << p.step) - 1), later = first >> p.step;  // step <= 16
     if (ours == 0)
@@ -177,6 +194,8 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
         const int hi = min(e - s, behind ? r + __ffs((int)behind) : e - s);
         const unsigned stored = __reduce_or_sync(0xffffffffu, lane - s >= lo && lane - s < hi ? 1u << (mine & 15) : 0u);
         const bool anew = stored & 1;
+        if (s == begin)
+            __syncthreads();  // the norms' weights are there
         const int place = (slot >> p.c.page_shift) * n_kv * p.c.page_size + (slot & (p.c.page_size - 1));  // fewer than 2^31 rows
 #pragma unroll 1
         for (int h0 = part * HEADS; h0 < heads; h0 += p.parts * HEADS) {
@@ -191,7 +210,7 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
             unpack8(nb, y);
             fetch(h0 + p.parts * HEADS);
             float inv = 1.f;
-            const uint4* gamma = reinterpret_cast<const uint4*>(is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr);
+            const bool norm = (is_q ? p.q_gamma : is_k ? p.k_gamma : nullptr) != nullptr;
             if (h0 < p.n_q + n_kv) {  // else the warp has values alone
                 float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
@@ -201,7 +220,7 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
 #pragma unroll
                 for (int o = LANES / 2; o > 0; o >>= 1)
                     sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (gamma != nullptr) {
+                if (norm) {
                     const float mean = sum * (1.f / HD) + p.eps, near = rsqrtf(mean);
                     inv = fmaf(near * 0.5f, fmaf(-mean * near, near, 1.f), near);  // a Newton step: the last bit counts too
                     if (!(mean < INFINITY)) {  // rare: as in a cache of bf16, finite values give 0 and infinite ones NaN
@@ -210,15 +229,13 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
                         for (int k = 0; k < 4; ++k)
                             x[k] = mul2(x[k], make_float2(near, near)), y[k] = mul2(y[k], make_float2(near, near));
                     }
-                    float2 g[4];
-                    unpack8(__ldg(gamma + c0), g);
+                    const float4(*g)[LANES] = gammas[is_q ? 0 : 1];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        x[k] = mul2(x[k], g[k]);
-                    unpack8(__ldg(gamma + c1), g);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        y[k] = mul2(y[k], g[k]);
+                    for (int k = 0; k < 2; ++k) {
+                        const float4 a = g[k][j], b = g[2 + k][j];
+                        x[2 * k] = mul2(x[2 * k], make_float2(a.x, a.y)), x[2 * k + 1] = mul2(x[2 * k + 1], make_float2(a.z, a.w));
+                        y[2 * k] = mul2(y[2 * k], make_float2(b.x, b.y)), y[2 * k + 1] = mul2(y[2 * k + 1], make_float2(b.z, b.w));
+                    }
                 }
                 if (rot && (is_q || is_k)) {
                     if (p.interleaved) {
