@@ -38,8 +38,8 @@
 // rest stay as they are; Q and the weights are fp16 too. The blocks' scales enter the scores and the weights, as in
 // tfq_attn_warp.cu: with the products' own constants for each 16 keys they cost nothing an element. The
 // converting warps also zero what lies behind a sequence's end and take out NaN. The 64-row trees above take 161 us so,
-// where bf16 takes 124: shared memory carries a tile once more in and out (some 1540 of 2060 cycles a tile are its
-// traffic, Q K^T's most of it), and the conversions share the softmax's issue slots (144 us with zeros in their place).
+// where bf16 takes 124: shared memory carries a tile once more in and out, and the conversions share the softmax's
+// issue slots (144 us with zeros in their place). Q in tensor memory, for which head_dim 64 has room, gained nothing.
 #include "tfq_attn.cuh"
 
 namespace tfq {
