@@ -458,7 +458,7 @@ int tf_generate_greedy(const tf_decoder_desc* d, const int32_t* prompt, int64_t 
  * book after a call depends on nothing but the book before it and the arguments.
  */
 typedef struct tf_kvcache {
-    uint32_t magic;     /* TF_KVCACHE_MAGIC once filled by tf_kvcache_init */
+    uint32_t magic;     /* TF_KVCACHE_MAGIC once filled by tf_kvcache_init, _E4M3 by tf_kvcache_init_e4m3 */
     int32_t n_layers;
     int32_t n_kv;       /* key/value heads, 1..256 */
     int32_t head_dim;   /* 64, 128 or 256 */
@@ -468,13 +468,16 @@ typedef struct tf_kvcache {
     int32_t max_pages;  /* page-table columns of a slot */
     void* data;         /* 16-byte aligned */
     int32_t* book;      /* 4-byte aligned */
-    int32_t code;       /* TF_KV_BF16 or TF_KV_E4M3 */
-    uint8_t* scales;    /* TF_KV_E4M3: the blocks' scales, 4-byte aligned; else NULL */
+    /* TF_KVCACHE_MAGIC_E4M3 alone: a bf16 descriptor ends here for every call, which neither writes nor reads what
+       follows, so that callers built when it did end here run as they are */
+    int32_t code;       /* TF_KV_E4M3 */
+    uint8_t* scales;    /* the blocks' scales, 4-byte aligned */
 } tf_kvcache;
 #define TF_KV_BF16 0
 #define TF_KV_E4M3 1
 #define TF_KV_BLOCK 16 /* rows of a page that share a scale */
 #define TF_KVCACHE_MAGIC 0x314B5654u /* "TVK1" */
+#define TF_KVCACHE_MAGIC_E4M3 0x324B5654u /* "TVK2" */
 #define TF_MAX_DRAFT_ROWS 64 /* rows of a sequence that one attention or keep call takes */
 
 /* Bytes of `data` and int32 elements of `book`; 0 for an unsupported shape. */

@@ -664,18 +664,19 @@ int check_cache(const tf_kvcache* c, const char* name, CacheView* v)
 {
     if (c == nullptr)
         return report_error(TF_E_INVALID_ARG, "%s: cache descriptor is NULL", name);
-    if (c->magic != TF_KVCACHE_MAGIC)
+    const bool e4m3 = c->magic == TF_KVCACHE_MAGIC_E4M3;  // else nothing behind `book` is looked at
+    if (!e4m3 && c->magic != TF_KVCACHE_MAGIC)
         return report_error(TF_E_INVALID_ARG, "%s: cache descriptor not filled by tf_kvcache_init", name);
     if (!shape_ok(c->n_layers, c->n_kv, c->head_dim, c->page_size, c->n_pages) ||
         !book_ok(c->n_seqs, c->max_pages, c->page_size))
         return report_error(TF_E_UNSUPPORTED_SHAPE, "%s: cache shape out of range", name);
     if (c->data == nullptr || c->book == nullptr || !is_aligned(c->data, 16) || !is_aligned(c->book, 4))
         return report_error(TF_E_INVALID_ARG, "%s: cache data or book NULL or misaligned", name);
-    if ((c->code != TF_KV_BF16 && c->code != TF_KV_E4M3) || (c->code == TF_KV_E4M3) != (c->scales != nullptr) || !is_aligned(c->scales, 4))
-        return report_error(TF_E_INVALID_ARG, "%s: cache code unknown, or its scales NULL, misaligned or not asked for", name);
+    if (e4m3 && (c->code != TF_KV_E4M3 || c->scales == nullptr || !is_aligned(c->scales, 4)))
+        return report_error(TF_E_INVALID_ARG, "%s: cache code unknown, or its scales NULL or misaligned", name);
     v->data = static_cast<uint16_t*>(c->data);
-    v->code = c->code;
-    v->scales = c->scales;
+    v->code = e4m3 ? TF_KV_E4M3 : TF_KV_BF16;
+    v->scales = e4m3 ? c->scales : nullptr;
     v->len = c->book;
     v->refs = c->book + c->n_seqs;
     v->table = v->refs + c->n_pages;
@@ -778,8 +779,6 @@ static int init_cache(const char* name, int n_layers, int n_kv, int head_dim, in
     desc->max_pages = (int32_t)max_pages;
     desc->data = data;
     desc->book = book;
-    desc->code = elem == 1 ? TF_KV_E4M3 : TF_KV_BF16;
-    desc->scales = nullptr;
     return TF_OK;
 }
 
@@ -805,6 +804,8 @@ int tf_kvcache_init_e4m3(int n_layers, int n_kv, int head_dim, int page_size, in
         return rc;
     if (scale_bytes < tf_kvcache_scale_bytes(n_layers, n_kv, page_size, n_pages))
         return report_error(TF_E_WORKSPACE_TOO_SMALL, "%s: scales too small for the shape", name);
+    made.magic = TF_KVCACHE_MAGIC_E4M3;
+    made.code = TF_KV_E4M3;
     made.scales = scales;
     *desc = made;
     return TF_OK;

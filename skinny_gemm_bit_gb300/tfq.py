@@ -41,6 +41,7 @@ TF_TUNE_WARPS = 4
 TF_TUNE_MODE = 5
 TF_TUNE_CHAIN = 6
 TF_KVCACHE_MAGIC = 0x314B5654
+TF_KVCACHE_MAGIC_E4M3 = 0x324B5654
 TF_KV_BF16 = 0
 TF_KV_E4M3 = 1
 TF_KV_BLOCK = 16
