@@ -245,20 +245,6 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v)
     return d;
 }
 
-// The four E4M3 bytes of v as two fp16 pairs, bytes 0 and 1 in r0.
-__device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t v, uint32_t& r0, uint32_t& r1)
-{
-    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;\n}" : "=r"(r0), "=r"(r1) : "r"(v));
-}
-
-// lo and hi as E4M3, rounded to nearest even, +-448 where larger (bits 0-7 and 8-15).
-__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi)
-{
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 // a * (low half of s, twice) and a * (high half of s, twice), fp16 pairs.
 __device__ __forceinline__ uint32_t hmul2_lo(uint32_t a, uint32_t s)
 {
