@@ -603,7 +603,9 @@ int tf_rope_turns(const double* inv_freq, int64_t n, uint64_t* turns);
  *   where it grows, the codes of the block's other rows are rounded to it (exact but where they become subnormal)
  *   code = e4m3(x / scale), +-448 for what is larger (infinities among them), NaN for NaN
  * Rows that go to one block are neighbours in the call, in the order of their slots, as tf_kvcache_extend gives
- * them, and a block's rows are stored in order over the calls. The same call again changes nothing.
+ * them, and a block's rows are stored in order over the calls. The same call again changes nothing. Rows behind
+ * others of their block, out of that order or not beside them, are not stored and record TF_E_INVALID_ARG, where
+ * those are among the 32 rows before; farther apart they are not looked for, and the block's scale is any of theirs.
  */
 int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, const uint16_t* q_gamma,
                         const uint16_t* k_gamma, float eps, const int32_t* positions, const uint64_t* turns,

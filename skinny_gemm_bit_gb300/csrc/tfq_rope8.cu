@@ -11,7 +11,7 @@
 // of two: the division, and the raising of a scale that the block has, are exact but for e4m3's subnormals, and an
 // attention adds exponents to its scores.
 //
-// 8191 rows of 16 + 2 * 8 heads of 128: 29.6 us, 4.0 TB/s of reads and writes, three quarters of the issue slots: what a row
+// 8191 rows of 16 + 2 * 8 heads of 128: 29.9 us, 3.9 TB/s of reads and writes, three quarters of the issue slots: what a row
 // costs before its first head (some 3 us for each part that its heads are dealt into) and the meetings at half of the sets
 // bound it (without norm and rotation 28.1). One warp to 16 rows of a head, which needs no meeting but 128 registers for
 // the values, took 46 us where this took 31; a pair of warps 35; CTAs that take equal runs of sets of heads in the place
@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
     // at or behind g0 + step. A run has 16 rows at most, so both lie within 32 rows.
     const int32_t mine = g0 + lane < p.M ? p.slots[g0 + lane] : -1;  // a row's slot a lane, and its position
     const int32_t my_pos = g0 + lane < p.M ? p.positions[g0 + lane] : 0;
+    const int32_t prior = g0 + lane >= 32 ? p.slots[g0 - 32 + lane] : -1;  // the 32 rows before g0 (8191 rows 29.6 us without)
     unsigned first;
     {
         int32_t before = __shfl_up_sync(0xffffffffu, mine, 1);
@@ -182,29 +183,32 @@ __global__ void __launch_bounds__(kThreads8, 2) qk_norm_rope8_kernel(const __gri
             }
         }
         int32_t slot = __shfl_sync(0xffffffffu, mine, at & 31);
-        const bool bad = row_in && slot >= (int64_t)p.c.n_pages << p.c.page_shift;
+        // the row's run: rows lo .. hi, from s; and which rows of its block those are
+        const unsigned runs = first >> s;
+        const int r = row_in ? warp : 0, lo = 31 - __clz((int)(runs & (2u << r) - 1));
+        // a run of its block's among the 32 rows before the row's own: two would race for the scale, so this one is refused
+        const int32_t other = lane < s + lo ? mine : prior;
+        const bool again = __any_sync(0xffffffffu, (uint32_t)(other ^ slot) < 16u);
+        const bool bad = row_in && slot >= 0 && (again || slot >= (int64_t)p.c.n_pages << p.c.page_shift);
         if (bad && part == 0 && lane == 0)
             record_status(p.status, TF_E_INVALID_ARG);
         const bool store = row_in && slot >= 0 && !bad;
         if (!store)
             slot = 0;
-        // the row's run: rows lo .. hi, from s; and which rows of its block those are
-        const unsigned runs = first >> s;
-        const int r = row_in ? warp : 0, lo = 31 - __clz((int)(runs & (2u << r) - 1));
         const unsigned behind = runs >> (r + 1);
         const int hi = min(e - s, behind ? r + __ffs((int)behind) : e - s);
         const unsigned stored = __reduce_or_sync(0xffffffffu, lane - s >= lo && lane - s < hi ? 1u << (mine & 15) : 0u);
         const bool anew = stored & 1;
         if (s == begin)
             __syncthreads();  // the norms' weights are there
-        const int place = (slot >> p.c.page_shift) * n_kv * p.c.page_size + (slot & (p.c.page_size - 1));  // fewer than 2^31 rows
+        const int place = store ? (slot >> p.c.page_shift) * n_kv * p.c.page_size + (slot & (p.c.page_size - 1)) : -1;  // fewer than 2^31 rows
 #pragma unroll 1
         for (int h0 = part * HEADS; h0 < heads; h0 += p.parts * HEADS) {
             const int h = h0 + sub;
             const bool is_q = h < p.n_q, is_k = !is_q && h < p.n_q + n_kv, live = row_in && h < heads;
             // the pool's row, and its block's scale before the call
             const int at_row = is_q ? 0 : place + ((p.layer * 2 + (is_k ? 0 : 1)) * p.c.n_pages * n_kv + h - p.n_q - (is_k ? 0 : n_kv)) * p.c.page_size;
-            const bool stores = store && live && !is_q;
+            const bool stores = place >= 0 && live && !is_q;
             const int was = stores && !anew ? p.c.scales[at_row >> 4] : 0;
             float2 x[4], y[4];
             unpack8(na, x);
@@ -334,7 +338,7 @@ cudaError_t launch_rope8(const RopeParams& given, bool pdl, cudaStream_t stream)
     const int per_warp = 512 / p.c.head_dim, most_parts = (p.n_q + 2 * p.c.n_kv + per_warp - 1) / per_warp;
     const int64_t want = (int64_t)device_sms() * 2;
     // few rows: a CTA begins at fewer of them, and its heads are spread over as many CTAs as run at once, twice over:
-    // 8191 rows 29.6 us in two parts, 30.1 in one, 35.6 in four
+    // 8191 rows 29.9 us in two parts; 0.5 more in one, 6 in four
     p.step = kRows8;
     while (p.step > 1 && (p.M + p.step / 2 - 1) / (p.step / 2) * most_parts <= want)
         p.step /= 2;
