@@ -648,8 +648,11 @@ int tf_qk_norm_rope_run(const uint16_t* qkv, int64_t ld, int64_t M, int n_q, con
  * records TF_E_UNSUPPORTED_SHAPE and writes nothing.
  * Over a cache of 8 bits the codes are multiplied as they are, in fp16, which holds every e4m3 value, and the blocks'
  * scales enter the scores and the weights. A query row is scaled by a power of two into fp16's range (2^60 at most; its
- * values below 2^-38 of its largest are lost), and the weights are rounded to fp16: 2^-11 of each, those
- * below 2^-32 of the row's largest lost. Its outputs are as near to 64 bits as their own rounding.
+ * values below 2^-38 of its largest are lost). What is rounded to fp16 is w_j = p_j * the scale of token j's block of
+ * values, p_j its softmax weight: by up to 2^-11 of itself down to 2^-21 of the row's largest w, and by up to 2^-32 of that
+ * largest below, where the least are lost; a token adds code * w_j, so up to 448 times that. Where the scales of the
+ * values that a row sees are alike, its outputs are as near to 64 bits as their own rounding; where they lie 2^20 and
+ * more apart, tokens of large p in blocks of small values are known the less well, beside values that much larger.
  */
 size_t tf_tree_attn_workspace_bytes(const tf_kvcache* c, int n_q, int64_t B, int max_rows);
 int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const tf_kvcache* c, int layer,

@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(tc_threads(E8), 1)
                     // they add 2^-8 of sum p |v| at most; 64-row trees over 16,001 tokens: 0.0023 of the output's
                     // norm against 64 bits, 0.0017 of it the output's own rounding
                     auto weigh = [&]() {
-                        if constexpr (E8) {  // fp16: 2^-11 of each, below 2^-29 of the row's reference 2^-40 of it
+                        if constexpr (E8) {  // fp16: 2^-11 of each, or 2^-32 of the row's reference (2^7) below 2^-21 of it
                             const float ref = (m == -INFINITY ? 0.f : m) - kHead;
                             float added = 0.f;
 #pragma unroll

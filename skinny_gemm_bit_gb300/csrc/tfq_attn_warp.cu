@@ -485,7 +485,8 @@ __global__ void __launch_bounds__(Cfg<HD, RW, E8>::kCtaThreads, Cfg<HD, RW, E8>:
             // against 64 bits, 0.0017 of it the output's own rounding. Their sum is of the unrounded ones. A second
             // product with what the rounding left took 64 ragged sequences from 174 to 176 us, one token over 4097
             // from 10.6 to 10.8 and 8 x 8 rows over 2000 from 20.0 to 21.8.
-            // Over 8 bits they are rounded to fp16: 2^-11 of each, below 2^-29 of the row's reference 2^-40 of it.
+            // Over 8 bits they (with V's scales in them) are rounded to fp16: 2^-11 of each, or 2^-32 of the row's
+            // reference, 2^7, where they are below 2^-21 of it and fp16 has no more digits.
             uint32_t w[RW][CH][4];
             auto pair = [](float lo, float hi) { return E8 ? f32x2_to_f16x2(lo, hi) : f32x2_to_bf16x2(lo, hi); };
 #pragma unroll
