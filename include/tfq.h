@@ -452,7 +452,10 @@ int tf_generate_greedy(const tf_decoder_desc* d, const int32_t* prompt, int64_t 
  *   scales  uint8 [n_layers][2][n_pages][n_kv][page_size / 16]: value = code * 2^(scale - 127), scales 95 .. 159
  *           (2^-32 .. 2^32); one below counts as 95, one above as 159
  * Every call below takes either kind, and the attentions and the decoder step too: what they store to such a cache
- * is described at tf_qk_norm_rope_run and tf_kvcache_keep.
+ * is described at tf_qk_norm_rope_run and tf_kvcache_keep. Such a cache takes half the memory. With 16 query and 8 key/value
+ * heads of 128 attention of few rows over it is the faster one over 16,000 tokens of one sequence, 4096 each of eight or
+ * 200 each of 64, and a decoder step over 4096 tokens; below, and for trees of more than 16 query rows to a key/value
+ * head, prompts and the store, whose codes have to be converted or joined, the bf16 cache is.
  *
  * Free pages are taken lowest index first, in slot order of the call's list, so the
  * book after a call depends on nothing but the book before it and the arguments.
@@ -663,7 +666,8 @@ int tf_tree_attn_run(const uint16_t* q, int64_t ldq, int64_t M, int n_q, const t
  * Attention of prompts over the cache: as tf_tree_attn_run with causal rows and no limit to a sequence's number of
  * them. Sequence b's rows q_start[b] .. q_start[b + 1) are the last T_b tokens of slot seqs[b], T_b >= 0, whose keys
  * and values are in the cache already; row i of them sees the tokens up to its own, len[seqs[b]] - T_b + i.
- * A whole prompt has T_b = len; a chunk of one has a context before it. A token's keys and values are read once for
+ * A whole prompt has T_b = len; a chunk of one has a context before it. The projections above take up to 8 rows, so a
+ * prompt's q, k and v come from elsewhere, and no other call here runs prompts. A token's keys and values are read once for
  * each 128 query rows (256 over 8 bits), the query heads that share a key/value head times the sequence's rows.
  *   head_dim 64 or 128; n_q a multiple of n_kv, at most 64 query heads to a key/value head; 1 <= B <= 1024;
  *   1 <= M < 2^21, M * n_q / n_kv < 2^25

@@ -25,7 +25,7 @@ int attn_rows(int max_rows, int group, int head_dim)
 }
 
 // A segment's own cost in key tiles of its kernel, by which the CTAs' shares are measured. With more
-// items than CTAs it is what evens out those that get several short ones (28 of the warp kernel's 32-key
+// items than SMs it is what evens out those that get several short ones (28 of the warp kernel's 32-key
 // tiles: 64 ragged sequences 176 us, 183 with 16, 199 with 8, side by side); with fewer, what a CTA gets should
 // still be a tile a warp (one token over 4097: 12.0 us with 16, 13.4 with 24).
 int attn_over(int rows, int64_t items)

@@ -33,7 +33,7 @@ struct AttnParams {
     const int32_t *seqs, *q_start;
     int B, max_rows;
     int over;  // a segment's own cost, in key tiles
-    bool few;  // no more items than CTAs, and no more sequences than threads
+    bool few;  // no more items than SMs, where one CTA or two run on each, and no more sequences than threads
     const uint64_t* masks;
     float scale_log2;  // scale * log2(e)
     uint16_t* o;
@@ -104,7 +104,10 @@ struct Shares {
     unsigned total, ctas;  // units; CTAs that have some: every one of them has at least one
     unsigned share, rest;  // total = ctas * share + rest
     int whole;             // units of an item when each has a CTA, else 0
-    static constexpr int kTorn = kLeast == 6 ? 24 : 64;  // tiles that an item more costs a split call, over all CTAs (6: two an SM)
+    // Tiles that an item more costs a split call, over all CTAs (6: two an SM). Two an SM with 24, and with another number: 8
+    // sequences' single rows over 768 tokens, 8 heads, 14.0 us and (64) 17.6, 16 over 1536 24.9 and 27.7; 8 of 8 rows over 544
+    // 14.05 and (8, 0) 14.4, single rows there 13.5 and 13.4
+    static constexpr int kTorn = kLeast == 6 ? 24 : 64;
     static constexpr int kMostTiles = 1 << 20;
 
     __host__ __device__ Shares(const AttnParams& params, void* smem)

@@ -27,8 +27,8 @@
 // Prompts (CAUSAL) have a limit in the place of a mask, and an item's key tiles end with its last row's. Over a bf16 cache
 // an item is 128 rows and each group works for itself (DUAL), with a producer warp, an MMA warp and half the ring of its
 // own, as two CTAs would (the runtime places one CTA with tcgen05 on an SM): while one begins or ends an item the
-// other computes. One prompt of 8191 rows, 16 / 8 heads of 128: 228 us, 1200 TFLOP/s (pairs of 256 rows 270); 24 packed ones
-// of up to 2047 rows 214 us (293): 3000 items of nine tiles on average, whose beginnings and ends still cost some three
+// other computes. One prompt of 8191 rows, 16 / 8 heads of 128: 225 us, 1220 TFLOP/s (pairs of 256 rows 270); 24 packed ones
+// of up to 2047 rows 213 us (293): 3000 items of nine tiles on average, whose beginnings and ends still cost some three
 // tiles each. An item's queries come by TMA as soon as the scores of the one before are formed (loaded and stored by the
 // softmax threads they took 8000 cycles an item: 250 and 268 us). Over 8 bits a pair shares its tiles, since each is
 // converted but once then: 1500 rows behind 14,001 tokens, 32 / 4 heads, 375 us, 970 TFLOP/s; apart 452.

@@ -25,7 +25,7 @@
 // w_j = 2^(x_j - m), and o = sum w_j code_j / sum w_j / vs_j. The same instructions a key for half the bytes: with eight
 // warps an SM the 64 ragged sequences took 166 us, bound by each warp's own chain of latencies; with two CTAs of six
 // 113, of which 33 are the items' beginnings and ends (7 us an item of one tile), and 80 us for each 537 MB
-// beyond that, 6.7 TB/s. 8 rows over 32,771 tokens 23 us, one token over 4097 11.7.
+// beyond that, 6.7 TB/s. 8 rows over 32,771 tokens 23.4 us, one token over 4097 11.9.
 #include "tfq_attn.cuh"
 
 namespace tfq {
@@ -44,7 +44,7 @@ struct Cfg {
     static constexpr int KT = 16 * CH;
     static constexpr int ROWS = 16 * RW;
     static constexpr int kSlotBytes = KT * HD * (E8 ? 1 : 2);  // K or V of a tile
-    // slots of a warp: 3, or 6 at head_dim 64; of 8 bits 5 to 12
+    // slots of a warp: 3, or 6 at head_dim 64; of 8 bits with one CTA an SM 5, or 10 at head_dim 64
     static constexpr int kSlots = (kCtas == 2 ? 12288 : E8 ? 20480 : 24576) / kSlotBytes;
     static constexpr int kCols = E8 ? (RW == 2 || kCtas == 2 ? 32 : 64) : RW == 2 ? 8 : 16;  // output columns joined at once, as shared memory allows
     static constexpr int kStride = kCols + 4;             // floats

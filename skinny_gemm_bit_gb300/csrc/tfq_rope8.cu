@@ -11,11 +11,12 @@
 // of two: the division, and the raising of a scale that the block has, are exact but for e4m3's subnormals, and an
 // attention adds exponents to its scores.
 //
-// 8191 rows of 16 + 2 * 8 heads of 128: 29.9 us, 3.9 TB/s of reads and writes, three quarters of the issue slots: what a row
+// 8191 rows of 16 + 2 * 8 heads of 128: 29.8 us, 3.9 TB/s of reads and writes, three quarters of the issue slots: what a row
 // costs before its first head (some 3 us for each part that its heads are dealt into) and the meetings at half of the sets
-// bound it (without norm and rotation 28.1). One warp to 16 rows of a head, which needs no meeting but 128 registers for
+// bound it (without norm and rotation 28.1; the pass into a bf16 cache 24.8). One warp to 16 rows of a head, which needs no meeting but 128 registers for
 // the values, took 46 us where this took 31; a pair of warps 35; CTAs that take equal runs of sets of heads in the place
-// of halves of them 31.0. One row 3.6 us, 64 rows of 64 sequences 5.0.
+// of halves of them 31.0. One row 3.5 us, 64 rows of 64 sequences 5.1: there one or two of the
+// 16 warps have a row. With four warps a CTA those 64 rows took 4.2, and a prompt more.
 #include "tfq_rope.cuh"
 
 namespace tfq {
@@ -338,7 +339,7 @@ cudaError_t launch_rope8(const RopeParams& given, bool pdl, cudaStream_t stream)
     const int per_warp = 512 / p.c.head_dim, most_parts = (p.n_q + 2 * p.c.n_kv + per_warp - 1) / per_warp;
     const int64_t want = (int64_t)device_sms() * 2;
     // few rows: a CTA begins at fewer of them, and its heads are spread over as many CTAs as run at once, twice over:
-    // 8191 rows 29.9 us in two parts; 0.5 more in one, 6 in four
+    // 8191 rows 29.8 us in two parts; 0.5 more in one, 6 in four
     p.step = kRows8;
     while (p.step > 1 && (p.M + p.step / 2 - 1) / (p.step / 2) * most_parts <= want)
         p.step /= 2;
